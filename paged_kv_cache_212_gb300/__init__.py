@@ -33,7 +33,11 @@ EXPORTS = ("pkv_status_string", "pkv_last_cuda_error", "pkv_set_pipeline_wait_ns
            "pkv_bm_fork", "pkv_bm_reserve_step", "pkv_bm_begin_step", "pkv_bm_end_step", "pkv_bm_export",
            # decode streamed from a host tier (include/pagedkv_stream.h)
            "pkv_sp_create", "pkv_sp_destroy", "pkv_sp_lookup", "pkv_sp_invalidate", "pkv_sp_plan_tile",
-           "paged_kv_stage_blocks", "pkv_streamed_workspace_bytes", "paged_decode_streamed")
+           "paged_kv_stage_blocks", "pkv_streamed_workspace_bytes", "paged_decode_streamed",
+           # rotary positions written into the pages (include/pagedkv_rope.h)
+           "pkv_rope_phases", "paged_kv_write_rope",
+           # sliding window with first tokens (include/pagedkv_window.h)
+           "paged_decode_attention_window", "paged_decode_step_window", "paged_prefill_attention_window")
 NOALLOC_DECODE_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -54,6 +58,12 @@ class Dims(ctypes.Structure):
     n_blocks + 1 with the scratch block last)."""
     _fields_ = [("n_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _RopeC(ctypes.Structure):
+    """pkv_rope."""
+    _fields_ = [("phases", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float)]
 
 
 _lib = None
@@ -126,6 +136,18 @@ def load_library(path: str = LIB_PATH):
                                           P, sz, P, P]
     for fn in ("pkv_sp_create", "pkv_sp_lookup", "pkv_sp_invalidate", "pkv_sp_plan_tile", "paged_kv_stage_blocks",
                "paged_decode_streamed"):
+        getattr(lib, fn).restype = ctypes.c_int
+    f32, f64, RP = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_RopeC)
+    lib.pkv_rope_phases.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, ctypes.POINTER(f32)]
+    lib.paged_kv_write_rope.argtypes = [P, i64, i32, P, i64, P, i64, RP, P, P, P, P, P, i32, Dims, P, i32, P, i32, i32,
+                                        P, P]
+    lib.paged_decode_attention_window.argtypes = [P, i32, P, P, P, P, i32, Dims, P, i32, P, i32, f32, i32, i32, P, P,
+                                                  P, P]
+    lib.paged_decode_step_window.argtypes = [P, i64, P, i64, P, P, i64, i32, RP, P, P, P, P, i32, Dims, P, i32, P, i32,
+                                             f32, i32, i32, P, P, P, P]
+    lib.paged_prefill_attention_window.argtypes = [P, i32, P, P, Dims, P, i32, P, i32, i32, f32, i32, i32, P, P, P, P]
+    for fn in ("pkv_rope_phases", "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
+               "paged_prefill_attention_window"):
         getattr(lib, fn).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -592,6 +614,296 @@ def paged_prefill_attention(q, k_pool, v_pool, block_tables, prefix_lens, softma
                                      chunk, float(softmax_scale), _ptr(out), _ptr(lse_out), _ptr(dev_status),
                                      _stream(stream))
     _check("paged_prefill_attention", st)
+    return out
+
+
+# ---- rotary positions and sliding windows -----------------------------------
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+_ROPE_TURNS = {"bands": (1.0, 4.0), "yarn": (1.0, 32.0)}      # low_turns, high_turns
+
+
+class Rope:
+    """The rotary turn of a model: rot_dim of each head's elements, pairs in the
+    half layout (i, i + rot_dim / 2) or interleaved (2 i, 2 i + 1), frequencies
+    base^(-2 i / rot_dim) scaled for contexts beyond original_context by
+    ``factor`` ("linear", "ntk", "bands", "yarn": include/pagedkv_rope.h gives
+    the formulas; low_turns / high_turns default to 1 / 4 for bands, 1 / 32 for
+    yarn).  Holds the phases on the device; made once per model."""
+
+    def __init__(self, rot_dim, base=10000.0, interleaved=False, scaling="none", factor=1.0, original_context=None,
+                 low_turns=None, high_turns=None, device="cuda"):
+        if scaling not in ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+        low, high = _ROPE_TURNS.get(scaling, (1.0, 2.0))
+        low, high = low if low_turns is None else low_turns, high if high_turns is None else high_turns
+        if scaling in _ROPE_TURNS and original_context is None:
+            raise ValueError(f"scaling {scaling!r} needs original_context")
+        self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
+        host = torch.empty(max(self.rot_dim, 0) // 2, dtype=torch.int64)
+        magnitude = ctypes.c_float()
+        _check("pkv_rope_phases", load_library().pkv_rope_phases(
+            self.rot_dim, float(base), ROPE_SCALINGS[scaling], float(factor), float(original_context or 0.0),
+            float(low), float(high), host.data_ptr(), ctypes.byref(magnitude)))
+        self.magnitude = magnitude.value
+        self.phases = host.to(device)             # 2^64 turns per position, as int64 bits
+        self._c = _RopeC(self.phases.data_ptr(), self.rot_dim, int(self.interleaved), self.magnitude)
+        self._p = ctypes.pointer(self._c)
+
+
+def _rope_arg(rope, head_dim, dev):
+    """The pkv_rope pointer of a Rope on the call's device (None: no turn)."""
+    if rope is None:
+        return None
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope")
+    if rope.phases.get_device() != dev:
+        raise ValueError(f"rope is on {rope.phases.device}, expected cuda:{dev}")
+    if rope.rot_dim > head_dim:
+        raise ValueError(f"rope turns {rope.rot_dim} elements of heads of {head_dim}")
+    return rope._p
+
+
+def _token_stride(t, name, ndim, dev):
+    """Elements between the tokens of t [..., heads, D] (bf16): its head rows lie
+    behind one another, its tokens one stride apart (so t may be a part of a
+    fused projection's rows)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {tuple(t.shape)}")
+    shape, stride = t.shape, t.stride()
+    heads, d = shape[-2], shape[-1]
+    if (d > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != d):
+        raise ValueError(f"{name}: the heads of a token must lie behind one another, got strides {stride}")
+    step = heads * d
+    if shape[0] > 1:
+        step = stride[0]
+    if ndim == 4 and shape[1] > 1:
+        if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
+            raise ValueError(f"{name}: tokens must be one stride apart, got strides {stride}")
+        step = stride[1]
+    return step
+
+
+def _count(x, name):
+    """A token count as int32: no length reaches 2^31, so larger ones mean that."""
+    x = int(x)
+    if x < 0:
+        raise ValueError(f"{name} must not be negative, got {x}")
+    return min(x, 0x7fffffff)
+
+
+def _elsewhere(dev):
+    """Whether the tensors' device is not the current one (the call is then made
+    with that device current, on its current stream)."""
+    return (_current_device() if _current_device is not None else torch.cuda.current_device()) != dev
+
+
+def _empty(shape, dtype, dev, stream):
+    """An output that belongs to the stream the call writes it on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev):
+    """Pools of bf16 or int8 (with scales) pages and their tables; True for int8."""
+    int8 = k_pool.dtype is torch.int8
+    kind = torch.int8 if int8 else torch.bfloat16
+    _need(k_pool, "k_pool", kind, 4, dev)
+    _need(v_pool, "v_pool", kind, 4, dev)
+    if int8:
+        _need(k_scales, "k_scales", torch.float32, 3, dev)
+        _need(v_scales, "v_scales", torch.float32, 3, dev)
+        _check_pools(k_pool, v_pool, k_scales, v_scales)
+    else:
+        _check_pools(k_pool, v_pool)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    return int8
+
+
+def paged_kv_write_rope(q, k_new, v_new, rope, k_pool, v_pool, block_tables, start_pos, k_scales=None, v_scales=None,
+                        q_out=None, dev_status=None, stream=None):
+    """Rotary positions and the page write in one launch: the query and key heads
+    of token j of sequence s are turned at position start_pos[s] + j, its key and
+    value rows go into the pages (bf16, or int8 with k_scales / v_scales).
+    q [n_seqs, n_new, Hq, D], k_new / v_new [n_seqs, n_new, Hkv, D] bf16; the
+    three may be parts of a fused projection's rows.  Returns the turned queries
+    (q_out, contiguous; q itself may be given)."""
+    dev = _device_of(k_pool, "k_pool")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_write_rope(q, k_new, v_new, rope, k_pool, v_pool, block_tables, start_pos, k_scales,
+                                       v_scales, q_out, dev_status, stream)
+    lib = load_library()
+    int8 = _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev)
+    qs, ks, vs = (_token_stride(t, n, 4, dev) for t, n in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")))
+    n_seqs, n_new, n_q_heads, D = q.shape
+    if rope is None:
+        raise TypeError("rope must be a Rope")
+    rp = _rope_arg(rope, D, dev)
+    _need(start_pos, "start_pos", torch.int32, 1, dev)
+    _shape(k_new, "k_new", (n_seqs, n_new) + tuple(k_pool.shape[2:]))
+    _shape(v_new, "v_new", k_new.shape)
+    if D != k_pool.shape[3]:
+        raise ValueError(f"q has head_dim {D}, the pool {k_pool.shape[3]}")
+    _check_batch(n_seqs, block_tables, start_pos, "start_pos")
+    _check_status(dev_status, dev)
+    if q_out is None:
+        q_out = _empty(q.shape, torch.bfloat16, dev, stream)
+    else:
+        _need(q_out, "q_out", torch.bfloat16, 4, dev)
+        _shape(q_out, "q_out", q.shape)
+    st = lib.paged_kv_write_rope(_ptr(q), qs, n_q_heads, _ptr(k_new), ks, _ptr(v_new), vs, rp, _ptr(q_out),
+                                 _ptr(k_pool), _ptr(v_pool), _ptr(k_scales), _ptr(v_scales),
+                                 PKV_KV_INT8 if int8 else PKV_KV_BF16, _dims(k_pool), _ptr(block_tables),
+                                 block_tables.shape[1], _ptr(start_pos), n_seqs, n_new, _ptr(dev_status),
+                                 _stream(stream))
+    _check("paged_kv_write_rope", st)
+    return q_out
+
+
+class WindowDecodePlan:
+    """paged_decode_attention_window / paged_decode_step_window with the arguments
+    that stay the same from call to call checked once, as DecodePlan does for the
+    unwindowed calls (and with the same conditions on the planned tensors).  No
+    workspace is needed.  ``run(q)`` attends; ``run(q, k_new, v_new, start_pos)``
+    is a whole step: turn (where the plan has a rope), page write, attention."""
+
+    def __init__(self, k_pool, v_pool, block_tables, ctx_lens, softmax_scale, n_q_heads, window, sinks=0, rope=None,
+                 k_scales=None, v_scales=None, out=None, lse_out=None, dev_status=None):
+        dev = _device_of(k_pool, "k_pool")
+        self._lib = load_library()
+        int8 = _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev)
+        _need(ctx_lens, "ctx_lens", torch.int32, 1, dev)
+        n_seqs, D = block_tables.shape[0], k_pool.shape[3]
+        self.q_shape = torch.Size((n_seqs, int(n_q_heads), D))
+        if out is None:
+            out = torch.empty(self.q_shape, dtype=torch.bfloat16, device=dev)
+        _need(out, "out", torch.bfloat16, 3, dev)
+        _shape(out, "out", self.q_shape)
+        if lse_out is not None:
+            _need(lse_out, "lse_out", torch.float32, 2, dev)
+            _shape(lse_out, "lse_out", self.q_shape[:2])
+        _check_batch(n_seqs, block_tables, ctx_lens, "ctx_lens")
+        _check_status(dev_status, dev)
+        self.device, self.out, self.n_q_heads = dev, out, int(n_q_heads)
+        self.new_shape = torch.Size((n_seqs, 1) + tuple(k_pool.shape[2:]))
+        self._rope = _rope_arg(rope, D, dev)
+        # held so that the pointers below stay valid
+        self._tensors = (k_pool, v_pool, k_scales, v_scales, block_tables, ctx_lens, out, lse_out, dev_status, rope)
+        self._args = (_ptr(k_pool), _ptr(v_pool), _ptr(k_scales), _ptr(v_scales),
+                      PKV_KV_INT8 if int8 else PKV_KV_BF16, pool_dims(k_pool), _ptr(block_tables),
+                      block_tables.shape[1], _ptr(ctx_lens), n_seqs, float(softmax_scale), _count(window, "window"),
+                      _count(sinks, "sinks"), _ptr(out), _ptr(lse_out), _ptr(dev_status))
+
+    def run(self, q, k_new=None, v_new=None, start_pos=None, stream=None):
+        """q [n_seqs, Hq, D] bf16 (contiguous for the attention alone); k_new /
+        v_new [n_seqs, 1, Hkv, D]; start_pos [n_seqs].  In a step the three may
+        be parts of a fused projection's rows.  Returns the plan's out."""
+        dev = self.device
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.run(q, k_new, v_new, start_pos, stream)
+        if k_new is None:
+            if v_new is not None or start_pos is not None:
+                raise ValueError("v_new and start_pos come with k_new")
+            if self._rope is not None:
+                raise ValueError("a plan with a rope runs steps: give k_new, v_new and start_pos")
+            _need(q, "q", torch.bfloat16, 3, dev)
+            _shape(q, "q", self.q_shape)
+            st = self._lib.paged_decode_attention_window(q.data_ptr(), self.n_q_heads, *self._args, _stream(stream))
+            _check("paged_decode_attention_window", st)
+            return self.out
+        qs = _token_stride(q, "q", 3, dev)
+        ks, vs = _token_stride(k_new, "k_new", 4, dev), _token_stride(v_new, "v_new", 4, dev)
+        _shape(q, "q", self.q_shape)
+        _shape(k_new, "k_new", self.new_shape)
+        _shape(v_new, "v_new", self.new_shape)
+        _need(start_pos, "start_pos", torch.int32, 1, dev)
+        _shape(start_pos, "start_pos", self.q_shape[:1])
+        st = self._lib.paged_decode_step_window(k_new.data_ptr(), ks, v_new.data_ptr(), vs, start_pos.data_ptr(),
+                                                q.data_ptr(), qs, self.n_q_heads, self._rope, *self._args,
+                                                _stream(stream))
+        _check("paged_decode_step_window", st)
+        return self.out
+
+
+def paged_decode_attention_window(q, k_pool, v_pool, block_tables, ctx_lens, softmax_scale, window, sinks=0,
+                                  k_scales=None, v_scales=None, out=None, lse_out=None, dev_status=None, stream=None):
+    """paged_decode_attention under a sliding window: the query of sequence s (at
+    position ctx_lens[s] - 1) sees the first ``sinks`` tokens and the last
+    ``window`` ones.  Blocks that hold none of them are never looked up.  Returns
+    out [n_seqs, Hq, D] bf16."""
+    dev = _device_of(q, "q")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    _need(q, "q", torch.bfloat16, 3, dev)
+    plan = WindowDecodePlan(k_pool, v_pool, block_tables, ctx_lens, softmax_scale, q.shape[1], window, sinks, None,
+                            k_scales, v_scales, out, lse_out, dev_status)
+    return plan.run(q, stream=stream)
+
+
+def paged_decode_step_window(k_new, v_new, start_pos, q, k_pool, v_pool, block_tables, ctx_lens, softmax_scale, window,
+                             sinks=0, rope=None, k_scales=None, v_scales=None, out=None, lse_out=None, dev_status=None,
+                             stream=None):
+    """One layer's step of one token per sequence in one launch: q and k_new
+    [n_seqs, 1, Hkv, D] turned at start_pos (rope None: as they are), k_new and
+    v_new written to the pages, then paged_decode_attention_window over ctx_lens
+    tokens (which count the new one).  Returns out [n_seqs, Hq, D] bf16."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    if k_new is None:
+        raise TypeError("k_new must be a torch.Tensor")
+    plan = WindowDecodePlan(k_pool, v_pool, block_tables, ctx_lens, softmax_scale, q.shape[1], window, sinks, rope,
+                            k_scales, v_scales, out, lse_out, dev_status)
+    return plan.run(q, k_new, v_new, start_pos, stream=stream)
+
+
+def paged_prefill_attention_window(q, k_pool, v_pool, block_tables, prefix_lens, softmax_scale, window, sinks=0,
+                                   out=None, lse_out=None, dev_status=None, stream=None):
+    """paged_prefill_attention under a sliding window: query i of sequence s (at
+    position prefix_lens[s] + i) sees the first ``sinks`` tokens and the last
+    ``window`` ones up to itself.  Returns out, same shape as q."""
+    dev = _device_of(q, "q")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_prefill_attention_window(q, k_pool, v_pool, block_tables, prefix_lens, softmax_scale, window,
+                                                  sinks, out, lse_out, dev_status, stream)
+    lib = load_library()
+    _need(q, "q", torch.bfloat16, 4, dev)
+    _need(k_pool, "k_pool", torch.bfloat16, 4, dev)
+    _need(v_pool, "v_pool", torch.bfloat16, 4, dev)
+    _check_pools(k_pool, v_pool)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    _need(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+    n_seqs, chunk, n_q_heads, D = q.shape
+    if k_pool.shape[3] != D:
+        raise ValueError(f"q has head_dim {D}, the pool {k_pool.shape[3]}")
+    _check_batch(n_seqs, block_tables, prefix_lens, "prefix_lens")
+    _check_status(dev_status, dev)
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    else:
+        _need(out, "out", torch.bfloat16, 4, dev)
+        _shape(out, "out", q.shape)
+    if lse_out is not None:
+        _need(lse_out, "lse_out", torch.float32, 3, dev)
+        _shape(lse_out, "lse_out", q.shape[:3])
+    st = lib.paged_prefill_attention_window(_ptr(q), n_q_heads, _ptr(k_pool), _ptr(v_pool), _dims(k_pool),
+                                            _ptr(block_tables), block_tables.shape[1], _ptr(prefix_lens), n_seqs, chunk,
+                                            float(softmax_scale), _count(window, "window"), _count(sinks, "sinks"),
+                                            _ptr(out), _ptr(lse_out), _ptr(dev_status), _stream(stream))
+    _check("paged_prefill_attention_window", st)
     return out
 
 

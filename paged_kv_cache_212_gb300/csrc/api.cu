@@ -9,6 +9,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "decode_small.h"
+#include "../../include/pagedkv_window.h"
 
 namespace pkv {
 
@@ -18,6 +19,8 @@ namespace {
 
 thread_local int g_last_cuda_error = 0;
 std::atomic<uint64_t> g_pipeline_wait_ns{kWaitTimeoutNs};
+
+}  // namespace
 
 int cuda_status(cudaError_t e)
 {
@@ -57,6 +60,8 @@ int check_dims(const pkv_dims &d)
     if ((int64_t)(d.n_blocks + 1) * d.block_size > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
     return PKV_OK;
 }
+
+namespace {
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
@@ -441,10 +446,11 @@ int paged_decode_step(const pkv_bf16 *k_new, const pkv_bf16 *v_new, const int32_
     return cuda_status(launch_decode(a, sms, (cudaStream_t)stream, &w));
 }
 
-int paged_prefill_attention(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool, const pkv_bf16 *v_pool,
-                            pkv_dims dims, const int32_t *block_tables, int32_t max_blocks,
-                            const int32_t *prefix_lens, int32_t n_seqs, int32_t chunk, float softmax_scale,
-                            pkv_bf16 *out, float *lse_out, int32_t *dev_status, pkv_stream_t stream)
+// window 0: every key up to the query.
+static int prefill(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool, const pkv_bf16 *v_pool, pkv_dims dims,
+                   const int32_t *block_tables, int32_t max_blocks, const int32_t *prefix_lens, int32_t n_seqs,
+                   int32_t chunk, float softmax_scale, int32_t window, int32_t sinks, pkv_bf16 *out, float *lse_out,
+                   int32_t *dev_status, pkv_stream_t stream)
 {
     int st = check_dims(dims);
     if (st != PKV_OK) return st;
@@ -462,8 +468,28 @@ int paged_prefill_attention(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16
     st = num_sms_of_current_device(&sms);
     if (st != PKV_OK) return st;
     PrefillArgs a{q, n_q_heads, k_pool, v_pool, dims, block_tables, max_blocks, prefix_lens, n_seqs, chunk,
-                  softmax_scale, out, lse_out, dev_status};
+                  softmax_scale, out, lse_out, dev_status, window, sinks};
     return cuda_status(launch_prefill(a, sms, (cudaStream_t)stream));
+}
+
+int paged_prefill_attention(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool, const pkv_bf16 *v_pool,
+                            pkv_dims dims, const int32_t *block_tables, int32_t max_blocks,
+                            const int32_t *prefix_lens, int32_t n_seqs, int32_t chunk, float softmax_scale,
+                            pkv_bf16 *out, float *lse_out, int32_t *dev_status, pkv_stream_t stream)
+{
+    return prefill(q, n_q_heads, k_pool, v_pool, dims, block_tables, max_blocks, prefix_lens, n_seqs, chunk,
+                   softmax_scale, 0, 0, out, lse_out, dev_status, stream);
+}
+
+int paged_prefill_attention_window(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool,
+                                   const pkv_bf16 *v_pool, pkv_dims dims, const int32_t *block_tables,
+                                   int32_t max_blocks, const int32_t *prefix_lens, int32_t n_seqs, int32_t chunk,
+                                   float softmax_scale, int32_t window, int32_t sinks, pkv_bf16 *out, float *lse_out,
+                                   int32_t *dev_status, pkv_stream_t stream)
+{
+    if (window < 1 || sinks < 0) return PKV_ERR_INVALID_ARG;
+    return prefill(q, n_q_heads, k_pool, v_pool, dims, block_tables, max_blocks, prefix_lens, n_seqs, chunk,
+                   softmax_scale, window, sinks, out, lse_out, dev_status, stream);
 }
 
 }  // extern "C"

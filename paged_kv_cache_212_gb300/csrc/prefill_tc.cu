@@ -38,6 +38,12 @@
 // bandwidth).  Query position P + p (P = prefix length) sees keys 0 .. P + p
 // (metrale impl_more.rs: a query at q_pos attends only slots <= q_pos of its
 // block).
+//
+// WIN: under a sliding window with first tokens (pagedkv_window.h) the CTA walks
+// the tiles that hold first tokens, then those from the window of its first
+// query on; 16-key groups between the two are neither looked up nor loaded, and
+// rows of loaded groups that no query sees are zeroed in V (a row of K needs
+// nothing: its scores are replaced).
 #include <math.h>
 
 #include "common.cuh"
@@ -77,6 +83,7 @@ struct PrefillTcParams {
     int32_t pairs_per_seq;        // CTAs per (sequence, kv head)
     int32_t n_seqs, n_kv_heads;
     unsigned long long wait_ns;   // limit of the pipeline waits
+    int32_t window, sinks;        // WIN: the mask
 };
 
 // Batches of at most this many sequences are scheduled longest prefix first.
@@ -193,7 +200,7 @@ __device__ __forceinline__ bool wg_and(uint32_t id, bool v)
 
 }  // namespace
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                                             const __grid_constant__ CUtensorMap k_map,
                                                             const __grid_constant__ CUtensorMap v_map,
@@ -266,9 +273,20 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     const int p0 = pair * kNQ * pos_per_tile;
     const int p_last = min(p0 + kNQ * pos_per_tile, p.chunk) - 1;
     const int32_t P = __ldg(p.prefix_lens + s);
-    const int32_t n_keys = P + p_last + 1;
-    const bool bad_len = P < 0 || (int64_t)n_keys > (int64_t)p.max_blocks * p.block_size;
-    const int n_kt = bad_len ? 0 : (n_keys + kTN - 1) / kTN;
+    const bool bad_len = P < 0 || (int64_t)P + p_last + 1 > (int64_t)p.max_blocks * p.block_size;
+    const int32_t n_keys = bad_len ? 0 : P + p_last + 1;
+    // WIN: keys in [sinks, w_lo) are seen by no query of the CTA; the tiles are
+    // the first n_sink ones, then those from tile w_tile on
+    const int32_t w_lo = WIN && !bad_len ? max(0, P + p0 - p.window + 1) : 0;
+    const int n_sink = WIN ? (min(p.sinks, n_keys) + kTN - 1) / kTN : 0;
+    const int w_tile = WIN ? max(w_lo / kTN, n_sink) : 0;
+    const int n_all = (n_keys + kTN - 1) / kTN;
+    const int n_kt = bad_len ? 0 : WIN ? n_sink + max(0, n_all - w_tile) : n_all;
+    // first key of the j-th tile; whether a 16-key group holds a key some query sees
+    auto tile_key = [&](int j) -> int32_t { return (WIN && j >= n_sink ? w_tile + j - n_sink : j) * kTN; };
+    auto group_seen = [&](int32_t key0) -> bool {
+        return key0 < n_keys && (!WIN || key0 < p.sinks || key0 + 15 >= w_lo);
+    };
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -327,16 +345,16 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // block ids are read one tile ahead and turned into pool rows when the
             // tile is issued
             auto load_block = [&](int j) -> int32_t {
-                const int32_t key0 = j * kTN + grp * 16;
-                return (lane < n_grp && key0 < n_keys) ? __ldg(trow + key0 / p.block_size) : 0;
+                const int32_t key0 = tile_key(j) + grp * 16;
+                return (lane < n_grp && group_seen(key0)) ? __ldg(trow + key0 / p.block_size) : 0;
             };
             int32_t blk = load_block(0);
             int issued = 0;
             for (int j = 0; j < n_kt; ++j) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
                 {
-                    const int32_t key0 = j * kTN + grp * 16;
-                    if (lane < n_grp && key0 < n_keys) {
+                    const int32_t key0 = tile_key(j) + grp * 16;
+                    if (lane < n_grp && group_seen(key0)) {
                         if (blk < 0 || blk > p.n_blocks)
                             report(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
                         else
@@ -468,9 +486,11 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[qt], j & 1, abort_flag, p.wait_ns));
             if (!ok) break;
             tc_fence_after();
-            const int32_t key_base = j * kTN;
+            const int32_t key_base = tile_key(j);
             // rows whose keys in this tile are all visible need no per-key test
-            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos);
+            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos ||
+                                                            (WIN && key_base <= qpos - p.window &&
+                                                             key_base + kTN > p.sinks));
             uint32_t sv[kTN];
 #pragma unroll
             for (int c = 0; c < kTN / 32; ++c) tmem_ld32_async(lane_base + c * 32, sv + c * 32);
@@ -478,9 +498,25 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // keys past this row's position get a score of -inf (exp2 gives 0);
             // only tiles crossing the diagonal take this branch
             if (masked) {
+                if constexpr (WIN) {
+                    // key i is seen when 0 <= back - i < window, or i < sinks left in
+                    // this tile and not past the row
+                    const int32_t back = qpos - key_base, first = min(p.sinks - key_base, back + 1);
+                    if (p.sinks > key_base) {
 #pragma unroll
-                for (int i = 0; i < kTN; ++i)
-                    if (key_base + i > qpos) sv[i] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < kTN; ++i)
+                            if ((uint32_t)(back - i) >= (uint32_t)p.window && i >= first)
+                                sv[i] = __float_as_uint(-INFINITY);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kTN; ++i)
+                            if ((uint32_t)(back - i) >= (uint32_t)p.window) sv[i] = __float_as_uint(-INFINITY);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < kTN; ++i)
+                        if (key_base + i > qpos) sv[i] = __float_as_uint(-INFINITY);
+                }
             }
             // row maximum: three-input max over four independent chains
             float mx;
@@ -498,6 +534,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             float alpha = 1.f;
             if (m == -INFINITY) {
                 m = mx;          // first tile: key 0 is always visible, so mx is finite
+                                 // (WIN: -inf until the first tile with a visible key)
             } else if (mx > m + kRescaleThreshold) {
                 alpha = fast_exp2(m - mx);
                 m = mx;
@@ -518,7 +555,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // probabilities (packed two-lane FMA for the exponent arguments) and
             // two packed partial row sums; P (bf16 pairs) over S's first 64
             // columns, each 16-column store after the S columns it covers were read
-            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m, -m);
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = WIN && m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
             float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < kTN / 32; ++c) {
@@ -539,17 +576,25 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             }
             l = l * alpha + ((la.x + la.y) + (lb.x + lb.y));
             tmem_wait_st();
-            // last tile: V rows of keys past the last one may hold anything; zero
-            // them once V_j has landed (both warpgroups write the same zeros)
-            if (j == n_kt - 1 && (n_keys & 15) != 0) {
+            // V rows of loaded groups that no query sees (past the last key; WIN:
+            // between the first tokens and the window) may hold anything; zero them
+            // once V_j has landed (both warpgroups write the same zeros)
+            const bool tail = j == n_kt - 1 && (n_keys & 15) != 0;
+            const bool gap = WIN && w_lo > p.sinks && key_base < w_lo && key_base + kTN > p.sinks;
+            if (tail || gap) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&v_full[j % NV], (j / NV) & 1, abort_flag, p.wait_ns));
                 if (!ok) break;
-                const int first = n_keys - key_base, stop = ((n_keys + 15) & ~15) - key_base;
                 uint8_t *vs = v_ring + (j % NV) * kSlotBytes;
-                for (int i = r; i < (stop - first) * PANELS * 8; i += kTM) {
-                    const int row = first + i / (PANELS * 8), pc = i % (PANELS * 8);
-                    *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 + swz128(row % 16, pc % 8)) =
-                        make_uint4(0, 0, 0, 0);
+                auto zero_rows = [&](int first, int stop) {
+                    for (int i = r; i < (stop - first) * PANELS * 8; i += kTM) {
+                        const int row = first + i / (PANELS * 8), pc = i % (PANELS * 8);
+                        *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 +
+                                                   swz128(row % 16, pc % 8)) = make_uint4(0, 0, 0, 0);
+                    }
+                };
+                if (tail) zero_rows(n_keys - key_base, ((n_keys + 15) & ~15) - key_base);
+                if (gap) {   // the whole gap within the tile: groups that were not loaded are zero already
+                    zero_rows(max(p.sinks - key_base, 0), min(w_lo - key_base, kTN));
                 }
                 fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
             }
@@ -599,7 +644,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             }
             if (pos <= p_last && p.lse_out)
                 p.lse_out[((int64_t)s * p.chunk + pos) * p.n_q_heads + h] = (m + __log2f(l)) * 0.69314718055994531f;
-        } else if (!ok) {
+        } else if (!ok && n_kt > 0) {       // n_kt 0: a bad length, reported above
             if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
             *abort_flag = 1;
         }
@@ -613,7 +658,8 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     }
 }
 
-cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
+template <bool WIN>
+static cudaError_t launch_prefill_tc_as(const PrefillArgs &a, cudaStream_t stream)
 {
     const pkv_dims &d = a.dims;
     const int G = a.n_q_heads / d.n_kv_heads;
@@ -638,6 +684,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
     p.pairs_per_seq = (p.tiles_per_seq + kNQ - 1) / kNQ;
     p.n_seqs = a.n_seqs;
     p.n_kv_heads = d.n_kv_heads;
+    p.window = a.window;
+    p.sinks = a.sinks;
 
     CUtensorMap qmap, kmap, vmap, omap;
     {
@@ -693,8 +741,8 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
     // a build whose kernel was given fewer (its setmaxnreg.inc could not complete).
     static const bool regs_ok = [] {
         cudaFuncAttributes fa128{}, fa64{};
-        return cudaFuncGetAttributes(&fa128, prefill_tc_kernel<128>) == cudaSuccess &&
-               cudaFuncGetAttributes(&fa64, prefill_tc_kernel<64>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
+        return cudaFuncGetAttributes(&fa128, prefill_tc_kernel<128, WIN>) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa64, prefill_tc_kernel<64, WIN>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
                fa64.numRegs >= kLaunchRegs;
     }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
@@ -712,13 +760,18 @@ cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
     lc.numAttrs = 1;
     cudaError_t e;
     if (d.head_dim == 128) {
-        e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<128>), 384, smem, nullptr);
+        e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<128, WIN>), 384, smem, nullptr);
         if (e != cudaSuccess) return e;
-        return cudaLaunchKernelEx(&lc, prefill_tc_kernel<128>, qmap, kmap, vmap, omap, p);
+        return cudaLaunchKernelEx(&lc, prefill_tc_kernel<128, WIN>, qmap, kmap, vmap, omap, p);
     }
-    e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<64>), 384, smem, nullptr);
+    e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<64, WIN>), 384, smem, nullptr);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&lc, prefill_tc_kernel<64>, qmap, kmap, vmap, omap, p);
+    return cudaLaunchKernelEx(&lc, prefill_tc_kernel<64, WIN>, qmap, kmap, vmap, omap, p);
+}
+
+cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
+{
+    return a.window > 0 ? launch_prefill_tc_as<true>(a, stream) : launch_prefill_tc_as<false>(a, stream);
 }
 
 }  // namespace pkv

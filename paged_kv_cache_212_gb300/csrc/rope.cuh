@@ -1,0 +1,101 @@
+// rope.cuh -- rotary positions as device functions, shared by the rotary page
+// write and the windowed decode step.
+//
+// Angles.  A pair's phase is its turns per position in units of 2^-64, so the
+// angle of position t is (t * phase mod 2^64) 2^-64 turns: an integer product,
+// exact for every position, where the binary32 product t * f loses 0.06 rad at
+// t = 10^6.  Its top 32 bits as a signed number are the angle in (-1/2, 1/2]
+// turns to 2^-32; sincospif takes twice that.
+//
+// Lanes.  A head row of D elements is the work of D / 16 lanes: lane `slot`
+// holds two 16-byte vectors (16 elements, 8 pairs) so that both members of
+// every pair are in one lane, in either layout; the 8 sines and cosines depend
+// on the slot and the position alone and serve every head of a token.
+#pragma once
+
+#include "common.cuh"
+
+namespace pkv {
+
+struct RopeArgs {
+    const uint64_t *phases;   // null: no turn
+    int32_t rot_dim;
+    int32_t interleaved;
+    float magnitude;
+};
+
+// Vectors (of 8 elements) of a head row that lane `slot` of its D / 16 holds,
+// and whether they are turned.  Half layout: the pair (slot, slot + rot / 16)
+// of the turned part, then neighbours of the rest; interleaved: neighbours.
+__device__ __forceinline__ bool rope_vectors(const RopeArgs &r, int slot, int &v0, int &v1)
+{
+    const int turned = r.phases ? r.rot_dim / 16 : 0;   // slots that hold turned pairs
+    const bool turn = slot < turned;
+    if (turn && !r.interleaved) {
+        v0 = slot;
+        v1 = slot + turned;
+    } else {
+        v0 = 2 * slot;
+        v1 = v0 + 1;
+    }
+    return turn;
+}
+
+// The 8 cosines and sines (times the magnitude) of pairs 8 slot .. 8 slot + 7
+// at position t.  phases is 16-byte aligned.
+__device__ __forceinline__ void rope_angles(const RopeArgs &r, int slot, int64_t t, float (&c)[8], float (&s)[8])
+{
+    const ulonglong2 *ph = reinterpret_cast<const ulonglong2 *>(r.phases + 8 * slot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const ulonglong2 p2 = __ldg(ph + i);
+        const unsigned long long p[2] = {p2.x, p2.y};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int32_t hi = (int32_t)((p[k] * (unsigned long long)t) >> 32);   // turns * 2^32, signed
+            sincospif((float)hi * 4.656612873077393e-10f, &s[2 * i + k], &c[2 * i + k]);   // 2^-31: half turns
+            s[2 * i + k] *= r.magnitude;
+            c[2 * i + k] *= r.magnitude;
+        }
+    }
+}
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 &raw, float *x)
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float *x)
+{
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+}
+
+// Turns the 8 pairs of a lane's 16 elements (x[0..7] of its first vector,
+// x[8..15] of its second).  The operations are spelled out so that every kernel
+// gives the same bits.
+__device__ __forceinline__ void rope_turn(bool interleaved, const float (&c)[8], const float (&s)[8], float (&x)[16])
+{
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = x[2 * i], b = x[2 * i + 1];
+            x[2 * i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
+            x[2 * i + 1] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = x[i], b = x[i + 8];
+            x[i] = __fmaf_rn(a, c[i], -__fmul_rn(b, s[i]));
+            x[i + 8] = __fmaf_rn(b, c[i], __fmul_rn(a, s[i]));
+        }
+    }
+}
+
+}  // namespace pkv

@@ -1,0 +1,263 @@
+// rope_write.cu -- rotary positions and the page write in one launch
+// (pagedkv_rope.h): queries and keys turned by the angles of their positions,
+// keys and values stored in the pages (bf16, or int8 codes with a scale per
+// row), turned queries returned.
+//
+// Every element is read once and written once, so the launch is bound by
+// memory (prefill chunks) or by its own latency (decode tokens).  A warp takes
+// some of the head rows (Hq + 2 Hkv of them) of one token: D / 16 lanes hold a
+// row (rope.cuh), 32 / (D / 16) rows go at once, and each lane computes its 8
+// sines and cosines once for all its rows.
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+#include "rope.cuh"
+#include "write_rows.cuh"
+#include "../../include/pagedkv_rope.h"
+
+namespace pkv {
+namespace {
+
+struct RopeWriteArgs {
+    const __nv_bfloat16 *q, *k_new, *v_new;
+    int64_t q_stride, k_stride, v_stride;
+    int32_t n_q_heads;
+    RopeArgs rope;
+    __nv_bfloat16 *q_out;
+    void *k_pool, *v_pool;
+    float *k_scales, *v_scales;
+    pkv_dims dims;
+    const int32_t *tables;
+    int32_t max_blocks;
+    const int32_t *start_pos;
+    int32_t n_new;
+    int64_t n_tokens;
+    int32_t parts;   // warps sharing a token
+    int32_t *dev_status;
+};
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(256) rope_write_kernel(const RopeWriteArgs a)
+{
+    constexpr int SLOTS = D / 16;        // lanes per head row
+    constexpr int ROWS = 32 / SLOTS;     // head rows a warp takes at once
+    constexpr int U = 2;                 // such groups in flight
+    grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, slot = lane % SLOTS, sub = lane / SLOTS;
+    const int hkv = a.dims.n_kv_heads, hq = a.n_q_heads;
+    const int n_rows = hq + 2 * hkv, groups = (n_rows + ROWS - 1) / ROWS;
+    int v0, v1;
+    const bool turn = rope_vectors(a.rope, slot, v0, v1);
+    const int64_t units = a.n_tokens * a.parts;
+    for (int64_t u = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units;
+         u += (int64_t)gridDim.x * (blockDim.x >> 5)) {
+        const int64_t tok = u / a.parts;
+        const int part = (int)(u % a.parts);
+        const int64_t s = tok / a.n_new;
+        const int64_t t = (int64_t)__ldg(a.start_pos + s) + (tok - s * a.n_new);
+        // the token's pool row, reported by one lane of the part that starts at row 0
+        const int64_t row = pool_row_of(a.tables + s * a.max_blocks, a.max_blocks, a.dims.n_blocks, a.dims.block_size,
+                                        t, part == 0 && lane == 0 ? a.dev_status : nullptr);
+        float c[8], sn[8];
+        if (turn) rope_angles(a.rope, slot, t, c, sn);
+        for (int g0 = part; g0 < groups; g0 += a.parts * U) {
+            uint4 x0[U], x1[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = (g0 + i * a.parts) * ROWS + sub;
+                x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+                if (r >= n_rows) continue;
+                const __nv_bfloat16 *src = r < hq         ? a.q + tok * a.q_stride + (int64_t)r * D
+                                           : r < hq + hkv ? a.k_new + tok * a.k_stride + (int64_t)(r - hq) * D
+                                                          : a.v_new + tok * a.v_stride + (int64_t)(r - hq - hkv) * D;
+                x0[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v0);
+                x1[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v1);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int r = (g0 + i * a.parts) * ROWS + sub;
+                const bool is_q = r < hq, is_v = r >= hq + hkv, live = r < n_rows;
+                const int h = is_q ? r : is_v ? r - hq - hkv : r - hq;
+                if (!INT8 || is_q) {
+                    if (turn && !is_v) {
+                        float x[16];
+                        unpack_bf16x8(x0[i], x);
+                        unpack_bf16x8(x1[i], x + 8);
+                        rope_turn(a.rope.interleaved, c, sn, x);
+                        x0[i] = pack_bf16x8(x);
+                        x1[i] = pack_bf16x8(x + 8);
+                    }
+                    if (live && (is_q || row >= 0)) {
+                        __nv_bfloat16 *dst =
+                            is_q ? a.q_out + (tok * hq + h) * D
+                                 : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
+                        reinterpret_cast<uint4 *>(dst)[v0] = x0[i];
+                        reinterpret_cast<uint4 *>(dst)[v1] = x1[i];
+                    }
+                }
+                if constexpr (INT8) {
+                    if (__all_sync(0xffffffffu, is_q)) continue;      // no row of the pages in this group
+                    float x[16];
+                    unpack_bf16x8(x0[i], x);
+                    unpack_bf16x8(x1[i], x + 8);
+                    if (turn && !is_v && !is_q) rope_turn(a.rope.interleaved, c, sn, x);
+                    float amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+                    for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                    int code[16];
+                    const float scale = int8_codes<16>(x, amax, code);
+                    if (is_q || !live || row < 0) continue;
+                    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
+                    int8_t *dst = static_cast<int8_t *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
+                    *reinterpret_cast<uint2 *>(dst + 8 * v0) = make_uint2(w[0], w[1]);
+                    *reinterpret_cast<uint2 *>(dst + 8 * v1) = make_uint2(w[2], w[3]);
+                    if (slot == 0) (is_v ? a.v_scales : a.k_scales)[row * hkv + h] = scale;
+                }
+            }
+        }
+    }
+}
+
+}  // namespace
+
+int check_rope(const pkv_rope *rope, int32_t head_dim)
+{
+    if (!rope || !rope->phases || !aligned16(rope->phases) || !std::isfinite(rope->magnitude))
+        return PKV_ERR_INVALID_ARG;
+    if (rope->rot_dim <= 0 || rope->rot_dim > head_dim) return PKV_ERR_INVALID_ARG;
+    if (rope->rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+bool row_stride_ok(int64_t stride, int32_t heads, int32_t head_dim)
+{
+    return stride % 8 == 0 && stride >= (int64_t)heads * head_dim;
+}
+
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" {
+
+int pkv_rope_phases(int32_t rot_dim, double base, int32_t scaling, double factor, double original_context,
+                    double low_turns, double high_turns, uint64_t *phases_out, float *magnitude_out)
+{
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    if (!phases_out || !magnitude_out || rot_dim <= 0 || rot_dim % 16 != 0) return PKV_ERR_INVALID_ARG;
+    if (!std::isfinite(base) || !(base > 1.0)) return PKV_ERR_INVALID_ARG;
+    if (scaling < PKV_ROPE_NONE || scaling > PKV_ROPE_YARN) return PKV_ERR_UNSUPPORTED;
+    if (scaling != PKV_ROPE_NONE && (!std::isfinite(factor) || !(factor >= 1.0))) return PKV_ERR_INVALID_ARG;
+    const bool by_turns = scaling == PKV_ROPE_BANDS || scaling == PKV_ROPE_YARN;
+    if (by_turns && (!std::isfinite(original_context) || !(original_context > 0.0) || !(low_turns > 0.0) ||
+                     !(high_turns > low_turns) || !std::isfinite(high_turns)))
+        return PKV_ERR_INVALID_ARG;
+    *magnitude_out = scaling == PKV_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    if (scaling == PKV_ROPE_NTK) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+    // YARN: the (real) pair index that makes n turns in the original context
+    const auto pair_of = [&](double n) { return rot_dim * log(original_context / (n * kTwoPi)) / (2.0 * log(base)); };
+    double lo = 0.0, hi = 0.0;
+    if (scaling == PKV_ROPE_YARN) {
+        lo = fmax(floor(pair_of(high_turns)), 0.0);
+        hi = fmin(ceil(pair_of(low_turns)), rot_dim - 1.0);
+    }
+    for (int32_t i = 0; i < rot_dim / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot_dim);
+        double divide = 0.0;                 // 0: f kept, 1: f / factor
+        if (scaling == PKV_ROPE_LINEAR) divide = 1.0;
+        if (scaling == PKV_ROPE_BANDS) {
+            const double n = original_context * f / kTwoPi;
+            divide = 1.0 - fmin(fmax((n - low_turns) / (high_turns - low_turns), 0.0), 1.0);
+        }
+        if (scaling == PKV_ROPE_YARN) divide = fmin(fmax((i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+        if (divide != 0.0) f = f * (1.0 - divide) + f / factor * divide;
+        // f <= 1 radian per position: less than a sixth of 2^64
+        phases_out[i] = (uint64_t)(f / kTwoPi * 18446744073709551616.0 + 0.5);
+    }
+    return PKV_OK;
+}
+
+int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, const pkv_bf16 *k_new,
+                        int64_t k_stride, const pkv_bf16 *v_new, int64_t v_stride, const pkv_rope *rope,
+                        pkv_bf16 *q_out, void *k_pool, void *v_pool, float *k_scales, float *v_scales,
+                        int32_t kv_dtype, pkv_dims dims, const int32_t *block_tables, int32_t max_blocks,
+                        const int32_t *start_pos, int32_t n_seqs, int32_t n_new, int32_t *dev_status,
+                        pkv_stream_t stream)
+{
+    int st = check_dims(dims);
+    if (st != PKV_OK) return st;
+    if (n_seqs < 0 || n_new < 0 || max_blocks <= 0 || n_q_heads <= 0) return PKV_ERR_INVALID_ARG;
+    if (kv_dtype != PKV_KV_BF16 && kv_dtype != PKV_KV_INT8) return PKV_ERR_UNSUPPORTED;
+    st = check_rope(rope, dims.head_dim);
+    if (st != PKV_OK) return st;
+    if (!row_stride_ok(q_stride, n_q_heads, dims.head_dim) || !row_stride_ok(k_stride, dims.n_kv_heads, dims.head_dim) ||
+        !row_stride_ok(v_stride, dims.n_kv_heads, dims.head_dim))
+        return PKV_ERR_INVALID_ARG;
+    if (n_seqs == 0 || n_new == 0) return PKV_OK;
+    const void *p[] = {q, k_new, v_new, q_out, k_pool, v_pool};
+    for (const void *x : p)
+        if (!x || !aligned16(x)) return PKV_ERR_INVALID_ARG;
+    if (!block_tables || !start_pos) return PKV_ERR_INVALID_ARG;
+    // a turned row may be written before another warp has read its source
+    if (q_out == q && q_stride != (int64_t)n_q_heads * dims.head_dim) return PKV_ERR_INVALID_ARG;
+    const bool int8 = kv_dtype == PKV_KV_INT8;
+    if (int8 && (!k_scales || !v_scales ||
+                 ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u)))
+        return PKV_ERR_INVALID_ARG;
+    if ((int64_t)n_new > (int64_t)max_blocks * dims.block_size) return PKV_ERR_OUT_OF_RANGE;
+    int sms = 0;
+    st = num_sms_of_current_device(&sms);
+    if (st != PKV_OK) return st;
+
+    RopeWriteArgs a{};
+    a.q = reinterpret_cast<const __nv_bfloat16 *>(q);
+    a.k_new = reinterpret_cast<const __nv_bfloat16 *>(k_new);
+    a.v_new = reinterpret_cast<const __nv_bfloat16 *>(v_new);
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.n_q_heads = n_q_heads;
+    a.rope = RopeArgs{rope->phases, rope->rot_dim, rope->interleaved != 0, rope->magnitude};
+    a.q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.dims = dims;
+    a.tables = block_tables;
+    a.max_blocks = max_blocks;
+    a.start_pos = start_pos;
+    a.n_new = n_new;
+    a.n_tokens = (int64_t)n_seqs * n_new;
+    a.dev_status = dev_status;
+    // few tokens: a token's rows are shared out until the warps fill the machine
+    const int rows_at_once = 32 / (dims.head_dim / 16);
+    const int64_t groups = (n_q_heads + 2 * (int64_t)dims.n_kv_heads + rows_at_once - 1) / rows_at_once;
+    const int64_t want = (int64_t)sms * 32;
+    int64_t parts = (want + a.n_tokens - 1) / a.n_tokens;
+    a.parts = (int32_t)(parts < groups ? parts : groups);
+    int64_t grid = (a.n_tokens * a.parts + 7) / 8;
+    if (grid > 0x7fffffffLL) grid = 0x7fffffffLL;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)grid);
+    lc.blockDim = dim3(256);
+    lc.stream = (cudaStream_t)stream;
+    lc.attrs = pdl;
+    lc.numAttrs = 1;
+    if (dims.head_dim == 128)
+        return cuda_status(int8 ? cudaLaunchKernelEx(&lc, rope_write_kernel<128, true>, a)
+                                : cudaLaunchKernelEx(&lc, rope_write_kernel<128, false>, a));
+    return cuda_status(int8 ? cudaLaunchKernelEx(&lc, rope_write_kernel<64, true>, a)
+                            : cudaLaunchKernelEx(&lc, rope_write_kernel<64, false>, a));
+}
+
+}  // extern "C"
