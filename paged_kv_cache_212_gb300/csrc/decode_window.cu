@@ -18,17 +18,20 @@
 // with a running maximum and sum in log2 units.  No barrier but the warp's own
 // until the end, where warps and then CTAs are joined by their maxima.
 //
-// Rounding.  Products are exact in binary32 when both factors are: the queries
-// of a step (turned in binary32) and the probabilities are therefore split into
-// a 16-bit value and its 16-bit remainder.  With up to 4 query heads both fit in
-// the 8 columns of the product (heads in columns 0-3, remainders in 4-7) and
-// cost nothing; with 5 to 8 the remainders take a second product.
+// Rounding.  bf16 pages: products are exact in binary32 when both factors are,
+// so the queries of a step (turned in binary32) and the probabilities are split
+// into a bf16 value and its bf16 remainder (2^-16 together).  With up to 4 query
+// heads both fit in the 8 columns of the product (heads in columns 0-3,
+// remainders in 4-7) and cost nothing; with 5 to 8 the remainders take a second
+// product.
 //
 // int8 pages are contracted as fp16 (a code and the value 1152 share one
-// exponent: byte permute, one subtraction).  The K scale multiplies the score;
-// the V scale joins the probability as exp2(s + log2 |v_scale| - m2) under a
-// maximum m2 of its own, so that the fp16 weights use their range whatever the
-// scales are.
+// exponent: a byte permute, and one subtraction or, for K, one correction by
+// 1152 times the query's sum).  Queries and weights are rounded once to fp16
+// (2^-11, eight times finer than the bf16 output).  The K scale multiplies the
+// score; the V scale joins the probability as exp2(s + log2 |v_scale| - m2)
+// under a maximum m2 of its own, so that the fp16 weights use their range
+// whatever the scales are.
 #include <math.h>
 
 #include "common.cuh"
@@ -45,6 +48,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;              // tokens per tile
 constexpr int kHeads = 8;              // query heads per kv head, padded
 constexpr int kMaxSplits = 8;          // CTAs per cluster
+constexpr int kCtasPerSm = 3;          // resident CTAs that fill an SM
 constexpr float kLazyMax = 8.0f;       // the running maximum may lag by this (log2 units)
 
 struct WindowArgs {
@@ -72,15 +76,18 @@ struct WindowArgs {
 
 template <int D, bool INT8>
 struct Shape {
-    static constexpr int kRowData = INT8 ? D : 2 * D;             // bytes of a row in the pool
-    static constexpr int kVecs = kRowData / 16;
-    static constexpr int kRow = kRowData + 16;                    // padded: 8 rows hit 32 banks once
+    static constexpr int kRow = INT8 ? D : 2 * D;                 // bytes of a head row in the pool
+    static constexpr int kVecs = kRow / 16;
     static constexpr int kStage = 2 * kTile * kRow + (INT8 ? 2 * kTile * 4 : 0);
-    static constexpr int kStages = INT8 ? (D == 128 ? 5 : 6) : (D == 128 ? 3 : 6);
+    static constexpr int kStages = 3;
     static constexpr int kAcc = D + 4;                            // floats per accumulator row
-    static constexpr size_t kSmem = (size_t)kWarps * kStages * kStage + (size_t)kHeads * kAcc * 4 + 2 * kRowData;
-    static_assert(kStages * kStage >= kHeads * kAcc * 4, "a warp's accumulator fits its ring");
-    static_assert(kStage % 16 == 0 && (kAcc * 4) % 16 == 0, "16-byte aligned parts");
+    static constexpr int kRing = kStages * kStage > kHeads * kAcc * 4 ? kStages * kStage : kHeads * kAcc * 4;
+    static constexpr size_t kSmem = 256 + (size_t)kWarps * kRing + (size_t)kHeads * kAcc * 4 + 2 * kRow;
+    static_assert(kRing % kRow == 0 && kStage % kRow == 0, "rows aligned to their size");
+    // a row's 16-byte chunks are permuted so that chunk c of 8 consecutive rows
+    // lies in 8 different bank groups
+    static __device__ __forceinline__ int swizzle(int row) { return kRow >= 128 ? row & 7 : (row >> 1) & 3; }
+    static __device__ __forceinline__ uint32_t at(int row, int chunk) { return row * kRow + ((chunk ^ swizzle(row)) << 4); }
 };
 
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool there)
@@ -112,11 +119,16 @@ __device__ __forceinline__ float ld_cluster(const float *a, uint32_t rank)
     return v;
 }
 
-// Two bytes of x (signed codes, biased by 128) as fp16 values.
+// Two bytes of x (codes + 128) as the fp16 values code + 1152, and as the codes.
 template <uint32_t SEL>
-__device__ __forceinline__ uint32_t codes_f16x2(uint32_t biased)
+__device__ __forceinline__ uint32_t biased_f16x2(uint32_t x)
 {
-    const uint32_t w = __byte_perm(biased, 0x64646464u, SEL);     // 1024 + code + 128
+    return __byte_perm(x, 0x64646464u, SEL);
+}
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_f16x2(uint32_t x)
+{
+    const uint32_t w = biased_f16x2<SEL>(x);
     const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(1152.f));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
@@ -148,16 +160,18 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         mma_bf16_16816(d, a, b0, b1);
 }
 
-// WIDE: 5 to 8 query heads per kv head (else up to 4, remainders in columns 4-7).
+// WIDE: 5 to 8 query heads per kv head (bf16; int8 pages have one form for all).
 template <int D, bool INT8, bool WIDE>
 __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArgs a)
 {
     using S = Shape<D, INT8>;
     constexpr int SLOTS = D / 16;                   // lanes per head row in the prologue
     constexpr int KS = D / 16;                      // 16-element steps over head_dim
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *ring = smem;                                                             // [warp][stage]
-    float *qf = reinterpret_cast<float *>(smem + (size_t)kWarps * S::kStages * S::kStage);   // [8][kAcc] queries
+    constexpr bool PAIRED = !INT8 && !WIDE;         // remainders in columns 4-7
+    constexpr bool REST2 = !INT8 && WIDE;           // remainders in a second product
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 255) & ~uintptr_t(255));
+    float *qf = reinterpret_cast<float *>(ring + (size_t)kWarps * S::kRing);          // [8][kAcc] queries
     uint8_t *new_rows = reinterpret_cast<uint8_t *>(qf + kHeads * S::kAcc);           // the step's K and V row
     __shared__ uint32_t present_s[kWarps][S::kStages];                                // tokens of the stage that are there
     __shared__ float new_scale[2], q_mul[kHeads];
@@ -190,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
     const int n_workers = kWarps * a.splits, worker = rank * kWarps + warp;
 
     // 2. the warp's pipeline
-    uint8_t *my_ring = ring + (size_t)warp * S::kStages * S::kStage;
+    uint8_t *my_ring = ring + (size_t)warp * S::kRing;
     auto token_of = [&](int tile) -> int32_t {      // of this lane (lanes 16-31 repeat 0-15); -1: none
         const int32_t c = tile * kTile + (lane & 15);
         return c >= n_vis ? -1 : c < first ? c : low + (c - first);
@@ -221,9 +235,9 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
             for (int i = 0; i < kTile * S::kVecs / 32; ++i) {
                 const int r = (i * 32 + lane) / S::kVecs, v = (i * 32 + lane) % S::kVecs;
                 const int32_t rr = __shfl_sync(0xffffffffu, row, r);
-                const int64_t src = ((int64_t)max(rr, 0) * hkv + h) * S::kRowData + v * 16;
-                cp_async16_or_zero(kdst + r * S::kRow + v * 16, static_cast<const uint8_t *>(a.k_pool) + src, rr >= 0);
-                cp_async16_or_zero(vdst + r * S::kRow + v * 16, static_cast<const uint8_t *>(a.v_pool) + src, rr >= 0);
+                const int64_t src = ((int64_t)max(rr, 0) * hkv + h) * S::kRow + v * 16;
+                cp_async16_or_zero(kdst + S::at(r, v), static_cast<const uint8_t *>(a.k_pool) + src, rr >= 0);
+                cp_async16_or_zero(vdst + S::at(r, v), static_cast<const uint8_t *>(a.v_pool) + src, rr >= 0);
             }
             if constexpr (INT8) {
                 const float *sc = (lane < 16 ? a.k_scales : a.v_scales) + (int64_t)max(row, 0) * hkv + h;
@@ -295,8 +309,8 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
                 }
             } else if (src) {
                 const int which = r - kHeads;
-                uint8_t *dst = new_rows + which * S::kRowData;
-                uint8_t *pool = static_cast<uint8_t *>(which ? a.v_pool : a.k_pool) + (new_row * hkv + h) * S::kRowData;
+                uint8_t *dst = new_rows + which * S::kRow;
+                uint8_t *pool = static_cast<uint8_t *>(which ? a.v_pool : a.k_pool) + (new_row * hkv + h) * S::kRow;
                 const bool write = rank == 0 && new_row >= 0;
                 if constexpr (INT8) {
                     uint32_t w[4] = {0, 0, 0, 0};
@@ -324,34 +338,48 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
     }
     __syncthreads();
 
-    // 4. the queries as B fragments.  Column g4 is head g4 (WIDE), or head g4 % 4
-    //    with its remainders in columns 4-7.  int8: the four bytes 4 q4 .. of a
-    //    16-byte chunk are the products' k = 2 q4, 2 q4 + 1, 2 q4 + 8, 2 q4 + 9.
-    uint32_t qb[KS][2], qr[WIDE ? KS : 1][2];
-    bool rest = false;                               // WIDE: some query has a remainder
+    // 4. the queries as B fragments.  bf16: column g4 is head g4 (WIDE), or head
+    //    g4 % 4 with its remainders in columns 4-7.  int8: column g4 is head g4, the
+    //    four bytes 4 q4 .. of a 16-byte chunk are the products' k = 2 q4, 2 q4 + 1,
+    //    2 q4 + 8, 2 q4 + 9, and bias is 1152 times the sum of the rounded query.
+    uint32_t qb[KS][2], qr[REST2 ? KS : 1][2];
+    bool rest = false;                               // REST2: some query has a remainder
+    float bias = 0.f;
     {
-        const float *src = qf + (WIDE ? g4 : (g4 & 3)) * S::kAcc;
+        const float *src = qf + (PAIRED ? (g4 & 3) : g4) * S::kAcc;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int d = 16 * kk + (INT8 ? 4 * q4 + 2 * j : 2 * q4 + 8 * j);
                 const float2 x = *reinterpret_cast<const float2 *>(src + d);
-                const uint32_t hi = pack16<INT8>(x.x, x.y), lo = pack16_rest<INT8>(x.x, x.y, hi);
-                if constexpr (WIDE) {
+                const uint32_t hi = pack16<INT8>(x.x, x.y);
+                if constexpr (INT8) {
+                    const float2 y = unpack16<true>(hi);
+                    bias += y.x + y.y;
                     qb[kk][j] = hi;
-                    qr[kk][j] = lo;
-                    rest |= (lo & 0x7fff7fffu) != 0;
                 } else {
-                    qb[kk][j] = g4 < 4 ? hi : lo;
+                    const uint32_t lo = pack16_rest<false>(x.x, x.y, hi);
+                    qb[kk][j] = PAIRED && g4 >= 4 ? lo : hi;
+                    if constexpr (REST2) {
+                        qr[kk][j] = lo;
+                        rest |= (lo & 0x7fff7fffu) != 0;
+                    }
                 }
             }
         }
-        rest = __any_sync(0xffffffffu, rest);
+        if constexpr (REST2) rest = __any_sync(0xffffffffu, rest);
     }
     // this lane's two heads (columns 2 q4, 2 q4 + 1 of the products)
-    const int h0 = WIDE ? 2 * q4 : (2 * q4) & 3;
+    const int h0 = PAIRED ? (2 * q4) & 3 : 2 * q4;
     const float mul0 = INT8 ? q_mul[h0] : a.scale_log2, mul1 = INT8 ? q_mul[h0 + 1] : a.scale_log2;
+    float bias0 = 0.f, bias1 = 0.f;
+    if constexpr (INT8) {
+        bias += __shfl_xor_sync(0xffffffffu, bias, 1);
+        bias += __shfl_xor_sync(0xffffffffu, bias, 2);         // of head g4, in its four lanes
+        bias0 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0);
+        bias1 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0 + 4);
+    }
 
     // 5. the tiles
     float o[KS][4];
@@ -372,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
             const int i = __ffs(present >> 16) - 1;
             for (int v = lane; v < 2 * S::kVecs; v += 32) {
                 uint8_t *dst = v < S::kVecs ? kt : vt;
-                *reinterpret_cast<uint4 *>(dst + i * S::kRow + (v % S::kVecs) * 16) =
+                *reinterpret_cast<uint4 *>(dst + S::at(i, v % S::kVecs)) =
                     *reinterpret_cast<const uint4 *>(new_rows + v * 16);
             }
             if (INT8 && lane < 2) const_cast<float *>(sc)[lane * kTile + i] = new_scale[lane];
@@ -380,37 +408,35 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
         }
 
         // S^T = K Q^T
-        float c[4] = {0.f, 0.f, 0.f, 0.f}, ca[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t kaddr = smem_u32(kt) + (uint32_t)(ri + 8 * (mi & 1)) * S::kRow + 16u * (mi >> 1);
+        float c[4] = {bias0, bias1, bias0, bias1}, ca[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t kaddr = smem_u32(kt) + S::at(ri + 8 * (mi & 1), mi >> 1);
         if constexpr (INT8) {
 #pragma unroll
             for (int k2 = 0; k2 < KS / 2; ++k2) {
                 uint32_t raw[4];
-                ldmatrix_x4(raw, kaddr + 32u * k2);
+                ldmatrix_x4(raw, kaddr ^ (32u * k2));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) raw[i] ^= 0x80808080u;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t af[4] = {codes_f16x2<0x4140>(raw[2 * j]), codes_f16x2<0x4140>(raw[2 * j + 1]),
-                                            codes_f16x2<0x4342>(raw[2 * j]), codes_f16x2<0x4342>(raw[2 * j + 1])};
+                    const uint32_t af[4] = {biased_f16x2<0x4140>(raw[2 * j]), biased_f16x2<0x4140>(raw[2 * j + 1]),
+                                            biased_f16x2<0x4342>(raw[2 * j]), biased_f16x2<0x4342>(raw[2 * j + 1])};
                     mma16<true>(j ? ca : c, af, qb[2 * k2 + j][0], qb[2 * k2 + j][1]);
-                    if constexpr (WIDE)
-                        if (rest) mma16<true>(j ? ca : c, af, qr[2 * k2 + j][0], qr[2 * k2 + j][1]);
                 }
             }
         } else {
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 uint32_t af[4];
-                ldmatrix_x4(af, kaddr + 32u * kk);
+                ldmatrix_x4(af, kaddr ^ (32u * kk));
                 mma16<false>(kk & 1 ? ca : c, af, qb[kk][0], qb[kk][1]);
-                if constexpr (WIDE)
+                if constexpr (REST2)
                     if (rest) mma16<false>(kk & 1 ? ca : c, af, qr[kk][0], qr[kk][1]);
             }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] += ca[e];
-        if constexpr (!WIDE) {
+        if constexpr (PAIRED) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) c[e] += __shfl_xor_sync(0xffffffffu, c[e], 2);
         }
@@ -435,31 +461,29 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
             if (!t0) w[0] = w[1] = -INFINITY;
             if (!t1) w[2] = w[3] = -INFINITY;
         }
+        // the maxima move (and what was summed is rescaled) only when a score
+        // passes one by more than kLazyMax: no reduction in the common case
         float mx[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])}, mx2[2] = {-INFINITY, -INFINITY};
+        bool grow = mx[0] > m[0] + kLazyMax || mx[1] > m[1] + kLazyMax;
         if constexpr (INT8) {
             mx2[0] = fmaxf(w[0], w[2]);
             mx2[1] = fmaxf(w[1], w[3]);
+            grow |= mx2[0] > m2[0] + kLazyMax || mx2[1] > m2[1] + kLazyMax;
         }
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-                if constexpr (INT8) mx2[k] = fmaxf(mx2[k], __shfl_xor_sync(0xffffffffu, mx2[k], off));
-            }
-        }
-        bool grow = mx[0] > m[0] + kLazyMax || mx[1] > m[1] + kLazyMax;
-        if constexpr (INT8) grow |= mx2[0] > m2[0] + kLazyMax || mx2[1] > m2[1] + kLazyMax;
         if (__any_sync(0xffffffffu, grow)) {
             float f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
                 const bool up = mx[k] > m[k] + kLazyMax;
-                const float al = up ? fast_exp2(m[k] - mx[k]) : 1.f;
+                f[k] = up ? fast_exp2(m[k] - mx[k]) : 1.f;
                 if (up) m[k] = mx[k];
-                l[k] *= al;
-                f[k] = al;
+                l[k] *= f[k];
                 if constexpr (INT8) {
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        mx2[k] = fmaxf(mx2[k], __shfl_xor_sync(0xffffffffu, mx2[k], off));
                     const bool up2 = mx2[k] > m2[k] + kLazyMax;
                     f[k] = up2 ? fast_exp2(m2[k] - mx2[k]) : 1.f;
                     if (up2) m2[k] = mx2[k];
@@ -482,13 +506,13 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
             for (int e = 0; e < 4; ++e) c[e] = copysignf(fast_exp2(w[e] - (e & 1 ? d1 : d0)), e < 2 ? sv0 : sv1);
         }
         uint32_t pa = pack16<INT8>(c[0], c[1]), pb = pack16<INT8>(c[2], c[3]);
-        const uint32_t ra = pack16_rest<INT8>(c[0], c[1], pa), rb = pack16_rest<INT8>(c[2], c[3], pb);
         uint32_t ra_t = 0, rb_t = 0;
-        if constexpr (WIDE) {
-            ra_t = movmatrix_trans(ra);
-            rb_t = movmatrix_trans(rb);
-        } else {
-            if (q4 >= 2) {                           // columns 4-7: the remainders of heads 0-3
+        if constexpr (!INT8) {
+            const uint32_t ra = pack16_rest<false>(c[0], c[1], pa), rb = pack16_rest<false>(c[2], c[3], pb);
+            if constexpr (REST2) {
+                ra_t = movmatrix_trans(ra);
+                rb_t = movmatrix_trans(rb);
+            } else if (q4 >= 2) {                    // columns 4-7: the remainders of heads 0-3
                 pa = ra;
                 pb = rb;
             }
@@ -497,11 +521,11 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
 
         // O^T += V^T P^T
         if constexpr (INT8) {
-            const uint32_t vaddr = smem_u32(vt) + (uint32_t)(ri + 8 * (mi & 1)) * S::kRow + 16u * (mi >> 1);
+            const uint32_t vaddr = smem_u32(vt) + S::at(ri + 8 * (mi & 1), mi >> 1);
 #pragma unroll
             for (int k2 = 0; k2 < KS / 2; ++k2) {
                 uint32_t raw[4];
-                ldmatrix_x4_trans(raw, vaddr + 32u * k2);
+                ldmatrix_x4_trans(raw, vaddr ^ (32u * k2));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) raw[i] ^= 0x80808080u;
 #pragma unroll
@@ -510,17 +534,16 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
                     const uint32_t af[4] = {codes_f16x2<0x4240>(raw[2 * j]), codes_f16x2<0x4341>(raw[2 * j]),
                                             codes_f16x2<0x4240>(raw[2 * j + 1]), codes_f16x2<0x4341>(raw[2 * j + 1])};
                     mma16<true>(o[2 * k2 + j], af, pa_t, pb_t);
-                    if constexpr (WIDE) mma16<true>(o[2 * k2 + j], af, ra_t, rb_t);
                 }
             }
         } else {
-            const uint32_t vaddr = smem_u32(vt) + (uint32_t)(ri + 8 * (mi >> 1)) * S::kRow + 16u * (mi & 1);
+            const uint32_t vaddr = smem_u32(vt) + S::at(ri + 8 * (mi >> 1), mi & 1);
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
                 uint32_t af[4];
-                ldmatrix_x4_trans(af, vaddr + 32u * i);
+                ldmatrix_x4_trans(af, vaddr ^ (32u * i));
                 mma16<false>(o[i], af, pa_t, pb_t);
-                if constexpr (WIDE) mma16<false>(o[i], af, ra_t, rb_t);
+                if constexpr (REST2) mma16<false>(o[i], af, ra_t, rb_t);
             }
         }
         st = st + 1 == S::kStages ? 0 : st + 1;
@@ -538,12 +561,12 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
     for (int i = 0; i < KS; ++i) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            if constexpr (!WIDE) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
+            if constexpr (PAIRED) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
             const int d = 16 * i + (INT8 ? 2 * g4 + (e >> 1) : g4 + 8 * (e >> 1));
-            if (WIDE || q4 < 2) acc[(h0 + (e & 1)) * S::kAcc + d] = o[i][e];
+            if (!PAIRED || q4 < 2) acc[(h0 + (e & 1)) * S::kAcc + d] = o[i][e];
         }
     }
-    if (g4 == 0 && (WIDE || q4 < 2)) {
+    if (g4 == 0 && (!PAIRED || q4 < 2)) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             w_m[warp][h0 + k] = m[k];
@@ -577,7 +600,7 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
         float v = 0.f;
 #pragma unroll
         for (int k = 0; k < kWarps; ++k)
-            v += w_f[k][g] * reinterpret_cast<const float *>(ring + (size_t)k * S::kStages * S::kStage)[g * S::kAcc + d];
+            v += w_f[k][g] * reinterpret_cast<const float *>(ring + (size_t)k * S::kRing)[g * S::kAcc + d];
         qf[g * S::kAcc + d] = v;
     }
 
@@ -644,12 +667,12 @@ cudaError_t launch_as(const WindowArgs &a, int64_t units, cudaStream_t stream)
     return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE>, a);
 }
 
-// CTAs per (sequence, kv head): enough for two CTAs per SM, as long as every
+// CTAs per (sequence, kv head): enough for kCtasPerSm CTAs per SM, as long as every
 // warp keeps two tiles or more of the longest window.
 int choose_splits(int64_t units, int64_t tiles, int sms)
 {
     int c = 1;
-    while (c < kMaxSplits && units * c < 2 * sms && tiles >= (int64_t)c * 2 * 2 * kWarps) c *= 2;
+    while (c < kMaxSplits && units * c < kCtasPerSm * sms && tiles >= (int64_t)c * 2 * 2 * kWarps) c *= 2;
     return c;
 }
 
@@ -661,10 +684,10 @@ cudaError_t launch_window(WindowArgs &a, int32_t head_dim, bool int8, int32_t n_
     a.splits = choose_splits(units, (seen + kTile - 1) / kTile, sms);
     const bool wide = a.group > 4;
     if (head_dim == 128) {
-        if (int8) return wide ? launch_as<128, true, true>(a, units, stream) : launch_as<128, true, false>(a, units, stream);
+        if (int8) return launch_as<128, true, true>(a, units, stream);
         return wide ? launch_as<128, false, true>(a, units, stream) : launch_as<128, false, false>(a, units, stream);
     }
-    if (int8) return wide ? launch_as<64, true, true>(a, units, stream) : launch_as<64, true, false>(a, units, stream);
+    if (int8) return launch_as<64, true, true>(a, units, stream);
     return wide ? launch_as<64, false, true>(a, units, stream) : launch_as<64, false, false>(a, units, stream);
 }
 

@@ -56,6 +56,7 @@ def _paged(seed, lens, window, sinks, m, hkv, d, bs, int8, spare=2):
             full = torch.zeros((x, hkv, d), dtype=torch.float64)
             if int8:
                 code = torch.randint(-127, 128, (len(t), hkv, d), generator=gen, dtype=torch.int8)
+                code[..., 3] = 127                # a quantised row's largest code
                 # scales spread over three powers of ten, some rows of zeros
                 sc = 10.0 ** (torch.rand((len(t), hkv), generator=gen) * 3 - 4.5)
                 sc[torch.rand((len(t), hkv), generator=gen) < 0.03] = 0
@@ -75,7 +76,7 @@ def _cuda(*ts):
     return [None if t is None else t.cuda() for t in ts]
 
 
-def _check_decode(out, lse, q, values, lens, window, sinks, hkv, scale, q_values=None):
+def _check_decode(out, lse, q, values, lens, window, sinks, hkv, scale, int8, q_values=None):
     """out [n, Hq, D], lse [n, Hq] against the reference; q bf16 (or q_values in 64 bits)."""
     n, hq, d = out.shape
     g = hq // hkv
@@ -88,13 +89,13 @@ def _check_decode(out, lse, q, values, lens, window, sinks, hkv, scale, q_values
         seen = R.visible(x - 1, x, window, sinks)[None]
         count = int(seen.sum())
         for h in range(hkv):
-            o, ls, absum, size = R.attend(qd[s, h][None], values[s][0][:, h], values[s][1][:, h], seen, scale)
-            o, ls, absum, size = o[0], ls[0], absum[0], size[0]
+            o, ls, absum, size, top = (x[0] for x in R.attend(qd[s, h][None], values[s][0][:, h], values[s][1][:, h],
+                                                              seen, scale))
             got = out[s].view(hkv, g, d)[h]
             assert torch.isfinite(got).all(), (s, h)
-            over = (got - o).abs() - R.decode_tolerance(o, absum, size, d, count)
+            over = (got - o).abs() - R.decode_tolerance(o, absum, size, d, count, top if int8 else None)
             assert (over <= 0).all(), (s, h, float(over.max()))
-            over = (lse[s].view(hkv, g)[h] - ls).abs() - R.lse_tolerance(ls, size, d, count)
+            over = (lse[s].view(hkv, g)[h] - ls).abs() - R.lse_tolerance(ls, size, d, count, int8)
             assert (over <= 0).all(), (s, h, float(over.max()))
 
 
@@ -131,7 +132,7 @@ def test_decode(P, lens, window, sinks, hkv, group, d, bs, int8):
                                           lse_out=lse, dev_status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == 0
-    _check_decode(out, lse, q, values, lens, window, sinks, hkv, scale)
+    _check_decode(out, lse, q, values, lens, window, sinks, hkv, scale, int8)
     # a second call gives the same bits (no order of summation is left to chance)
     again = P.paged_decode_attention_window(q.cuda(), kp, vp, tab, ctx, scale, window, sinks, k_scales=ks, v_scales=vs)
     assert torch.equal(again, out)
@@ -167,16 +168,17 @@ def test_bad_blocks_and_lengths_are_reported(P, int8):
                                           lse_out=lse, dev_status=st)
     torch.cuda.synchronize()
     assert int(st.item()) == 1 | 4
-    _check_decode(out[:1], lse[:1], q[:1], values[:1], lens[:1], window, sinks, hkv, 0.125)
+    _check_decode(out[:1], lse[:1], q[:1], values[:1], lens[:1], window, sinks, hkv, 0.125, int8)
     assert torch.isfinite(out.float()).all() and not out[2].any()
     # the bad block's tokens are absent from the second sequence
     k, v = values[1]
     seen = R.visible(99, 100, window, sinks)
     seen[5 * bs:6 * bs] = False
     for h in range(hkv):
-        o, _, absum, size = R.attend(q[1].double().view(hkv, group, d)[h][None], k[:, h], v[:, h], seen[None], 0.125)
-        assert ((out[1].cpu().double().view(hkv, group, d)[h] - o[0]).abs()
-                <= R.decode_tolerance(o[0], absum[0], size[0], d, int(seen.sum()))).all()
+        o, _, absum, size, top = (x[0] for x in R.attend(q[1].double().view(hkv, group, d)[h][None], k[:, h], v[:, h],
+                                                         seen[None], 0.125))
+        assert ((out[1].cpu().double().view(hkv, group, d)[h] - o).abs()
+                <= R.decode_tolerance(o, absum, size, d, int(seen.sum()), top if int8 else None)).all()
 
 
 # starts (tokens before the new one), window, sinks, hkv, group, d, bs, rot (0: no turn), interleaved, packed
@@ -245,7 +247,7 @@ def test_step_is_turn_write_attend(P, starts, window, sinks, hkv, group, d, bs, 
         for which, (pool, sc) in enumerate(((kp, ks), (vp, vs))):
             new = pool.view(-1, hkv, d)[row].cpu().double()
             values[s][which][y] = new * sc.view(-1, hkv)[row].cpu().double()[:, None] if int8 else new
-    _check_decode(out, lse, None, values, lens, window, sinks, hkv, scale, qd[:, 0])
+    _check_decode(out, lse, None, values, lens, window, sinks, hkv, scale, int8, qd[:, 0])
 
 
 # prefix, chunk, window, sinks, hkv, group, d, bs
@@ -282,7 +284,7 @@ def test_prefill(P, prefix, chunk, window, sinks, hkv, group, d, bs):
         seen = torch.stack([R.visible(prefix[s] + i, x, window, sinks) for i in range(chunk)])
         count = int(seen.sum(1).max())
         for h in range(hkv):
-            o, ls, absum, size = R.attend(q[s].double().view(chunk, hkv, group, d)[:, h], values[s][0][:, h],
+            o, ls, absum, size, _ = R.attend(q[s].double().view(chunk, hkv, group, d)[:, h], values[s][0][:, h],
                                           values[s][1][:, h], seen, scale)
             assert torch.isfinite(got[s, :, h]).all()
             over = (got[s, :, h] - o).abs() - R.prefill_tolerance(o, absum, size, d, count)
@@ -439,7 +441,7 @@ def test_prompt_in_chunks_then_steps(P, int8):
         seen = torch.stack([R.visible(i, total[s], window, sinks) for i in range(total[s])])
         out = torch.stack(got[s]).view(total[s], hkv, group, d)
         for h in range(hkv):
-            o, _, absum, size = R.attend(qt.view(total[s], hkv, group, d)[:, h], kt[:, h], vt[:, h], seen, scale)
+            o, _, absum, size, _ = R.attend(qt.view(total[s], hkv, group, d)[:, h], kt[:, h], vt[:, h], seen, scale)
             # queries of the chunks, and keys where the two sides round across a step, are
             # off by up to a bf16 rounding each: 2 (u16 + u16) more on every score
             tol = R.prefill_tolerance(o, absum, size, d, window + sinks) + absum * 4 * R.U16 * size[..., None]

@@ -208,7 +208,7 @@ def test_reference_attention_against_a_loop():
     k, v = (torch.randn((n, d), generator=gen, dtype=torch.float64) for _ in range(2))
     q = torch.randn((n, 1, d), generator=gen, dtype=torch.float64)
     seen = torch.stack([R.visible(i, n, window, sinks) for i in range(n)])
-    o, lse, _, _ = R.attend(q, k, v, seen, 0.3)
+    o, lse, _, _, _ = R.attend(q, k, v, seen, 0.3)
     for i in range(n):
         ts = [t for t in range(n) if t <= i and (t < sinks or t > i - window)]
         w = [math.exp(0.3 * float(q[i, 0] @ k[t])) for t in ts]

@@ -76,15 +76,16 @@ def visible(q_pos, n, window, sinks):
 
 def attend(q, k, v, seen, scale):
     """One kv head: q [m, G, D], k / v [n, D], seen [m, n] -> o [m, G, D], lse
-    [m, G], sum p |v| [m, G, D] and the largest scale * sum |q| |k| [m, G] (for
-    the error bound); float64.  A row that sees nothing gives 0 and -inf."""
+    [m, G] and, for the error bound, sum p |v| [m, G, D], the largest scale *
+    sum |q| |k| [m, G] and the largest p max |v| of a token [m, G]; float64.  A
+    row that sees nothing gives 0 and -inf."""
     k, v = (torch.where(seen.any(0)[:, None], x, torch.zeros_like(x)) for x in (k, v))
     s = torch.einsum("mgd,nd->mgn", q, k) * scale
     s = s.masked_fill(~seen[:, None, :], -math.inf)
     lse = torch.logsumexp(s, dim=-1)
     p = torch.exp(s - torch.where(lse > -math.inf, lse, torch.zeros_like(lse))[..., None])
     size = torch.einsum("mgd,nd->mgn", q.abs(), k.abs()).masked_fill(~seen[:, None, :], 0).amax(-1) * scale
-    return p @ v, lse, p @ v.abs(), size
+    return p @ v, lse, p @ v.abs(), size, (p * v.abs().amax(-1)).amax(-1)
 
 
 def score_error(d, size):
@@ -93,13 +94,19 @@ def score_error(d, size):
     return (2 * d + 8) * U32 * size + 2.0 ** -22
 
 
-def decode_tolerance(o, absum, size, d, n):
-    """Absolute error of one output: the final rounding to bf16; queries and
-    probabilities are held to 2^-16 (a bf16 value and its remainder); scores'
-    errors twice (weights and their sum); sums of n / 16 products of 16 and the
-    joins, 16 truncated additions each."""
-    return U16 * o.abs() + absum * (2 * (score_error(d, size)[..., None] + 2.0 ** -16 * size[..., None]) + 2.0 ** -15
-                                    + (n / 16 + 32) * 32 * U32)
+def decode_tolerance(o, absum, size, d, n, int8_top=None):
+    """Absolute error of one output: the final rounding to bf16; scores' errors
+    twice (weights and their sum); sums of n / 16 products of 16 and the joins,
+    16 truncated additions each.  bf16 pages hold queries and probabilities to
+    2^-16 (a bf16 value and its remainder).  int8 pages (int8_top: the largest
+    p |v| of a token) round queries and weights to fp16 once: 2^-11, and 2^-25 of
+    2^8 times the largest weight for weights below fp16's normal range; their
+    scores are summed under a bias of 1152 / 127 times the largest key."""
+    if int8_top is None:
+        held, low, scores = 2.0 ** -16, 0.0, score_error(d, size)
+    else:
+        held, low, scores = 2.0 ** -11, n * 2.0 ** -17 * int8_top[..., None], 10 * score_error(d, size)
+    return U16 * o.abs() + low + absum * (2 * (scores + held * size)[..., None] + 2 * held + (n / 16 + 32) * 32 * U32)
 
 
 def prefill_tolerance(o, absum, size, d, n):
@@ -107,5 +114,6 @@ def prefill_tolerance(o, absum, size, d, n):
     return U16 * o.abs() + absum * (2 * score_error(d, size)[..., None] + U16 * (1 + U16) + (n / 16 + 32) * 32 * U32)
 
 
-def lse_tolerance(lse, size, d, n):
-    return score_error(d, size) + 2.0 ** -16 * size + (n / 16 + 32) * 32 * U32 + 4 * U32 * lse.abs()
+def lse_tolerance(lse, size, d, n, int8=False):
+    scores = 10 * score_error(d, size) + 2.0 ** -11 * size if int8 else score_error(d, size) + 2.0 ** -16 * size
+    return scores + (n / 16 + 32) * 32 * U32 + 4 * U32 * lse.abs()
