@@ -4,19 +4,19 @@
 //
 // The host knows how many tokens a query can see (window + sinks), so no plan
 // and no workspace is needed: a (sequence, kv head) unit is the work of one
-// thread-block cluster of 1 .. 8 CTAs, and its pieces are joined through the
+// thread-block cluster of 1 .. 16 CTAs, whose partials are joined through the
 // cluster's shared memory, all in one launch.
 //
-// The visible tokens of a sequence are counted through: c < first is token c,
-// the rest continue at the window's first token.  Sixteen consecutive c make a
-// tile; warp w of the cluster takes tiles w, w + n_warps, ...  A warp works alone:
-// it looks its tiles' blocks up one tile ahead, copies their K and V rows (16
-// bytes a lane, asynchronously) into a ring of its own, and contracts them with
-// the G query heads of its kv head on the tensor cores (mma.sync m16n8k16):
+// A tile is 16 tokens from a multiple of 16 on, so it lies in one block; tokens of
+// it that the query does not see are not read.  Warp w of the cluster takes the
+// unit's tiles w, w + n_warps, ...  A warp works alone: it looks its tiles' blocks up
+// one tile ahead, copies their K and V rows (16 bytes a lane, asynchronously) into a
+// ring of its own, and contracts them with the G query heads of its kv head on the
+// tensor cores (mma.sync m16n8k16):
 //   S^T = K Q^T     16 tokens as M, query heads as N = 8
 //   O^T += V^T P^T  head_dim as M, query heads as N, tokens as K
-// with a running maximum and sum in log2 units.  No barrier but the warp's own
-// until the end, where warps and then CTAs are joined by their maxima.
+// with a running maximum and sum in log2 units.  Warps and CTAs meet once, at the
+// end, where they are joined by their maxima in a fixed order.
 //
 // Rounding.  bf16 pages: products are exact in binary32 when both factors are,
 // so the queries of a step (turned in binary32) and the probabilities are split
@@ -43,12 +43,9 @@
 namespace pkv {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kTile = 16;              // tokens per tile
 constexpr int kHeads = 8;              // query heads per kv head, padded
-constexpr int kMaxSplits = 8;          // CTAs per cluster
-constexpr int kCtasPerSm = 3;          // resident CTAs that fill an SM
+constexpr int kMaxSplits = 16;         // CTAs per cluster
 constexpr float kLazyMax = 8.0f;       // the running maximum may lag by this (log2 units)
 
 struct WindowArgs {
@@ -80,10 +77,10 @@ struct Shape {
     static constexpr int kVecs = kRow / 16;
     static constexpr int kStage = 2 * kTile * kRow + (INT8 ? 2 * kTile * 4 : 0);
     static constexpr int kStages = 3;
-    static constexpr int kAcc = D + 4;                            // floats per accumulator row
-    static constexpr int kRing = kStages * kStage > kHeads * kAcc * 4 ? kStages * kStage : kHeads * kAcc * 4;
-    static constexpr size_t kSmem = 256 + (size_t)kWarps * kRing + (size_t)kHeads * kAcc * 4 + 2 * kRow;
-    static_assert(kRing % kRow == 0 && kStage % kRow == 0, "rows aligned to their size");
+    static constexpr int kAcc = D + 4;                            // floats per staged row
+    static constexpr size_t smem(int warps) { return 256 + (size_t)warps * (kStages * kStage + 2 * kRow); }
+    static_assert(kStage % kRow == 0, "rows aligned to their size");
+    static_assert(kStage >= kHeads * kAcc * 4, "a free stage holds 8 rows of binary32");
     // a row's 16-byte chunks are permuted so that chunk c of 8 consecutive rows
     // lies in 8 different bank groups
     static __device__ __forceinline__ int swizzle(int row) { return kRow >= 128 ? row & 7 : (row >> 1) & 3; }
@@ -93,6 +90,10 @@ struct Shape {
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void *src, bool there)
 {
@@ -109,13 +110,16 @@ __device__ __forceinline__ void cluster_sync_all()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// a float of the CTA `rank` of the cluster, at the same place as local address a
-__device__ __forceinline__ float ld_cluster(const float *a, uint32_t rank)
+// four floats of the CTA `rank` of the cluster, at the same place as local address a
+__device__ __forceinline__ float4 ld_cluster(const float4 *a, uint32_t rank)
 {
     uint32_t r;
-    float v;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(a)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(r) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(r)
+                 : "memory");
     return v;
 }
 
@@ -160,23 +164,46 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         mma_bf16_16816(d, a, b0, b1);
 }
 
+// The tiles that hold the tokens seen by the query of a sequence of length L:
+// tiles 0 .. n_first - 1, then those from tile w_tile on.
+struct Seen {
+    int32_t L, first, low, n_first, w_tile, tiles;
+    __device__ __forceinline__ Seen(const WindowArgs &a, int32_t len)
+    {
+        L = len < 0 || (int64_t)len > (int64_t)a.max_blocks * a.block_size ? 0 : len;
+        first = min(a.sinks, L);                // tokens below are seen
+        low = max(first, L - a.window);         // and tokens from here on
+        n_first = (first + kTile - 1) / kTile;
+        w_tile = max(low / kTile, n_first);
+        tiles = n_first + max(0, (L + kTile - 1) / kTile - w_tile);
+    }
+    // first token of tile i, and which of its 16 are seen
+    __device__ __forceinline__ int32_t token(int32_t i) const { return (i < n_first ? i : w_tile + i - n_first) * kTile; }
+    __device__ __forceinline__ uint32_t mask(int32_t t) const
+    {
+        const uint32_t below_L = L - t >= kTile ? 0xffffu : (1u << max(L - t, 0)) - 1u;
+        const uint32_t below_first = first - t >= kTile ? 0xffffu : (1u << max(first - t, 0)) - 1u;
+        const uint32_t from_low = low <= t ? 0xffffu : low - t >= kTile ? 0u : 0xffffu << (low - t);
+        return below_L & (below_first | from_low) & 0xffffu;
+    }
+};
+
 // WIDE: 5 to 8 query heads per kv head (bf16; int8 pages have one form for all).
-template <int D, bool INT8, bool WIDE>
-__global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArgs a)
+template <int D, bool INT8, bool WIDE, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode_window_kernel(const WindowArgs a)
 {
     using S = Shape<D, INT8>;
-    constexpr int SLOTS = D / 16;                   // lanes per head row in the prologue
+    constexpr int SLOTS = D / 16;                   // lanes that hold a head row (rope.cuh)
     constexpr int KS = D / 16;                      // 16-element steps over head_dim
     constexpr bool PAIRED = !INT8 && !WIDE;         // remainders in columns 4-7
     constexpr bool REST2 = !INT8 && WIDE;           // remainders in a second product
+    constexpr int QROWS = PAIRED ? 4 : 8;           // query rows that the products read
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 255) & ~uintptr_t(255));
-    float *qf = reinterpret_cast<float *>(ring + (size_t)kWarps * S::kRing);          // [8][kAcc] queries
-    uint8_t *new_rows = reinterpret_cast<uint8_t *>(qf + kHeads * S::kAcc);           // the step's K and V row
-    __shared__ uint32_t present_s[kWarps][S::kStages];                                // tokens of the stage that are there
-    __shared__ float new_scale[2], q_mul[kHeads];
-    __shared__ float w_m[kWarps][kHeads], w_m2[kWarps][kHeads], w_l[kWarps][kHeads], w_f[kWarps][kHeads];
-    __shared__ float c_m[kHeads], c_m2[kHeads], c_l[kHeads];                          // of the CTA
+    __shared__ uint32_t present_s[WARPS][S::kStages];                                 // tokens of the stage that are there
+    __shared__ float new_scale[WARPS][2], q_mul[WARPS][kHeads];
+    __shared__ float w_m[WARPS][kHeads], w_m2[WARPS][kHeads], w_l[WARPS][kHeads];
+    __shared__ float4 c_stat[kHeads];               // of the CTA: maximum, maximum of the weights, sum
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, q4 = lane & 3;        // mma fragment row group / column pair
@@ -186,100 +213,129 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
     const int s = unit / hkv, h = unit % hkv;
     const bool step = a.k_new != nullptr;
     const int32_t *trow = a.tables + (int64_t)s * a.max_blocks;
+    uint8_t *my_ring = ring + (size_t)warp * S::kStages * S::kStage;
+    uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + warp * 2 * S::kRow;   // a step's K and V row
 
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     grid_dependency_wait();
 
-    // 1. the visible tokens
-    int32_t L = __ldg(a.ctx_lens + s);
+    // 1. the tiles
+    const int32_t len = __ldg(a.ctx_lens + s);
     const int32_t t_new = step ? __ldg(a.start_pos + s) : -1;
-    if (L < 0 || (int64_t)L > (int64_t)a.max_blocks * bs) {
-        if (tid == 0 && h == 0 && rank == 0) report(a.dev_status, PKV_DEV_BAD_LENGTH);
-        L = 0;
-    }
-    const int32_t first = min(a.sinks, L);          // seen as first tokens
-    const int32_t low = max(first, L - a.window);   // and from here on
-    const int32_t n_vis = first + (L - low);
-    const int n_tiles = (n_vis + kTile - 1) / kTile;
-    const int n_workers = kWarps * a.splits, worker = rank * kWarps + warp;
+    const Seen seen(a, len);
+    if (tid == 0 && h == 0 && rank == 0 && len != seen.L) report(a.dev_status, PKV_DEV_BAD_LENGTH);
+    const int n_workers = WARPS * a.splits, worker = rank * WARPS + warp;
 
-    // 2. the warp's pipeline
-    uint8_t *my_ring = ring + (size_t)warp * S::kRing;
-    auto token_of = [&](int tile) -> int32_t {      // of this lane (lanes 16-31 repeat 0-15); -1: none
-        const int32_t c = tile * kTile + (lane & 15);
-        return c >= n_vis ? -1 : c < first ? c : low + (c - first);
+    // 2. the warp's copies, which run ahead of its products by kStages - 1 tiles
+    int32_t a_tile = worker, a_token = 0, a_off = 0, id = 0;
+    auto look_up = [&]() {                          // the block of the next tile to copy
+        if (a_tile >= seen.tiles) return;
+        a_token = seen.token(a_tile);
+        const int32_t blk = (uint32_t)a_token / (uint32_t)bs;
+        a_off = a_token - blk * bs;
+        id = __ldg(trow + blk);
     };
-    auto load_id = [&](int tile) -> int32_t {
-        const int32_t t = token_of(tile);
-        return t >= 0 ? __ldg(trow + (uint32_t)t / (uint32_t)bs) : 0;
-    };
-    int32_t id = worker < n_tiles ? load_id(worker) : 0;
-    // copies of one tile into a stage; id is its lanes' block, and the next tile's after
-    auto issue = [&](int tile, int st) {
-        if (tile < n_tiles) {
-            const int32_t t = token_of(tile);
-            int32_t row = -1;
-            if (t >= 0) {
-                if (id < 0 || id > a.n_blocks)
-                    report(a.dev_status, PKV_DEV_BAD_BLOCK_ID);
-                else
-                    row = id * bs + (int32_t)((uint32_t)t % (uint32_t)bs);
+    look_up();
+    const uint32_t lane_dst = S::at(lane / S::kVecs, lane % S::kVecs);   // of the lane's first vector in a tile
+    const int64_t token_bytes = (int64_t)hkv * S::kRow;
+    const uint8_t *k_lane = static_cast<const uint8_t *>(a.k_pool) + lane / S::kVecs * token_bytes + (int64_t)h * S::kRow +
+                            (lane % S::kVecs) * 16;
+    const int64_t k_to_v = static_cast<const uint8_t *>(a.v_pool) - static_cast<const uint8_t *>(a.k_pool);
+    constexpr int RPI = 32 / S::kVecs;              // rows that the warp copies at once
+    auto issue = [&](int st) {
+        if (a_tile < seen.tiles) {
+            uint32_t there = seen.mask(a_token);
+            if (id < 0 || id > a.n_blocks) {
+                if (lane == 0) report(a.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                there = 0;
             }
+            const int32_t row = there ? id * bs + a_off : 0;
             // bits 0-15: there; 16-31: the step's new token, which comes from new_rows
-            const uint32_t there = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
-            const uint32_t fresh = __ballot_sync(0xffffffffu, step && row >= 0 && t == t_new) & 0xffffu;
+            const uint32_t fresh = step && (uint32_t)(t_new - a_token) < (uint32_t)kTile ? there & (1u << (t_new - a_token)) : 0u;
             if (lane == 0) present_s[warp][st] = there | (fresh << 16);
-            id = load_id(tile + n_workers);
-            const uint32_t kdst = smem_u32(my_ring + st * S::kStage), vdst = kdst + kTile * S::kRow;
+            a_tile += n_workers;
+            look_up();
+            const uint32_t dst = smem_u32(my_ring + st * S::kStage);
+            const uint8_t *src = k_lane + row * token_bytes;
+            if (there == 0xffffu) {
 #pragma unroll
-            for (int i = 0; i < kTile * S::kVecs / 32; ++i) {
-                const int r = (i * 32 + lane) / S::kVecs, v = (i * 32 + lane) % S::kVecs;
-                const int32_t rr = __shfl_sync(0xffffffffu, row, r);
-                const int64_t src = ((int64_t)max(rr, 0) * hkv + h) * S::kRow + v * 16;
-                cp_async16_or_zero(kdst + S::at(r, v), static_cast<const uint8_t *>(a.k_pool) + src, rr >= 0);
-                cp_async16_or_zero(vdst + S::at(r, v), static_cast<const uint8_t *>(a.v_pool) + src, rr >= 0);
+                for (int i = 0; i < kTile / RPI; ++i) {
+                    // row i * RPI + lane / kVecs, whose swizzle is that of its two parts
+                    const uint32_t off = i * RPI * S::kRow + (lane_dst ^ (S::swizzle(i * RPI) << 4));
+                    cp_async16(dst + off, src);
+                    cp_async16(dst + kTile * S::kRow + off, src + k_to_v);
+                    src += RPI * token_bytes;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kTile / RPI; ++i) {
+                    const uint32_t off = i * RPI * S::kRow + (lane_dst ^ (S::swizzle(i * RPI) << 4));
+                    const bool in = (there >> (i * RPI + lane / S::kVecs)) & 1;
+                    cp_async16_or_zero(dst + off, in ? src : k_lane, in);
+                    cp_async16_or_zero(dst + kTile * S::kRow + off, (in ? src : k_lane) + k_to_v, in);
+                    src += RPI * token_bytes;
+                }
             }
             if constexpr (INT8) {
-                const float *sc = (lane < 16 ? a.k_scales : a.v_scales) + (int64_t)max(row, 0) * hkv + h;
-                cp_async4_or_zero(kdst + 2 * kTile * S::kRow + lane * 4, sc, row >= 0);
+                const int r = lane & 15;
+                const bool in = (there >> r) & 1;
+                cp_async4_or_zero(dst + 2 * kTile * S::kRow + lane * 4,
+                                  (lane < 16 ? a.k_scales : a.v_scales) + (row + (in ? r : 0)) * (int64_t)hkv + h, in);
             }
         }
         cp_async_commit();
     };
 #pragma unroll
-    for (int k = 0; k < S::kStages - 1; ++k) issue(worker + k * n_workers, k);
+    for (int k = 0; k < S::kStages - 1; ++k) issue(k);
 
-    // 3. the queries in binary32 (turned in a step), and a step's new rows: a head
-    //    row is the work of SLOTS lanes (rope.cuh)
-    const int64_t new_row = step ? pool_row_of(trow, a.max_blocks, a.n_blocks, bs, t_new,
-                                               tid == 0 && h == 0 && rank == 0 ? a.dev_status : nullptr)
-                                 : -1;
+    // 3. the queries in binary32 (turned in a step) into the free stage, and a
+    //    step's new rows: a head row is the work of SLOTS lanes (rope.cuh)
+    uint32_t qb[KS][2], qr[INT8 ? 1 : KS][2];
+    bool rest = false;                           // bf16: some query has a remainder
+    float bias = 0.f;
+    const int h0 = PAIRED ? (2 * q4) & 3 : 2 * q4;   // this lane's two heads: columns 2 q4, 2 q4 + 1
+    float mul0 = a.scale_log2, mul1 = a.scale_log2, bias0 = 0.f, bias1 = 0.f;
     {
-        const int slot = tid % SLOTS;
-        for (int r0 = 0; r0 < kHeads + 2; r0 += kThreads / SLOTS) {
-            const int r = r0 + tid / SLOTS;          // 0 .. 7 queries, 8 the K row, 9 the V row
-            int v0, v1;
-            const bool turn = rope_vectors(a.rope, slot, v0, v1) && r <= kHeads;
-            const __nv_bfloat16 *src = nullptr;
-            if (r < kHeads) {
-                if (r < G) src = a.q + s * a.q_stride + ((int64_t)h * G + r) * D;
-            } else if (step && r < kHeads + 2) {
-                src = r == kHeads ? a.k_new + s * a.k_stride + (int64_t)h * D : a.v_new + s * a.v_stride + (int64_t)h * D;
-            }
-            uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+        constexpr int PER = 32 / SLOTS;          // rows at once
+        constexpr int NIT = (QROWS + PER - 1) / PER + 1;
+        float *qf = reinterpret_cast<float *>(my_ring + (S::kStages - 1) * S::kStage);
+        const int slot = lane % SLOTS;
+        int v0, v1;
+        const bool turn = rope_vectors(a.rope, slot, v0, v1);
+        // row it * PER + lane / SLOTS of the queries; the last round is K and V
+        auto source = [&](int it) -> const __nv_bfloat16 * {
+            const int r = it * PER + lane / SLOTS;
+            if (it < NIT - 1) return r < G ? a.q + s * a.q_stride + ((int64_t)h * G + r) * D : nullptr;
+            if (!step || lane / SLOTS > 1) return nullptr;
+            return lane / SLOTS == 0 ? a.k_new + s * a.k_stride + (int64_t)h * D : a.v_new + s * a.v_stride + (int64_t)h * D;
+        };
+        uint4 x0[NIT], x1[NIT];
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+            const __nv_bfloat16 *src = source(it);
+            x0[it] = x1[it] = make_uint4(0, 0, 0, 0);
             if (src) {
-                x0 = __ldg(reinterpret_cast<const uint4 *>(src) + v0);
-                x1 = __ldg(reinterpret_cast<const uint4 *>(src) + v1);
+                x0[it] = __ldg(reinterpret_cast<const uint4 *>(src) + v0);
+                x1[it] = __ldg(reinterpret_cast<const uint4 *>(src) + v1);
             }
+        }
+        float c[8], sn[8];
+        if (turn) rope_angles(a.rope, slot, t_new, c, sn);
+        // every warp has the new rows, the first one writes them
+        const int64_t new_row = step && worker == 0 ? pool_row_of(trow, a.max_blocks, a.n_blocks, bs, t_new,
+                                                                  lane == 0 && h == 0 ? a.dev_status : nullptr)
+                                                    : -1;
+#pragma unroll
+        for (int it = 0; it < NIT; ++it) {
+            if (it == NIT - 1 && !step) break;
+            const int r = it * PER + lane / SLOTS;
             float x[16];
-            unpack_bf16x8(x0, x);
-            unpack_bf16x8(x1, x + 8);
-            if (turn && src) {
-                float c[8], sn[8];
-                rope_angles(a.rope, slot, t_new, c, sn);
+            unpack_bf16x8(x0[it], x);
+            unpack_bf16x8(x1[it], x + 8);
+            if (turn && (it < NIT - 1 || lane / SLOTS == 0)) {
                 rope_turn(a.rope.interleaved, c, sn, x);
-                x0 = pack_bf16x8(x);
-                x1 = pack_bf16x8(x + 8);
+                x0[it] = pack_bf16x8(x);
+                x1[it] = pack_bf16x8(x + 8);
             }
             float amax = 0.f;
             if constexpr (INT8) {
@@ -288,64 +344,60 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
 #pragma unroll
                 for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
             }
-            int code[16];
-            float scale = 0.f;
-            if constexpr (INT8) scale = int8_codes<16>(x, amax, code);
-            if (r < kHeads) {
+            if (it < NIT - 1) {
+                if (r >= QROWS) continue;
                 if constexpr (INT8) {
                     // fp16 holds the query as multiples of the power of two below its largest element
                     const int e = min(max((int)((__float_as_uint(amax) >> 23) & 0xff) - 127, -126), 126);
                     const float down = amax > 0.f ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) x[k] *= down;
-                    if (slot == 0) q_mul[r] = a.scale_log2 * (amax > 0.f ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f);
+                    for (int i = 0; i < 16; ++i) x[i] *= down;
+                    if (slot == 0)
+                        q_mul[warp][r] = a.scale_log2 * (amax > 0.f ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f);
                 }
                 float *dst = qf + r * S::kAcc;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    *reinterpret_cast<float4 *>(dst + 8 * v0 + 4 * k) = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-                    *reinterpret_cast<float4 *>(dst + 8 * v1 + 4 * k) =
-                        make_float4(x[8 + 4 * k], x[9 + 4 * k], x[10 + 4 * k], x[11 + 4 * k]);
+                for (int i = 0; i < 2; ++i) {
+                    *reinterpret_cast<float4 *>(dst + 8 * v0 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    *reinterpret_cast<float4 *>(dst + 8 * v1 + 4 * i) =
+                        make_float4(x[8 + 4 * i], x[9 + 4 * i], x[10 + 4 * i], x[11 + 4 * i]);
                 }
-            } else if (src) {
-                const int which = r - kHeads;
-                uint8_t *dst = new_rows + which * S::kRow;
+            } else {
+                const int which = lane / SLOTS;
+                uint8_t *dst = new_rows + (which & 1) * S::kRow;
                 uint8_t *pool = static_cast<uint8_t *>(which ? a.v_pool : a.k_pool) + (new_row * hkv + h) * S::kRow;
-                const bool write = rank == 0 && new_row >= 0;
                 if constexpr (INT8) {
+                    int code[16];
+                    const float scale = int8_codes<16>(x, amax, code);
                     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
                     const uint2 y0 = make_uint2(w[0], w[1]), y1 = make_uint2(w[2], w[3]);
+                    if (which > 1) continue;
                     *reinterpret_cast<uint2 *>(dst + 8 * v0) = y0;
                     *reinterpret_cast<uint2 *>(dst + 8 * v1) = y1;
-                    if (slot == 0) new_scale[which] = scale;
-                    if (write) {
+                    if (slot == 0) new_scale[warp][which] = scale;
+                    if (new_row >= 0) {
                         *reinterpret_cast<uint2 *>(pool + 8 * v0) = y0;
                         *reinterpret_cast<uint2 *>(pool + 8 * v1) = y1;
                         if (slot == 0) (which ? a.v_scales : a.k_scales)[new_row * hkv + h] = scale;
                     }
                 } else {
-                    *reinterpret_cast<uint4 *>(dst + 16 * v0) = x0;
-                    *reinterpret_cast<uint4 *>(dst + 16 * v1) = x1;
-                    if (write) {
-                        *reinterpret_cast<uint4 *>(pool + 16 * v0) = x0;
-                        *reinterpret_cast<uint4 *>(pool + 16 * v1) = x1;
+                    if (which > 1) continue;
+                    *reinterpret_cast<uint4 *>(dst + 16 * v0) = x0[it];
+                    *reinterpret_cast<uint4 *>(dst + 16 * v1) = x1[it];
+                    if (new_row >= 0) {
+                        *reinterpret_cast<uint4 *>(pool + 16 * v0) = x0[it];
+                        *reinterpret_cast<uint4 *>(pool + 16 * v1) = x1[it];
                     }
                 }
             }
         }
-    }
-    __syncthreads();
-
-    // 4. the queries as B fragments.  bf16: column g4 is head g4 (WIDE), or head
-    //    g4 % 4 with its remainders in columns 4-7.  int8: column g4 is head g4, the
-    //    four bytes 4 q4 .. of a 16-byte chunk are the products' k = 2 q4, 2 q4 + 1,
-    //    2 q4 + 8, 2 q4 + 9, and bias is 1152 times the sum of the rounded query.
-    uint32_t qb[KS][2], qr[REST2 ? KS : 1][2];
-    bool rest = false;                               // REST2: some query has a remainder
-    float bias = 0.f;
-    {
+        __syncwarp();
+        // as B fragments.  bf16: column g4 is head g4 (WIDE), or head g4 % 4 with
+        // its remainders in columns 4-7.  int8: column g4 is head g4, the four bytes
+        // 4 q4 .. of a 16-byte chunk are the products' k = 2 q4, 2 q4 + 1, 2 q4 + 8,
+        // 2 q4 + 9, and bias is 1152 times the sum of the rounded query.
         const float *src = qf + (PAIRED ? (g4 & 3) : g4) * S::kAcc;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
@@ -360,39 +412,43 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
                     qb[kk][j] = hi;
                 } else {
                     const uint32_t lo = pack16_rest<false>(x.x, x.y, hi);
-                    qb[kk][j] = PAIRED && g4 >= 4 ? lo : hi;
-                    if constexpr (REST2) {
-                        qr[kk][j] = lo;
-                        rest |= (lo & 0x7fff7fffu) != 0;
-                    }
+                    qb[kk][j] = hi;
+                    qr[kk][j] = lo;
+                    rest |= (lo & 0x7fff7fffu) != 0;
                 }
             }
         }
-        if constexpr (REST2) rest = __any_sync(0xffffffffu, rest);
-    }
-    // this lane's two heads (columns 2 q4, 2 q4 + 1 of the products)
-    const int h0 = PAIRED ? (2 * q4) & 3 : 2 * q4;
-    const float mul0 = INT8 ? q_mul[h0] : a.scale_log2, mul1 = INT8 ? q_mul[h0 + 1] : a.scale_log2;
-    float bias0 = 0.f, bias1 = 0.f;
-    if constexpr (INT8) {
-        bias += __shfl_xor_sync(0xffffffffu, bias, 1);
-        bias += __shfl_xor_sync(0xffffffffu, bias, 2);         // of head g4, in its four lanes
-        bias0 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0);
-        bias1 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0 + 4);
+        if constexpr (!INT8) rest = __any_sync(0xffffffffu, rest);
+        if constexpr (PAIRED) {                  // columns 4-7: the remainders, or the heads again
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (rest && g4 >= 4) qb[kk][j] = qr[kk][j];
+        }
+        if constexpr (INT8) {
+            mul0 = q_mul[warp][h0];
+            mul1 = q_mul[warp][h0 + 1];
+            bias += __shfl_xor_sync(0xffffffffu, bias, 1);
+            bias += __shfl_xor_sync(0xffffffffu, bias, 2);         // of head g4, in its four lanes
+            bias0 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0);
+            bias1 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0 + 4);
+        }
+        __syncwarp();                            // the free stage is read
     }
 
-    // 5. the tiles
+    // 4. the tiles
     float o[KS][4];
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, m2[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    int st = 0;
-    for (int tile = worker; tile < n_tiles; tile += n_workers) {
+    int st = 0;                                  // stage of the next tile; the one before it is free
+    for (int tile = worker; tile < seen.tiles; tile += n_workers) {
         cp_async_wait<S::kStages - 2>();
         __syncwarp();                                // the tile is there, the stage before it is free
-        issue(tile + (S::kStages - 1) * n_workers, st == 0 ? S::kStages - 1 : st - 1);
+        issue(st == 0 ? S::kStages - 1 : st - 1);
         uint8_t *kt = my_ring + st * S::kStage, *vt = kt + kTile * S::kRow;
         const float *sc = reinterpret_cast<const float *>(vt + kTile * S::kRow);     // int8: K, V scales
         const uint32_t present = present_s[warp][st];
@@ -403,7 +459,7 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
                 *reinterpret_cast<uint4 *>(dst + S::at(i, v % S::kVecs)) =
                     *reinterpret_cast<const uint4 *>(new_rows + v * 16);
             }
-            if (INT8 && lane < 2) const_cast<float *>(sc)[lane * kTile + i] = new_scale[lane];
+            if (INT8 && lane < 2) const_cast<float *>(sc)[lane * kTile + i] = new_scale[warp][lane];
             __syncwarp();
         }
 
@@ -436,18 +492,19 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) c[e] += ca[e];
-        if constexpr (PAIRED) {
+        if constexpr (PAIRED) {                      // every column's lane has its head's whole score
+            if (rest) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] += __shfl_xor_sync(0xffffffffu, c[e], 2);
+                for (int e = 0; e < 4; ++e) c[e] += __shfl_xor_sync(0xffffffffu, c[e], 2);
+            }
         }
 
         // scores in log2 units: c[0], c[1] of token g4, c[2], c[3] of token g4 + 8
-        const bool t0 = (present >> g4) & 1, t1 = (present >> (g4 + 8)) & 1;
         const float k0 = INT8 ? sc[g4] : 1.f, k1 = INT8 ? sc[g4 + 8] : 1.f;
-        c[0] = t0 ? c[0] * (k0 * mul0) : -INFINITY;
-        c[1] = t0 ? c[1] * (k0 * mul1) : -INFINITY;
-        c[2] = t1 ? c[2] * (k1 * mul0) : -INFINITY;
-        c[3] = t1 ? c[3] * (k1 * mul1) : -INFINITY;
+        c[0] *= k0 * mul0;
+        c[1] *= k0 * mul1;
+        c[2] *= k1 * mul0;
+        c[3] *= k1 * mul1;
         float w[4];                                  // int8: scores with the V scale
         float sv0 = 0.f, sv1 = 0.f;
         if constexpr (INT8) {
@@ -458,8 +515,10 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
             w[1] = c[1] + lv0;
             w[2] = c[2] + lv1;
             w[3] = c[3] + lv1;
-            if (!t0) w[0] = w[1] = -INFINITY;
-            if (!t1) w[2] = w[3] = -INFINITY;
+        }
+        if ((present & 0xffffu) != 0xffffu) {
+            if (!((present >> g4) & 1)) c[0] = c[1] = w[0] = w[1] = -INFINITY;
+            if (!((present >> (g4 + 8)) & 1)) c[2] = c[3] = w[2] = w[3] = -INFINITY;
         }
         // the maxima move (and what was summed is rescaled) only when a score
         // passes one by more than kLazyMax: no reduction in the common case
@@ -549,13 +608,14 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
         st = st + 1 == S::kStages ? 0 : st + 1;
     }
 
-    // 6. the warp's partial: sums over its tokens, remainders added to their heads
+    // 5. the warp's partial, into its ring: sums over its tokens, remainders added
+    //    to their heads
     cp_async_wait<0>();
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) l[k] += __shfl_xor_sync(0xffffffffu, l[k], off);
+        for (int off = 4; off < 32; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
     float *acc = reinterpret_cast<float *>(my_ring);
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -568,88 +628,108 @@ __global__ void __launch_bounds__(kThreads) decode_window_kernel(const WindowArg
     }
     if (g4 == 0 && (!PAIRED || q4 < 2)) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            w_m[warp][h0 + k] = m[k];
-            w_m2[warp][h0 + k] = INT8 ? m2[k] : m[k];
-            w_l[warp][h0 + k] = l[k];
+        for (int i = 0; i < 2; ++i) {
+            w_m[warp][h0 + i] = m[i];
+            w_m2[warp][h0 + i] = INT8 ? m2[i] : m[i];
+            w_l[warp][h0 + i] = l[i];
         }
     }
     __syncthreads();
 
-    // 7. the CTA's partial
-    if (tid < G) {
-        float M = -INFINITY, M2 = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            M = fmaxf(M, w_m[k][tid]);
-            M2 = fmaxf(M2, w_m2[k][tid]);
-        }
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k) {
-            if (w_m[k][tid] != -INFINITY) sum += fast_exp2(w_m[k][tid] - M) * w_l[k][tid];
-            else sum += w_l[k][tid];                 // 0, or the NaN of a score
-            w_f[k][tid] = w_m2[k][tid] == -INFINITY ? 1.f : fast_exp2(w_m2[k][tid] - M2);
-        }
-        c_m[tid] = M;
-        c_m2[tid] = M2;
-        c_l[tid] = sum;
-    }
-    __syncthreads();
-    for (int i = tid; i < G * D; i += kThreads) {
-        const int g = i / D, d = i % D;
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < kWarps; ++k)
-            v += w_f[k][g] * reinterpret_cast<const float *>(ring + (size_t)k * S::kRing)[g * S::kAcc + d];
-        qf[g * S::kAcc + d] = v;
-    }
-
-    // 8. joined over the cluster; each CTA writes its share of the outputs
-    __nv_bfloat16 *out = a.out + ((int64_t)s * a.n_q_heads + (int64_t)h * G) * D;
-    if (a.splits > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
-    for (int i = rank * kThreads + tid; i < G * D / 2; i += a.splits * kThreads) {
-        const int g = i / (D / 2), d = (i % (D / 2)) * 2;
-        float M = -INFINITY, M2 = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
-        float rm[kMaxSplits], rm2[kMaxSplits], rl[kMaxSplits], ra[kMaxSplits], rb[kMaxSplits];
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r) {
-            rm[r] = rm2[r] = -INFINITY;
-            rl[r] = ra[r] = rb[r] = 0.f;
-            if (r >= a.splits) continue;
-            rm[r] = a.splits > 1 ? ld_cluster(&c_m[g], r) : c_m[g];
-            rm2[r] = a.splits > 1 ? ld_cluster(&c_m2[g], r) : c_m2[g];
-            rl[r] = a.splits > 1 ? ld_cluster(&c_l[g], r) : c_l[g];
-            ra[r] = a.splits > 1 ? ld_cluster(&qf[g * S::kAcc + d], r) : qf[g * S::kAcc + d];
-            rb[r] = a.splits > 1 ? ld_cluster(&qf[g * S::kAcc + d + 1], r) : qf[g * S::kAcc + d + 1];
-            M = fmaxf(M, rm[r]);
-            M2 = fmaxf(M2, rm2[r]);
-        }
-#pragma unroll
-        for (int r = 0; r < kMaxSplits; ++r) {
-            sum += rm[r] == -INFINITY ? rl[r] : fast_exp2(rm[r] - M) * rl[r];
-            const float f = rm2[r] == -INFINITY ? 1.f : fast_exp2(rm2[r] - M2);
-            v0 += f * ra[r];
-            v1 += f * rb[r];
-        }
+    // 6. joined over the warps, in place of the first warp's, then over the cluster,
+    //    where each CTA writes its share of the outputs
+    const int64_t head0 = (int64_t)s * a.n_q_heads + (int64_t)h * G;
+    auto finish = [&](int g, int d, const float4 &v, float M, float M2, float sum) {
         // o = 2^M2 v / (2^M sum); no token seen: 0
         const float inv = sum == 0.f ? 0.f : (M2 == -INFINITY ? 1.f : INT8 ? fast_exp2(M2 - M) : 1.f) / sum;
-        *reinterpret_cast<uint32_t *>(out + g * D + d) = pack_bf16x2(v0 * inv, v1 * inv);
+        *reinterpret_cast<uint2 *>(a.out + (head0 + g) * D + d) =
+            make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
         if (a.lse_out && d == 0)
-            a.lse_out[(int64_t)s * a.n_q_heads + (int64_t)h * G + g] =
-                sum == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * 0.69314718055994531f + logf(sum);
+            a.lse_out[head0 + g] = sum == 0.f ? -INFINITY : (M == -INFINITY ? 0.f : M) * 0.69314718055994531f + logf(sum);
+    };
+    // joins a partial to what was joined before it.  One without a maximum has seen
+    // nothing: its sums are 0 (or the NaN of a score).
+    auto join = [&](float4 &v, float &M, float &M2, float &sum, const float4 &x, float xm, float xm2, float xl) {
+        const float N = fmaxf(M, xm), N2 = fmaxf(M2, xm2);
+        sum = sum * (M == -INFINITY ? 1.f : fast_exp2(M - N)) + xl * (xm == -INFINITY ? 1.f : fast_exp2(xm - N));
+        const float f = M2 == -INFINITY ? 1.f : fast_exp2(M2 - N2), g = xm2 == -INFINITY ? 1.f : fast_exp2(xm2 - N2);
+        v = make_float4(v.x * f + x.x * g, v.y * f + x.y * g, v.z * f + x.z * g, v.w * f + x.w * g);
+        M = N;
+        M2 = N2;
+    };
+    float4 *acc0 = reinterpret_cast<float4 *>(ring);
+    for (int i = tid; i < G * (D / 4); i += 32 * WARPS) {
+        const int g = i / (D / 4), d = (i % (D / 4)) * 4, at = (g * S::kAcc + d) / 4;
+        float4 v = acc0[at];
+        float M = w_m[0][g], M2 = w_m2[0][g], sum = w_l[0][g];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+            join(v, M, M2, sum, reinterpret_cast<const float4 *>(ring + (size_t)w * S::kStages * S::kStage)[at], w_m[w][g],
+                 w_m2[w][g], w_l[w][g]);
+        if (a.splits == 1) {
+            finish(g, d, v, M, M2, sum);
+        } else {
+            acc0[at] = v;
+            if (d == 0) c_stat[g] = make_float4(M, M2, sum, 0.f);
+        }
     }
-    if (a.splits > 1) cluster_sync_all();            // no CTA leaves while another reads it
+    if (a.splits == 1) return;
+    cluster_sync_all();
+    for (int i = rank * 32 * WARPS + tid; i < G * (D / 4); i += a.splits * 32 * WARPS) {
+        const int g = i / (D / 4), d = (i % (D / 4)) * 4, at = (g * S::kAcc + d) / 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float M = -INFINITY, M2 = -INFINITY, sum = 0.f;
+        constexpr int kRound = 8;                    // partials in flight
+        for (int r0 = 0; r0 < a.splits; r0 += kRound) {
+            float4 x[kRound], stat[kRound];
+#pragma unroll
+            for (int k = 0; k < kRound; ++k) {
+                if (r0 + k >= a.splits) break;
+                x[k] = ld_cluster(acc0 + at, r0 + k);
+                stat[k] = ld_cluster(&c_stat[g], r0 + k);
+            }
+#pragma unroll
+            for (int k = 0; k < kRound; ++k) {
+                if (r0 + k >= a.splits) break;
+                join(v, M, M2, sum, x[k], stat[k].x, stat[k].y, stat[k].z);
+            }
+        }
+        finish(g, d, v, M, M2, sum);
+    }
+    cluster_sync_all();                              // no CTA leaves while another reads it
 }
 
-template <int D, bool INT8, bool WIDE>
-cudaError_t launch_as(const WindowArgs &a, int64_t units, cudaStream_t stream)
+struct Choice {
+    int splits = 0, occupancy = 0;
+    int64_t warps = -1;      // resident at once
+};
+
+// The most CTAs per unit with which all CTAs of WARPS warps are resident at once
+// and every warp keeps two tiles of the longest window.
+template <int D, bool INT8, bool WIDE, int WARPS>
+cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
-    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE>);
-    const cudaError_t e = prepare_kernel(kern, kThreads, Shape<D, INT8>::kSmem, nullptr);
+    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, WARPS>);
+    const cudaError_t e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), &c->occupancy);
     if (e != cudaSuccess) return e;
+    const int64_t slots = (int64_t)sms * c->occupancy;
+    int64_t n = slots / units;
+    if (n > tiles / (2 * WARPS)) n = tiles / (2 * WARPS);
+    if (n > kMaxSplits) n = kMaxSplits;
+    c->splits = n < 1 ? 1 : (int)n;
+    c->warps = (units * c->splits < slots ? units * c->splits : slots) * WARPS;
+    return cudaSuccess;
+}
+
+template <int D, bool INT8, bool WIDE, int WARPS>
+cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, cudaStream_t stream)
+{
+    const auto kern = decode_window_kernel<D, INT8, WIDE, WARPS>;
+    a.splits = c.splits;
+    if (a.splits > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -659,36 +739,44 @@ cudaError_t launch_as(const WindowArgs &a, int64_t units, cudaStream_t stream)
     at[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(units * a.splits));
-    lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = Shape<D, INT8>::kSmem;
+    lc.blockDim = dim3(32 * WARPS);
+    lc.dynamicSmemBytes = Shape<D, INT8>::smem(WARPS);
     lc.stream = stream;
     lc.attrs = at;
     lc.numAttrs = a.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE>, a);
+    return cudaLaunchKernelEx(&lc, kern, a);
 }
 
-// CTAs per (sequence, kv head): enough for kCtasPerSm CTAs per SM, as long as every
-// warp keeps two tiles or more of the longest window.
-int choose_splits(int64_t units, int64_t tiles, int sms)
+// CTAs of 4 warps, or of 2 where that lets more warps be resident (a batch whose
+// units are more than the larger CTAs' places, but not the smaller ones').
+template <int D, bool INT8, bool WIDE>
+cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
-    int c = 1;
-    while (c < kMaxSplits && units * c < kCtasPerSm * sms && tiles >= (int64_t)c * 2 * 2 * kWarps) c *= 2;
-    return c;
+    Choice c4, c2;
+    cudaError_t e = choose<D, INT8, WIDE, 4>(units, tiles, sms, &c4);
+    if (e != cudaSuccess) return e;
+    e = choose<D, INT8, WIDE, 2>(units, tiles, sms, &c2);
+    if (e != cudaSuccess) return e;
+    const int64_t places4 = (int64_t)sms * c4.occupancy, places2 = (int64_t)sms * c2.occupancy;
+    const bool small = (units > places4 && units <= places2) || (units <= places4 && c2.warps > c4.warps);
+    return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, stream) : launch_as<D, INT8, WIDE, 4>(a, c4, units, stream);
 }
 
 cudaError_t launch_window(WindowArgs &a, int32_t head_dim, bool int8, int32_t n_seqs, int sms, cudaStream_t stream)
 {
     const int64_t units = (int64_t)n_seqs * a.n_kv_heads;
-    int64_t seen = (int64_t)a.max_blocks * a.block_size;
-    if ((int64_t)a.window + a.sinks < seen) seen = (int64_t)a.window + a.sinks;
-    a.splits = choose_splits(units, (seen + kTile - 1) / kTile, sms);
+    int64_t tokens = (int64_t)a.max_blocks * a.block_size;
+    if ((int64_t)a.window + a.sinks < tokens) tokens = (int64_t)a.window + a.sinks;
+    const int64_t tiles = (tokens + kTile - 1) / kTile;
     const bool wide = a.group > 4;
     if (head_dim == 128) {
-        if (int8) return launch_as<128, true, true>(a, units, stream);
-        return wide ? launch_as<128, false, true>(a, units, stream) : launch_as<128, false, false>(a, units, stream);
+        if (int8) return launch_sized<128, true, true>(a, units, tiles, sms, stream);
+        return wide ? launch_sized<128, false, true>(a, units, tiles, sms, stream)
+                    : launch_sized<128, false, false>(a, units, tiles, sms, stream);
     }
-    if (int8) return launch_as<64, true, true>(a, units, stream);
-    return wide ? launch_as<64, false, true>(a, units, stream) : launch_as<64, false, false>(a, units, stream);
+    if (int8) return launch_sized<64, true, true>(a, units, tiles, sms, stream);
+    return wide ? launch_sized<64, false, true>(a, units, tiles, sms, stream)
+                : launch_sized<64, false, false>(a, units, tiles, sms, stream);
 }
 
 // Host checks of both calls; fills *a.
