@@ -34,6 +34,8 @@
 // whatever the scales are.
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
@@ -700,9 +702,57 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 }
 
 struct Choice {
-    int splits = 0, occupancy = 0;
-    int64_t warps = -1;      // resident at once
+    int splits = 0;
+    int64_t places = 0;      // CTAs of one unit each that are resident at once
+    int64_t warps = 0;       // resident warps of the launch
 };
+
+template <int D, bool INT8, bool WIDE, int WARPS>
+cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int64_t units, int splits, cudaStream_t stream)
+{
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)splits;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)(units * splits));
+    lc.blockDim = dim3(32 * WARPS);
+    lc.dynamicSmemBytes = Shape<D, INT8>::smem(WARPS);
+    lc.stream = stream;
+    lc.attrs = at;
+    lc.numAttrs = splits > 1 ? 2 : 1;
+    return lc;
+}
+
+// How many clusters of `splits` CTAs are resident at once on the current device
+// (clusters stay within a GPC, so not every SM can hold one); asked once.
+template <int D, bool INT8, bool WIDE, int WARPS>
+cudaError_t resident_clusters(int splits, int *out)
+{
+    static std::atomic<int> known[64][kMaxSplits + 1];   // the number + 1; 0: not asked yet
+    const auto kern = decode_window_kernel<D, INT8, WIDE, WARPS>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && known[dev][splits] > 0) {
+        *out = known[dev][splits] - 1;
+        return cudaSuccess;
+    }
+    if (splits > 8) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, 1, splits, nullptr);
+    lc.attrs = at + 1;
+    lc.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(out, kern, &lc);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) known[dev][splits] = *out + 1;
+    return cudaSuccess;
+}
 
 // The most CTAs per unit with which all CTAs of WARPS warps are resident at once
 // and every warp keeps two tiles of the longest window.
@@ -710,41 +760,31 @@ template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
     const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, WARPS>);
-    const cudaError_t e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), &c->occupancy);
+    int occupancy = 0;
+    cudaError_t e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), &occupancy);
     if (e != cudaSuccess) return e;
-    const int64_t slots = (int64_t)sms * c->occupancy;
-    int64_t n = slots / units;
+    c->places = (int64_t)sms * occupancy;
+    int64_t n = c->places / units;
     if (n > tiles / (2 * WARPS)) n = tiles / (2 * WARPS);
     if (n > kMaxSplits) n = kMaxSplits;
+    for (; n > 1; --n) {
+        int clusters = 0;
+        e = resident_clusters<D, INT8, WIDE, WARPS>((int)n, &clusters);
+        if (e != cudaSuccess) return e;
+        if (clusters >= units) break;
+    }
     c->splits = n < 1 ? 1 : (int)n;
-    c->warps = (units * c->splits < slots ? units * c->splits : slots) * WARPS;
+    c->warps = (units * c->splits < c->places ? units * c->splits : c->places) * WARPS;
     return cudaSuccess;
 }
 
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, cudaStream_t stream)
 {
-    const auto kern = decode_window_kernel<D, INT8, WIDE, WARPS>;
     a.splits = c.splits;
-    if (a.splits > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)a.splits;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3((unsigned)(units * a.splits));
-    lc.blockDim = dim3(32 * WARPS);
-    lc.dynamicSmemBytes = Shape<D, INT8>::smem(WARPS);
-    lc.stream = stream;
-    lc.attrs = at;
-    lc.numAttrs = a.splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&lc, kern, a);
+    const cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, units, c.splits, stream);
+    return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, WARPS>, a);
 }
 
 // CTAs of 4 warps, or of 2 where that lets more warps be resident (a batch whose
@@ -757,8 +797,7 @@ cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, c
     if (e != cudaSuccess) return e;
     e = choose<D, INT8, WIDE, 2>(units, tiles, sms, &c2);
     if (e != cudaSuccess) return e;
-    const int64_t places4 = (int64_t)sms * c4.occupancy, places2 = (int64_t)sms * c2.occupancy;
-    const bool small = (units > places4 && units <= places2) || (units <= places4 && c2.warps > c4.warps);
+    const bool small = units > c4.places ? units <= c2.places : c2.warps > c4.warps;
     return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, stream) : launch_as<D, INT8, WIDE, 4>(a, c4, units, stream);
 }
 
