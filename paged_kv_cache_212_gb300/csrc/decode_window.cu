@@ -29,9 +29,9 @@
 // exponent: a byte permute, and one subtraction or, for K, one correction by
 // 1152 times the query's sum).  Queries and weights are rounded once to fp16
 // (2^-11, eight times finer than the bf16 output).  The K scale multiplies the
-// score; the V scale joins the probability as exp2(s + log2 |v_scale| - m2)
-// under a maximum m2 of its own, so that the fp16 weights use their range
-// whatever the scales are.
+// score; the V scale joins the probability, and the weight is multiplied by a
+// running power of two r that keeps the largest one in fp16's range whatever the
+// scales are.
 #include <math.h>
 
 #include <atomic>
@@ -48,6 +48,7 @@ namespace {
 constexpr int kTile = 16;              // tokens per tile
 constexpr int kHeads = 8;              // query heads per kv head, padded
 constexpr int kMaxSplits = 16;         // CTAs per cluster
+constexpr float kMostLr = 120.f;       // int8: log2 of the largest factor on the weights
 constexpr float kLazyMax = 8.0f;       // the running maximum may lag by this (log2 units)
 
 struct WindowArgs {
@@ -57,6 +58,7 @@ struct WindowArgs {
     void *k_pool, *v_pool;
     float *k_scales, *v_scales;
     int32_t n_blocks, block_size, n_kv_heads;
+    uint32_t tiles_per_block, block_magic;   // tile / tiles_per_block = the product's upper half, above one tile
     const int32_t *tables;
     int32_t max_blocks;
     const int32_t *ctx_lens;
@@ -179,10 +181,11 @@ struct Seen {
         w_tile = max(low / kTile, n_first);
         tiles = n_first + max(0, (L + kTile - 1) / kTile - w_tile);
     }
-    // first token of tile i, and which of its 16 are seen
-    __device__ __forceinline__ int32_t token(int32_t i) const { return (i < n_first ? i : w_tile + i - n_first) * kTile; }
+    // the place of tile i in the sequence, in tiles, and which of its 16 tokens are seen
+    __device__ __forceinline__ int32_t place(int32_t i) const { return i < n_first ? i : w_tile + i - n_first; }
     __device__ __forceinline__ uint32_t mask(int32_t t) const
     {
+        if (t >= low && t + kTile <= L) return 0xffffu;
         const uint32_t below_L = L - t >= kTile ? 0xffffu : (1u << max(L - t, 0)) - 1u;
         const uint32_t below_first = first - t >= kTile ? 0xffffu : (1u << max(first - t, 0)) - 1u;
         const uint32_t from_low = low <= t ? 0xffffu : low - t >= kTile ? 0u : 0xffffu << (low - t);
@@ -232,9 +235,10 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     int32_t a_tile = worker, a_token = 0, a_off = 0, id = 0;
     auto look_up = [&]() {                          // the block of the next tile to copy
         if (a_tile >= seen.tiles) return;
-        a_token = seen.token(a_tile);
-        const int32_t blk = (uint32_t)a_token / (uint32_t)bs;
-        a_off = a_token - blk * bs;
+        const uint32_t at = (uint32_t)seen.place(a_tile);
+        const uint32_t blk = a.tiles_per_block == 1 ? at : __umulhi(at, a.block_magic);
+        a_token = (int32_t)at * kTile;
+        a_off = (int32_t)(at - blk * a.tiles_per_block) * kTile;
         id = __ldg(trow + blk);
     };
     look_up();
@@ -445,7 +449,8 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, m2[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float lr[2] = {kMostLr, kMostLr}, r[2] = {fast_exp2(kMostLr), fast_exp2(kMostLr)};   // int8: log2 r, r
     int st = 0;                                  // stage of the next tile; the one before it is free
     for (int tile = worker; tile < seen.tiles; tile += n_workers) {
         cp_async_wait<S::kStages - 2>();
@@ -507,47 +512,29 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         c[1] *= k0 * mul1;
         c[2] *= k1 * mul0;
         c[3] *= k1 * mul1;
-        float w[4];                                  // int8: scores with the V scale
-        float sv0 = 0.f, sv1 = 0.f;
-        if constexpr (INT8) {
-            sv0 = sc[kTile + g4];
-            sv1 = sc[kTile + g4 + 8];
-            const float lv0 = __log2f(fabsf(sv0)), lv1 = __log2f(fabsf(sv1));
-            w[0] = c[0] + lv0;
-            w[1] = c[1] + lv0;
-            w[2] = c[2] + lv1;
-            w[3] = c[3] + lv1;
-        }
         if ((present & 0xffffu) != 0xffffu) {
-            if (!((present >> g4) & 1)) c[0] = c[1] = w[0] = w[1] = -INFINITY;
-            if (!((present >> (g4 + 8)) & 1)) c[2] = c[3] = w[2] = w[3] = -INFINITY;
+            if (!((present >> g4) & 1)) c[0] = c[1] = -INFINITY;
+            if (!((present >> (g4 + 8)) & 1)) c[2] = c[3] = -INFINITY;
         }
         // the maxima move (and what was summed is rescaled) only when a score
         // passes one by more than kLazyMax: no reduction in the common case
-        float mx[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])}, mx2[2] = {-INFINITY, -INFINITY};
-        bool grow = mx[0] > m[0] + kLazyMax || mx[1] > m[1] + kLazyMax;
-        if constexpr (INT8) {
-            mx2[0] = fmaxf(w[0], w[2]);
-            mx2[1] = fmaxf(w[1], w[3]);
-            grow |= mx2[0] > m2[0] + kLazyMax || mx2[1] > m2[1] + kLazyMax;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
+        float mx[2] = {fmaxf(c[0], c[2]), fmaxf(c[1], c[3])};
+        if (__any_sync(0xffffffffu, mx[0] > m[0] + kLazyMax || mx[1] > m[1] + kLazyMax)) {
             float f[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
                 const bool up = mx[k] > m[k] + kLazyMax;
-                f[k] = up ? fast_exp2(m[k] - mx[k]) : 1.f;
+                const float by = up ? mx[k] - m[k] : 0.f;
+                f[k] = fast_exp2(-by);
                 if (up) m[k] = mx[k];
                 l[k] *= f[k];
-                if constexpr (INT8) {
-#pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
-                        mx2[k] = fmaxf(mx2[k], __shfl_xor_sync(0xffffffffu, mx2[k], off));
-                    const bool up2 = mx2[k] > m2[k] + kLazyMax;
-                    f[k] = up2 ? fast_exp2(m2[k] - mx2[k]) : 1.f;
-                    if (up2) m2[k] = mx2[k];
+                if constexpr (INT8) {                // r grows as the weights so far shrink
+                    const float lr_new = fminf(lr[k] + ceilf(by), kMostLr);
+                    f[k] = fast_exp2(lr_new - lr[k] - by);
+                    lr[k] = lr_new;
+                    r[k] = fast_exp2(lr_new);
                 }
             }
 #pragma unroll
@@ -562,9 +549,32 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         l[0] += c[0] + c[2];
         l[1] += c[1] + c[3];
         if constexpr (INT8) {
-            const float d0 = m2[0] == -INFINITY ? 0.f : m2[0], d1 = m2[1] == -INFINITY ? 0.f : m2[1];
+            const float sv0 = sc[kTile + g4], sv1 = sc[kTile + g4 + 8];
+            float w[4] = {c[0] * sv0, c[1] * sv0, c[2] * sv1, c[3] * sv1};
+            // a weight over 2^8 moves r (which starts far too high) to the largest
+            if (__any_sync(0xffffffffu, fmaxf(fabsf(w[0]), fabsf(w[2])) * r[0] > 256.f ||
+                                            fmaxf(fabsf(w[1]), fabsf(w[3])) * r[1] > 256.f)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) c[e] = copysignf(fast_exp2(w[e] - (e & 1 ? d1 : d0)), e < 2 ? sv0 : sv1);
+                for (int k = 0; k < 2; ++k) {
+                    float top = fmaxf(fabsf(w[k]), fabsf(w[k + 2]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                    if (top * r[k] > 256.f) {
+                        // the power of two at or below 1 / top
+                        const float lr_new = 127.f - (float)min((int)(__float_as_uint(top) >> 23), 252);
+                        const float by = fast_exp2(lr_new - lr[k]);
+                        lr[k] = lr_new;
+                        r[k] = fast_exp2(lr_new);
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[i][k] *= by;
+                            o[i][k + 2] *= by;
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[e] = w[e] * r[e & 1];
         }
         uint32_t pa = pack16<INT8>(c[0], c[1]), pb = pack16<INT8>(c[2], c[3]);
         uint32_t ra_t = 0, rb_t = 0;
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             w_m[warp][h0 + i] = m[i];
-            w_m2[warp][h0 + i] = INT8 ? m2[i] : m[i];
+            w_m2[warp][h0 + i] = INT8 ? m[i] - lr[i] : m[i];     // int8: o holds exp2(s - m) v_scale r
             w_l[warp][h0 + i] = l[i];
         }
     }
@@ -852,6 +862,9 @@ int prepare_window(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, void 
     a->n_blocks = dims.n_blocks;
     a->block_size = dims.block_size;
     a->n_kv_heads = dims.n_kv_heads;
+    // ceil(2^32 / n) times a tile index below 2^27 is off by less than 2^27 * 16 / 2^32 < 1 / n
+    a->tiles_per_block = (uint32_t)dims.block_size / kTile;
+    a->block_magic = (uint32_t)((0x100000000ull + a->tiles_per_block - 1) / a->tiles_per_block);
     a->tables = block_tables;
     a->max_blocks = max_blocks;
     a->ctx_lens = ctx_lens;

@@ -154,6 +154,31 @@ def test_decode_agrees_with_the_unwindowed_decode(P, int8):
     assert float((a.double() - b.double()).abs().max()) <= (2e-2 if int8 else 1e-2)
 
 
+@pytest.mark.parametrize("d,group", [(128, 8), (64, 3)])
+def test_int8_scales_far_apart(P, d, group):
+    """Tokens whose V scales differ by up to 2^60 and whose scores by hundreds: each
+    head's weights have to stay in fp16's range whichever token leads."""
+    lens, hkv, bs, scale = [400, 90, 257], 2, 16, 0.5
+    pools, scales, tables, values = _paged(31, lens, 300, 4, 1, hkv, d, bs, True)
+    gen = torch.Generator().manual_seed(9)
+    factor = 2.0 ** torch.randint(-30, 31, scales[1].shape, generator=gen).float()
+    scales[1] *= factor
+    # keys grow along the sequence, so that the maximum moves again and again
+    for s, x in enumerate(lens):
+        t = torch.arange(x)
+        rows = tables[s].long()[t // bs].clamp(min=0) * bs + t % bs
+        scales[0].view(-1, hkv)[rows] *= (1 + t[:, None] / 20.0)
+        for which in range(2):
+            sc = scales[which].view(-1, hkv)[rows].double()
+            values[s][which] = torch.nan_to_num(pools[which].view(-1, hkv, d)[rows].double() * sc[..., None])
+    q = torch.randn((3, hkv * group, d), generator=gen).to(torch.bfloat16)
+    kp, vp, ks, vs, tab = _cuda(*pools, *scales, tables)
+    ctx = torch.tensor(lens, dtype=torch.int32).cuda()
+    lse = torch.zeros((3, hkv * group), device="cuda")
+    out = P.paged_decode_attention_window(q.cuda(), kp, vp, tab, ctx, scale, 300, 4, k_scales=ks, v_scales=vs, lse_out=lse)
+    _check_decode(out, lse, q, values, lens, 300, 4, hkv, scale, True)
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_bad_blocks_and_lengths_are_reported(P, int8):
     lens, window, sinks, hkv, group, d, bs = [100, 100, 100], 40, 4, 2, 4, 64, 16
