@@ -41,22 +41,30 @@ __device__ __forceinline__ bool rope_vectors(const RopeArgs &r, int slot, int &v
     return turn;
 }
 
-// The 8 cosines and sines (times the magnitude) of pairs 8 slot .. 8 slot + 7
-// at position t.  phases is 16-byte aligned.
+// The cosine and sine (times the magnitude) of a phase at position t.
+__device__ __forceinline__ void rope_angle_of(const RopeArgs &r, unsigned long long phase, int64_t t, float &c, float &s)
+{
+    const int32_t hi = (int32_t)((phase * (unsigned long long)t) >> 32);   // turns * 2^32, signed
+    sincospif((float)hi * 4.656612873077393e-10f, &s, &c);                 // 2^-31: half turns
+    s *= r.magnitude;
+    c *= r.magnitude;
+}
+
+// Those of pair i.
+__device__ __forceinline__ void rope_angle(const RopeArgs &r, int i, int64_t t, float &c, float &s)
+{
+    rope_angle_of(r, __ldg(reinterpret_cast<const unsigned long long *>(r.phases) + i), t, c, s);
+}
+
+// Those of pairs 8 slot .. 8 slot + 7.  phases is 16-byte aligned.
 __device__ __forceinline__ void rope_angles(const RopeArgs &r, int slot, int64_t t, float (&c)[8], float (&s)[8])
 {
     const ulonglong2 *ph = reinterpret_cast<const ulonglong2 *>(r.phases + 8 * slot);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const ulonglong2 p2 = __ldg(ph + i);
-        const unsigned long long p[2] = {p2.x, p2.y};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int32_t hi = (int32_t)((p[k] * (unsigned long long)t) >> 32);   // turns * 2^32, signed
-            sincospif((float)hi * 4.656612873077393e-10f, &s[2 * i + k], &c[2 * i + k]);   // 2^-31: half turns
-            s[2 * i + k] *= r.magnitude;
-            c[2 * i + k] *= r.magnitude;
-        }
+        const ulonglong2 p = __ldg(ph + i);
+        rope_angle_of(r, p.x, t, c[2 * i], s[2 * i]);
+        rope_angle_of(r, p.y, t, c[2 * i + 1], s[2 * i + 1]);
     }
 }
 

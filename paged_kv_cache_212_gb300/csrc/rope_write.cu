@@ -4,10 +4,10 @@
 // row), turned queries returned.
 //
 // Every element is read once and written once, so the launch is bound by
-// memory (prefill chunks) or by its own latency (decode tokens).  A warp takes
-// some of the head rows (Hq + 2 Hkv of them) of one token: D / 16 lanes hold a
-// row (rope.cuh), 32 / (D / 16) rows go at once, and each lane computes its 8
-// sines and cosines once for all its rows.
+// memory (prefill chunks) or by its own latency (decode tokens).  A block takes
+// one token: its threads compute the token's sines and cosines once, one pair
+// each, while the rows they will turn are on their way; a warp holds several of
+// the token's head rows (Hq + 2 Hkv of them) at once, D / 16 lanes a row (rope.cuh).
 #include <math.h>
 
 #include "common.cuh"
@@ -32,93 +32,101 @@ struct RopeWriteArgs {
     int32_t max_blocks;
     const int32_t *start_pos;
     int32_t n_new;
-    int64_t n_tokens;
-    int32_t parts;   // warps sharing a token
     int32_t *dev_status;
 };
 
+constexpr int kMaxWarps = 8;   // of a block
+constexpr int kGroups = 3;     // groups of head rows that a warp holds at once
+
 template <int D, bool INT8>
-__global__ void __launch_bounds__(256) rope_write_kernel(const RopeWriteArgs a)
+__global__ void __launch_bounds__(32 * kMaxWarps) rope_write_kernel(const RopeWriteArgs a)
 {
     constexpr int SLOTS = D / 16;        // lanes per head row
-    constexpr int ROWS = 32 / SLOTS;     // head rows a warp takes at once
-    constexpr int U = 2;                 // such groups in flight
+    constexpr int ROWS = 32 / SLOTS;     // head rows in a group
+    __shared__ __align__(16) float cos_s[D / 2], sin_s[D / 2];
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, slot = lane % SLOTS, sub = lane / SLOTS;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int hkv = a.dims.n_kv_heads, hq = a.n_q_heads;
-    const int n_rows = hq + 2 * hkv, groups = (n_rows + ROWS - 1) / ROWS;
+    const int n_rows = hq + 2 * hkv;
+    const int64_t tok = blockIdx.x;
     int v0, v1;
     const bool turn = rope_vectors(a.rope, slot, v0, v1);
-    const int64_t units = a.n_tokens * a.parts;
-    for (int64_t u = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); u < units;
-         u += (int64_t)gridDim.x * (blockDim.x >> 5)) {
-        const int64_t tok = u / a.parts;
-        const int part = (int)(u % a.parts);
-        const int64_t s = tok / a.n_new;
-        const int64_t t = (int64_t)__ldg(a.start_pos + s) + (tok - s * a.n_new);
-        // the token's pool row, reported by one lane of the part that starts at row 0
-        const int64_t row = pool_row_of(a.tables + s * a.max_blocks, a.max_blocks, a.dims.n_blocks, a.dims.block_size,
-                                        t, part == 0 && lane == 0 ? a.dev_status : nullptr);
-        float c[8], sn[8];
-        if (turn) rope_angles(a.rope, slot, t, c, sn);
-        for (int g0 = part; g0 < groups; g0 += a.parts * U) {
-            uint4 x0[U], x1[U];
+    uint4 x0[kGroups], x1[kGroups];
+    auto load = [&](int g0) {            // the warp's groups g0, g0 + warps, ...
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int r = (g0 + i * a.parts) * ROWS + sub;
-                x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
-                if (r >= n_rows) continue;
-                const __nv_bfloat16 *src = r < hq         ? a.q + tok * a.q_stride + (int64_t)r * D
-                                           : r < hq + hkv ? a.k_new + tok * a.k_stride + (int64_t)(r - hq) * D
-                                                          : a.v_new + tok * a.v_stride + (int64_t)(r - hq - hkv) * D;
-                x0[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v0);
-                x1[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v1);
-            }
+        for (int i = 0; i < kGroups; ++i) {
+            const int r = (g0 + i * warps) * ROWS + sub;
+            x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
+            if (r >= n_rows) continue;
+            const __nv_bfloat16 *src = r < hq         ? a.q + tok * a.q_stride + (int64_t)r * D
+                                       : r < hq + hkv ? a.k_new + tok * a.k_stride + (int64_t)(r - hq) * D
+                                                      : a.v_new + tok * a.v_stride + (int64_t)(r - hq - hkv) * D;
+            x0[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v0);
+            x1[i] = __ldcs(reinterpret_cast<const uint4 *>(src) + v1);
+        }
+    };
+    load(warp);
+    const int64_t s = (uint32_t)blockIdx.x / (uint32_t)a.n_new;
+    const int64_t t = (int64_t)__ldg(a.start_pos + s) + (tok - s * a.n_new);
+    for (int i = threadIdx.x; i < a.rope.rot_dim / 2; i += blockDim.x) rope_angle(a.rope, i, t, cos_s[i], sin_s[i]);
+    const int64_t row = pool_row_of(a.tables + s * a.max_blocks, a.max_blocks, a.dims.n_blocks, a.dims.block_size, t,
+                                    threadIdx.x == 0 ? a.dev_status : nullptr);
+    __syncthreads();
+    float c[8], sn[8];
+    if (turn) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int r = (g0 + i * a.parts) * ROWS + sub;
-                const bool is_q = r < hq, is_v = r >= hq + hkv, live = r < n_rows;
-                const int h = is_q ? r : is_v ? r - hq - hkv : r - hq;
-                if (!INT8 || is_q) {
-                    if (turn && !is_v) {
-                        float x[16];
-                        unpack_bf16x8(x0[i], x);
-                        unpack_bf16x8(x1[i], x + 8);
-                        rope_turn(a.rope.interleaved, c, sn, x);
-                        x0[i] = pack_bf16x8(x);
-                        x1[i] = pack_bf16x8(x + 8);
-                    }
-                    if (live && (is_q || row >= 0)) {
-                        __nv_bfloat16 *dst =
-                            is_q ? a.q_out + (tok * hq + h) * D
-                                 : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
-                        reinterpret_cast<uint4 *>(dst)[v0] = x0[i];
-                        reinterpret_cast<uint4 *>(dst)[v1] = x1[i];
-                    }
-                }
-                if constexpr (INT8) {
-                    if (__all_sync(0xffffffffu, is_q)) continue;      // no row of the pages in this group
+        for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<float4 *>(c + 4 * i) = *reinterpret_cast<const float4 *>(cos_s + 8 * slot + 4 * i);
+            *reinterpret_cast<float4 *>(sn + 4 * i) = *reinterpret_cast<const float4 *>(sin_s + 8 * slot + 4 * i);
+        }
+    }
+    for (int g0 = warp; g0 * ROWS < n_rows; g0 += kGroups * warps) {
+        if (g0 != warp) load(g0);
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int r0 = (g0 + i * warps) * ROWS, r = r0 + sub;
+            if (r0 >= n_rows) break;
+            const bool is_q = r < hq, is_v = r >= hq + hkv, live = r < n_rows;
+            const int h = is_q ? r : is_v ? r - hq - hkv : r - hq;
+            if (!INT8 || is_q) {
+                if (turn && !is_v) {
                     float x[16];
                     unpack_bf16x8(x0[i], x);
                     unpack_bf16x8(x1[i], x + 8);
-                    if (turn && !is_v && !is_q) rope_turn(a.rope.interleaved, c, sn, x);
-                    float amax = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
-#pragma unroll
-                    for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                    int code[16];
-                    const float scale = int8_codes<16>(x, amax, code);
-                    if (is_q || !live || row < 0) continue;
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
-                    int8_t *dst = static_cast<int8_t *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
-                    *reinterpret_cast<uint2 *>(dst + 8 * v0) = make_uint2(w[0], w[1]);
-                    *reinterpret_cast<uint2 *>(dst + 8 * v1) = make_uint2(w[2], w[3]);
-                    if (slot == 0) (is_v ? a.v_scales : a.k_scales)[row * hkv + h] = scale;
+                    rope_turn(a.rope.interleaved, c, sn, x);
+                    x0[i] = pack_bf16x8(x);
+                    x1[i] = pack_bf16x8(x + 8);
                 }
+                if (live && (is_q || row >= 0)) {
+                    __nv_bfloat16 *dst = is_q ? a.q_out + (tok * hq + h) * D
+                                              : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
+                    reinterpret_cast<uint4 *>(dst)[v0] = x0[i];
+                    reinterpret_cast<uint4 *>(dst)[v1] = x1[i];
+                }
+            }
+            if constexpr (INT8) {
+                if (r0 + ROWS <= hq) continue;        // no row of the pages in this group
+                float x[16];
+                unpack_bf16x8(x0[i], x);
+                unpack_bf16x8(x1[i], x + 8);
+                if (turn && !is_v && !is_q) rope_turn(a.rope.interleaved, c, sn, x);
+                float amax = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+                for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                int code[16];
+                const float scale = int8_codes<16>(x, amax, code);
+                if (is_q || !live || row < 0) continue;
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
+                int8_t *dst = static_cast<int8_t *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
+                *reinterpret_cast<uint2 *>(dst + 8 * v0) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2 *>(dst + 8 * v1) = make_uint2(w[2], w[3]);
+                if (slot == 0) (is_v ? a.v_scales : a.k_scales)[row * hkv + h] = scale;
             }
         }
     }
@@ -211,6 +219,7 @@ int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, 
                  ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u)))
         return PKV_ERR_INVALID_ARG;
     if ((int64_t)n_new > (int64_t)max_blocks * dims.block_size) return PKV_ERR_OUT_OF_RANGE;
+    if ((int64_t)n_seqs * n_new > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
     int sms = 0;
     st = num_sms_of_current_device(&sms);
     if (st != PKV_OK) return st;
@@ -234,22 +243,20 @@ int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, 
     a.max_blocks = max_blocks;
     a.start_pos = start_pos;
     a.n_new = n_new;
-    a.n_tokens = (int64_t)n_seqs * n_new;
     a.dev_status = dev_status;
-    // few tokens: a token's rows are shared out until the warps fill the machine
+    // four warps a token, each with a few groups of its head rows; eight where there
+    // are too few tokens to fill the machine
+    const int64_t tokens = (int64_t)n_seqs * n_new;
     const int rows_at_once = 32 / (dims.head_dim / 16);
     const int64_t groups = (n_q_heads + 2 * (int64_t)dims.n_kv_heads + rows_at_once - 1) / rows_at_once;
-    const int64_t want = (int64_t)sms * 32;
-    int64_t parts = (want + a.n_tokens - 1) / a.n_tokens;
-    a.parts = (int32_t)(parts < groups ? parts : groups);
-    int64_t grid = (a.n_tokens * a.parts + 7) / 8;
-    if (grid > 0x7fffffffLL) grid = 0x7fffffffLL;
+    const int64_t most = tokens > 4 * (int64_t)sms ? 4 : kMaxWarps;
+    const int warps = (int)(groups < most ? groups : most);
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t lc{};
-    lc.gridDim = dim3((unsigned)grid);
-    lc.blockDim = dim3(256);
+    lc.gridDim = dim3((unsigned)tokens);
+    lc.blockDim = dim3((unsigned)(32 * warps));
     lc.stream = (cudaStream_t)stream;
     lc.attrs = pdl;
     lc.numAttrs = 1;

@@ -92,6 +92,7 @@ def test_rope_write_argument_checks(P):
     for kw in (dict(dt=2), dict(dims=D(8, 16, 2, 96)), dict(dims=D(8, 24, 2, 64)), dict(rope=_rope(P, rot=24))):
         assert f(*_write_args(P, **kw)) == 2, kw
     assert f(*_write_args(P, n_new=65)) == 3
+    assert f(*_write_args(P, n=1 << 30)) == 3
 
 
 def _decode_args(P, **kw):
