@@ -39,11 +39,13 @@
 // (metrale impl_more.rs: a query at q_pos attends only slots <= q_pos of its
 // block).
 //
-// WIN: under a sliding window with first tokens (pagedkv_window.h) the CTA walks
-// the tiles that hold first tokens, then those from the window of its first
-// query on; 16-key groups between the two are neither looked up nor loaded, and
-// rows of loaded groups that no query sees are zeroed in V (a row of K needs
-// nothing: its scores are replaced).
+// WIN: under a sliding window with first tokens (pagedkv_window.h) the CTA's keys
+// are the 16-key groups that hold first tokens, then those from the window of its
+// first query on, packed behind one another into tiles of eight groups: a few
+// first tokens or a window that starts inside a tile cost a group and not a tile.
+// Groups between the two are neither looked up nor loaded, and rows of loaded
+// groups that no query sees are zeroed in V (a row of K needs nothing: its scores
+// are replaced).
 #include <math.h>
 
 #include "common.cuh"
@@ -275,18 +277,15 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     const int32_t P = __ldg(p.prefix_lens + s);
     const bool bad_len = P < 0 || (int64_t)P + p_last + 1 > (int64_t)p.max_blocks * p.block_size;
     const int32_t n_keys = bad_len ? 0 : P + p_last + 1;
-    // WIN: keys in [sinks, w_lo) are seen by no query of the CTA; the tiles are
-    // the first n_sink ones, then those from tile w_tile on
+    // WIN: keys in [sinks, w_lo) are seen by no query of the CTA.  Place c of the
+    // packed keys is key c below n_first (the groups with first tokens), else key
+    // c + skip.
     const int32_t w_lo = WIN && !bad_len ? max(0, P + p0 - p.window + 1) : 0;
-    const int n_sink = WIN ? (min(p.sinks, n_keys) + kTN - 1) / kTN : 0;
-    const int w_tile = WIN ? max(w_lo / kTN, n_sink) : 0;
-    const int n_all = (n_keys + kTN - 1) / kTN;
-    const int n_kt = bad_len ? 0 : WIN ? n_sink + max(0, n_all - w_tile) : n_all;
-    // first key of the j-th tile; whether a 16-key group holds a key some query sees
-    auto tile_key = [&](int j) -> int32_t { return (WIN && j >= n_sink ? w_tile + j - n_sink : j) * kTN; };
-    auto group_seen = [&](int32_t key0) -> bool {
-        return key0 < n_keys && (!WIN || key0 < p.sinks || key0 + 15 >= w_lo);
-    };
+    const int32_t n_first = WIN ? (min(p.sinks, n_keys) + 15) & ~15 : 0;
+    const int32_t skip = WIN ? max((w_lo & ~15) - n_first, 0) : 0;
+    const int32_t n_places = n_keys - skip;
+    const int n_kt = bad_len ? 0 : (n_places + kTN - 1) / kTN;
+    auto key_of = [&](int32_t place) -> int32_t { return WIN && place >= n_first ? place + skip : place; };
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -345,20 +344,20 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // block ids are read one tile ahead and turned into pool rows when the
             // tile is issued
             auto load_block = [&](int j) -> int32_t {
-                const int32_t key0 = tile_key(j) + grp * 16;
-                return (lane < n_grp && group_seen(key0)) ? __ldg(trow + key0 / p.block_size) : 0;
+                const int32_t place = j * kTN + grp * 16;
+                return (lane < n_grp && place < n_places) ? __ldg(trow + key_of(place) / p.block_size) : 0;
             };
             int32_t blk = load_block(0);
             int issued = 0;
             for (int j = 0; j < n_kt; ++j) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
                 {
-                    const int32_t key0 = tile_key(j) + grp * 16;
-                    if (lane < n_grp && group_seen(key0)) {
+                    const int32_t place = j * kTN + grp * 16;
+                    if (lane < n_grp && place < n_places) {
                         if (blk < 0 || blk > p.n_blocks)
                             report(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
                         else
-                            row = blk * p.block_size + key0 % p.block_size;
+                            row = blk * p.block_size + key_of(place) % p.block_size;
                     }
                 }
                 if (j + 1 < n_kt) blk = load_block(j + 1);
@@ -486,9 +485,11 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[qt], j & 1, abort_flag, p.wait_ns));
             if (!ok) break;
             tc_fence_after();
-            const int32_t key_base = tile_key(j);
+            const int32_t key_base = j * kTN + (WIN && j * kTN >= n_first ? skip : 0);
+            // WIN: groups with first tokens, of the tile that goes on with the window
+            const int n_mixed = WIN && skip > 0 && j * kTN < n_first ? min(n_first - j * kTN, kTN) : 0;
             // rows whose keys in this tile are all visible need no per-key test
-            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos ||
+            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos || n_mixed > 0 ||
                                                             (WIN && key_base <= qpos - p.window &&
                                                              key_base + kTN > p.sinks));
             uint32_t sv[kTN];
@@ -499,14 +500,16 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // only tiles crossing the diagonal take this branch
             if (masked) {
                 if constexpr (WIN) {
-                    // key i is seen when 0 <= back - i < window, or i < sinks left in
-                    // this tile and not past the row
+                    // key i is seen when 0 <= back - i < window, or when it is a first
+                    // token (i < first) not past the row
                     const int32_t back = qpos - key_base, first = min(p.sinks - key_base, back + 1);
+                    const int32_t back_w = n_mixed > 0 ? back - skip : back;   // behind the tile's first tokens
                     if (p.sinks > key_base) {
 #pragma unroll
-                        for (int i = 0; i < kTN; ++i)
-                            if ((uint32_t)(back - i) >= (uint32_t)p.window && i >= first)
-                                sv[i] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < kTN; ++i) {
+                            const int32_t b = i < n_mixed ? back : back_w;
+                            if ((uint32_t)(b - i) >= (uint32_t)p.window && i >= first) sv[i] = __float_as_uint(-INFINITY);
+                        }
                     } else {
 #pragma unroll
                         for (int i = 0; i < kTN; ++i)
@@ -579,8 +582,11 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // V rows of loaded groups that no query sees (past the last key; WIN:
             // between the first tokens and the window) may hold anything; zero them
             // once V_j has landed (both warpgroups write the same zeros)
-            const bool tail = j == n_kt - 1 && (n_keys & 15) != 0;
-            const bool gap = WIN && w_lo > p.sinks && key_base < w_lo && key_base + kTN > p.sinks;
+            const int32_t place0 = j * kTN;
+            const bool tail = j == n_kt - 1 && (n_places & 15) != 0;
+            // WIN: places [gap0, gap1) hold keys [sinks, w_lo) of loaded groups
+            const int32_t gap0 = p.sinks, gap1 = WIN ? w_lo - skip : 0;
+            const bool gap = WIN && w_lo > p.sinks && place0 < gap1 && place0 + kTN > gap0;
             if (tail || gap) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&v_full[j % NV], (j / NV) & 1, abort_flag, p.wait_ns));
                 if (!ok) break;
@@ -592,10 +598,8 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
                                                    swz128(row % 16, pc % 8)) = make_uint4(0, 0, 0, 0);
                     }
                 };
-                if (tail) zero_rows(n_keys - key_base, ((n_keys + 15) & ~15) - key_base);
-                if (gap) {   // the whole gap within the tile: groups that were not loaded are zero already
-                    zero_rows(max(p.sinks - key_base, 0), min(w_lo - key_base, kTN));
-                }
+                if (tail) zero_rows(n_places - place0, ((n_places + 15) & ~15) - place0);
+                if (gap) zero_rows(max(gap0 - place0, 0), min(gap1 - place0, kTN));
                 fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
             }
             tc_fence_before();
