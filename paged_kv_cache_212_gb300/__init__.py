@@ -4,19 +4,24 @@ sm_103a CUDA kernels behind the C ABI of ``libpagedkv.so`` (``include/pagedkv.h`
 
 This module is argument marshalling only: it checks tensor shapes, dtypes and
 devices, passes raw device pointers and the current CUDA stream to the
-library, and turns a non-zero status into an exception.  Every step of the
+library, and turns a non-zero status into an exception.  (The rotary and
+windowed calls are marshalled in native code, binding/native.cpp, as long as
+they pass its checks; the ones here then say what is wrong.)  Every step of the
 computation runs in the library's kernels; there is no CPU or PyTorch
 fallback, and using any call without the built library raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpagedkv.so")
+# binding/native.cpp, built against this version of torch
+NATIVE_PATH = os.path.join(HERE, f"_native-{torch.__version__}.so")
 
 PKV_KV_BF16, PKV_KV_INT8 = 0, 1
 DEV_BAD_BLOCK_ID, DEV_BAD_POSITION, DEV_BAD_LENGTH = 1, 2, 4
@@ -67,11 +72,25 @@ class _RopeC(ctypes.Structure):
 
 
 _lib = None
+_native = None          # the native marshalling, once the library is loaded
+
+
+def _load_native(lib):
+    """binding/native.cpp with the library's entry points (None: not built)."""
+    if not os.path.exists(NATIVE_PATH):
+        return None
+    spec = importlib.util.spec_from_file_location("_native", NATIVE_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.set_functions(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
+        "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
+        "paged_prefill_attention_window")))
+    return mod
 
 
 def load_library(path: str = LIB_PATH):
     """Load libpagedkv.so (raises if it has not been built)."""
-    global _lib
+    global _lib, _native
     if _lib is not None:
         return _lib
     if not os.path.exists(path):
@@ -149,6 +168,7 @@ def load_library(path: str = LIB_PATH):
     for fn in ("pkv_rope_phases", "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
                "paged_prefill_attention_window"):
         getattr(lib, fn).restype = ctypes.c_int
+    _native = _load_native(lib)
     _lib = lib
     return lib
 
@@ -648,7 +668,7 @@ class Rope:
         self.magnitude = magnitude.value
         self.phases = host.to(device)             # 2^64 turns per position, as int64 bits
         self._c = _RopeC(self.phases.data_ptr(), self.rot_dim, int(self.interleaved), self.magnitude)
-        self._p = ctypes.pointer(self._c)
+        self._p, self._address = ctypes.pointer(self._c), ctypes.addressof(self._c)
 
 
 def _rope_arg(rope, head_dim, dev):
@@ -736,6 +756,13 @@ def paged_kv_write_rope(q, k_new, v_new, rope, k_pool, v_pool, block_tables, sta
     q [n_seqs, n_new, Hq, D], k_new / v_new [n_seqs, n_new, Hkv, D] bf16; the
     three may be parts of a fused projection's rows.  Returns the turned queries
     (q_out, contiguous; q itself may be given)."""
+    if stream is None and _native is not None and type(rope) is Rope:
+        done = _native.write_rope(q, k_new, v_new, rope._address, rope.phases, k_pool, v_pool, block_tables, start_pos,
+                                  k_scales, v_scales, q_out, dev_status)
+        if done is not None:
+            if type(done) is int:
+                _check("paged_kv_write_rope", done)
+            return done
     dev = _device_of(k_pool, "k_pool")
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -802,11 +829,23 @@ class WindowDecodePlan:
                       PKV_KV_INT8 if int8 else PKV_KV_BF16, pool_dims(k_pool), _ptr(block_tables),
                       block_tables.shape[1], _ptr(ctx_lens), n_seqs, float(softmax_scale), _count(window, "window"),
                       _count(sinks, "sinks"), _ptr(out), _ptr(lse_out), _ptr(dev_status))
+        self._plan = None
+        if _native is not None:
+            kp, vp, ks, vs, kind, dims, tab, width, ctx, n, scale, window, sinks, o, lse, st = self._args
+            self._plan = _native.make_plan(dev, self.n_q_heads, 0 if rope is None else rope._address, kp, vp, ks or 0,
+                                           vs or 0, kind, dims.n_blocks, dims.block_size, dims.n_kv_heads, dims.head_dim,
+                                           tab, width, ctx, n, scale, window, sinks, o, lse or 0, st or 0)
 
     def run(self, q, k_new=None, v_new=None, start_pos=None, stream=None):
         """q [n_seqs, Hq, D] bf16 (contiguous for the attention alone); k_new /
         v_new [n_seqs, 1, Hkv, D]; start_pos [n_seqs].  In a step the three may
         be parts of a fused projection's rows.  Returns the plan's out."""
+        if stream is None and self._plan is not None:
+            st = _native.run_plan(self._plan, q, k_new, v_new, start_pos)
+            if st is not None:
+                if st:
+                    _check("paged_decode_attention_window" if k_new is None else "paged_decode_step_window", st)
+                return self.out
         dev = self.device
         if _elsewhere(dev):
             with torch.cuda.device(dev):
@@ -874,6 +913,13 @@ def paged_prefill_attention_window(q, k_pool, v_pool, block_tables, prefix_lens,
     """paged_prefill_attention under a sliding window: query i of sequence s (at
     position prefix_lens[s] + i) sees the first ``sinks`` tokens and the last
     ``window`` ones up to itself.  Returns out, same shape as q."""
+    if stream is None and _native is not None:
+        done = _native.prefill_window(q, k_pool, v_pool, block_tables, prefix_lens, softmax_scale, window, sinks, out,
+                                      lse_out, dev_status)
+        if done is not None:
+            if type(done) is int:
+                _check("paged_prefill_attention_window", done)
+            return done
     dev = _device_of(q, "q")
     if _elsewhere(dev):
         with torch.cuda.device(dev):

@@ -3,8 +3,10 @@
 Each .cu (device) and .cpp (host-only) translation unit compiles in parallel
 to an object file, then one
 link step produces the shared library (cudart linked statically, so the
-library needs only the driver at run time).  Rebuilds only when a source or
-header is newer than the library.
+library needs only the driver at run time).  Beside them g++ compiles the
+native part of the Python binding (binding/native.cpp, against the installed
+torch) into a CPython extension of its own.  Rebuilds only when a source or
+header is newer than what was built from it.
 """
 from __future__ import annotations
 
@@ -14,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
+NATIVE_SRC = os.path.join(HERE, "binding", "native.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -46,8 +50,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def native_lib() -> str:
+    import torch
+    return os.path.join(HERE, f"_native-{torch.__version__}.so")
+
+
+def native_up_to_date() -> bool:
+    lib = native_lib()
+    deps = [NATIVE_SRC, os.path.abspath(__file__)] + glob.glob(os.path.join(ROOT, "include", "*.h"))
+    return os.path.exists(lib) and all(os.path.getmtime(p) <= os.path.getmtime(lib) for p in deps)
+
+
+def build_native() -> str:
+    """The binding's native part, for the torch that is installed."""
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib, cuda = native_lib(), os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = lib + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc), NATIVE_SRC,
+           "-o", tmp, f"-L{os.path.join(home, 'lib')}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
+    return lib
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    native = force or not native_up_to_date()
     if not force and up_to_date():
+        if native:
+            build_native()
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -65,7 +101,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
+        binding = ex.submit(build_native) if native else None
         results = list(ex.map(compile_one, _sources()))
+        if binding:
+            binding.result()
     if verbose or ptxas_verbose:
         for _, err in results:
             if err.strip():

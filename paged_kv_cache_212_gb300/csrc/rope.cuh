@@ -4,8 +4,7 @@
 // Angles.  A pair's phase is its turns per position in units of 2^-64, so the
 // angle of position t is (t * phase mod 2^64) 2^-64 turns: an integer product,
 // exact for every position, where the binary32 product t * f loses 0.06 rad at
-// t = 10^6.  Its top 32 bits as a signed number are the angle in (-1/2, 1/2]
-// turns to 2^-32; sincospif takes twice that.
+// t = 10^6.
 //
 // Lanes.  A head row of D elements is the work of D / 16 lanes: lane `slot`
 // holds two 16-byte vectors (16 elements, 8 pairs) so that both members of
@@ -41,13 +40,20 @@ __device__ __forceinline__ bool rope_vectors(const RopeArgs &r, int slot, int &v
     return turn;
 }
 
-// The cosine and sine (times the magnitude) of a phase at position t.
+// The cosine and sine (times the magnitude) of a phase at position t.  The
+// quadrant is taken off in integers, so that what is rounded to binary32 is at
+// most an eighth of a turn: the angle is off by 2^-25 of that, where rounding the
+// whole angle left an error above that of the sine itself.
 __device__ __forceinline__ void rope_angle_of(const RopeArgs &r, unsigned long long phase, int64_t t, float &c, float &s)
 {
-    const int32_t hi = (int32_t)((phase * (unsigned long long)t) >> 32);   // turns * 2^32, signed
-    sincospif((float)hi * 4.656612873077393e-10f, &s, &c);                 // 2^-31: half turns
-    s *= r.magnitude;
-    c *= r.magnitude;
+    const unsigned long long a = phase * (unsigned long long)t;           // turns * 2^64
+    const uint32_t q = (uint32_t)((a + (1ull << 61)) >> 62) & 3u;          // the nearest quarter turn
+    const int32_t rest = (int32_t)((int64_t)(a - ((unsigned long long)q << 62)) >> 30);
+    float x, y;
+    sincospif((float)rest * 1.1641532182693481e-10f, &y, &x);              // 2^-33: half turns
+    const float cq = q & 1 ? y : x, sq = q & 1 ? x : y;
+    c = (q == 1 || q == 2 ? -cq : cq) * r.magnitude;
+    s = (q >= 2 ? -sq : sq) * r.magnitude;
 }
 
 // Those of pair i.

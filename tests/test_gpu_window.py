@@ -402,6 +402,29 @@ def test_wrappers_refuse_mismatched_tensors(P):
     assert e.value.status == 1
 
 
+def test_native_and_python_marshalling_agree(P, monkeypatch):
+    """The calls give the same bits through either part of the binding."""
+    assert P._native is not None
+    lens, window, sinks, hkv, group, d, bs = [50, 300], 64, 4, 2, 4, 128, 16
+    hq, n = hkv * group, 2
+    pools, _, tables, _ = _paged(2, lens, window, sinks, 40, hkv, d, bs, False)
+    x = torch.randn((n, 40, hq + 2 * hkv, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    ctx = torch.tensor(lens, dtype=torch.int32).cuda()
+    rope = P.Rope(128)
+    got = []
+    for native in (P._native, None):
+        monkeypatch.setattr(P, "_native", native)
+        kp, vp, tab = _cuda(*pools, tables)
+        q, k, v = x.split((hq, hkv, hkv), dim=2)
+        qt = P.paged_kv_write_rope(q, k, v, rope, kp, vp, tab, ctx - 40)
+        o = P.paged_prefill_attention_window(qt, kp, vp, tab, ctx - 40, d ** -0.5, window, sinks)
+        plan = P.WindowDecodePlan(kp, vp, tab, ctx, d ** -0.5, hq, window, sinks, rope=rope)
+        step = plan.run(q[:, -1], k[:, -1:], v[:, -1:], ctx - 1).clone()
+        plain = P.WindowDecodePlan(kp, vp, tab, ctx, d ** -0.5, hq, window, sinks).run(qt[:, -1].contiguous())
+        got.append((qt, o, step, plain.clone(), kp.view(torch.int16), vp.view(torch.int16)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 @pytest.mark.parametrize("int8", [False])
 def test_prompt_in_chunks_then_steps(P, int8):
     """A run of the operators as a server uses them: a prompt written and attended

@@ -215,3 +215,28 @@ def test_reference_attention_against_a_loop():
         w = [math.exp(0.3 * float(q[i, 0] @ k[t])) for t in ts]
         assert abs(math.log(sum(w)) - float(lse[i, 0])) < 1e-12
         assert torch.allclose(sum(x * v[t] for x, t in zip(w, ts)) / sum(w), o[i, 0], atol=1e-12)
+
+
+def test_native_marshalling_refuses_what_it_does_not_know(P):
+    """The native part of the binding answers None, without a call, to anything but
+    CUDA tensors of the right kinds; the Python part then says what is wrong."""
+    n = P._native
+    assert n is not None
+    q = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16)
+    kv = torch.zeros((1, 1, 2, 64), dtype=torch.bfloat16)
+    pool, tab, lens = torch.zeros((3, 16, 2, 64), dtype=torch.bfloat16), torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    rope = P.Rope(64, device="cpu")
+    args = [q, kv, kv, rope._address, rope.phases, pool, pool, tab, lens, None, None, None, None]
+    assert n.write_rope(*args) is None and n.write_rope() is None
+    for i in range(len(args)):
+        assert n.write_rope(*args[:i], "x", *args[i + 1:]) is None
+    args = [q, pool, pool, tab, lens, 0.1, 8, 0, None, None, None]
+    assert n.prefill_window(*args) is None and n.prefill_window(None) is None
+    for i in range(len(args)):
+        assert n.prefill_window(*args[:i], None, *args[i + 1:]) is None
+    assert n.prefill_window(*args[:6], 2 ** 70, *args[7:]) is None
+    with pytest.raises(ValueError):
+        n.run_plan(None, q, None, None, None)
+    plan = n.make_plan(0, 4, 0, 1, 1, 0, 0, 0, 2, 16, 2, 64, 1, 2, 1, 1, 0.1, 8, 0, 1, 0, 0)
+    for a in ((None, None, None, None), (q[:, 0], None, None, None), (q[:, 0], kv, kv, lens)):
+        assert n.run_plan(plan, *a) is None
