@@ -14,6 +14,7 @@
 namespace pkv {
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
+cudaError_t launch_prefill_window(const PrefillArgs &a, int num_sms, cudaStream_t stream);
 
 namespace {
 
@@ -214,11 +215,11 @@ cudaError_t prepare_kernel(const void *kern, int threads, size_t smem, int *occu
     return cudaSuccess;
 }
 
-// Prefill runs on the tcgen05 kernel (prefill_tc.cu).
+// Prefill runs on the tcgen05 kernels (prefill_tc.cu; under a window
+// prefill_window.cu).
 cudaError_t launch_prefill(const PrefillArgs &a, int num_sms, cudaStream_t stream)
 {
-    (void)num_sms;
-    return launch_prefill_tc(a, stream);
+    return a.window > 0 ? launch_prefill_window(a, num_sms, stream) : launch_prefill_tc(a, stream);
 }
 
 }  // namespace pkv

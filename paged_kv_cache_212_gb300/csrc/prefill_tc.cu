@@ -38,14 +38,6 @@
 // bandwidth).  Query position P + p (P = prefix length) sees keys 0 .. P + p
 // (metrale impl_more.rs: a query at q_pos attends only slots <= q_pos of its
 // block).
-//
-// WIN: under a sliding window with first tokens (pagedkv_window.h) the CTA's keys
-// are the 16-key groups that hold first tokens, then those from the window of its
-// first query on, packed behind one another into tiles of eight groups: a few
-// first tokens or a window that starts inside a tile cost a group and not a tile.
-// Groups between the two are neither looked up nor loaded, and rows of loaded
-// groups that no query sees are zeroed in V (a row of K needs nothing: its scores
-// are replaced).
 #include <math.h>
 
 #include "common.cuh"
@@ -85,7 +77,6 @@ struct PrefillTcParams {
     int32_t pairs_per_seq;        // CTAs per (sequence, kv head)
     int32_t n_seqs, n_kv_heads;
     unsigned long long wait_ns;   // limit of the pipeline waits
-    int32_t window, sinks;        // WIN: the mask
 };
 
 // Batches of at most this many sequences are scheduled longest prefix first.
@@ -100,71 +91,6 @@ constexpr int kLaunchRegs = 168;             // 65536 / 384, rounded down to a m
 constexpr int kRegsIssue = 72;
 constexpr int kRegsSoftmax = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= 384 * kLaunchRegs, "register split above the launch");
-
-// ---- tcgen05 helpers -------------------------------------------------------
-
-// The 8 products of one 128-row tile step in one asm block, so that the
-// predicates are set once (first product: accumulate_first; the rest
-// accumulate) rather than once per instruction.  A and B shared-memory
-// descriptors (SS form).
-__device__ __forceinline__ void umma_bf16_x8(uint32_t d_tmem, const uint64_t (&a)[8], const uint64_t (&b)[8],
-                                             uint32_t idesc, uint32_t accumulate_first)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %17, 0;\n\t"
-        "setp.eq.b32 q, %17, %17;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %9, %18, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %10, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %11, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %12, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %13, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %14, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %15, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %16, %18, q;\n\t}" ::"r"(d_tmem),
-        "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(a[4]), "l"(a[5]), "l"(a[6]), "l"(a[7]), "l"(b[0]),
-        "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]), "r"(accumulate_first),
-        "r"(idesc)
-        : "memory");
-}
-
-// The 8 products of one tile step in the TS form: D (TMEM) += A (TMEM, M x 16,
-// K-major: lane = row, column c = bf16 pair 2c, 2c + 1; product k at a_tmem +
-// 8 k) * B (shared-memory descriptor), predicates set once as above.
-__device__ __forceinline__ void umma_bf16_ts_x8(uint32_t d_tmem, uint32_t a_tmem, const uint64_t (&b)[8],
-                                                uint32_t idesc, uint32_t accumulate_first)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-        "setp.ne.b32 p, %10, 0;\n\t"
-        "setp.eq.b32 q, %10, %10;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\t"
-        "add.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %11, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %3, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %4, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], %5, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %6, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], %7, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], %8, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], %9, %11, q;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]),
-        "r"(accumulate_first), "r"(idesc)
-        : "memory");
-}
-
-// max(a, b, c) in one instruction (sm_100 and later).
-__device__ __forceinline__ float fmax3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk)
-{
-    return row * 128u + ((chunk ^ (row & 7u)) << 4);
-}
 
 // Shared memory -> global through a 4-D tensor map (elements past the map's
 // extent are not written), then the commit of the bulk group.
@@ -184,31 +110,9 @@ __device__ __forceinline__ void bulk_wait_read_all()
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Bits 0 .. n - 1 of a word (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t bits_below(int32_t n)
-{
-    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// AND of v over the 128 threads of a warpgroup (named barrier id); every
-// thread of the warpgroup must reach it.
-__device__ __forceinline__ bool wg_and(uint32_t id, bool v)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id)
-        : "memory");
-    return r != 0;
-}
-
 }  // namespace
 
-template <int D, bool WIN>
+template <int D>
 __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constant__ CUtensorMap q_map,
                                                             const __grid_constant__ CUtensorMap k_map,
                                                             const __grid_constant__ CUtensorMap v_map,
@@ -261,7 +165,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     const int pair = pairs - 1 - unit / p.n_kv_heads;
     const int kvh = unit % p.n_kv_heads;
     int s = (int)(blockIdx.x / units);
-    if (!WIN && p.n_seqs <= kSortMaxSeqs) {   // WIN: the window levels the sequences' work
+    if (p.n_seqs <= kSortMaxSeqs) {
         if (threadIdx.x < p.n_seqs) sched[threadIdx.x] = __ldg(p.prefix_lens + threadIdx.x);
         __syncthreads();
         if (threadIdx.x < p.n_seqs) {
@@ -283,15 +187,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     const int32_t P = __ldg(p.prefix_lens + s);
     const bool bad_len = P < 0 || (int64_t)P + p_last + 1 > (int64_t)p.max_blocks * p.block_size;
     const int32_t n_keys = bad_len ? 0 : P + p_last + 1;
-    // WIN: keys in [sinks, w_lo) are seen by no query of the CTA.  Place c of the
-    // packed keys is key c below n_first (the groups with first tokens), else key
-    // c + skip.
-    const int32_t w_lo = WIN && !bad_len ? max(0, P + p0 - p.window + 1) : 0;
-    const int32_t n_first = WIN ? (min(p.sinks, n_keys) + 15) & ~15 : 0;
-    const int32_t skip = WIN ? max((w_lo & ~15) - n_first, 0) : 0;
-    const int32_t n_places = n_keys - skip;
-    const int n_kt = bad_len ? 0 : (n_places + kTN - 1) / kTN;
-    auto key_of = [&](int32_t place) -> int32_t { return WIN && place >= n_first ? place + skip : place; };
+    const int n_kt = bad_len ? 0 : (n_keys + kTN - 1) / kTN;
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -350,20 +246,20 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // block ids are read one tile ahead and turned into pool rows when the
             // tile is issued
             auto load_block = [&](int j) -> int32_t {
-                const int32_t place = j * kTN + grp * 16;
-                return (lane < n_grp && place < n_places) ? __ldg(trow + key_of(place) / p.block_size) : 0;
+                const int32_t key0 = j * kTN + grp * 16;
+                return (lane < n_grp && key0 < n_keys) ? __ldg(trow + key0 / p.block_size) : 0;
             };
             int32_t blk = load_block(0);
             int issued = 0;
             for (int j = 0; j < n_kt; ++j) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
                 {
-                    const int32_t place = j * kTN + grp * 16;
-                    if (lane < n_grp && place < n_places) {
+                    const int32_t key0 = j * kTN + grp * 16;
+                    if (lane < n_grp && key0 < n_keys) {
                         if (blk < 0 || blk > p.n_blocks)
                             report(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
                         else
-                            row = blk * p.block_size + key_of(place) % p.block_size;
+                            row = blk * p.block_size + key0 % p.block_size;
                     }
                 }
                 if (j + 1 < n_kt) blk = load_block(j + 1);
@@ -491,13 +387,9 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             ok = __all_sync(0xffffffffu, mbar_wait(&s_full[qt], j & 1, abort_flag, p.wait_ns));
             if (!ok) break;
             tc_fence_after();
-            const int32_t key_base = j * kTN + (WIN && j * kTN >= n_first ? skip : 0);
-            // WIN: groups with first tokens, of the tile that goes on with the window
-            const int n_mixed = WIN && skip > 0 && j * kTN < n_first ? min(n_first - j * kTN, kTN) : 0;
+            const int32_t key_base = j * kTN;
             // rows whose keys in this tile are all visible need no per-key test
-            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos || n_mixed > 0 ||
-                                                            (WIN && key_base <= qpos - p.window &&
-                                                             key_base + kTN > p.sinks));
+            const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos);
             uint32_t sv[kTN];
 #pragma unroll
             for (int c = 0; c < kTN / 32; ++c) tmem_ld32_async(lane_base + c * 32, sv + c * 32);
@@ -505,32 +397,9 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // keys past this row's position get a score of -inf (exp2 gives 0);
             // only tiles crossing the diagonal take this branch
             if (masked) {
-                if constexpr (WIN) {
-                    // The seen keys of the tile as bits, 32 at a time: those of the window
-                    // [back - window, back] (behind n_mixed: the same, skip further on) and
-                    // the first tokens up to the row.  Testing bits that way costs a third of
-                    // comparing every key's index (first tile 2.5 -> 1.0 us).
-                    const int32_t back = qpos - key_base + 1, first = min(p.sinks - key_base, back);
-                    const int32_t back_w = n_mixed > 0 ? back - skip : back;
-                    const int32_t low = back < p.window ? 0 : back - p.window;
-                    const int32_t low_w = back_w < p.window ? 0 : back_w - p.window;
 #pragma unroll
-                    for (int c = 0; c < kTN / 32; ++c) {
-                        uint32_t seen = bits_below(back_w - c * 32) & ~bits_below(low_w - c * 32);
-                        if (n_mixed > 0) {
-                            const uint32_t mixed = bits_below(n_mixed - c * 32);
-                            seen = (seen & ~mixed) | (mixed & bits_below(back - c * 32) & ~bits_below(low - c * 32));
-                        }
-                        seen |= bits_below(first - c * 32);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((seen >> i) & 1)) sv[c * 32 + i] = __float_as_uint(-INFINITY);
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < kTN; ++i)
-                        if (key_base + i > qpos) sv[i] = __float_as_uint(-INFINITY);
-                }
+                for (int i = 0; i < kTN; ++i)
+                    if (key_base + i > qpos) sv[i] = __float_as_uint(-INFINITY);
             }
             // row maximum: three-input max over four independent chains
             float mx;
@@ -548,7 +417,6 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             float alpha = 1.f;
             if (m == -INFINITY) {
                 m = mx;          // first tile: key 0 is always visible, so mx is finite
-                                 // (WIN: -inf until the first tile with a visible key)
             } else if (mx > m + kRescaleThreshold) {
                 alpha = fast_exp2(m - mx);
                 m = mx;
@@ -569,7 +437,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             // probabilities (packed two-lane FMA for the exponent arguments) and
             // two packed partial row sums; P (bf16 pairs) over S's first 64
             // columns, each 16-column store after the S columns it covers were read
-            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = WIN && m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2), nm2 = make_float2(-m, -m);
             float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
 #pragma unroll
             for (int c = 0; c < kTN / 32; ++c) {
@@ -590,27 +458,18 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             }
             l = l * alpha + ((la.x + la.y) + (lb.x + lb.y));
             tmem_wait_st();
-            // V rows of loaded groups that no query sees (past the last key; WIN:
-            // between the first tokens and the window) may hold anything; zero them
-            // once V_j has landed (both warpgroups write the same zeros)
-            const int32_t place0 = j * kTN;
-            const bool tail = j == n_kt - 1 && (n_places & 15) != 0;
-            // WIN: places [gap0, gap1) hold keys [sinks, w_lo) of loaded groups
-            const int32_t gap0 = p.sinks, gap1 = WIN ? w_lo - skip : 0;
-            const bool gap = WIN && w_lo > p.sinks && place0 < gap1 && place0 + kTN > gap0;
-            if (tail || gap) {
+            // last tile: V rows of keys past the last one may hold anything; zero
+            // them once V_j has landed (both warpgroups write the same zeros)
+            if (j == n_kt - 1 && (n_keys & 15) != 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&v_full[j % NV], (j / NV) & 1, abort_flag, p.wait_ns));
                 if (!ok) break;
+                const int first = n_keys - key_base, stop = ((n_keys + 15) & ~15) - key_base;
                 uint8_t *vs = v_ring + (j % NV) * kSlotBytes;
-                auto zero_rows = [&](int first, int stop) {
-                    for (int i = r; i < (stop - first) * PANELS * 8; i += kTM) {
-                        const int row = first + i / (PANELS * 8), pc = i % (PANELS * 8);
-                        *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 +
-                                                   swz128(row % 16, pc % 8)) = make_uint4(0, 0, 0, 0);
-                    }
-                };
-                if (tail) zero_rows(n_places - place0, ((n_places + 15) & ~15) - place0);
-                if (gap) zero_rows(max(gap0 - place0, 0), min(gap1 - place0, kTN));
+                for (int i = r; i < (stop - first) * PANELS * 8; i += kTM) {
+                    const int row = first + i / (PANELS * 8), pc = i % (PANELS * 8);
+                    *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 + swz128(row % 16, pc % 8)) =
+                        make_uint4(0, 0, 0, 0);
+                }
                 fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
             }
             tc_fence_before();
@@ -673,8 +532,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     }
 }
 
-template <bool WIN>
-static cudaError_t launch_prefill_tc_as(const PrefillArgs &a, cudaStream_t stream)
+cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
 {
     const pkv_dims &d = a.dims;
     const int G = a.n_q_heads / d.n_kv_heads;
@@ -699,8 +557,6 @@ static cudaError_t launch_prefill_tc_as(const PrefillArgs &a, cudaStream_t strea
     p.pairs_per_seq = (p.tiles_per_seq + kNQ - 1) / kNQ;
     p.n_seqs = a.n_seqs;
     p.n_kv_heads = d.n_kv_heads;
-    p.window = a.window;
-    p.sinks = a.sinks;
 
     CUtensorMap qmap, kmap, vmap, omap;
     {
@@ -756,8 +612,8 @@ static cudaError_t launch_prefill_tc_as(const PrefillArgs &a, cudaStream_t strea
     // a build whose kernel was given fewer (its setmaxnreg.inc could not complete).
     static const bool regs_ok = [] {
         cudaFuncAttributes fa128{}, fa64{};
-        return cudaFuncGetAttributes(&fa128, prefill_tc_kernel<128, WIN>) == cudaSuccess &&
-               cudaFuncGetAttributes(&fa64, prefill_tc_kernel<64, WIN>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
+        return cudaFuncGetAttributes(&fa128, prefill_tc_kernel<128>) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa64, prefill_tc_kernel<64>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
                fa64.numRegs >= kLaunchRegs;
     }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
@@ -775,18 +631,13 @@ static cudaError_t launch_prefill_tc_as(const PrefillArgs &a, cudaStream_t strea
     lc.numAttrs = 1;
     cudaError_t e;
     if (d.head_dim == 128) {
-        e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<128, WIN>), 384, smem, nullptr);
+        e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<128>), 384, smem, nullptr);
         if (e != cudaSuccess) return e;
-        return cudaLaunchKernelEx(&lc, prefill_tc_kernel<128, WIN>, qmap, kmap, vmap, omap, p);
+        return cudaLaunchKernelEx(&lc, prefill_tc_kernel<128>, qmap, kmap, vmap, omap, p);
     }
-    e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<64, WIN>), 384, smem, nullptr);
+    e = prepare_kernel(reinterpret_cast<const void *>(prefill_tc_kernel<64>), 384, smem, nullptr);
     if (e != cudaSuccess) return e;
-    return cudaLaunchKernelEx(&lc, prefill_tc_kernel<64, WIN>, qmap, kmap, vmap, omap, p);
-}
-
-cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream)
-{
-    return a.window > 0 ? launch_prefill_tc_as<true>(a, stream) : launch_prefill_tc_as<false>(a, stream);
+    return cudaLaunchKernelEx(&lc, prefill_tc_kernel<64>, qmap, kmap, vmap, omap, p);
 }
 
 }  // namespace pkv

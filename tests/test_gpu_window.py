@@ -318,6 +318,58 @@ def test_prefill(P, prefix, chunk, window, sinks, hkv, group, d, bs):
             assert (over <= 0).all(), (s, h, float(over.max()))
 
 
+def test_prefill_of_many_units_and_odd_addresses(P):
+    """More units than CTAs, some of bad length among them, and an output on a
+    16-byte boundary: the same bits as one sequence at a time, wide stores or not."""
+    hkv, group, d, bs, window, sinks, chunk = 8, 4, 128, 16, 70, 5, 200
+    prefix = [0, 300, 5, 77, 1000, 16, 450, 123]
+    lens = [x + chunk for x in prefix]
+    pools, _, tables, _ = _paged(6, lens, window, sinks, chunk, hkv, d, bs, False)
+    q = torch.randn((8, chunk, hkv * group, d), generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    kp, vp, tab = _cuda(*pools, tables)
+    pre = torch.tensor(prefix, dtype=torch.int32).cuda()
+    pre[2], pre[5] = -1, tables.shape[1] * bs
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(q, 3.0)
+    P.paged_prefill_attention_window(q, kp, vp, tab, pre, d ** -0.5, window, sinks, out=out, dev_status=st)
+    odd = torch.full((q.numel() + 8,), 3.0, dtype=torch.bfloat16, device="cuda")[8:].view(q.shape)
+    assert odd.data_ptr() % 32 == 16
+    P.paged_prefill_attention_window(q, kp, vp, tab, pre, d ** -0.5, window, sinks, out=odd)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 4 and torch.equal(out, odd)
+    assert (out[[2, 5]] == 3.0).all()                      # a bad length leaves its rows as they were
+    for s in (0, 1, 3, 4, 6, 7):
+        one = P.paged_prefill_attention_window(q[s:s + 1], kp, vp, tab[s:s + 1], pre[s:s + 1], d ** -0.5, window, sinks)
+        assert torch.equal(one[0], out[s]), s
+
+
+def test_prefill_wait_runs_out_then_recovers(P):
+    """With a limit of 1 ns on its pipeline waits the kernel reports the timeout and
+    returns; the next call on the stream is right."""
+    hkv, group, d, bs, window, sinks, chunk = 4, 4, 128, 16, 300, 4, 300
+    lens = [chunk + 500, chunk]
+    pools, _, tables, _ = _paged(6, lens, window, sinks, chunk, hkv, d, bs, False)
+    q = torch.randn((2, chunk, hkv * group, d), generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    kp, vp, tab = _cuda(*pools, tables)
+    pre = torch.tensor([500, 0], dtype=torch.int32).cuda()
+    run = lambda st: P.paged_prefill_attention_window(q, kp, vp, tab, pre, d ** -0.5, window, sinks, dev_status=st)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = run(st)
+    lib = P.load_library()
+    try:
+        lib.pkv_set_pipeline_wait_ns(1)
+        for _ in range(5):                                 # at least one of them must run out
+            run(st)
+        torch.cuda.synchronize()
+    finally:
+        lib.pkv_set_pipeline_wait_ns(0)
+    assert int(st.item()) & 16
+    st.zero_()
+    got = run(st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and torch.equal(got, want)
+
+
 def test_prefill_reports_bad_blocks_and_lengths(P):
     prefix, chunk, window, sinks, hkv, group, d, bs = [200, 200, 200], 40, 50, 4, 1, 4, 64, 16
     pools, _, tables, _ = _paged(3, [x + chunk for x in prefix], window, sinks, chunk, hkv, d, bs, False)
