@@ -22,6 +22,10 @@
 // loaded, and rows of loaded groups that no query sees are zeroed in V (a row of K
 // needs nothing: its scores are replaced).
 //
+// Half units.  What is left over when the units are dealt out to the CTAs is cut into
+// units of one query tile where that gives every CTA at most one more (512 units on
+// 152 CTAs: three rounds and 112 halves in place of four rounds).
+//
 // O goes out from registers, a row of head_dim values a thread: the shared memory
 // that could stage it holds the next unit's tiles by then.
 #include <math.h>
@@ -68,7 +72,7 @@ struct WinParams {
     int32_t *dev_status;
     int32_t pairs_per_seq;        // units per (sequence, kv head)
     int32_t n_kv_heads;
-    int32_t n_units;              // below 2^31 - 2 * the grid
+    int32_t n_full, n_units;      // units of two tiles, then those of one; below 2^31 - 2 * the grid
     int32_t window, sinks;
     int32_t wide_out;             // out is 32-byte aligned
     unsigned long long wait_ns;   // limit of the pipeline waits
@@ -77,7 +81,7 @@ struct WinParams {
 // A unit and its keys.  Place c of the packed keys is key c below n_first (the
 // groups with first tokens), else key c + skip; keys in [sinks, w_lo) are seen by
 // no query of the unit.  A sequence of bad length has one tile without keys, whose
-// output is not written (p_last -1).
+// output is not written (p_last -1), and so has a half unit past the chunk's end.
 struct Unit {
     int32_t s, kvh, p0, p_last, P;
     int32_t w_lo, n_first, skip, n_places, n_kt;
@@ -89,22 +93,26 @@ struct Unit {
 __device__ __noinline__ void find_unit(const WinParams &p, int32_t u, Unit *out)
 {
     Unit w;
+    const int32_t half = u >= p.n_full ? (u - p.n_full) & 1 : 0, tiles = u >= p.n_full ? 1 : kNQ;
+    if (u >= p.n_full) u = p.n_full + (u - p.n_full) / 2;
     const int32_t per_seq = p.pairs_per_seq * p.n_kv_heads;
     w.s = u / per_seq;
     const int32_t in = u - w.s * per_seq, pair = in / p.n_kv_heads;
     w.kvh = in - pair * p.n_kv_heads;
-    const int32_t positions = kNQ * (kTM / p.group);
-    w.p0 = (p.pairs_per_seq - 1 - pair) * positions;
-    w.p_last = min(w.p0 + positions, p.chunk) - 1;
+    const int32_t positions = kTM / p.group;         // of a query tile
+    w.p0 = ((p.pairs_per_seq - 1 - pair) * kNQ + half) * positions;
+    w.p_last = min(w.p0 + tiles * positions, p.chunk) - 1;
     w.P = __ldg(p.prefix_lens + w.s);
     int32_t n_keys = 0;
     w.w_lo = 0;
     if (w.P < 0 || (int64_t)w.P + w.p_last + 1 > (int64_t)p.max_blocks * p.block_size) {
         w.P = 0;
         w.p_last = -1;
-    } else {
+    } else if (w.p0 <= w.p_last) {
         n_keys = w.P + w.p_last + 1;
-        w.w_lo = max(0, w.P + w.p0 - p.window + 1);
+        // (of the whole unit: a row's keys are packed alike in both, so that its result does
+        // not depend on which of the two the batch made it)
+        w.w_lo = max(0, w.P + (p.pairs_per_seq - 1 - pair) * kNQ * positions - p.window + 1);
     }
     w.n_first = (min(p.sinks, n_keys) + 15) & ~15;
     w.skip = max((w.w_lo & ~15) - w.n_first, 0);
@@ -235,6 +243,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     const int G = p.group;
     const int pos_per_tile = kTM / G;
 
+    // a half unit is the last of its CTA
+    auto is_half = [&](int i) { return (int)blockIdx.x + i * (int)gridDim.x >= p.n_full; };
+
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -358,8 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                             *abort_flag = 1;
                         } else {
                             const Unit &w = unit_s[t_unit & 3];
-                            mbar_arrive_expect_tx(q_full, kNQ * kQTile);
-                            for (int i = 0; i < kNQ; ++i)
+                            const int n_q = is_half(t_unit) ? 1 : kNQ;
+                            mbar_arrive_expect_tx(q_full, n_q * kQTile);
+                            for (int i = 0; i < n_q; ++i)
                                 for (int h = 0; h < PANELS; ++h)
                                     tma_load_3d(q_s + i * kQTile + h * kQPanel, &q_map, h * 64, t_kvh * G,
                                                 w.s * p.chunk + w.p0 + i * pos_per_tile, q_full);
@@ -420,14 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 n_kt = tiles_of(0);
                 tc_fence_after();
 #pragma unroll 1
-                for (int t = 0; t < kNQ; ++t) issue_s(t, 0);
+                for (int t = 0; t < (is_half(0) ? 1 : kNQ); ++t) issue_s(t, 0);
                 commit_one(leader, &k_empty[0]);
                 if (n_kt == 1) commit_one(leader, q_empty);
             }
             int units = 0, left = n_kt;
             uint32_t phase = 0;                   // of p_full
             while (ok) {
-                const bool first = left == n_kt, last = left == 1;
+                const bool first = left == n_kt, last = left == 1, half = is_half(units);
                 if (++ks == NK) {                 // the next tile's K
                     ks = 0;
                     k_phase ^= 1;
@@ -435,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 ok = wait(&v_full[vs], v_phase);
 #pragma unroll
                 for (int t = 0; t < kNQ; ++t) {
-                    if (!ok) break;
+                    if (!ok || (t > 0 && half)) break;
                     ok = wait(&p_full[t], phase);
                     if (!ok) break;
                     tc_fence_after();
@@ -461,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     tc_fence_after();
                     // (S_t's columns hold a P that the tensor core reads before)
 #pragma unroll 1
-                    for (int t = 0; t < kNQ; ++t) issue_s(t, ks);
+                    for (int t = 0; t < (is_half(units) ? 1 : kNQ); ++t) issue_s(t, ks);
                     left = n_kt + 1;
                 }
                 commit_one(leader, &k_empty[ks]);
@@ -490,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         // (the unit stays in shared memory: a row's scores need the registers)
         int c = 0;                               // tiles so far
         bool ok = true;
-        for (int units = 0; units < n_mine; ++units) {
+        for (int units = 0; units < n_mine && !(qt > 0 && is_half(units)); ++units) {
             const volatile Unit &w = unit_s[units & 3];
             int n_kt = 1;                        // read with the unit's first tile
             int32_t pos = 0, qpos = 0;
@@ -692,8 +704,10 @@ cudaError_t launch_prefill_window(const PrefillArgs &a, int num_sms, cudaStream_
     p.pairs_per_seq = (a.chunk + kNQ * pos_per_tile - 1) / (kNQ * pos_per_tile);
     p.n_kv_heads = d.n_kv_heads;
     const int64_t units = (int64_t)p.pairs_per_seq * d.n_kv_heads * a.n_seqs;
-    if (units > INT32_MAX - 2 * (int64_t)num_sms) return cudaErrorInvalidValue;
-    p.n_units = (int32_t)units;
+    if (units > INT32_MAX - 4 * (int64_t)num_sms) return cudaErrorInvalidValue;
+    const int32_t over = (int32_t)(units % num_sms), halves = 2 * over <= num_sms ? over : 0;
+    p.n_full = (int32_t)units - halves;
+    p.n_units = p.n_full + 2 * halves;
     p.window = a.window;
     p.sinks = a.sinks;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
