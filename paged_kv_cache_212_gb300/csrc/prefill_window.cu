@@ -548,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                             seen = (seen & ~mixed) | (mixed & bits_below(back - i0) & ~bits_below(low - i0));
                         }
                         seen |= bits_below(first - i0);
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
