@@ -26,6 +26,11 @@
 extern "C" {
 #endif
 
+/* The most tokens a table row may span in the calls below (max_blocks *
+ * block_size; PKV_ERR_OUT_OF_RANGE above): positions are int32, with room for a
+ * tile behind the last one. */
+#define PKV_WINDOW_MAX_TOKENS 0x7fffff00
+
 /*
  * paged_decode_attention_window -- one query per sequence, at position
  * ctx_lens[s] - 1, over bf16 or int8 pages.  Arguments as in

@@ -9,12 +9,12 @@
 #include "common.cuh"
 #include "launch.h"
 #include "decode_small.h"
+#include "window.h"
 #include "../../include/pagedkv_window.h"
 
 namespace pkv {
 
 cudaError_t launch_prefill_tc(const PrefillArgs &a, cudaStream_t stream);
-cudaError_t launch_prefill_window(const PrefillArgs &a, int num_sms, cudaStream_t stream);
 
 namespace {
 
@@ -215,11 +215,11 @@ cudaError_t prepare_kernel(const void *kern, int threads, size_t smem, int *occu
     return cudaSuccess;
 }
 
-// Prefill runs on the tcgen05 kernels (prefill_tc.cu; under a window
-// prefill_window.cu).
+// Prefill runs on the tcgen05 kernel (prefill_tc.cu).
 cudaError_t launch_prefill(const PrefillArgs &a, int num_sms, cudaStream_t stream)
 {
-    return a.window > 0 ? launch_prefill_window(a, num_sms, stream) : launch_prefill_tc(a, stream);
+    (void)num_sms;
+    return launch_prefill_tc(a, stream);
 }
 
 }  // namespace pkv
@@ -469,8 +469,9 @@ static int prefill(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool,
     st = num_sms_of_current_device(&sms);
     if (st != PKV_OK) return st;
     PrefillArgs a{q, n_q_heads, k_pool, v_pool, dims, block_tables, max_blocks, prefix_lens, n_seqs, chunk,
-                  softmax_scale, out, lse_out, dev_status, window, sinks};
-    return cuda_status(launch_prefill(a, sms, (cudaStream_t)stream));
+                  softmax_scale, out, lse_out, dev_status};
+    return cuda_status(window > 0 ? launch_prefill_window(a, window, sinks, sms, (cudaStream_t)stream)
+                                  : launch_prefill(a, sms, (cudaStream_t)stream));
 }
 
 int paged_prefill_attention(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool, const pkv_bf16 *v_pool,
@@ -489,6 +490,7 @@ int paged_prefill_attention_window(const pkv_bf16 *q, int32_t n_q_heads, const p
                                    int32_t *dev_status, pkv_stream_t stream)
 {
     if (window < 1 || sinks < 0) return PKV_ERR_INVALID_ARG;
+    if (dims.block_size > 0 && (int64_t)max_blocks * dims.block_size > PKV_WINDOW_MAX_TOKENS) return PKV_ERR_OUT_OF_RANGE;
     return prefill(q, n_q_heads, k_pool, v_pool, dims, block_tables, max_blocks, prefix_lens, n_seqs, chunk,
                    softmax_scale, window, sinks, out, lse_out, dev_status, stream);
 }

@@ -39,6 +39,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
+#include "window.h"
 #include "write_rows.cuh"
 #include "../../include/pagedkv_window.h"
 
@@ -185,7 +186,7 @@ struct Seen {
     __device__ __forceinline__ int32_t place(int32_t i) const { return i < n_first ? i : w_tile + i - n_first; }
     __device__ __forceinline__ uint32_t mask(int32_t t) const
     {
-        if (t >= low && t + kTile <= L) return 0xffffu;
+        if (t >= low && L - t >= kTile) return 0xffffu;
         const uint32_t below_L = L - t >= kTile ? 0xffffu : (1u << max(L - t, 0)) - 1u;
         const uint32_t below_first = first - t >= kTile ? 0xffffu : (1u << max(first - t, 0)) - 1u;
         const uint32_t from_low = low <= t ? 0xffffu : low - t >= kTile ? 0u : 0xffffu << (low - t);
@@ -840,7 +841,7 @@ int prepare_window(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, void 
     if (n_q_heads % dims.n_kv_heads != 0) return PKV_ERR_INVALID_ARG;
     if (n_q_heads / dims.n_kv_heads > kHeads) return PKV_ERR_UNSUPPORTED;
     if (kv_dtype != PKV_KV_BF16 && kv_dtype != PKV_KV_INT8) return PKV_ERR_UNSUPPORTED;
-    if ((int64_t)max_blocks * dims.block_size > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
+    if ((int64_t)max_blocks * dims.block_size > PKV_WINDOW_MAX_TOKENS) return PKV_ERR_OUT_OF_RANGE;
     if ((int64_t)n_seqs * dims.n_kv_heads * kMaxSplits > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
     if (!row_stride_ok(q_stride, n_q_heads, dims.head_dim)) return PKV_ERR_INVALID_ARG;
     if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.f)) return PKV_ERR_INVALID_ARG;

@@ -7,7 +7,6 @@
 #include <stdint.h>
 
 #include "../../include/pagedkv.h"
-#include "../../include/pagedkv_rope.h"
 
 namespace pkv {
 
@@ -92,21 +91,7 @@ struct PrefillArgs {
     void *out;
     float *lse_out;
     int32_t *dev_status;
-    int32_t window, sinks;  // window 0: every key up to the query
 };
-
-// Host checks shared by the entry points (api.cu): PKV_OK or PKV_ERR_CUDA with
-// the error recorded; 16-byte alignment; the SM count of the current device;
-// the geometry every kernel supports.
-int cuda_status(cudaError_t e);
-bool aligned16(const void *p);
-int num_sms_of_current_device(int *out);
-int check_dims(const pkv_dims &d);
-
-// Checks of a rotary turn for heads of head_dim elements, and of a stride between
-// tokens of `heads` head rows (rope_write.cu).
-int check_rope(const pkv_rope *rope, int32_t head_dim);
-bool row_stride_ok(int64_t stride, int32_t heads, int32_t head_dim);
 
 cudaError_t launch_write_bf16(const WriteArgs &a, cudaStream_t stream);
 cudaError_t launch_write_int8(const WriteArgs &a, float *k_scales, float *v_scales,

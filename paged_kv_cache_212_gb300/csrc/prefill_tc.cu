@@ -92,6 +92,71 @@ constexpr int kRegsIssue = 72;
 constexpr int kRegsSoftmax = 216;
 static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= 384 * kLaunchRegs, "register split above the launch");
 
+// ---- tcgen05 helpers -------------------------------------------------------
+
+// The 8 products of one 128-row tile step in one asm block, so that the
+// predicates are set once (first product: accumulate_first; the rest
+// accumulate) rather than once per instruction.  A and B shared-memory
+// descriptors (SS form).
+__device__ __forceinline__ void umma_bf16_x8(uint32_t d_tmem, const uint64_t (&a)[8], const uint64_t (&b)[8],
+                                             uint32_t idesc, uint32_t accumulate_first)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %17, 0;\n\t"
+        "setp.eq.b32 q, %17, %17;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %9, %18, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %10, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %11, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %12, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %13, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %14, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %15, %18, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %16, %18, q;\n\t}" ::"r"(d_tmem),
+        "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(a[4]), "l"(a[5]), "l"(a[6]), "l"(a[7]), "l"(b[0]),
+        "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]), "r"(accumulate_first),
+        "r"(idesc)
+        : "memory");
+}
+
+// The 8 products of one tile step in the TS form: D (TMEM) += A (TMEM, M x 16,
+// K-major: lane = row, column c = bf16 pair 2c, 2c + 1; product k at a_tmem +
+// 8 k) * B (shared-memory descriptor), predicates set once as above.
+__device__ __forceinline__ void umma_bf16_ts_x8(uint32_t d_tmem, uint32_t a_tmem, const uint64_t (&b)[8],
+                                                uint32_t idesc, uint32_t accumulate_first)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
+        "setp.ne.b32 p, %10, 0;\n\t"
+        "setp.eq.b32 q, %10, %10;\n\t"
+        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\t"
+        "add.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %11, p;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %3, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %4, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], %5, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %6, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], %7, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], %8, %11, q;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], %9, %11, q;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]),
+        "r"(accumulate_first), "r"(idesc)
+        : "memory");
+}
+
+// max(a, b, c) in one instruction (sm_100 and later).
+__device__ __forceinline__ float fmax3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk)
+{
+    return row * 128u + ((chunk ^ (row & 7u)) << 4);
+}
+
 // Shared memory -> global through a 4-D tensor map (elements past the map's
 // extent are not written), then the commit of the bulk group.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int32_t c0, int32_t c1,
@@ -108,6 +173,22 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void 
 __device__ __forceinline__ void bulk_wait_read_all()
 {
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
+// AND of v over the 128 threads of a warpgroup (named barrier id); every
+// thread of the warpgroup must reach it.
+__device__ __forceinline__ bool wg_and(uint32_t id, bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
 }
 
 }  // namespace
@@ -185,8 +266,8 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
     const int p0 = pair * kNQ * pos_per_tile;
     const int p_last = min(p0 + kNQ * pos_per_tile, p.chunk) - 1;
     const int32_t P = __ldg(p.prefix_lens + s);
-    const bool bad_len = P < 0 || (int64_t)P + p_last + 1 > (int64_t)p.max_blocks * p.block_size;
-    const int32_t n_keys = bad_len ? 0 : P + p_last + 1;
+    const int32_t n_keys = P + p_last + 1;
+    const bool bad_len = P < 0 || (int64_t)n_keys > (int64_t)p.max_blocks * p.block_size;
     const int n_kt = bad_len ? 0 : (n_keys + kTN - 1) / kTN;
 
     if (threadIdx.x == 0) {
@@ -518,7 +599,7 @@ __global__ void __launch_bounds__(384, 1) prefill_tc_kernel(const __grid_constan
             }
             if (pos <= p_last && p.lse_out)
                 p.lse_out[((int64_t)s * p.chunk + pos) * p.n_q_heads + h] = (m + __log2f(l)) * 0.69314718055994531f;
-        } else if (!ok && n_kt > 0) {       // n_kt 0: a bad length, reported above
+        } else if (!ok) {
             if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
             *abort_flag = 1;
         }

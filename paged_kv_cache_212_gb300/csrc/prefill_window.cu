@@ -33,6 +33,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
+#include "window.h"
 
 namespace pkv {
 namespace {
@@ -119,6 +120,20 @@ __device__ __noinline__ void find_unit(const WinParams &p, int32_t u, Unit *out)
     w.n_places = n_keys - w.skip;
     w.n_kt = max(1, (w.n_places + kTN - 1) / kTN);
     *out = w;
+}
+
+// max(a, b, c) in one instruction (sm_100 and later).
+__device__ __forceinline__ float fmax3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Byte of 16-byte chunk `chunk` of row `row` in a tile of 128-byte rows (128-byte swizzle).
+__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk)
+{
+    return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
 
 // Bits 0 .. n - 1 of a word (none for n <= 0, all for n >= 32).
@@ -681,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
 
 }  // namespace
 
-cudaError_t launch_prefill_window(const PrefillArgs &a, int num_sms, cudaStream_t stream)
+cudaError_t launch_prefill_window(const PrefillArgs &a, int32_t window, int32_t sinks, int num_sms, cudaStream_t stream)
 {
     const pkv_dims &d = a.dims;
     const int G = a.n_q_heads / d.n_kv_heads;
@@ -709,8 +724,8 @@ cudaError_t launch_prefill_window(const PrefillArgs &a, int num_sms, cudaStream_
     const int32_t over = (int32_t)(units % num_sms), halves = 2 * over <= num_sms ? over : 0;
     p.n_full = (int32_t)units - halves;
     p.n_units = p.n_full + 2 * halves;
-    p.window = a.window;
-    p.sinks = a.sinks;
+    p.window = window;
+    p.sinks = sinks;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
 
     CUtensorMap qmap, kmap, vmap;

@@ -13,8 +13,8 @@
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
+#include "window.h"
 #include "write_rows.cuh"
-#include "../../include/pagedkv_rope.h"
 
 namespace pkv {
 namespace {

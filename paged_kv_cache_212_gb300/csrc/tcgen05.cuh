@@ -117,83 +117,4 @@ __device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t *r)
         : "r"(taddr));
 }
 
-// The 8 products of one 128-row tile step in one asm block, so that the
-// predicates are set once (first product: accumulate_first; the rest
-// accumulate) rather than once per instruction.  A and B shared-memory
-// descriptors (SS form).
-__device__ __forceinline__ void umma_bf16_x8(uint32_t d_tmem, const uint64_t (&a)[8], const uint64_t (&b)[8],
-                                             uint32_t idesc, uint32_t accumulate_first)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.b32 p, %17, 0;\n\t"
-        "setp.eq.b32 q, %17, %17;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %9, %18, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %2, %10, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %3, %11, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %4, %12, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %5, %13, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %6, %14, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %7, %15, %18, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %8, %16, %18, q;\n\t}" ::"r"(d_tmem),
-        "l"(a[0]), "l"(a[1]), "l"(a[2]), "l"(a[3]), "l"(a[4]), "l"(a[5]), "l"(a[6]), "l"(a[7]), "l"(b[0]),
-        "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]), "r"(accumulate_first),
-        "r"(idesc)
-        : "memory");
-}
-
-// The 8 products of one tile step in the TS form: D (TMEM) += A (TMEM, M x 16,
-// K-major: lane = row, column c = bf16 pair 2c, 2c + 1; product k at a_tmem +
-// 8 k) * B (shared-memory descriptor), predicates set once as above.
-__device__ __forceinline__ void umma_bf16_ts_x8(uint32_t d_tmem, uint32_t a_tmem, const uint64_t (&b)[8],
-                                                uint32_t idesc, uint32_t accumulate_first)
-{
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 a1, a2, a3, a4, a5, a6, a7;\n\t"
-        "setp.ne.b32 p, %10, 0;\n\t"
-        "setp.eq.b32 q, %10, %10;\n\t"
-        "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\tadd.u32 a4, %1, 32;\n\t"
-        "add.u32 a5, %1, 40;\n\tadd.u32 a6, %1, 48;\n\tadd.u32 a7, %1, 56;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %11, p;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %3, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %4, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], %5, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], %6, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], %7, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], %8, %11, q;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], %9, %11, q;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b[0]), "l"(b[1]), "l"(b[2]), "l"(b[3]), "l"(b[4]), "l"(b[5]), "l"(b[6]), "l"(b[7]),
-        "r"(accumulate_first), "r"(idesc)
-        : "memory");
-}
-
-// max(a, b, c) in one instruction (sm_100 and later).
-__device__ __forceinline__ float fmax3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t swz128(uint32_t row, uint32_t chunk)
-{
-    return row * 128u + ((chunk ^ (row & 7u)) << 4);
-}
-
-// AND of v over the 128 threads of a warpgroup (named barrier id); every
-// thread of the warpgroup must reach it.
-__device__ __forceinline__ bool wg_and(uint32_t id, bool v)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id)
-        : "memory");
-    return r != 0;
-}
-
 }  // namespace pkv

@@ -112,7 +112,7 @@ def test_window_decode_argument_checks(P):
         assert f(*_decode_args(P, **kw)) == 1, kw
     for kw in (dict(hq=18), dict(dt=7), dict(dims=D(8, 16, 2, 32)), dict(dims=D(8, 512, 2, 64))):
         assert f(*_decode_args(P, **kw)) == 2, kw
-    for kw in (dict(mb=1 << 30), dict(n=1 << 30)):
+    for kw in (dict(mb=1 << 30), dict(mb=0x7fffff00 // 16 + 1), dict(n=1 << 30)):
         assert f(*_decode_args(P, **kw)) == 3, kw
 
 
@@ -136,7 +136,7 @@ def test_window_prefill_argument_checks(P):
     d = P.Dims(8, 16, 2, 64)
 
     def args(**kw):
-        return [kw.get("q", FAKE), kw.get("hq", 8), FAKE, FAKE, d, FAKE, 4, FAKE, kw.get("n", 1), kw.get("chunk", 16), 0.1,
+        return [kw.get("q", FAKE), kw.get("hq", 8), FAKE, FAKE, d, FAKE, kw.get("mb", 4), FAKE, kw.get("n", 1), kw.get("chunk", 16), 0.1,
                 kw.get("win", 9), kw.get("sinks", 0), kw.get("out", FAKE), None, None, None]
 
     assert f(*args(n=0)) == 0 and f(*args(chunk=0)) == 0
@@ -144,6 +144,7 @@ def test_window_prefill_argument_checks(P):
         assert f(*args(**kw)) == 1, kw
     assert f(*args(hq=6)) == 2
     assert f(*args(chunk=65)) == 3
+    assert f(*args(mb=0x7fffff00 // 16 + 1)) == 3
 
 
 def test_token_strides(P):
