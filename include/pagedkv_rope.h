@@ -40,12 +40,12 @@ enum pkv_rope_scaling {
 };
 
 /* The turn of a call.  phases: rot_dim / 2 values in device memory, 16-byte
- * aligned.  rot_dim: a multiple of 16, at most head_dim.  magnitude: finite. */
+ * aligned.  rot_dim: a multiple of 16, at most head_dim.  magnitude: finite (as a float). */
 typedef struct pkv_rope {
     const uint64_t *phases;
     int32_t rot_dim;
     int32_t interleaved; /* 0: half layout */
-    float magnitude;
+    double magnitude;
 } pkv_rope;
 
 /*
@@ -59,7 +59,7 @@ typedef struct pkv_rope {
  * another scaling.
  */
 int pkv_rope_phases(int32_t rot_dim, double base, int32_t scaling, double factor, double original_context,
-                    double low_turns, double high_turns, uint64_t *phases_out, float *magnitude_out);
+                    double low_turns, double high_turns, uint64_t *phases_out, double *magnitude_out);
 
 /*
  * paged_kv_write_rope -- token j < n_new of sequence s sits at position

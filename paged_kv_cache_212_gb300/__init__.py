@@ -68,7 +68,7 @@ class Dims(ctypes.Structure):
 class _RopeC(ctypes.Structure):
     """pkv_rope."""
     _fields_ = [("phases", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("magnitude", ctypes.c_float)]
+                ("magnitude", ctypes.c_double)]
 
 
 _lib = None
@@ -157,7 +157,7 @@ def load_library(path: str = LIB_PATH):
                "paged_decode_streamed"):
         getattr(lib, fn).restype = ctypes.c_int
     f32, f64, RP = ctypes.c_float, ctypes.c_double, ctypes.POINTER(_RopeC)
-    lib.pkv_rope_phases.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, ctypes.POINTER(f32)]
+    lib.pkv_rope_phases.argtypes = [i32, f64, i32, f64, f64, f64, f64, P, ctypes.POINTER(f64)]
     lib.paged_kv_write_rope.argtypes = [P, i64, i32, P, i64, P, i64, RP, P, P, P, P, P, i32, Dims, P, i32, P, i32, i32,
                                         P, P]
     lib.paged_decode_attention_window.argtypes = [P, i32, P, P, P, P, i32, Dims, P, i32, P, i32, f32, i32, i32, P, P,
@@ -661,7 +661,7 @@ class Rope:
             raise ValueError(f"scaling {scaling!r} needs original_context")
         self.rot_dim, self.interleaved = int(rot_dim), bool(interleaved)
         host = torch.empty(max(self.rot_dim, 0) // 2, dtype=torch.int64)
-        magnitude = ctypes.c_float()
+        magnitude = ctypes.c_double()
         _check("pkv_rope_phases", load_library().pkv_rope_phases(
             self.rot_dim, float(base), ROPE_SCALINGS[scaling], float(factor), float(original_context or 0.0),
             float(low), float(high), host.data_ptr(), ctypes.byref(magnitude)))

@@ -927,7 +927,7 @@ int paged_decode_step_window(const pkv_bf16 *k_new, int64_t k_stride, const pkv_
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.start_pos = start_pos;
-    if (rope) a.rope = RopeArgs{rope->phases, rope->rot_dim, rope->interleaved != 0, rope->magnitude};
+    if (rope) a.rope = rope_args(rope->phases, rope->rot_dim, rope->interleaved, rope->magnitude);
     int sms = 0;
     st = num_sms_of_current_device(&sms);
     if (st != PKV_OK) return st;

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) rope_write_kernel(const RopeWr
 
 int check_rope(const pkv_rope *rope, int32_t head_dim)
 {
-    if (!rope || !rope->phases || !aligned16(rope->phases) || !std::isfinite(rope->magnitude))
+    if (!rope || !rope->phases || !aligned16(rope->phases) || !std::isfinite((float)rope->magnitude))
         return PKV_ERR_INVALID_ARG;
     if (rope->rot_dim <= 0 || rope->rot_dim > head_dim) return PKV_ERR_INVALID_ARG;
     if (rope->rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
@@ -155,7 +155,7 @@ using namespace pkv;
 extern "C" {
 
 int pkv_rope_phases(int32_t rot_dim, double base, int32_t scaling, double factor, double original_context,
-                    double low_turns, double high_turns, uint64_t *phases_out, float *magnitude_out)
+                    double low_turns, double high_turns, uint64_t *phases_out, double *magnitude_out)
 {
     constexpr double kTwoPi = 6.283185307179586476925286766559;
     if (!phases_out || !magnitude_out || rot_dim <= 0 || rot_dim % 16 != 0) return PKV_ERR_INVALID_ARG;
@@ -166,7 +166,7 @@ int pkv_rope_phases(int32_t rot_dim, double base, int32_t scaling, double factor
     if (by_turns && (!std::isfinite(original_context) || !(original_context > 0.0) || !(low_turns > 0.0) ||
                      !(high_turns > low_turns) || !std::isfinite(high_turns)))
         return PKV_ERR_INVALID_ARG;
-    *magnitude_out = scaling == PKV_ROPE_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
+    *magnitude_out = scaling == PKV_ROPE_YARN ? 0.1 * log(factor) + 1.0 : 1.0;
     if (scaling == PKV_ROPE_NTK) base *= pow(factor, rot_dim / (rot_dim - 2.0));
     // YARN: the (real) pair index that makes n turns in the original context
     const auto pair_of = [&](double n) { return rot_dim * log(original_context / (n * kTwoPi)) / (2.0 * log(base)); };
@@ -232,7 +232,7 @@ int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, 
     a.k_stride = k_stride;
     a.v_stride = v_stride;
     a.n_q_heads = n_q_heads;
-    a.rope = RopeArgs{rope->phases, rope->rot_dim, rope->interleaved != 0, rope->magnitude};
+    a.rope = rope_args(rope->phases, rope->rot_dim, rope->interleaved, rope->magnitude);
     a.q_out = reinterpret_cast<__nv_bfloat16 *>(q_out);
     a.k_pool = k_pool;
     a.v_pool = v_pool;
