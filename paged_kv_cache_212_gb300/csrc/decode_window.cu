@@ -714,8 +714,8 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 
 struct Choice {
     int splits = 0;
-    int64_t places = 0;      // CTAs of one unit each that are resident at once
-    int64_t warps = 0;       // resident warps of the launch
+    int64_t places = 0;      // CTAs that are resident at once
+    int64_t room = 0;        // units that the machine's rounds of this launch have room for
 };
 
 template <int D, bool INT8, bool WIDE, int WARPS>
@@ -766,7 +766,12 @@ cudaError_t resident_clusters(int splits, int *out)
 }
 
 // The most CTAs per unit with which all CTAs of WARPS warps are resident at once
-// and every warp keeps two tiles of the longest window.
+// and every warp keeps two tiles of the longest window; then as few as leave the
+// longest share of a warp as it is.  Measured (windows of 1024, 8 kv heads of 128,
+// bf16 / int8 pages where not said): two sequences of 16 K visible tokens take 26 us
+// with the 13 CTAs per unit that are resident at once and 40 with 16; four sequences
+// over int8 pages 9.9 us with the 8 CTAs that two tiles a warp allow, 8.2 with the 6
+// that give the longest share, three tiles, as well, and 12.0 with one tile a warp.
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
@@ -779,13 +784,16 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
     if (n > tiles / (2 * WARPS)) n = tiles / (2 * WARPS);
     if (n > kMaxSplits) n = kMaxSplits;
     for (; n > 1; --n) {
+        const int64_t share = (tiles + n * WARPS - 1) / (n * WARPS);
+        n = (tiles + share * WARPS - 1) / (share * WARPS);
+        if (n == 1) break;
         int clusters = 0;
         e = resident_clusters<D, INT8, WIDE, WARPS>((int)n, &clusters);
         if (e != cudaSuccess) return e;
         if (clusters >= units) break;
     }
     c->splits = n < 1 ? 1 : (int)n;
-    c->warps = (units * c->splits < c->places ? units * c->splits : c->places) * WARPS;
+    c->room = (units * c->splits + c->places - 1) / c->places * c->places / c->splits;
     return cudaSuccess;
 }
 
@@ -798,8 +806,12 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, cudaStream_
     return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, WARPS>, a);
 }
 
-// CTAs of 4 warps, or of 2 where that lets more warps be resident (a batch whose
-// units are more than the larger CTAs' places, but not the smaller ones').
+// CTAs of 4 warps, or of 2 where their rounds leave less of the machine idle: by a
+// fifth, or by anything once the units are more than the larger CTAs' places.
+// Measured (4 warps / 2 warps; windows of 1024, 8 kv heads of 128): bf16 pages, 32
+// sequences 23.6 / 24.7 us, 40: 37.9 / 30.3, 64: 45.4 / 42.9, 80: 61.7 / 66.4,
+// 128: 87.5 / 82.3; int8 pages, 12 sequences 11.1 / 11.5, 48: 29.4 / 24.5,
+// 64: 31.0 / 38.6, 80: 43.2 / 39.2, 128: 52.3 / 68.4.
 template <int D, bool INT8, bool WIDE>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
@@ -808,7 +820,7 @@ cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, c
     if (e != cudaSuccess) return e;
     e = choose<D, INT8, WIDE, 2>(units, tiles, sms, &c2);
     if (e != cudaSuccess) return e;
-    const bool small = units > c4.places ? units <= c2.places : c2.warps > c4.warps;
+    const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
     return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, stream) : launch_as<D, INT8, WIDE, 4>(a, c4, units, stream);
 }
 
