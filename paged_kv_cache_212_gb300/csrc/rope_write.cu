@@ -8,6 +8,14 @@
 // one token: its threads compute the token's sines and cosines once, one pair
 // each, while the rows they will turn are on their way; a warp holds several of
 // the token's head rows (Hq + 2 Hkv of them) at once, D / 16 lanes a row (rope.cuh).
+//
+// Measured (32 query and 8 kv heads of 128, kernels back to back in a graph): a chunk
+// of 8 x 512 tokens 17.2 us = 5.9 TB/s, 86 % of the copy rate, of which 2.1 us are a
+// launch of one token; 64 tokens of one position each 2.4 us; 5 x 301 tokens into
+// int8 pages 10.6 us (3.2 TB/s: the two true divisions of each element's code fill
+// the instruction slots).  Rows are loaded before the position is known, and sines
+// and cosines shared by the block: 22.8 -> 18.6 us on the chunk; read and written
+// once, so loads and stores are streamed: 18.6 -> 17.6.
 #include <math.h>
 
 #include "common.cuh"
@@ -35,12 +43,27 @@ struct RopeWriteArgs {
     int32_t *dev_status;
 };
 
-constexpr int kMaxWarps = 8;   // of a block
-constexpr int kGroups = 3;     // groups of head rows that a warp holds at once
+// Warps of a block and groups of head rows that a warp holds at once.  Chunks take
+// narrow blocks (4 warps, 3 groups: 48 rows of 128 elements in one go), many of
+// them on an SM; a few tokens take wide ones, while all of their blocks are
+// resident at once.  Measured, narrow / wide: 64 tokens 2.5 / 2.3 us (bf16 pages),
+// 3.3 / 3.1 (int8); 600 tokens 3.6 / 3.4 and 4.6 / 6.5; 1024 tokens 5.5 / 6.9 and
+// 8.0 / 11.6; 4096 tokens 17.2 / 19.5 and 24 / 35.
+constexpr int kNarrowWarps = 4, kNarrowGroups = 3;
+constexpr int kWideWarps = 8, kWideGroups = 2;
+// blocks that are resident on an SM; the registers are bounded to it (narrow blocks
+// for bf16 pages on 4096 tokens: 18.3 us with 5, 17.2 with 6, 17.6 with 8; one more
+// for int8 pages spills)
+template <bool INT8>
+constexpr int wide_blocks() { return INT8 ? 2 : 4; }
+template <bool INT8>
+constexpr int narrow_blocks() { return INT8 ? 4 : 6; }
 
-template <int D, bool INT8>
-__global__ void __launch_bounds__(32 * kMaxWarps) rope_write_kernel(const RopeWriteArgs a)
+template <int D, bool INT8, bool WIDE>
+__global__ void __launch_bounds__(32 * (WIDE ? kWideWarps : kNarrowWarps), WIDE ? wide_blocks<INT8>() : narrow_blocks<INT8>())
+    rope_write_kernel(const RopeWriteArgs a)
 {
+    constexpr int kGroups = WIDE ? kWideGroups : kNarrowGroups;
     constexpr int SLOTS = D / 16;        // lanes per head row
     constexpr int ROWS = 32 / SLOTS;     // head rows in a group
     __shared__ __align__(16) float cos_s[D / 2], sin_s[D / 2];
@@ -102,7 +125,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) rope_write_kernel(const RopeWr
                 if (live && (is_q || row >= 0)) {
                     __nv_bfloat16 *dst = is_q ? a.q_out + (tok * hq + h) * D
                                               : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
-                    __stcs(reinterpret_cast<uint4 *>(dst) + v0, x0[i]);   // streamed: 18.6 -> 17.6 us on 4096 tokens
+                    __stcs(reinterpret_cast<uint4 *>(dst) + v0, x0[i]);
                     __stcs(reinterpret_cast<uint4 *>(dst) + v1, x1[i]);
                 }
             }
@@ -244,12 +267,11 @@ int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, 
     a.start_pos = start_pos;
     a.n_new = n_new;
     a.dev_status = dev_status;
-    // four warps a token, each with a few groups of its head rows; eight where there
-    // are too few tokens to fill the machine
     const int64_t tokens = (int64_t)n_seqs * n_new;
     const int rows_at_once = 32 / (dims.head_dim / 16);
     const int64_t groups = (n_q_heads + 2 * (int64_t)dims.n_kv_heads + rows_at_once - 1) / rows_at_once;
-    const int64_t most = tokens > 4 * (int64_t)sms ? 4 : kMaxWarps;
+    const bool wide = tokens <= (int64_t)sms * (int8 ? wide_blocks<true>() : wide_blocks<false>());
+    const int64_t most = wide ? kWideWarps : kNarrowWarps;
     const int warps = (int)(groups < most ? groups : most);
     cudaLaunchAttribute pdl[1];
     pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -260,11 +282,18 @@ int paged_kv_write_rope(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, 
     lc.stream = (cudaStream_t)stream;
     lc.attrs = pdl;
     lc.numAttrs = 1;
+    cudaError_t e;
     if (dims.head_dim == 128)
-        return cuda_status(int8 ? cudaLaunchKernelEx(&lc, rope_write_kernel<128, true>, a)
-                                : cudaLaunchKernelEx(&lc, rope_write_kernel<128, false>, a));
-    return cuda_status(int8 ? cudaLaunchKernelEx(&lc, rope_write_kernel<64, true>, a)
-                            : cudaLaunchKernelEx(&lc, rope_write_kernel<64, false>, a));
+        e = int8 ? (wide ? cudaLaunchKernelEx(&lc, rope_write_kernel<128, true, true>, a)
+                         : cudaLaunchKernelEx(&lc, rope_write_kernel<128, true, false>, a))
+                 : (wide ? cudaLaunchKernelEx(&lc, rope_write_kernel<128, false, true>, a)
+                         : cudaLaunchKernelEx(&lc, rope_write_kernel<128, false, false>, a));
+    else
+        e = int8 ? (wide ? cudaLaunchKernelEx(&lc, rope_write_kernel<64, true, true>, a)
+                         : cudaLaunchKernelEx(&lc, rope_write_kernel<64, true, false>, a))
+                 : (wide ? cudaLaunchKernelEx(&lc, rope_write_kernel<64, false, true>, a)
+                         : cudaLaunchKernelEx(&lc, rope_write_kernel<64, false, false>, a));
+    return cuda_status(e);
 }
 
 }  // extern "C"
