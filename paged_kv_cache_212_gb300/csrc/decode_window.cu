@@ -374,11 +374,8 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                 uint8_t *dst = new_rows + (which & 1) * S::kRow;
                 uint8_t *pool = static_cast<uint8_t *>(which ? a.v_pool : a.k_pool) + (new_row * hkv + h) * S::kRow;
                 if constexpr (INT8) {
-                    int code[16];
-                    const float scale = int8_codes<16>(x, amax, code);
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
+                    uint32_t w[4];
+                    const float scale = int8_codes16(x, amax, w);
                     const uint2 y0 = make_uint2(w[0], w[1]), y1 = make_uint2(w[2], w[3]);
                     if (which > 1) continue;
                     *reinterpret_cast<uint2 *>(dst + 8 * v0) = y0;

@@ -145,4 +145,43 @@ __device__ __forceinline__ void rope_turn(bool interleaved, const float (&c)[8],
     }
 }
 
+// The scale amax / 127 (correctly rounded) and the codes clamp(rint(fl(x / scale)),
+// -127, 127) of a lane's 16 elements of a row of absolute maximum amax, four codes
+// to a word; amax 0 gives scale and codes 0.
+//
+// With rcp = fl(1 / scale), q = fl(x rcp) is within 1.6e-5 of x / scale
+// (|x / scale| < 128), whose own rounding is below 4e-6.  Added to 1.5 * 2^23, q is
+// rounded to an integer, ties to even, which stands in the sum's low byte; where it
+// is nearer than 3e-5 to a half, and where it is no number, the division decides.
+__device__ __forceinline__ float int8_codes16(const float (&x)[16], float amax, uint32_t (&w)[4])
+{
+    constexpr float kInteger = 12582912.f;
+    const float scale = __fdiv_rn(amax, 127.0f);
+    const bool normal = scale >= 1.17549435e-38f;      // below, 1 / scale may not be finite
+    const float rcp = normal ? __frcp_rn(scale) : 0.f;
+    auto is_clear = [&](float q, float t) { return fabsf(__fsub_rn(q, __fsub_rn(t, kInteger))) < 0.5f - 3.0e-5f; };
+    bool clear = normal;
+    uint32_t c[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        const float q = __fmul_rn(x[e], rcp), t = __fadd_rn(q, kInteger);
+        clear = clear && is_clear(q, t);
+        c[e] = __float_as_uint(t);
+    }
+    if (!clear && amax != 0.f) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const float q = __fmul_rn(x[e], rcp);
+            if (normal && is_clear(q, __uint_as_float(c[e]))) continue;
+            c[e] = (uint32_t)max(-127, min(127, __float2int_rn(__fdiv_rn(x[e], scale))));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+        if (amax == 0.f) w[i] = 0;
+    }
+    return scale;
+}
+
 }  // namespace pkv

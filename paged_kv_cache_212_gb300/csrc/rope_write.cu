@@ -12,8 +12,8 @@
 // Measured (32 query and 8 kv heads of 128, kernels back to back in a graph): a chunk
 // of 8 x 512 tokens 17.2 us = 5.9 TB/s, 86 % of the copy rate, of which 2.1 us are a
 // launch of one token; 64 tokens of one position each 2.4 us; 5 x 301 tokens into
-// int8 pages 10.6 us (3.2 TB/s: the two true divisions of each element's code fill
-// the instruction slots).  Rows are loaded before the position is known, and sines
+// int8 pages 10.2 us, 8 x 512 of them 23 us (4.0 TB/s: 110 registers a thread leave
+// 16 warps on an SM, whose instructions wait for one another).  Rows are loaded before the position is known, and sines
 // and cosines shared by the block: 22.8 -> 18.6 us on the chunk; read and written
 // once, so loads and stores are streamed: 18.6 -> 17.6.
 #include <math.h>
@@ -48,7 +48,7 @@ struct RopeWriteArgs {
 // them on an SM; a few tokens take wide ones, while all of their blocks are
 // resident at once.  Measured, narrow / wide: 64 tokens 2.5 / 2.3 us (bf16 pages),
 // 3.3 / 3.1 (int8); 600 tokens 3.6 / 3.4 and 4.6 / 6.5; 1024 tokens 5.5 / 6.9 and
-// 8.0 / 11.6; 4096 tokens 17.2 / 19.5 and 24 / 35.
+// 7.9 / 11.6; 4096 tokens 17.2 / 19.5 and 23 / 35.
 constexpr int kNarrowWarps = 4, kNarrowGroups = 3;
 constexpr int kWideWarps = 8, kWideGroups = 2;
 // blocks that are resident on an SM; the registers are bounded to it (narrow blocks
@@ -140,12 +140,9 @@ __global__ void __launch_bounds__(32 * (WIDE ? kWideWarps : kNarrowWarps), WIDE 
                 for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
                 for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                int code[16];
-                const float scale = int8_codes<16>(x, amax, code);
+                uint32_t w[4];
+                const float scale = int8_codes16(x, amax, w);
                 if (is_q || !live || row < 0) continue;
-                uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int e = 0; e < 16; ++e) w[e / 4] |= (uint32_t)(code[e] & 0xff) << (8 * (e % 4));
                 int8_t *dst = static_cast<int8_t *>(is_v ? a.v_pool : a.k_pool) + (row * hkv + h) * D;
                 *reinterpret_cast<uint2 *>(dst + 8 * v0) = make_uint2(w[0], w[1]);
                 *reinterpret_cast<uint2 *>(dst + 8 * v1) = make_uint2(w[2], w[3]);

@@ -69,42 +69,6 @@ __device__ __forceinline__ void write_bf16_vectors(const WriteArgs &a, int64_t f
     }
 }
 
-// The scale amax / 127 and the codes clamp(rint(x / scale), -127, 127) of a
-// lane's EPL elements of a row whose absolute maximum is amax (the same for
-// every lane of the row; 0: scale and codes are 0).  The whole warp calls it.
-template <int EPL>
-__device__ __forceinline__ float int8_codes(const float (&x)[EPL], float amax, int (&c)[EPL])
-{
-    const float scale = __fdiv_rn(amax, 127.0f);
-    // code = rint(fl(x / scale)) without a division per element: with the
-    // correctly rounded reciprocal rcp = fl(1 / scale) (scale normal), the
-    // product q = fl(x * rcp) is within |x / scale| * (2^-23 + 2^-48) <= 1.53e-5
-    // of x / scale (|x / scale| < 128), and fl(x / scale) within half an ulp
-    // (<= 3.8e-6) of it; so when q is farther than 3e-5 from every
-    // half-integer, q and fl(x / scale) round to the same integer.  The
-    // rare q closer than that (a tie or a near-tie) takes the division.
-    const bool fast = scale >= 1.17549435e-38f;            // normal: rcp is finite and within 2^-24
-    const float rcp = fast ? __frcp_rn(scale) : 0.0f;
-    bool need_div = false;
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-        const float q = __fmul_rn(x[e], rcp);
-        const float frac = q - floorf(q);                   // exact for |q| < 2^23
-        c[e] = __float2int_rn(q);
-        need_div |= !(fast && fabsf(frac - 0.5f) > 3.0e-5f);
-    }
-    if (__any_sync(0xffffffffu, need_div && amax != 0.0f)) {    // rare: a (near-)tie in the warp's rows
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-            const float q = __fmul_rn(x[e], rcp);
-            if (!(fast && fabsf(q - floorf(q) - 0.5f) > 3.0e-5f)) c[e] = __float2int_rn(__fdiv_rn(x[e], scale));
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) c[e] = amax != 0.0f ? max(-127, min(127, c[e])) : 0;
-    return scale;
-}
-
 // Symmetric int8 quantisation in IEEE binary32 with round-to-nearest-even
 // (libmir-metal paged/mod.rs, KvPageFormat::Int8PerTokenHead): per (token,
 // kv head) row of K or of V, amax by a max-reduction, scale = amax / 127
@@ -164,8 +128,32 @@ __device__ __forceinline__ void write_int8_units(const WriteArgs &a, float *k_sc
         for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const float scale = __fdiv_rn(amax, 127.0f);
+        // code = rint(fl(x / scale)) without a division per element: with the
+        // correctly rounded reciprocal rcp = fl(1 / scale) (scale normal), the
+        // product q = fl(x * rcp) is within |x / scale| * (2^-23 + 2^-48) <= 1.53e-5
+        // of x / scale (|x / scale| < 128), and fl(x / scale) within half an ulp
+        // (<= 3.8e-6) of it; so when q is farther than 3e-5 from every
+        // half-integer, q and fl(x / scale) round to the same integer.  The
+        // rare q closer than that (a tie or a near-tie) takes the division.
+        const bool fast = scale >= 1.17549435e-38f;            // normal: rcp is finite and within 2^-24
+        const float rcp = fast ? __frcp_rn(scale) : 0.0f;
         int c[EPL];
-        const float scale = int8_codes<EPL>(x, amax, c);
+        bool need_div = false;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+            const float q = __fmul_rn(x[e], rcp);
+            const float frac = q - floorf(q);                   // exact for |q| < 2^23
+            c[e] = __float2int_rn(q);
+            need_div |= !(fast && fabsf(frac - 0.5f) > 3.0e-5f);
+        }
+        if (__any_sync(0xffffffffu, need_div && amax != 0.0f)) {    // rare: a (near-)tie in the warp's rows
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) {
+                const float q = __fmul_rn(x[e], rcp);
+                if (!(fast && fabsf(q - floorf(q) - 0.5f) > 3.0e-5f)) c[e] = __float2int_rn(__fdiv_rn(x[e], scale));
+            }
+        }
         if (!active) continue;
         uint32_t packed[EPL / 4];
 #pragma unroll
@@ -173,7 +161,8 @@ __device__ __forceinline__ void write_int8_units(const WriteArgs &a, float *k_sc
             packed[w] = 0;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                packed[w] |= (uint32_t)(c[4 * w + k] & 0xff) << (8 * k);
+                const int ce = amax != 0.0f ? max(-127, min(127, c[4 * w + k])) : 0;
+                packed[w] |= (uint32_t)(ce & 0xff) << (8 * k);
             }
         }
         int8_t *dst = static_cast<int8_t *>(which ? a.v_pool : a.k_pool) + (row * hkv + h) * D + part * EPL;
