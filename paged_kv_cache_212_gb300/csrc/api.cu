@@ -131,7 +131,7 @@ struct KernelEntry {
     size_t smem, smem_set;
     int occupancy;
 };
-constexpr int kKernelCacheEntries = 64;
+constexpr int kKernelCacheEntries = 256;
 KernelEntry g_kernels[kKernelCacheEntries];
 int g_kernels_used = 0;
 std::mutex g_kernel_mu;

@@ -710,13 +710,21 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 }
 
 struct Choice {
-    int splits = 0;
+    int splits = 0, occupancy = 0;   // CTAs of a unit, CTAs that an SM holds
     int64_t places = 0;      // CTAs that are resident at once
     int64_t room = 0;        // units that the machine's rounds of this launch have room for
 };
 
+// Dynamic shared memory with which an SM (228 KB, 1 KB of them kept back for each
+// CTA) holds at most `per_sm` CTAs, which may be fewer than it has room for.
+constexpr size_t smem_for(size_t need, int per_sm)
+{
+    const size_t most = 228 * 1024 / (size_t)(per_sm + 1) - 1024 + 128;
+    return most > need ? most : need;
+}
+
 template <int D, bool INT8, bool WIDE, int WARPS>
-cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int64_t units, int splits, cudaStream_t stream)
+cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int64_t units, int splits, int per_sm, cudaStream_t stream)
 {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -727,25 +735,50 @@ cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int64_t units, in
     cudaLaunchConfig_t lc{};
     lc.gridDim = dim3((unsigned)(units * splits));
     lc.blockDim = dim3(32 * WARPS);
-    lc.dynamicSmemBytes = Shape<D, INT8>::smem(WARPS);
+    lc.dynamicSmemBytes = smem_for(Shape<D, INT8>::smem(WARPS), per_sm);
     lc.stream = stream;
     lc.attrs = at;
     lc.numAttrs = splits > 1 ? 2 : 1;
     return lc;
 }
 
-// How many clusters of `splits` CTAs are resident at once on the current device
-// (clusters stay within a GPC, so not every SM can hold one); asked once.
+constexpr int kDevices = 16;   // whose occupancies are remembered
+
+// How many CTAs an SM of the current device holds; asked once, when the kernel's
+// limit of shared memory is raised to the most that a launch asks for.
 template <int D, bool INT8, bool WIDE, int WARPS>
-cudaError_t resident_clusters(int splits, int *out)
+cudaError_t resident_ctas(int *out)
 {
-    static std::atomic<int> known[64][kMaxSplits + 1];   // the number + 1; 0: not asked yet
+    static std::atomic<int> known[kDevices];   // 0: not asked yet
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && (*out = known[dev]) > 0) return cudaSuccess;
+    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, WARPS>);
+    e = prepare_kernel(kern, 32 * WARPS, smem_for(Shape<D, INT8>::smem(WARPS), 1), nullptr);
+    if (e != cudaSuccess) return e;
+    e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), out);
+    if (e != cudaSuccess) return e;
+    if (*out < 1) return cudaErrorInvalidConfiguration;
+    if (dev < kDevices) known[dev] = *out;
+    return cudaSuccess;
+}
+
+// How many clusters of `splits` CTAs are resident at once on the current device with
+// at most `per_sm` CTAs on an SM (clusters stay within a GPC, so not every SM can
+// hold one); asked once.
+template <int D, bool INT8, bool WIDE, int WARPS>
+cudaError_t resident_clusters(int splits, int per_sm, int *out)
+{
+    constexpr int kPerSm = 32;
+    static std::atomic<int> known[kDevices][kMaxSplits + 1][kPerSm + 1];   // the number + 1; 0: not asked yet
     const auto kern = decode_window_kernel<D, INT8, WIDE, WARPS>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 64 && known[dev][splits] > 0) {
-        *out = known[dev][splits] - 1;
+    const bool keep = dev < kDevices && per_sm <= kPerSm;
+    if (keep && known[dev][splits][per_sm] > 0) {
+        *out = known[dev][splits][per_sm] - 1;
         return cudaSuccess;
     }
     if (splits > 8) {
@@ -753,12 +786,12 @@ cudaError_t resident_clusters(int splits, int *out)
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, 1, splits, nullptr);
+    cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, 1, splits, per_sm, nullptr);
     lc.attrs = at + 1;
     lc.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(out, kern, &lc);
     if (e != cudaSuccess) return e;
-    if (dev < 64) known[dev][splits] = *out + 1;
+    if (keep) known[dev][splits][per_sm] = *out + 1;
     return cudaSuccess;
 }
 
@@ -772,11 +805,9 @@ cudaError_t resident_clusters(int splits, int *out)
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
-    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, WARPS>);
-    int occupancy = 0;
-    cudaError_t e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), &occupancy);
+    cudaError_t e = resident_ctas<D, INT8, WIDE, WARPS>(&c->occupancy);
     if (e != cudaSuccess) return e;
-    c->places = (int64_t)sms * occupancy;
+    c->places = (int64_t)sms * c->occupancy;
     int64_t n = c->places / units;
     if (n > tiles / (2 * WARPS)) n = tiles / (2 * WARPS);
     if (n > kMaxSplits) n = kMaxSplits;
@@ -785,7 +816,7 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
         n = (tiles + share * WARPS - 1) / (share * WARPS);
         if (n == 1) break;
         int clusters = 0;
-        e = resident_clusters<D, INT8, WIDE, WARPS>((int)n, &clusters);
+        e = resident_clusters<D, INT8, WIDE, WARPS>((int)n, c->occupancy, &clusters);
         if (e != cudaSuccess) return e;
         if (clusters >= units) break;
     }
@@ -794,12 +825,26 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
     return cudaSuccess;
 }
 
+// CTAs that do not fill the machine are spread over it by shared memory that is
+// asked for but not used: placed as they come, behind a kernel that is draining,
+// some SMs take as many as they hold and others none.  Measured (windows of 1024,
+// 8 kv heads of 128, int8 pages, as placed / spread): 8 sequences 10.8 / 9.3 us,
+// 28: 19.7 / 17.0, 56: 29.7 / 25.5; bf16 pages, bound by memory, are 0 to 4 % faster.
 template <int D, bool INT8, bool WIDE, int WARPS>
-cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, cudaStream_t stream)
+cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cudaStream_t stream)
 {
     a.splits = c.splits;
+    const int64_t even = (units * c.splits + sms - 1) / sms;
+    int per_sm = even < c.occupancy ? (int)even : c.occupancy;
+    cudaError_t e;
+    for (; c.splits > 1 && per_sm < c.occupancy; ++per_sm) {
+        int clusters = 0;
+        e = resident_clusters<D, INT8, WIDE, WARPS>(c.splits, per_sm, &clusters);
+        if (e != cudaSuccess) return e;
+        if (clusters >= units) break;
+    }
     cudaLaunchAttribute at[2];
-    const cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, units, c.splits, stream);
+    const cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, WARPS>(at, units, c.splits, per_sm, stream);
     return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, WARPS>, a);
 }
 
@@ -818,7 +863,8 @@ cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, c
     e = choose<D, INT8, WIDE, 2>(units, tiles, sms, &c2);
     if (e != cudaSuccess) return e;
     const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
-    return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, stream) : launch_as<D, INT8, WIDE, 4>(a, c4, units, stream);
+    return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, sms, stream)
+                 : launch_as<D, INT8, WIDE, 4>(a, c4, units, sms, stream);
 }
 
 cudaError_t launch_window(WindowArgs &a, int32_t head_dim, bool int8, int32_t n_seqs, int sms, cudaStream_t stream)
