@@ -13,9 +13,9 @@
 // of 8 x 512 tokens 17.2 us = 5.9 TB/s, 86 % of the copy rate, of which 2.1 us are a
 // launch of one token; 64 tokens of one position each 2.4 us; 5 x 301 tokens into
 // int8 pages 10.2 us, 8 x 512 of them 23 us (4.0 TB/s: 110 registers a thread leave
-// 16 warps on an SM, whose instructions wait for one another).  Rows are loaded before the position is known, and sines
-// and cosines shared by the block: 22.8 -> 18.6 us on the chunk; read and written
-// once, so loads and stores are streamed: 18.6 -> 17.6.
+// 16 warps on an SM, whose instructions wait for one another).  Rows are loaded before
+// the position is known, and sines and cosines shared by the block: 22.8 -> 18.6 us on
+// the chunk; read and written once, so loads and stores are streamed: 18.6 -> 17.6.
 #include <math.h>
 
 #include "common.cuh"
