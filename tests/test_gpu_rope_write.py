@@ -100,6 +100,9 @@ CASES = [
     ([3, 70], 21, 4, 2, 64, 16, 48, False, True, False, dict()),
     ([0, 250], 150, 32, 8, 128, 16, 128, False, True, True, dict()),
     ([0, 11, 800], 200, 32, 8, 128, 16, 128, False, False, True, dict()),
+    ([40, 1], 320, 40, 8, 128, 16, 128, True, False, True, dict()),           # chunks: narrow blocks, two rounds
+    ([40, 1], 160, 40, 8, 128, 16, 128, False, True, True, dict()),
+    ([7], 700, 8, 8, 64, 16, 32, False, True, False, dict(scaling="linear", factor=2.0)),
 ]
 
 
@@ -149,6 +152,36 @@ def test_int8_values_are_those_of_the_page_write(P):
     p2, s2 = [p.cuda() for p in pools], [t.cuda() for t in scales]
     P.paged_kv_write_int8(k, v, p2[0], p2[1], s2[0], s2[1], tables.cuda(), start.cuda())
     assert st == 0 and torch.equal(p2[1].cpu(), gp[1]) and torch.equal(s2[1].cpu(), gs[1])
+
+
+def test_int8_codes_next_to_halves_and_of_odd_rows(P):
+    """Ties (x / scale exactly between two codes go to the even one), rows of one
+    element, of the smallest normal and of subnormal numbers, with infinities and NaN:
+    the codes are paged_kv_write_int8's, and keys turned by an angle of 0 too."""
+    hq, hkv, d = 2, 4, 64
+    qkv, tables, start, pools, scales = _inputs(16, [0], 12, hq, hkv, d, 16, True)
+    half = (torch.arange(d) - 31.5).to(torch.bfloat16)           # absmax 127: the scale is 1
+    half[5] = 127
+    tiny = torch.finfo(torch.bfloat16).tiny
+    one = torch.zeros(d, dtype=torch.bfloat16)
+    one[17] = -3.25
+    rows = [half, -half, half * 2 ** -20, half * 2 ** 40, one, half * tiny, half * tiny / 128, one * 0 + tiny,
+            torch.where(torch.arange(d) == 9, torch.inf, half.float()).to(torch.bfloat16),
+            torch.where(torch.arange(d) == 9, torch.nan, half.float()).to(torch.bfloat16)]
+    for i, x in enumerate(rows):
+        qkv[0, i, hq:] = x
+    rope = P.Rope(16, base=10000.0)
+    rope.phases.zero_()                                          # no turn at any position
+    _, gp, gs, st = _run(P, qkv, tables, start, pools, scales, hq, hkv, rope)
+    k, v = (t.contiguous().cuda() for t in qkv.split((hq, hkv, hkv), dim=2)[1:])
+    p2, s2 = [p.cuda() for p in pools], [t.cuda() for t in scales]
+    P.paged_kv_write_int8(k, v, p2[0], p2[1], s2[0], s2[1], tables.cuda(), start.cuda())
+    assert st == 0
+    assert torch.equal(p2[1].cpu(), gp[1]) and torch.equal(s2[1].cpu(), gs[1])
+    pos = torch.arange(8)                                        # the finite rows (0 times inf is NaN in a turn)
+    at = tables[0, 0].long() * 16 + pos
+    assert torch.equal(p2[0].cpu().view(-1, hkv, d)[at], gp[0].view(-1, hkv, d)[at])
+    assert torch.equal(s2[0].cpu().view(-1, hkv)[at], gs[0].view(-1, hkv)[at])
 
 
 @pytest.mark.parametrize("int8", [False, True])

@@ -139,6 +139,25 @@ def test_decode(P, lens, window, sinks, hkv, group, d, bs, int8):
 
 
 @pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("n", [3, 11, 20, 33, 40, 52, 66])
+def test_decode_batches(P, n, int8):
+    """Batches between one that leaves most of the machine idle and one that overfills
+    it: clusters of several sizes, CTAs of both, spread over the SMs or not."""
+    lens = [300 + 37 * (i % 10) for i in range(n)]
+    window, sinks, hkv, group, d = 500, 4, 8, 2, 128
+    pools, scales, tables, values = _paged(n, lens, window, sinks, 1, hkv, d, 16, int8)
+    q = torch.randn((n, hkv * group, d), generator=torch.Generator().manual_seed(n)).to(torch.bfloat16)
+    kp, vp, ks, vs, tab = _cuda(*pools, *scales, tables)
+    lse = torch.empty((n, hkv * group), device="cuda")
+    plan = P.WindowDecodePlan(kp, vp, tab, torch.tensor(lens, dtype=torch.int32).cuda(), d ** -0.5, hkv * group, window,
+                              sinks, k_scales=ks, v_scales=vs, lse_out=lse)
+    out = plan.run(q.cuda()).clone()
+    _check_decode(out, lse, q, values, lens, window, sinks, hkv, d ** -0.5, int8)
+    for _ in range(3):                       # calls behind one another
+        assert torch.equal(plan.run(q.cuda()), out)
+
+
+@pytest.mark.parametrize("int8", [False, True])
 def test_decode_agrees_with_the_unwindowed_decode(P, int8):
     """A window of the whole context: the split-KV decode's result within both tolerances."""
     lens, hkv, group, d, bs = [700, 33, 256], 4, 4, 128, 16
