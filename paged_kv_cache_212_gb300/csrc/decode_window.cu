@@ -722,6 +722,7 @@ struct Choice {
     int splits = 0, occupancy = 0;   // CTAs of a unit, CTAs that an SM holds
     int64_t places = 0;      // CTAs that are resident at once
     int64_t room = 0;        // units that the machine's rounds of this launch have room for
+    int64_t share = 0;       // the most tiles of a warp
 };
 
 // Dynamic shared memory with which an SM (228 KB, 1 KB of them kept back for each
@@ -806,11 +807,12 @@ cudaError_t resident_clusters(int splits, int per_sm, int *out)
 
 // The most CTAs per unit with which all CTAs of WARPS warps are resident at once
 // and every warp keeps two tiles of the longest window; then as few as leave the
-// longest share of a warp as it is.  Measured (windows of 1024, 8 kv heads of 128,
-// bf16 / int8 pages where not said): two sequences of 16 K visible tokens take 26 us
+// longest share of a warp as it is.  Measured (8 kv heads of 128, windows of 1024
+// where not said): two sequences of 16 K visible tokens over bf16 pages take 26 us
 // with the 13 CTAs per unit that are resident at once and 40 with 16; four sequences
-// over int8 pages 9.9 us with the 8 CTAs that two tiles a warp allow, 8.2 with the 6
-// that give the longest share, three tiles, as well, and 12.0 with one tile a warp.
+// over int8 pages 9.9 us with the 8 CTAs (of 4 warps) that two tiles a warp allow, 8.2
+// with the 6 that give the longest share, three tiles, as well, and 12.0 with one
+// tile a warp.
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
@@ -830,6 +832,7 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
         if (clusters >= units) break;
     }
     c->splits = n < 1 ? 1 : (int)n;
+    c->share = (tiles + c->splits * WARPS - 1) / (c->splits * WARPS);
     c->room = (units * c->splits + c->places - 1) / c->places * c->places / c->splits;
     return cudaSuccess;
 }
@@ -857,20 +860,35 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cu
     return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, WARPS>, a);
 }
 
-// CTAs of 4 warps, or of 2 where their rounds leave less of the machine idle: by a
-// fifth, or by anything once the units are more than the larger CTAs' places.
-// Measured (4 warps / 2 warps; windows of 1024, 8 kv heads of 128): bf16 pages, 32
-// sequences 23.6 / 24.7 us, 40: 37.9 / 30.3, 64: 45.4 / 42.9, 80: 61.7 / 66.4,
-// 128: 87.5 / 82.3; int8 pages, 12 sequences 11.1 / 11.5, 48: 29.4 / 24.5,
-// 64: 31.0 / 38.6, 80: 43.2 / 39.2, 128: 52.3 / 68.4.
+// CTAs of 4 warps, of 2 or of 8.
+//
+// Of 2 where their rounds leave less of the machine idle: by a fifth, or by anything
+// once the units are more than the larger CTAs' places.  Measured (4 warps / 2 warps;
+// windows of 1024, 8 kv heads of 128): bf16 pages, 32 sequences 23.6 / 24.7 us,
+// 40: 37.9 / 30.3, 64: 45.4 / 42.9, 80: 61.7 / 66.4, 128: 87.5 / 82.3; int8 pages,
+// 12 sequences 11.1 / 11.5, 48: 29.4 / 24.5, 64: 31.0 / 38.6, 80: 43.2 / 39.2,
+// 128: 52.3 / 68.4.
+//
+// Of 8, for units that are all resident, where that shortens the longest share of a
+// warp (a cluster has 16 CTAs at most), where it needs no cluster and CTAs of 4 do, or
+// where there are more CTAs of 4 than SMs anyway.  Measured (4 warps / 8 warps; window
+// and first tokens together): bf16 pages, 4 sequences of 256 visible tokens 5.4 / 5.0
+// us, 12: 6.4 / 5.4; 1024 tokens, one sequence 5.7 / 6.1, 4: 7.4 / 6.4, 16: 15.0 / 14.1;
+// 16 K tokens, one 19.7 / 17.4, two 26.4 / 27.3; int8 pages, 1024 tokens, 4: 12.1 / 7.1,
+// 16: 13.9 / 11.6; 16 K, one 21.1 / 16.0, two 27.1 / 24.2.
 template <int D, bool INT8, bool WIDE>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
-    Choice c4, c2;
+    Choice c4, c2, c8;
     cudaError_t e = choose<D, INT8, WIDE, 4>(units, tiles, sms, &c4);
     if (e != cudaSuccess) return e;
     e = choose<D, INT8, WIDE, 2>(units, tiles, sms, &c2);
     if (e != cudaSuccess) return e;
+    e = choose<D, INT8, WIDE, 8>(units, tiles, sms, &c8);
+    if (e != cudaSuccess) return e;
+    const bool alone = c8.splits == 1 && c4.splits > 1 && c8.share <= c4.share;
+    if (units <= c8.places && (alone || c8.share < c4.share || (units * c4.splits > sms && c8.room <= c4.room)))
+        return launch_as<D, INT8, WIDE, 8>(a, c8, units, sms, stream);
     const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
     return small ? launch_as<D, INT8, WIDE, 2>(a, c2, units, sms, stream)
                  : launch_as<D, INT8, WIDE, 4>(a, c4, units, sms, stream);
