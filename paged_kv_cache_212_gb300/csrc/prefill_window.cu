@@ -24,18 +24,25 @@
 //
 // Half units.  What is left over when the units are dealt out to the CTAs is cut into
 // units of one query tile where that gives every CTA at most one more (512 units on
-// 152 CTAs: three rounds and 112 halves in place of four rounds; whole units / halves:
-// 64 units 22.5 / 20.6 us, 192: 42.7 / 41.5, 320: 60.1 / 58.5, 512: 78.6 / 77.6).
+// 152 CTAs: three rounds and 112 halves in place of four rounds).  In a half unit both
+// softmax warpgroups work on the one query tile, each on 64 of a tile's 128 keys; they
+// exchange row maxima through shared memory, and S goes to the columns of the two query
+// tiles in turn, so that the next S is computed during a softmax.  A tile takes 1.03 us
+// there (1.47 with one warpgroup); 64 units take 22.5 us whole, 16.4 as halves,
+// 192: 42.7 / 37.8, 320: 60.1 / 55.1, 512: 78.6 / 74.1.  Sums of a row are kept over the
+// first and the last 64 keys of its tiles in whole units too, so that a row has the
+// same bits in both and its result does not depend on the batch.
 //
 // O goes out from registers, a row of head_dim values a thread: the shared memory
 // that could stage it holds the next unit's tiles by then.
 //
 // Measured (32 query and 8 kv heads of 128, kernels back to back).  8 x 512 tokens,
-// window 1024, prefixes up to 8 K: 77.9 us, 813 TFLOP/s of products that the mask asks
-// for: a tile of 128 keys takes 1.56 us (1.63 PFLOP/s on 152 SMs) and a unit 4.1 us
-// beside its nine (masked tiles, O, the hand-over), three rounds of whole units and one
-// of halves, which take 16 us to a whole one's 18.  A prompt of 4095 tokens, window
-// 1000: 68.2 us, 876 TFLOP/s.  2 x 37 tokens: 8.1 us, the latency of one tile's chain.
+// window 1024: 74.1 us with prefixes of 2 to 8 K, and 77.9 with prefixes of 0 to 8 K whose
+// last sequence is the shortest (the halves are small ones then), 813 TFLOP/s of
+// products that the mask asks for: a tile of 128 keys takes 1.56 us (1.63 PFLOP/s on 152
+// SMs) and a unit 4.1 us beside its nine (masked tiles, O, the hand-over).  A prompt of
+// 4095 tokens, window 1000: 67.4 us, 886 TFLOP/s.  2 x 37 tokens: 7.7 us, the latency of
+// a launch and of one tile's chain.
 #include <math.h>
 
 #include "common.cuh"
@@ -222,6 +229,129 @@ __device__ __forceinline__ void st_global_32(void *dst, const uint32_t (&w)[8])
                  : "memory");
 }
 
+// ---- a row's scores: NC keys of a tile, from column col0 on -----------------------
+
+// The scores of keys that the row does not see become -inf (exp2 gives 0).  The seen
+// keys as bits, 32 at a time: those of the window (behind n_mixed columns: the same,
+// skip further on) and the first tokens up to the row.
+template <int NC>
+__device__ __forceinline__ void mask_scores(uint32_t (&sv)[NC], int32_t col0, int32_t key_base, int32_t qpos, int32_t n_mixed,
+                                            int32_t skip, int32_t window, int32_t sinks)
+{
+    const int32_t back = qpos - key_base + 1, first = min(sinks - key_base, back);
+    const int32_t back_w = n_mixed > 0 ? back - skip : back;
+    const int32_t low = back < window ? 0 : back - window;
+    const int32_t low_w = back_w < window ? 0 : back_w - window;
+#pragma unroll
+    for (int i0 = 0; i0 < NC; i0 += 32) {
+        const int32_t at = col0 + i0;
+        uint32_t seen = bits_below(back_w - at) & ~bits_below(low_w - at);
+        if (n_mixed > 0) {
+            const uint32_t mixed = bits_below(n_mixed - at);
+            seen = (seen & ~mixed) | (mixed & bits_below(back - at) & ~bits_below(low - at));
+        }
+        seen |= bits_below(first - at);
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
+    }
+}
+
+// The largest score: three-input maxima over four independent chains.
+template <int NC>
+__device__ __forceinline__ float largest(const uint32_t (&sv)[NC])
+{
+    float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NC; i += 8) {
+        a0 = fmax3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
+        a1 = fmax3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
+        a2 = fmax3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
+        a3 = fmax3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
+    }
+    return fmax3(a0, a1, fmaxf(a2, a3));
+}
+
+// The running maximum m (log2 units) moved by a tile's; the factor on what was summed.
+__device__ __forceinline__ float move_maximum(float &m, float mx)
+{
+    float alpha = 1.f;
+    if (m == -INFINITY) {
+        m = mx;          // -inf until the first tile with a visible key
+    } else if (mx > m + kRescaleThreshold) {
+        alpha = fast_exp2(m - mx);
+        m = mx;
+    }
+    return alpha;
+}
+
+// Probabilities of 64 scores from sv[I0] on (packed two-lane FMA for the exponent
+// arguments), as bf16 pairs into 32 TMEM columns from taddr on; their sum.
+template <int I0, int NC>
+__device__ __forceinline__ float probabilities64(const uint32_t (&sv)[NC], float2 sc2, float2 nm2, uint32_t taddr)
+{
+    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            const int k = I0 + i * 32 + 2 * e;
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), sc2, nm2);
+            const float2 ee = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            if (e & 1)
+                lb = __fadd2_rn(lb, ee);
+            else
+                la = __fadd2_rn(la, ee);
+            pk[e] = pack_bf16x2(ee.x, ee.y);
+        }
+        tmem_st16_async(taddr + i * 16, pk);
+    }
+    return (la.x + la.y) + (lb.x + lb.y);
+}
+
+// The O of a row from taddr on, 32 columns at a time, times alpha.
+template <int COLS>
+__device__ __forceinline__ void rescale_o(uint32_t taddr, float alpha)
+{
+#pragma unroll 1
+    for (int i = 0; i < COLS / 32; ++i) {
+        uint32_t v[32];
+        tmem_ld32_async(taddr + i * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+        tmem_st32(taddr + i * 32, v);
+    }
+}
+
+// The O of a row from taddr on, times inv, to out where the row is live.
+template <int COLS>
+__device__ __forceinline__ void write_o(uint32_t taddr, float inv, bool live, bool wide, __nv_bfloat16 *out)
+{
+#pragma unroll
+    for (int i = 0; i < COLS / 32; ++i) {
+        uint32_t v[32];
+        tmem_ld32_async(taddr + i * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+            uint32_t x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                x[e] = pack_bf16x2(__uint_as_float(v[16 * q2 + 2 * e]) * inv, __uint_as_float(v[16 * q2 + 2 * e + 1]) * inv);
+            if (!live) continue;
+            if (wide) {
+                st_global_32(out + i * 32 + q2 * 16, x);
+            } else {
+                *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16 + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+        }
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                      const __grid_constant__ CUtensorMap k_map,
@@ -259,6 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     // loads a unit's Q (unit i at i % 4: by then everyone is past unit i - 3), and [4]
     // of warps 8-11, which run ahead of that.
     Unit *unit_s = reinterpret_cast<Unit *>(bars + 32);
+    // Half units: a warp of one softmax warpgroup meets the one with the same rows of the
+    // other; their maxima and sums go through the second Q tile, which a half unit leaves.
+    __shared__ uint64_t pair_bar[4];
+    float *pair_s = reinterpret_cast<float *>(q_s + kQTile);   // [2][2 warpgroups][128 rows]
     const int n_mine = (p.n_units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // units of this CTA
     static_assert(2 + 2 * (NK + NV) + 3 * kNQ + 3 <= 32, "barriers fit their 256 bytes");
 
@@ -285,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -424,9 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             const uint32_t q_addr = smem_u32(q_s) >> 4, k_addr = smem_u32(k_ring) >> 4, v_addr = smem_u32(v_ring) >> 4;
             const uint64_t kd = umma_desc_sw128(0, 16, 1024), vd = umma_desc_sw128(0, 2048, 1024);
             const uint32_t k_hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, v_hi = (uint32_t)(vd >> 32), v_lo = (uint32_t)vd;
-            // S_t = Q_t K^T of the K in a ring slot, then the commit that hands it to
-            // warpgroup t; it covers the product issued before it, too
-            auto issue_s = [&](int t, int slot) {
+            // S = Q_t K^T of the K in a ring slot, in the S columns of query tile `at`, then
+            // the commit that hands it on; it covers the product issued before it, too
+            auto issue_s = [&](int t, int at, int slot) {
                 constexpr int STEPS = D / 16;
                 uint32_t qa[STEPS], kb[STEPS];
 #pragma unroll
@@ -434,15 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     qa[k] = k_lo | (q_addr + (t * kQTile + (k / 4) * kQPanel + (k % 4) * 32) / 16);
                     kb[k] = k_lo | (k_addr + (slot * kSlotBytes + (k / 4) * kKVPanel + (k % 4) * 32) / 16);
                 }
-                mma_ss<STEPS>(leader, tmem + t * kTileCols, k_hi, qa, kb, idesc_s);
-                commit_one(leader, &s_full[t]);
+                mma_ss<STEPS>(leader, tmem + at * kTileCols, k_hi, qa, kb, idesc_s);
+                commit_one(leader, &s_full[at]);
             };
-            // O_t += P_t V: A = P (TMEM), B = V (MN-major: 16-key group k at k * kVGroup)
-            auto issue_o = [&](int t, int slot, bool accumulate) {
+            // O_t += P V: A = P (TMEM, in the columns of query tile `at`), B = V (MN-major:
+            // 16-key group k at k * kVGroup)
+            auto issue_o = [&](int t, int at, int slot, bool accumulate) {
                 uint32_t vb[kTN / 16];
 #pragma unroll
                 for (int k = 0; k < kTN / 16; ++k) vb[k] = v_lo | (v_addr + (slot * kSlotBytes + k * kVGroup) / 16);
-                mma_ts<kTN / 16>(leader, tmem + t * kTileCols + kOCol, tmem + t * kTileCols, v_hi, vb, idesc_o,
+                mma_ts<kTN / 16>(leader, tmem + t * kTileCols + kOCol, tmem + at * kTileCols, v_hi, vb, idesc_o,
                                  accumulate ? 1u : 0u);
             };
             // The tile at hand is the last of its unit's when left is 1.  The S of the next tile
@@ -455,26 +591,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 n_kt = tiles_of(0);
                 tc_fence_after();
 #pragma unroll 1
-                for (int t = 0; t < (is_half(0) ? 1 : kNQ); ++t) issue_s(t, 0);
+                for (int t = 0; t < (is_half(0) ? 1 : kNQ); ++t) issue_s(t, t, 0);
                 commit_one(leader, &k_empty[0]);
                 if (n_kt == 1) commit_one(leader, q_empty);
             }
             int units = 0, left = n_kt;
             uint32_t phase = 0;                   // of p_full
-            while (ok) {
-                const bool first = left == n_kt, last = left == 1, half = is_half(units);
-                if (++ks == NK) {                 // the next tile's K
+            auto next_k = [&]() {                 // the next tile's K
+                if (++ks == NK) {
                     ks = 0;
                     k_phase ^= 1;
                 }
+            };
+            auto next_v = [&]() {
+                phase ^= 1;
+                if (++vs == NV) {
+                    vs = 0;
+                    v_phase ^= 1;
+                }
+            };
+            bool whole = !is_half(0);
+            while (ok && whole) {
+                const bool first = left == n_kt, last = left == 1;
+                next_k();
                 ok = wait(&v_full[vs], v_phase);
 #pragma unroll
                 for (int t = 0; t < kNQ; ++t) {
-                    if (!ok || (t > 0 && half)) break;
+                    if (!ok) break;
                     ok = wait(&p_full[t], phase);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_o(t, vs, !first);
+                    issue_o(t, t, vs, !first);
                     if (last) {
                         commit_one(leader, &o_done[t]);
                     } else {
@@ -483,28 +630,52 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                             if (!ok) break;
                             tc_fence_after();
                         }
-                        issue_s(t, ks);
+                        issue_s(t, t, ks);
                     }
                 }
                 if (!ok) break;
                 commit_one(leader, &v_empty[vs]);
                 if (last) {
                     if (++units == n_mine) break;
+                    whole = !is_half(units);
                     ok = wait(&k_full[ks], k_phase) && wait(q_full, units & 1);
                     if (!ok) break;
                     n_kt = tiles_of(units);
                     tc_fence_after();
                     // (S_t's columns hold a P that the tensor core reads before)
 #pragma unroll 1
-                    for (int t = 0; t < (is_half(units) ? 1 : kNQ); ++t) issue_s(t, ks);
+                    for (int t = 0; t < (whole ? kNQ : 1); ++t) issue_s(t, t, ks);
                     left = n_kt + 1;
                 }
                 commit_one(leader, &k_empty[ks]);
                 if (--left == 1) commit_one(leader, q_empty);   // S of the unit's last tile is issued
-                phase ^= 1;
-                if (++vs == NV) {
-                    vs = 0;
-                    v_phase ^= 1;
+                next_v();
+            }
+            // A half unit (the last): tile j's S, then its P, in the columns of query tile
+            // j & 1, so that the next S is computed while the softmax of this one runs
+            if (ok && units < n_mine) {
+                auto issue_next = [&](int j) {
+                    next_k();
+                    ok = wait(&k_full[ks], k_phase);
+                    if (!ok) return;
+                    tc_fence_after();
+                    issue_s(0, j & 1, ks);
+                    commit_one(leader, &k_empty[ks]);
+                };
+                if (n_kt > 1) issue_next(1);
+#pragma unroll 1
+                for (int j = 0; ok && j < n_kt; ++j) {
+                    ok = wait(&v_full[vs], v_phase) && wait(&p_full[0], phase) && wait(&p_full[1], phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_o(0, j & 1, vs, j > 0);
+                    if (j + 1 == n_kt) {
+                        commit_one(leader, &o_done[0]);
+                        commit_one(leader, &o_done[1]);
+                    }
+                    commit_one(leader, &v_empty[vs]);
+                    next_v();
+                    if (j + 2 < n_kt) issue_next(j + 2);
                 }
             }
             if (!ok) {
@@ -518,18 +689,45 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
-        // ===================== softmax warpgroups: row r of tile qt = TMEM lane r =====================
+        // ===================== softmax warpgroups: row r = TMEM lane r =====================
         const int qt = warp / 4;
         const int r = threadIdx.x % kTM;
-        const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16) + qt * kTileCols;
+        const uint32_t lanes = tmem + ((uint32_t)((warp % 4) * 32) << 16);
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
         // (the unit stays in shared memory: a row's scores need the registers)
         int c = 0;                               // tiles so far
         bool ok = true;
-        for (int units = 0; units < n_mine && !(qt > 0 && is_half(units)); ++units) {
+        // V rows of a tile that were loaded but that no query of the unit sees may hold
+        // anything.  There are some past the last key (tail) and at places [sinks, w_lo -
+        // skip), between the first tokens and the window (gap).
+        auto has_tail = [&](const volatile Unit &w, bool last) { return last && (w.n_places & 15) != 0; };
+        auto has_gap = [&](const volatile Unit &w, int32_t place0, int32_t skip) {
+            return w.w_lo > p.sinks && place0 < w.w_lo - skip && place0 + kTN > p.sinks;
+        };
+        // They are zeroed once V has landed (both warpgroups write the same zeros).
+        auto clean_v = [&](const volatile Unit &w, int32_t place0, bool tail, bool gap) -> bool {
+            const int32_t skip = w.skip, n_places = w.n_places;
+            if (!__all_sync(0xffffffffu, mbar_wait(&v_full[c % NV], (c / NV) & 1, abort_flag, p.wait_ns))) return false;
+            uint8_t *vs = v_ring + (c % NV) * kSlotBytes;
+            auto zero_rows = [&](int from, int stop) {
+                for (int i = r; i < (stop - from) * PANELS * 8; i += kTM) {
+                    const int row = from + i / (PANELS * 8), pc = i % (PANELS * 8);
+                    *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 + swz128(row % 16, pc % 8)) =
+                        make_uint4(0, 0, 0, 0);
+                }
+            };
+            if (tail) zero_rows(n_places - place0, ((n_places + 15) & ~15) - place0);
+            if (gap) zero_rows(max(p.sinks - place0, 0), min(w.w_lo - skip - place0, kTN));
+            fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
+            return true;
+        };
+        int units = 0;
+        for (; units < n_mine && !is_half(units); ++units) {
             const volatile Unit &w = unit_s[units & 3];
+            const uint32_t lane_base = lanes + qt * kTileCols;   // of this warpgroup's query tile
             int n_kt = 1;                        // read with the unit's first tile
             int32_t pos = 0, qpos = 0;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l0 = 0.f, l1 = 0.f;             // sums over the first and last 64 keys of the tiles
             for (int j = 0; j < n_kt; ++j, ++c) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&s_full[qt], c & 1, abort_flag, p.wait_ns));
                 if (!ok) break;
@@ -550,106 +748,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 // rows whose keys in this tile are all visible need no per-key test
                 const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos || n_mixed > 0 ||
                                                                 (key_base <= qpos - p.window && key_base + kTN > p.sinks));
-                // V rows of loaded groups that no query sees (past the last key; places
-                // [sinks, w_lo - skip), between the first tokens and the window)
-                const bool tail = j == n_kt - 1 && (w.n_places & 15) != 0;
-                const bool gap = w.w_lo > p.sinks && place0 < w.w_lo - skip && place0 + kTN > p.sinks;
+                const bool tail = has_tail(w, j == n_kt - 1), gap = has_gap(w, place0, skip);
                 tmem_wait_ld();
-                if (masked) {
-                    // The seen keys of the tile as bits, 32 at a time: those of the window
-                    // (behind n_mixed: the same, skip further on) and the first tokens up to
-                    // the row; the scores of the others become -inf (exp2 gives 0).
-                    const int32_t back = qpos - key_base + 1, first = min(p.sinks - key_base, back);
-                    const int32_t back_w = n_mixed > 0 ? back - skip : back;
-                    const int32_t low = back < p.window ? 0 : back - p.window;
-                    const int32_t low_w = back_w < p.window ? 0 : back_w - p.window;
-#pragma unroll
-                    for (int i0 = 0; i0 < kTN; i0 += 32) {
-                        uint32_t seen = bits_below(back_w - i0) & ~bits_below(low_w - i0);
-                        if (n_mixed > 0) {
-                            const uint32_t mixed = bits_below(n_mixed - i0);
-                            seen = (seen & ~mixed) | (mixed & bits_below(back - i0) & ~bits_below(low - i0));
-                        }
-                        seen |= bits_below(first - i0);
-                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
-                    }
-                }
-                // row maximum: three-input max over four independent chains
-                float mx;
-                {
-                    float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < kTN; i += 8) {
-                        a0 = fmax3(a0, __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
-                        a1 = fmax3(a1, __uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3]));
-                        a2 = fmax3(a2, __uint_as_float(sv[i + 4]), __uint_as_float(sv[i + 5]));
-                        a3 = fmax3(a3, __uint_as_float(sv[i + 6]), __uint_as_float(sv[i + 7]));
-                    }
-                    mx = fmax3(a0, a1, fmaxf(a2, a3)) * p.scale_log2;
-                }
-                float alpha = 1.f;
-                if (m == -INFINITY) {
-                    m = mx;          // -inf until the first tile with a visible key
-                } else if (mx > m + kRescaleThreshold) {
-                    alpha = fast_exp2(m - mx);
-                    m = mx;
-                }
+                if (masked) mask_scores(sv, 0, key_base, qpos, n_mixed, skip, p.window, p.sinks);
+                const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
                 // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
                 // commit came after it
-                if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) {
-#pragma unroll 1
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t v[32];
-                        tmem_ld32_async(lane_base + kOCol + i * 32, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
-                        tmem_st32(lane_base + kOCol + i * 32, v);
-                    }
-                }
-                // probabilities (packed two-lane FMA for the exponent arguments) and two
-                // packed partial row sums; P (bf16 pairs) over S's first 64 columns, each
-                // 16-column store after the S columns it covers were read
-                const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+                if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
+                // columns it covers were read
                 const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < kTN / 32; ++i) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int k = i * 32 + 2 * e;
-                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), sc2, nm2);
-                        const float2 ee = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-                        if (e & 1)
-                            lb = __fadd2_rn(lb, ee);
-                        else
-                            la = __fadd2_rn(la, ee);
-                        pk[e] = pack_bf16x2(ee.x, ee.y);
-                    }
-                    tmem_st16_async(lane_base + i * 16, pk);
-                }
-                l = l * alpha + ((la.x + la.y) + (lb.x + lb.y));
+                l0 = l0 * alpha + probabilities64<0>(sv, sc2, nm2, lane_base);
+                l1 = l1 * alpha + probabilities64<64>(sv, sc2, nm2, lane_base + 32);
                 tmem_wait_st();
-                // those rows may hold anything; zero them once V has landed (both
-                // warpgroups write the same zeros)
                 if (tail || gap) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&v_full[c % NV], (c / NV) & 1, abort_flag, p.wait_ns));
+                    ok = clean_v(w, place0, tail, gap);
                     if (!ok) break;
-                    uint8_t *vs = v_ring + (c % NV) * kSlotBytes;
-                    auto zero_rows = [&](int from, int stop) {
-                        for (int i = r; i < (stop - from) * PANELS * 8; i += kTM) {
-                            const int row = from + i / (PANELS * 8), pc = i % (PANELS * 8);
-                            *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 +
-                                                       swz128(row % 16, pc % 8)) = make_uint4(0, 0, 0, 0);
-                        }
-                    };
-                    if (tail) zero_rows(w.n_places - place0, ((w.n_places + 15) & ~15) - place0);
-                    if (gap) zero_rows(max(p.sinks - place0, 0), min(w.w_lo - skip - place0, kTN));
-                    fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -662,31 +776,89 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             // row r of O, normalised.  (O is read before this warp's next P is handed over,
             // and the next unit's first product into O comes after that.)
             const bool live = pos <= w.p_last;
-            const float inv = 1.f / l;
+            const float l = l0 + l1;
             const int64_t out_row = ((int64_t)w.s * p.chunk + pos) * p.n_q_heads + w.kvh * G + r % G;
-            __nv_bfloat16 *out = p.out + out_row * D;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t v[32];
-                tmem_ld32_async(lane_base + kOCol + i * 32, v);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q2 = 0; q2 < 2; ++q2) {
-                    uint32_t x[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = pack_bf16x2(__uint_as_float(v[16 * q2 + 2 * e]) * inv, __uint_as_float(v[16 * q2 + 2 * e + 1]) * inv);
-                    if (!live) continue;
-                    if (p.wide_out) {
-                        st_global_32(out + i * 32 + q2 * 16, x);
-                    } else {
-                        *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16) = make_uint4(x[0], x[1], x[2], x[3]);
-                        *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16 + 8) = make_uint4(x[4], x[5], x[6], x[7]);
-                    }
-                }
-            }
+            write_o<D>(lane_base + kOCol, 1.f / l, live, p.wide_out, p.out + out_row * D);
             if (live && p.lse_out) p.lse_out[out_row] = (m + __log2f(l)) * 0.69314718055994531f;
             tc_fence_before();
+        }
+        // A half unit: both warpgroups work on its query tile, each on 64 keys of a tile and
+        // then on half of O; maxima and sums meet as they do in a row of a whole unit, so the
+        // bits are the same.
+        if (ok && units < n_mine) {
+            const volatile Unit &w = unit_s[units & 3];
+            uint64_t *pair = &pair_bar[warp % 4];
+            // hands x to the other warpgroup's thread of this row and takes its x: the n-th time
+            auto swap = [&](int n, float x) -> float {
+                float *at = pair_s + (n & 1) * 2 * kTM + r;
+                at[qt * kTM] = x;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pair);
+                ok = __all_sync(0xffffffffu, mbar_wait(pair, n & 1, abort_flag, p.wait_ns));
+                tc_fence_after();
+                return at[(1 - qt) * kTM];
+            };
+            const int c0 = c;
+            int n_kt = 1;
+            int32_t pos = 0, qpos = 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n_kt; ++j, ++c) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (c0 + j / 2) & 1, abort_flag, p.wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t s_base = lanes + (j & 1) * kTileCols;
+                uint32_t sv[kTN / 2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) tmem_ld32_async(s_base + qt * 64 + i * 32, sv + i * 32);
+                if (j == 0) {
+                    n_kt = w.n_kt;
+                    pos = w.p0 + r / G;
+                    qpos = w.P + pos;
+                }
+                const int32_t place0 = j * kTN, n_first = w.n_first, skip = w.skip;
+                const int32_t key_base = place0 + (place0 >= n_first ? skip : 0);
+                const int n_mixed = skip > 0 && place0 < n_first ? min(n_first - place0, kTN) : 0;
+                const bool masked = __any_sync(0xffffffffu, key_base + kTN - 1 > qpos || n_mixed > 0 ||
+                                                                (key_base <= qpos - p.window && key_base + kTN > p.sinks));
+                const bool tail = has_tail(w, j == n_kt - 1), gap = has_gap(w, place0, skip);
+                tmem_wait_ld();
+                if (masked) mask_scores(sv, qt * 64, key_base, qpos, n_mixed, skip, p.window, p.sinks);
+                // (behind it both warps have read S, which P is written over)
+                const float mine = largest(sv), other = swap(j, mine);
+                if (!ok) break;
+                const float alpha = move_maximum(m, fmaxf(mine, other) * p.scale_log2);
+                if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) {
+                    // the P V of the tile before this one frees its V
+                    ok = __all_sync(0xffffffffu, mbar_wait(&v_empty[(c - 1) % NV], ((c - 1) / NV) & 1, abort_flag, p.wait_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    rescale_o<D / 2>(lanes + kOCol + qt * (D / 2), alpha);
+                }
+                const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                l = l * alpha + probabilities64<0>(sv, sc2, nm2, s_base + qt * 32);
+                tmem_wait_st();
+                if (tail || gap) {
+                    ok = clean_v(w, place0, tail, gap);
+                    if (!ok) break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[qt]);
+            }
+            if (ok) {
+                const float other = swap(n_kt, l);
+                l = qt == 0 ? l + other : other + l;
+            }
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&o_done[qt], units & 1, abort_flag, p.wait_ns));
+            if (ok) {
+                tc_fence_after();
+                const bool live = pos <= w.p_last;
+                const int64_t out_row = ((int64_t)w.s * p.chunk + pos) * p.n_q_heads + w.kvh * G + r % G;
+                write_o<D / 2>(lanes + kOCol + qt * (D / 2), 1.f / l, live, p.wide_out, p.out + out_row * D + qt * (D / 2));
+                if (live && qt == 0 && p.lse_out) p.lse_out[out_row] = (m + __log2f(l)) * 0.69314718055994531f;
+                tc_fence_before();
+            }
         }
         if (!ok) {
             if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);

@@ -362,6 +362,35 @@ def test_prefill_of_many_units_and_odd_addresses(P):
         assert torch.equal(one[0], out[s]), s
 
 
+@pytest.mark.parametrize("d,hkv,group,chunk,window,sinks", [(128, 8, 4, 512, 500, 4), (64, 4, 2, 300, 133, 20),
+                                                           (128, 2, 8, 130, 77, 0), (128, 1, 16, 70, 2 ** 31 - 1, 0)])
+def test_prefill_rows_do_not_depend_on_the_batch(P, d, hkv, group, chunk, window, sinks):
+    """A row's bits are the same whatever else is in the call (and so whether its unit
+    was computed whole or as two halves)."""
+    gen = torch.Generator().manual_seed(chunk)
+    n, bs = 20, 16
+    prefix = torch.randint(0, 1500, (n,), generator=gen, dtype=torch.int32)
+    width = (1500 + chunk) // bs + 1
+    pools = [torch.randn((n * width + 1, bs, hkv, d), generator=gen).to(torch.bfloat16).cuda() for _ in range(2)]
+    tables = torch.randperm(n * width, generator=gen).to(torch.int32).view(n, width).cuda()
+    # large scores, so that maxima move
+    q = (torch.randn((n, chunk, hkv * group, d), generator=gen) * 4).to(torch.bfloat16).cuda()
+    prefix = prefix.cuda()
+
+    def call(a, b):
+        lse = torch.empty((b - a, chunk, hkv * group), device="cuda")
+        out = P.paged_prefill_attention_window(q[a:b].contiguous(), *pools, tables[a:b].contiguous(), prefix[a:b].contiguous(),
+                                               d ** -0.5, window, sinks, lse_out=lse)
+        return out, lse
+
+    whole = call(0, n)
+    assert torch.isfinite(whole[0].float()).all()
+    for m in (1, 2, 3, 5, 11):
+        for a in range(0, n - m, m + 2):
+            for x, y in zip(call(a, a + m), whole):
+                assert torch.equal(x, y[a:a + m]), (m, a)
+
+
 def test_prefill_wait_runs_out_then_recovers(P):
     """With a limit of 1 ns on its pipeline waits the kernel reports the timeout and
     returns; the next call on the stream is right."""
