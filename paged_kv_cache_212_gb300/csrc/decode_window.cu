@@ -34,11 +34,11 @@
 // scales are.
 //
 // Measured (one launch among others; 8 kv heads of 128, window 1024, 4 first tokens).
-// 64 sequences, bf16 pages, 32 query heads: 41.6 us = 6.25 TB/s, 92 % of the copy rate;
-// memory bounds it.  The same over int8 pages with 64 query heads: 31.5 us, 4.3 TB/s;
+// 64 sequences, bf16 pages, 32 query heads: 41.4 us = 6.28 TB/s, 92 % of the copy rate;
+// memory bounds it.  The same over int8 pages with 64 query heads: 30.3 us, 4.5 TB/s;
 // half of the issue slots are taken and the rest is the latency of an SM's 16 warps.
-// Two sequences of 16 K visible tokens, 64 query heads: 26.4 us, 5.1 TB/s.  Four
-// sequences of 68 visible tokens (2 kv heads of 64): 2.8 us, a launch and three
+// Two sequences of 16 K visible tokens, 64 query heads: 26.5 us, 5.1 TB/s.  Four
+// sequences of 68 visible tokens (2 kv heads of 64): 2.7 us, a launch and three
 // dependent reads.
 #include <math.h>
 
@@ -92,7 +92,11 @@ struct Shape {
     // 64 sequences, bf16 pages: 44.5 us with 2, 40.9 with 3, 52.2 with 4 (fewer CTAs are resident)
     static constexpr int kStages = 3;
     static constexpr int kAcc = D + 4;                            // floats per staged row
-    static constexpr size_t smem(int warps) { return 256 + (size_t)warps * (kStages * kStage + 2 * kRow); }
+    static constexpr int kQRow = 2 * D + 16;                      // bytes of a staged query row of 16-bit elements
+    static constexpr int kQueries = (INT8 ? 1 : 2) * kHeads * kQRow;   // the queries and (bf16) their remainders
+    static constexpr bool kShared = INT8;                         // staged once for all warps of a CTA
+    static_assert(kShared || kStage >= kQueries, "a free stage holds them");
+    static constexpr size_t smem(int warps) { return 256 + (size_t)warps * kStages * kStage + (kShared ? 1 : warps) * 2 * kRow + (kShared ? kQueries : 0); }
     static_assert(kStage % kRow == 0, "rows aligned to their size");
     static_assert(kStage >= kHeads * kAcc * 4, "a free stage holds 8 rows of binary32");
     // a row's 16-byte chunks are permuted so that chunk c of 8 consecutive rows
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 255) & ~uintptr_t(255));
     __shared__ uint32_t present_s[WARPS][S::kStages];                                 // tokens of the stage that are there
-    __shared__ float new_scale[WARPS][2], q_mul[WARPS][kHeads];
+    __shared__ float new_scale[2], q_mul[kHeads], q_sum[kHeads];
     __shared__ float w_m[WARPS][kHeads], w_m2[WARPS][kHeads], w_l[WARPS][kHeads];
     __shared__ float4 c_stat[kHeads];               // of the CTA: maximum, maximum of the weights, sum
 
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     const bool step = a.k_new != nullptr;
     const int32_t *trow = a.tables + (int64_t)s * a.max_blocks;
     uint8_t *my_ring = ring + (size_t)warp * S::kStages * S::kStage;
-    uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + warp * 2 * S::kRow;   // a step's K and V row
+    uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + (S::kShared ? 0 : warp) * 2 * S::kRow;   // a step's K and V row
 
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     grid_dependency_wait();
@@ -304,17 +308,21 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 #pragma unroll
     for (int k = 0; k < S::kStages - 1; ++k) issue(k);
 
-    // 3. the queries in binary32 (turned in a step) into the free stage, and a
-    //    step's new rows: a head row is the work of SLOTS lanes (rope.cuh)
-    uint32_t qb[KS][2], qr[INT8 ? 1 : KS][2];
+    // 3. the queries (turned in a step) in 16 bits into shared memory, and a step's new
+    //    rows: a head row is the work of SLOTS lanes (rope.cuh).  int8: the rounds of rows
+    //    are shared out to the warps (64 sequences 31.6 -> 30.4 us, 4 of 256 tokens 6.1 ->
+    //    5.5); bf16: each warp has its own, in its free stage (a barrier of all warps made
+    //    the smallest call 2.8 -> 2.9 us, two sequences of 16 K tokens 26.4 -> 26.8).
+    uint32_t qb[KS][2], qr[REST2 ? KS : 1][2];
     bool rest = false;                           // bf16: some query has a remainder
-    float bias = 0.f;
     const int h0 = PAIRED ? (2 * q4) & 3 : 2 * q4;   // this lane's two heads: columns 2 q4, 2 q4 + 1
     float mul0 = a.scale_log2, mul1 = a.scale_log2, bias0 = 0.f, bias1 = 0.f;
     {
         constexpr int PER = 32 / SLOTS;          // rows at once
-        constexpr int NIT = (QROWS + PER - 1) / PER + 1;
-        float *qf = reinterpret_cast<float *>(my_ring + (S::kStages - 1) * S::kStage);
+        constexpr int NIT = (QROWS + PER - 1) / PER + 1, TEAM = S::kShared ? WARPS : 1, MINE = (NIT + TEAM - 1) / TEAM;
+        const int member = S::kShared ? warp : 0;
+        // 8 rows, then (bf16) their remainders
+        uint8_t *q_s = S::kShared ? new_rows + 2 * S::kRow : my_ring + (S::kStages - 1) * S::kStage;
         const int slot = lane % SLOTS;
         int v0, v1;
         const bool turn = rope_vectors(a.rope, slot, v0, v1);
@@ -322,36 +330,33 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         auto source = [&](int it) -> const __nv_bfloat16 * {
             const int r = it * PER + lane / SLOTS;
             if (it < NIT - 1) return r < G ? a.q + s * a.q_stride + ((int64_t)h * G + r) * D : nullptr;
-            if (!step || lane / SLOTS > 1) return nullptr;
+            if (it > NIT - 1 || !step || lane / SLOTS > 1) return nullptr;
             return lane / SLOTS == 0 ? a.k_new + s * a.k_stride + (int64_t)h * D : a.v_new + s * a.v_stride + (int64_t)h * D;
         };
-        uint4 x0[NIT], x1[NIT];
+        uint4 x0[MINE], x1[MINE];
 #pragma unroll
-        for (int it = 0; it < NIT; ++it) {
-            const __nv_bfloat16 *src = source(it);
-            x0[it] = x1[it] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < MINE; ++i) {
+            const __nv_bfloat16 *src = source(member + i * TEAM);
+            x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
             if (src) {
-                x0[it] = __ldg(reinterpret_cast<const uint4 *>(src) + v0);
-                x1[it] = __ldg(reinterpret_cast<const uint4 *>(src) + v1);
+                x0[i] = __ldg(reinterpret_cast<const uint4 *>(src) + v0);
+                x1[i] = __ldg(reinterpret_cast<const uint4 *>(src) + v1);
             }
         }
         float c[8], sn[8];
-        if (turn) rope_angles(a.rope, slot, t_new, c, sn);
-        // every warp has the new rows, the first one writes them
-        const int64_t new_row = step && worker == 0 ? pool_row_of(trow, a.max_blocks, a.n_blocks, bs, t_new,
-                                                                  lane == 0 && h == 0 ? a.dev_status : nullptr)
-                                                    : -1;
+        if (turn && member < NIT) rope_angles(a.rope, slot, t_new, c, sn);
 #pragma unroll
-        for (int it = 0; it < NIT; ++it) {
-            if (it == NIT - 1 && !step) break;
+        for (int i = 0; i < MINE; ++i) {
+            const int it = member + i * TEAM;
+            if (it > NIT - 1 || (it == NIT - 1 && !step)) break;
             const int r = it * PER + lane / SLOTS;
             float x[16];
-            unpack_bf16x8(x0[it], x);
-            unpack_bf16x8(x1[it], x + 8);
+            unpack_bf16x8(x0[i], x);
+            unpack_bf16x8(x1[i], x + 8);
             if (turn && (it < NIT - 1 || lane / SLOTS == 0)) {
                 rope_turn(a.rope.interleaved, c, sn, x);
-                x0[it] = pack_bf16x8(x);
-                x1[it] = pack_bf16x8(x + 8);
+                x0[i] = pack_bf16x8(x);
+                x1[i] = pack_bf16x8(x + 8);
             }
             float amax = 0.f;
             if constexpr (INT8) {
@@ -361,24 +366,47 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                 for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
             }
             if (it < NIT - 1) {
-                if (r >= QROWS) continue;
+                uint4 *dst = reinterpret_cast<uint4 *>(q_s + r * S::kQRow);
+                uint32_t hi[8], lo[8];
                 if constexpr (INT8) {
-                    // fp16 holds the query as multiples of the power of two below its largest element
+                    // fp16 holds the query as multiples of the power of two below its largest element;
+                    // its products with the codes' bias are taken off by the sum of what was rounded
                     const int e = min(max((int)((__float_as_uint(amax) >> 23) & 0xff) - 127, -126), 126);
                     const float down = amax > 0.f ? __uint_as_float((uint32_t)(127 - e) << 23) : 1.f;
+                    float sum = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] *= down;
-                    if (slot == 0)
-                        q_mul[warp][r] = a.scale_log2 * (amax > 0.f ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f);
+                    for (int k = 0; k < 8; ++k) {
+                        hi[k] = pack16<true>(x[2 * k] * down, x[2 * k + 1] * down);
+                        const float2 y = unpack16<true>(hi[k]);
+                        sum += y.x + y.y;
+                    }
+#pragma unroll
+                    for (int off = 1; off < SLOTS; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                    if (slot == 0 && r < QROWS) {
+                        q_mul[r] = a.scale_log2 * (amax > 0.f ? __uint_as_float((uint32_t)(127 + e) << 23) : 1.f);
+                        q_sum[r] = sum;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        hi[k] = pack16<false>(x[2 * k], x[2 * k + 1]);
+                        lo[k] = pack16_rest<false>(x[2 * k], x[2 * k + 1], hi[k]);
+                        rest |= (lo[k] & 0x7fff7fffu) != 0;
+                    }
                 }
-                float *dst = qf + r * S::kAcc;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    *reinterpret_cast<float4 *>(dst + 8 * v0 + 4 * i) = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    *reinterpret_cast<float4 *>(dst + 8 * v1 + 4 * i) =
-                        make_float4(x[8 + 4 * i], x[9 + 4 * i], x[10 + 4 * i], x[11 + 4 * i]);
+                if (r >= QROWS) continue;
+                dst[v0] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                dst[v1] = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                if constexpr (!INT8) {
+                    uint4 *low = reinterpret_cast<uint4 *>(q_s + (kHeads + r) * S::kQRow);
+                    low[v0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    low[v1] = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 }
             } else {
+                // every CTA (bf16: every warp) has the new rows, the first one writes them
+                const int64_t new_row = (S::kShared ? rank : worker) == 0 ? pool_row_of(trow, a.max_blocks, a.n_blocks, bs, t_new,
+                                                                lane == 0 && h == 0 ? a.dev_status : nullptr)
+                                                  : -1;
                 const int which = lane / SLOTS;
                 uint8_t *dst = new_rows + (which & 1) * S::kRow;
                 uint8_t *pool = static_cast<uint8_t *>(which ? a.v_pool : a.k_pool) + (new_row * hkv + h) * S::kRow;
@@ -389,7 +417,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                     if (which > 1) continue;
                     *reinterpret_cast<uint2 *>(dst + 8 * v0) = y0;
                     *reinterpret_cast<uint2 *>(dst + 8 * v1) = y1;
-                    if (slot == 0) new_scale[warp][which] = scale;
+                    if (slot == 0) new_scale[which] = scale;
                     if (new_row >= 0) {
                         *reinterpret_cast<uint2 *>(pool + 8 * v0) = y0;
                         *reinterpret_cast<uint2 *>(pool + 8 * v1) = y1;
@@ -397,57 +425,48 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                     }
                 } else {
                     if (which > 1) continue;
-                    *reinterpret_cast<uint4 *>(dst + 16 * v0) = x0[it];
-                    *reinterpret_cast<uint4 *>(dst + 16 * v1) = x1[it];
+                    *reinterpret_cast<uint4 *>(dst + 16 * v0) = x0[i];
+                    *reinterpret_cast<uint4 *>(dst + 16 * v1) = x1[i];
                     if (new_row >= 0) {
-                        *reinterpret_cast<uint4 *>(pool + 16 * v0) = x0[it];
-                        *reinterpret_cast<uint4 *>(pool + 16 * v1) = x1[it];
+                        *reinterpret_cast<uint4 *>(pool + 16 * v0) = x0[i];
+                        *reinterpret_cast<uint4 *>(pool + 16 * v1) = x1[i];
                     }
                 }
             }
         }
-        __syncwarp();
+        if constexpr (S::kShared) {
+            __syncthreads();
+        } else {
+            rest = __any_sync(0xffffffffu, rest);
+            __syncwarp();
+        }
         // as B fragments.  bf16: column g4 is head g4 (WIDE), or head g4 % 4 with
         // its remainders in columns 4-7.  int8: column g4 is head g4, the four bytes
         // 4 q4 .. of a 16-byte chunk are the products' k = 2 q4, 2 q4 + 1, 2 q4 + 8,
-        // 2 q4 + 9, and bias is 1152 times the sum of the rounded query.
-        const float *src = qf + (PAIRED ? (g4 & 3) : g4) * S::kAcc;
+        // 2 q4 + 9.
+        const uint8_t *src = q_s + (PAIRED ? (g4 & 3) + (rest && g4 >= 4 ? kHeads : 0) : g4) * S::kQRow;
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
+            if constexpr (INT8) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src + 2 * (16 * kk + 4 * q4));
+                qb[kk][0] = x.x;
+                qb[kk][1] = x.y;
+            } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int d = 16 * kk + (INT8 ? 4 * q4 + 2 * j : 2 * q4 + 8 * j);
-                const float2 x = *reinterpret_cast<const float2 *>(src + d);
-                const uint32_t hi = pack16<INT8>(x.x, x.y);
-                if constexpr (INT8) {
-                    const float2 y = unpack16<true>(hi);
-                    bias += y.x + y.y;
-                    qb[kk][j] = hi;
-                } else {
-                    const uint32_t lo = pack16_rest<false>(x.x, x.y, hi);
-                    qb[kk][j] = hi;
-                    qr[kk][j] = lo;
-                    rest |= (lo & 0x7fff7fffu) != 0;
+                for (int j = 0; j < 2; ++j) {
+                    const int at = 2 * (16 * kk + 2 * q4 + 8 * j);
+                    qb[kk][j] = *reinterpret_cast<const uint32_t *>(src + at);
+                    if constexpr (REST2) qr[kk][j] = *reinterpret_cast<const uint32_t *>(src + kHeads * S::kQRow + at);
                 }
             }
         }
-        if constexpr (!INT8) rest = __any_sync(0xffffffffu, rest);
-        if constexpr (PAIRED) {                  // columns 4-7: the remainders, or the heads again
-#pragma unroll
-            for (int kk = 0; kk < KS; ++kk)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (rest && g4 >= 4) qb[kk][j] = qr[kk][j];
-        }
         if constexpr (INT8) {
-            mul0 = q_mul[warp][h0];
-            mul1 = q_mul[warp][h0 + 1];
-            bias += __shfl_xor_sync(0xffffffffu, bias, 1);
-            bias += __shfl_xor_sync(0xffffffffu, bias, 2);         // of head g4, in its four lanes
-            bias0 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0);
-            bias1 = -1152.f * __shfl_sync(0xffffffffu, bias, 4 * h0 + 4);
+            mul0 = q_mul[h0];
+            mul1 = q_mul[h0 + 1];
+            bias0 = -1152.f * q_sum[h0];
+            bias1 = -1152.f * q_sum[h0 + 1];
         }
-        __syncwarp();                            // the free stage is read
+        __syncwarp();                            // a free stage is read
     }
 
     // 4. the tiles
@@ -473,7 +492,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                 *reinterpret_cast<uint4 *>(dst + S::at(i, v % S::kVecs)) =
                     *reinterpret_cast<const uint4 *>(new_rows + v * 16);
             }
-            if (INT8 && lane < 2) const_cast<float *>(sc)[lane * kTile + i] = new_scale[warp][lane];
+            if (INT8 && lane < 2) const_cast<float *>(sc)[lane * kTile + i] = new_scale[lane];
             __syncwarp();
         }
 

@@ -37,11 +37,11 @@
 // that could stage it holds the next unit's tiles by then.
 //
 // Measured (32 query and 8 kv heads of 128, kernels back to back).  8 x 512 tokens,
-// window 1024: 74.1 us with prefixes of 2 to 8 K, and 77.9 with prefixes of 0 to 8 K whose
-// last sequence is the shortest (the halves are small ones then), 813 TFLOP/s of
+// window 1024: 74 us with prefixes of 2 to 8 K, and 77.5 with prefixes of 0 to 8 K whose
+// last sequence is the shortest (the halves are small ones then), 818 TFLOP/s of
 // products that the mask asks for: a tile of 128 keys takes 1.56 us (1.63 PFLOP/s on 152
 // SMs) and a unit 4.1 us beside its nine (masked tiles, O, the hand-over).  A prompt of
-// 4095 tokens, window 1000: 67.4 us, 886 TFLOP/s.  2 x 37 tokens: 7.7 us, the latency of
+// 4095 tokens, window 1000: 67.9 us, 878 TFLOP/s.  2 x 37 tokens: 7.5 us, the latency of
 // a launch and of one tile's chain.
 #include <math.h>
 
