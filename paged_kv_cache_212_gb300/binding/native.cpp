@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -54,6 +55,13 @@ int64_t token_stride(const at::Tensor &t, int64_t ndim, int dev)
         step = stride[1];
     }
     return step;
+}
+
+// An uninitialised tensor of t's sizes, contiguous, on t's device (straight from the
+// allocator: through the dispatcher it takes 0.3 us longer).
+at::Tensor new_like(const at::Tensor &t)
+{
+    return at::Tensor(at::detail::empty_cuda(t.sizes(), t.scalar_type(), t.device(), std::nullopt));
 }
 
 struct Pools {
@@ -150,7 +158,7 @@ PyObject *write_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
             return none();
         at::Tensor out;
         if (a[11] == Py_None) {
-            out = at::empty(q->sizes(), q->options());
+            out = new_like(*q);
         } else {
             const at::Tensor *o = need(a[11], at::kBFloat16, 4, dev);
             if (!o || o->sizes() != q->sizes()) return none();
@@ -204,7 +212,7 @@ PyObject *prefill_window(PyObject *, PyObject *const *a, Py_ssize_t n)
         }
         at::Tensor out;
         if (a[8] == Py_None) {
-            out = at::empty(q->sizes(), q->options());
+            out = new_like(*q);
         } else {
             const at::Tensor *o = need(a[8], at::kBFloat16, 4, dev);
             if (!o || o->sizes() != q->sizes()) return none();
