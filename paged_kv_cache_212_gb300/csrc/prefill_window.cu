@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             };
             load_unit(0);
             int32_t blk = load_block(0);
-            int j = 0, issued = 0, unit = 0, q_loads = 0;   // tile of the unit, tiles so far, unit, Qs so far
+            int j = 0, issued = 0, unit = 0, q_loads = 0;   // tile of the unit, tiles so far, unit, Qs that lane 0 has issued
             while (unit < n_mine) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
                 const int32_t place = j * kTN + grp * 16;
@@ -547,10 +547,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                                 for (int h = 0; h < PANELS; ++h)
                                     tma_load_3d(q_s + i * kQTile + h * kQPanel, &q_map, h * 64, t_kvh * G,
                                                 w.s * p.chunk + w.p0 + i * pos_per_tile, q_full);
+                            ++q_loads;   // (lane 0's: another role may have raised the flag by now)
                         }
                     }
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
-                    ++q_loads;
                 }
             }
             // every copy this warp issued has landed before the CTA can exit

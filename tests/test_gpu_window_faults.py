@@ -1,0 +1,42 @@
+"""The windowed and rotary calls where something is wrong with a call or its
+neighbour: waits that run out with another call behind them, chunks that run past
+the table, and the calls around them, which have to stay right."""
+import pytest
+import torch
+
+from test_gpu_window import P, _cuda, _paged  # noqa: F401  (P: the fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+# d, n_seqs, hkv, group, chunk, window, sinks: units of at most the tiles that the rings
+# hold, one unit or two halves a CTA; then about three units a CTA, of one tile each
+@pytest.mark.parametrize("d,n,hkv,group,chunk,window,sinks", [(128, 2, 4, 4, 60, 100, 4), (64, 8, 8, 4, 448, 32, 0)])
+def test_prefill_behind_one_whose_waits_ran_out(P, d, n, hkv, group, chunk, window, sinks):  # noqa: F811
+    """A call that gives up has no copy on its way into shared memory when it ends: the
+    call behind it, which takes over its SMs, gives the bits that it gives alone."""
+    bs = 16
+    lens = [chunk + 13 * s for s in range(n)]
+    pools, _, tables, _ = _paged(d + n, lens, window, sinks, chunk, hkv, d, bs, False)
+    gen = torch.Generator().manual_seed(8)
+    q, other = (torch.randn((n, chunk, hkv * group, d), generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    kp, vp, tab = _cuda(*pools, tables)
+    pre = torch.tensor([x - chunk for x in lens], dtype=torch.int32).cuda()
+    call = lambda x, st, out: P.paged_prefill_attention_window(x, kp, vp, tab, pre, d ** -0.5, window, sinks, out=out,
+                                                               dev_status=st)
+    bad, good = (torch.zeros(1, dtype=torch.int32, device="cuda") for _ in range(2))
+    want = call(q, good, torch.empty_like(q)).clone()
+    lost, got = torch.empty_like(q), torch.empty_like(q)
+    lib = P.load_library()
+    for ns in (1, 100, 1000, 1, 3000, 300, 1):
+        got.zero_()
+        torch.cuda.synchronize()
+        try:
+            lib.pkv_set_pipeline_wait_ns(ns)               # read when a launch is prepared
+            call(other, bad, lost)
+        finally:
+            lib.pkv_set_pipeline_wait_ns(0)
+        call(q, good, got)
+        torch.cuda.synchronize()
+        assert int(good.item()) == 0 and torch.equal(got, want), ns
+    assert int(bad.item()) & ~16 == 0 and int(bad.item()) == 16
