@@ -68,8 +68,9 @@ int paged_decode_step_window(const pkv_bf16 *k_new, int64_t k_stride, const pkv_
  * paged_prefill_attention_window -- paged_prefill_attention under the mask
  * above: query i of sequence s sits at position prefix_lens[s] + i.  Key tiles
  * that no query of a CTA's rows sees are not loaded, so the work grows with
- * the window and not with the prefix.  A sequence whose length is bad
- * (PKV_DEV_BAD_LENGTH) leaves its output rows as they were.
+ * the window and not with the prefix.  A sequence whose length is bad (prefix_lens[s]
+ * negative, or prefix_lens[s] + chunk more than its table row spans:
+ * PKV_DEV_BAD_LENGTH) leaves all of its output rows as they were.
  */
 int paged_prefill_attention_window(const pkv_bf16 *q, int32_t n_q_heads, const pkv_bf16 *k_pool,
                                    const pkv_bf16 *v_pool, pkv_dims dims, const int32_t *block_tables,

@@ -121,7 +121,7 @@ __device__ __noinline__ void find_unit(const WinParams &p, int32_t u, Unit *out)
     w.P = __ldg(p.prefix_lens + w.s);
     int32_t n_keys = 0;
     w.w_lo = 0;
-    if (w.P < 0 || (int64_t)w.P + w.p_last + 1 > (int64_t)p.max_blocks * p.block_size) {
+    if (w.P < 0 || (int64_t)w.P + p.chunk > (int64_t)p.max_blocks * p.block_size) {   // alike for all units of a sequence
         w.P = 0;
         w.p_last = -1;
     } else if (w.p0 <= w.p_last) {

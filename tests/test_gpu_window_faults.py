@@ -40,3 +40,38 @@ def test_prefill_behind_one_whose_waits_ran_out(P, d, n, hkv, group, chunk, wind
         torch.cuda.synchronize()
         assert int(good.item()) == 0 and torch.equal(got, want), ns
     assert int(bad.item()) & ~16 == 0 and int(bad.item()) == 16
+
+
+# hkv, group, d, chunk: whole units, and halves (one sequence), of which only the last
+# reach past the table
+@pytest.mark.parametrize("n", [1, 3, 25])
+@pytest.mark.parametrize("hkv,group,d,chunk", [(2, 4, 64, 300), (8, 8, 128, 130)])
+def test_prefill_chunk_that_ends_past_the_table(P, hkv, group, d, chunk, n):  # noqa: F811
+    """A chunk whose end alone is past the table is a bad length for all of it: its
+    rows stay as they were, whatever its units are, and the other sequences' are right."""
+    bs, window, sinks, bad = 16, 70, 4, n // 2
+    lens = [chunk + 29 * s for s in range(n)]
+    pools, _, tables, _ = _paged(n + d, lens, window, sinks, chunk, hkv, d, bs, False)
+    q = torch.randn((n, chunk, hkv * group, d), generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).cuda()
+    kp, vp, tab = _cuda(*pools, tables)
+    pre = torch.tensor([x - chunk for x in lens], dtype=torch.int32).cuda()
+    capacity = tables.shape[1] * bs
+
+    def call(prefix):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = torch.full_like(q, 3.0), torch.full(q.shape[:3], 7.0, device="cuda")
+        P.paged_prefill_attention_window(q, kp, vp, tab, prefix, d ** -0.5, window, sinks, out=out, lse_out=lse, dev_status=st)
+        torch.cuda.synchronize()
+        return int(st.item()), out, lse
+
+    st, want, want_lse = call(pre)
+    assert st == 0 and torch.isfinite(want.float()).all()
+    others = [s for s in range(n) if s != bad]
+    for past in (1, chunk // 2, chunk - 1):
+        pre[bad] = capacity - chunk + past                 # the first chunk - past rows are inside
+        # (the bad sequence's blocks are not looked up either: its table entries are ids outside the pool)
+        tab[bad] = pools[0].shape[0]
+        st, out, lse = call(pre)
+        assert st == 4, (past, st)
+        assert (out[bad] == 3.0).all() and (lse[bad] == 7.0).all(), past
+        assert torch.equal(out[others], want[others]) and torch.equal(lse[others], want_lse[others]), past
