@@ -4,7 +4,7 @@
 // Angles.  A pair's phase is its turns per position in units of 2^-64, so the
 // angle of position t is (t * phase mod 2^64) 2^-64 turns: an integer product,
 // exact for every position, where the binary32 product t * f loses 0.06 rad at
-// t = 10^6.
+// t = 10^6.  rope_angle.h makes sine and cosine of it.
 //
 // Lanes.  A head row of D elements is the work of D / 16 lanes: lane `slot`
 // holds two 16-byte vectors (16 elements, 8 pairs) so that both members of
@@ -13,20 +13,9 @@
 #pragma once
 
 #include "common.cuh"
+#include "rope_angle.h"
 
 namespace pkv {
-
-struct RopeArgs {
-    const uint64_t *phases;   // null: no turn
-    int32_t rot_dim;
-    int32_t interleaved;
-    float mag_high, mag_low;  // the magnitude in two parts
-};
-
-inline RopeArgs rope_args(const uint64_t *phases, int32_t rot_dim, int32_t interleaved, double magnitude)
-{
-    return RopeArgs{phases, rot_dim, interleaved != 0, (float)magnitude, (float)(magnitude - (double)(float)magnitude)};
-}
 
 // Vectors (of 8 elements) of a head row that lane `slot` of its D / 16 holds,
 // and whether they are turned.  Half layout: the pair (slot, slot + rot / 16)
@@ -45,51 +34,7 @@ __device__ __forceinline__ bool rope_vectors(const RopeArgs &r, int slot, int &v
     return turn;
 }
 
-// The cosine and sine (times the magnitude) of a phase at position t, rounded
-// once.  The nearest quarter turn is taken off in integers, which leaves an angle
-// th + tl of at most an eighth of a turn, held to twice binary32; sine and cosine
-// are their Taylor series there (the first terms left out are below 1e-11 and
-// 2e-10), summed with the largest term last and apart:
-//   sin = th + (tl (1 - u / 2) + th u (-1/6 + u / 5! - ...)),  u = th^2
-//   cos = (1 - u / 2) + ((rest of that difference) - ue / 2 + u^2 (1/4! - ...)).
-// Both are within 0.73 steps of the last place of the exact value (0.29 on
-// average, as rounding the exact one would be); a sine and cosine of the angle in
-// binary32 are not, and the keys they turn would be rounded to another bf16 twice
-// as often.
-__device__ __forceinline__ void rope_angle_of(const RopeArgs &r, unsigned long long phase, int64_t t, float &c, float &s)
-{
-    const unsigned long long a = phase * (unsigned long long)t;           // turns * 2^64
-    const uint32_t q = (uint32_t)((a + (1ull << 61)) >> 62) & 3u;          // the nearest quarter turn
-    const int32_t rest = (int32_t)((int64_t)(a - ((unsigned long long)q << 62)) >> 30);   // turns * 2^34
-    // times pi 2^-33, in two parts
-    constexpr float kPi = (float)(3.14159265358979323846 / 8589934592.0);
-    constexpr float kPiLow = (float)(3.14159265358979323846 / 8589934592.0 - (double)kPi);
-    const float x = (float)rest, xl = (float)(rest - __float2int_rn(x));
-    const float th = __fmul_rn(x, kPi);
-    const float tl = __fadd_rn(__fmaf_rn(x, kPi, -th), __fmaf_rn(x, kPiLow, __fmul_rn(xl, kPi)));
-    const float u = __fmul_rn(th, th), ue = __fmaf_rn(2.f * th, tl, __fmaf_rn(th, th, -u));
-    float ps = __fmaf_rn(u, -1.f / 39916800.f, 1.f / 362880.f);
-    ps = __fmaf_rn(u, ps, -1.f / 5040.f);
-    ps = __fmaf_rn(u, ps, 1.f / 120.f);
-    ps = __fmaf_rn(u, ps, -1.f / 6.f);
-    const float sin_low = __fmaf_rn(__fmul_rn(th, u), ps, __fmaf_rn(-0.5f * u, tl, tl));
-    float pc = __fmaf_rn(u, -1.f / 3628800.f, 1.f / 40320.f);
-    pc = __fmaf_rn(u, pc, -1.f / 720.f);
-    pc = __fmaf_rn(u, pc, 1.f / 24.f);
-    const float cos_high = __fsub_rn(1.f, 0.5f * u);
-    const float cos_low = __fmaf_rn(__fmul_rn(u, u), pc, __fmaf_rn(-0.5f, ue, __fsub_rn(__fsub_rn(1.f, cos_high), 0.5f * u)));
-    // times the magnitude, then to their quarter
-    auto scaled = [&](float high, float low) {
-        const float h = __fmul_rn(high, r.mag_high);
-        return __fadd_rn(h, __fmaf_rn(low, r.mag_high, __fmaf_rn(high, r.mag_low, __fmaf_rn(high, r.mag_high, -h))));
-    };
-    const float y = scaled(th, sin_low), z = scaled(cos_high, cos_low);
-    const float cq = q & 1 ? y : z, sq = q & 1 ? z : y;
-    c = q == 1 || q == 2 ? -cq : cq;
-    s = q >= 2 ? -sq : sq;
-}
-
-// Those of pair i.
+// The cosine and sine (times the magnitude) of pair i at position t.
 __device__ __forceinline__ void rope_angle(const RopeArgs &r, int i, int64_t t, float &c, float &s)
 {
     rope_angle_of(r, __ldg(reinterpret_cast<const unsigned long long *>(r.phases) + i), t, c, s);

@@ -4,6 +4,8 @@ the table, and the calls around them, which have to stay right."""
 import pytest
 import torch
 
+import window_reference as R
+
 from test_gpu_window import P, _cuda, _paged  # noqa: F401  (P: the fixture)
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +77,25 @@ def test_prefill_chunk_that_ends_past_the_table(P, hkv, group, d, chunk, n):  # 
         assert st == 4, (past, st)
         assert (out[bad] == 3.0).all() and (lse[bad] == 7.0).all(), past
         assert torch.equal(out[others], want[others]) and torch.equal(lse[others], want_lse[others]), past
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_slow_pairs_near_position_0(P, interleaved):  # noqa: F811
+    """The sine of a pair of 1e-12 rad a position is right relative to itself: a pair
+    (1, 0) becomes (cos, sin), each rounded once to bf16."""
+    d, bs, n_new, base, factor = 128, 16, 9, 1e10, 32.0
+    rope = P.Rope(d, base=base, interleaved=interleaved, scaling="linear", factor=factor)
+    inv, _ = R.frequencies(d, base, "linear", factor)
+    x = torch.zeros((1, n_new, 1, d), dtype=torch.bfloat16)
+    x[..., 0::2] = 1
+    if not interleaved:
+        x = torch.cat((x[..., 0::2], x[..., 1::2]), dim=-1)
+    new, pool = torch.zeros((1, n_new, 1, d), dtype=torch.bfloat16), torch.zeros((2, bs, 1, d), dtype=torch.bfloat16)
+    x, k, v, kp, vp = _cuda(x, new, new, pool, pool)
+    tab, start = torch.zeros((1, 1), dtype=torch.int32).cuda(), torch.zeros(1, dtype=torch.int32).cuda()
+    out = P.paged_kv_write_rope(x, k, v, rope, kp, vp, tab, start).cpu().double()[0, :, 0]
+    cos, sin = (out[:, 0::2], out[:, 1::2]) if interleaved else (out[:, :d // 2], out[:, d // 2:])
+    angle = torch.arange(n_new).double()[:, None] * torch.tensor(inv, dtype=torch.float64)
+    for got, want in ((cos, angle.cos()), (sin, angle.sin())):
+        # bf16's rounding, and 6 steps of binary32
+        assert ((got - want).abs() <= (R.U16 + 12 * R.U32) * want.abs()).all()
