@@ -5,8 +5,8 @@ to an object file, then one
 link step produces the shared library (cudart linked statically, so the
 library needs only the driver at run time).  Beside them g++ compiles the
 native part of the Python binding (binding/native.cpp, against the installed
-torch) into a CPython extension of its own.  Rebuilds only when a source or
-header is newer than what was built from it.
+torch) into a CPython extension of its own, which the library does not need.
+Rebuilds only when a source or header is newer than what was built from it.
 """
 from __future__ import annotations
 
@@ -17,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -80,12 +81,36 @@ def build_native() -> str:
     return lib
 
 
-def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    native = force or not native_up_to_date()
-    if not force and up_to_date():
-        if native:
+def try_native(force: bool = False):
+    """The binding's native part, where it is out of date.  The calls work without it, so
+    what went wrong (no torch, no g++, errors) is returned; what an older source left is
+    removed then, as it may not fit the library."""
+    try:
+        if force or not native_up_to_date():
             build_native()
-        return LIB
+        return None
+    except Exception as e:
+        try:
+            os.remove(native_lib())
+        except (ImportError, OSError):
+            pass
+        return e
+
+
+def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Builds what is out of date; the path of the library.  Raises where that cannot be
+    built, and warns where the binding's native part cannot."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(try_native, force)
+        if force or not up_to_date():
+            build_library(verbose, ptxas_verbose)
+        error = binding.result()
+    if error is not None:
+        warnings.warn(f"the native part of the binding was not built, its calls go through Python: {error!r}", RuntimeWarning)
+    return LIB
+
+
+def build_library(verbose: bool = False, ptxas_verbose: bool = False) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
     flags = ["-O3", "-std=c++17", "-lineinfo", *ARCH, "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -102,10 +127,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 2)) as ex:
-        binding = ex.submit(build_native) if native else None
         results = list(ex.map(compile_one, _sources()))
-        if binding:
-            binding.result()
     if verbose or ptxas_verbose:
         for _, err in results:
             if err.strip():
@@ -117,7 +139,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
