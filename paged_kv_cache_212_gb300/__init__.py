@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import warnings
 
 import torch
 
@@ -76,12 +77,17 @@ _native = None          # the native marshalling, once the library is loaded
 
 
 def _load_native(lib):
-    """binding/native.cpp with the library's entry points (None: not built)."""
+    """binding/native.cpp with the library's entry points (None: not built, or it does
+    not load, and the calls go through Python)."""
     if not os.path.exists(NATIVE_PATH):
         return None
-    spec = importlib.util.spec_from_file_location("_native", NATIVE_PATH)
-    mod = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(mod)
+    try:
+        spec = importlib.util.spec_from_file_location("_native", NATIVE_PATH)
+        mod = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(mod)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"the native part of the binding was not loaded, its calls go through Python: {e!r}", RuntimeWarning)
+        return None
     mod.set_functions(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
         "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
         "paged_prefill_attention_window")))

@@ -54,3 +54,14 @@ def test_a_library_that_does_not_compile_is_an_error(B, monkeypatch, tmp_path):
     (tmp_path / "native.cpp").write_text("#error not today\n")
     with pytest.raises(RuntimeError, match="one.cpp"):
         B.build()
+
+
+def test_a_binding_that_does_not_load_is_left_out(monkeypatch, tmp_path):
+    import paged_kv_cache_212_gb300 as P
+    bad = tmp_path / "_native.so"
+    bad.write_bytes(b"no shared object")
+    monkeypatch.setattr(P, "NATIVE_PATH", str(bad))
+    with pytest.warns(RuntimeWarning, match="binding"):
+        assert P._load_native(None) is None
+    monkeypatch.setattr(P, "NATIVE_PATH", str(tmp_path / "absent.so"))
+    assert P._load_native(None) is None
