@@ -15,14 +15,15 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sysconfig
 import warnings
 
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libpagedkv.so")
-# binding/native.cpp, built against this version of torch
-NATIVE_PATH = os.path.join(HERE, f"_native-{torch.__version__}.so")
+# binding/native.cpp, built against this torch for this Python (build.native_lib)
+NATIVE_PATH = os.path.join(HERE, f"_native-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 PKV_KV_BF16, PKV_KV_INT8 = 0, 1
 DEV_BAD_BLOCK_ID, DEV_BAD_POSITION, DEV_BAD_LENGTH = 1, 2, 4

@@ -53,7 +53,7 @@ def up_to_date() -> bool:
 
 def native_lib() -> str:
     import torch
-    return os.path.join(HERE, f"_native-{torch.__version__}.so")
+    return os.path.join(HERE, f"_native-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def native_up_to_date() -> bool:

@@ -65,3 +65,16 @@ def test_a_binding_that_does_not_load_is_left_out(monkeypatch, tmp_path):
         assert P._load_native(None) is None
     monkeypatch.setattr(P, "NATIVE_PATH", str(tmp_path / "absent.so"))
     assert P._load_native(None) is None
+
+
+def test_the_binding_is_named_after_what_it_was_built_for():
+    """Another Python, machine or torch looks for another file."""
+    import sysconfig
+
+    import torch
+
+    import paged_kv_cache_212_gb300 as P
+    from paged_kv_cache_212_gb300 import build as B
+    name = os.path.basename(P.NATIVE_PATH)
+    assert B.native_lib() == P.NATIVE_PATH
+    assert torch.__version__ in name and name.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
