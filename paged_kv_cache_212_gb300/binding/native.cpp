@@ -29,6 +29,13 @@ decltype(&paged_decode_attention_window) g_decode_window;
 decltype(&paged_decode_step_window) g_step_window;
 decltype(&paged_prefill_attention_window) g_prefill_window;
 
+// Lets other Python threads run while it lives: a launch waits where the stream's queue
+// is full.  (The caller holds the arguments meanwhile.)
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The tensor of a Python argument, or null.
 const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariable_Unpack(o) : nullptr; }
 
@@ -164,11 +171,15 @@ PyObject *write_rope(PyObject *, PyObject *const *a, Py_ssize_t n)
             if (!o || o->sizes() != q->sizes()) return none();
             out = *o;
         }
-        const int st = g_write_rope(ptr<const pkv_bf16>(q), qs, (int32_t)hq, ptr<const pkv_bf16>(k), ks, ptr<const pkv_bf16>(v),
-                                    vs, rope, ptr<pkv_bf16>(&out), p.k->data_ptr(), p.v->data_ptr(), ptr<float>(p.ks),
-                                    ptr<float>(p.vs), p.kv_dtype, p.dims, ptr<const int32_t>(p.tables),
-                                    (int32_t)p.tables->size(1), ptr<const int32_t>(sp), (int32_t)n_seqs, (int32_t)n_new, status,
-                                    reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_write_rope(ptr<const pkv_bf16>(q), qs, (int32_t)hq, ptr<const pkv_bf16>(k), ks, ptr<const pkv_bf16>(v), vs,
+                              rope, ptr<pkv_bf16>(&out), p.k->data_ptr(), p.v->data_ptr(), ptr<float>(p.ks),
+                              ptr<float>(p.vs), p.kv_dtype, p.dims, ptr<const int32_t>(p.tables),
+                              (int32_t)p.tables->size(1), ptr<const int32_t>(sp), (int32_t)n_seqs, (int32_t)n_new, status,
+                              reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+        }
         if (st != 0) return status_result(st);
         if (a[11] != Py_None) {
             Py_INCREF(a[11]);
@@ -218,11 +229,16 @@ PyObject *prefill_window(PyObject *, PyObject *const *a, Py_ssize_t n)
             if (!o || o->sizes() != q->sizes()) return none();
             out = *o;
         }
-        const int st = g_prefill_window(
-            ptr<const pkv_bf16>(q), (int32_t)q->size(2), ptr<const pkv_bf16>(p.k), ptr<const pkv_bf16>(p.v), p.dims,
-            ptr<const int32_t>(p.tables), (int32_t)p.tables->size(1), ptr<const int32_t>(pre), (int32_t)q->size(0),
-            (int32_t)q->size(1), (float)PyFloat_AS_DOUBLE(a[5]), (int32_t)window, (int32_t)sinks, ptr<pkv_bf16>(&out), lse,
-            status, reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+        const float scale = (float)PyFloat_AS_DOUBLE(a[5]);
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_prefill_window(ptr<const pkv_bf16>(q), (int32_t)q->size(2), ptr<const pkv_bf16>(p.k),
+                                  ptr<const pkv_bf16>(p.v), p.dims, ptr<const int32_t>(p.tables), (int32_t)p.tables->size(1),
+                                  ptr<const int32_t>(pre), (int32_t)q->size(0), (int32_t)q->size(1), scale, (int32_t)window,
+                                  (int32_t)sinks, ptr<pkv_bf16>(&out), lse, status,
+                                  reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()));
+        }
         if (st != 0) return status_result(st);
         if (a[8] != Py_None) {
             Py_INCREF(a[8]);
@@ -292,10 +308,14 @@ PyObject *run_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
         const auto stream = reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(p->dev).stream());
         if (a[2] == Py_None) {
             if (a[3] != Py_None || a[4] != Py_None || p->rope || !q->is_contiguous()) return none();
-            return status_result(g_decode_window(ptr<const pkv_bf16>(q), p->n_q_heads, p->k_pool, p->v_pool, p->k_scales,
-                                                 p->v_scales, p->kv_dtype, p->dims, p->tables, p->max_blocks, p->ctx_lens,
-                                                 p->n_seqs, p->scale, p->window, p->sinks, p->out, p->lse_out, p->dev_status,
-                                                 stream));
+            int st;
+            {
+                const Unlocked other_threads_run;
+                st = g_decode_window(ptr<const pkv_bf16>(q), p->n_q_heads, p->k_pool, p->v_pool, p->k_scales, p->v_scales,
+                                     p->kv_dtype, p->dims, p->tables, p->max_blocks, p->ctx_lens, p->n_seqs, p->scale,
+                                     p->window, p->sinks, p->out, p->lse_out, p->dev_status, stream);
+            }
+            return status_result(st);
         }
         const at::Tensor *k = tensor(a[2]), *v = tensor(a[3]), *sp = need(a[4], at::kInt, 1, p->dev);
         if (!k || !v || !sp) return none();
@@ -304,11 +324,15 @@ PyObject *run_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
         if (ks < 0 || vs < 0 || k->sizes() != at::IntArrayRef(new_size, 4) || v->sizes() != k->sizes() ||
             sp->size(0) != p->n_seqs)
             return none();
-        return status_result(g_step_window(ptr<const pkv_bf16>(k), ks, ptr<const pkv_bf16>(v), vs, ptr<const int32_t>(sp),
-                                           ptr<const pkv_bf16>(q), qs, p->n_q_heads, p->rope, p->k_pool, p->v_pool,
-                                           p->k_scales, p->v_scales, p->kv_dtype, p->dims, p->tables, p->max_blocks,
-                                           p->ctx_lens, p->n_seqs, p->scale, p->window, p->sinks, p->out, p->lse_out,
-                                           p->dev_status, stream));
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_step_window(ptr<const pkv_bf16>(k), ks, ptr<const pkv_bf16>(v), vs, ptr<const int32_t>(sp),
+                               ptr<const pkv_bf16>(q), qs, p->n_q_heads, p->rope, p->k_pool, p->v_pool, p->k_scales,
+                               p->v_scales, p->kv_dtype, p->dims, p->tables, p->max_blocks, p->ctx_lens, p->n_seqs, p->scale,
+                               p->window, p->sinks, p->out, p->lse_out, p->dev_status, stream);
+        }
+        return status_result(st);
     } catch (const std::exception &e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
         return nullptr;
