@@ -57,7 +57,7 @@ int check_dims(const pkv_dims &d)
     if (d.n_blocks < 0 || d.block_size <= 0 || d.n_kv_heads <= 0 || d.head_dim <= 0)
         return PKV_ERR_INVALID_ARG;
     if (d.head_dim != 64 && d.head_dim != 128) return PKV_ERR_UNSUPPORTED;
-    if (d.block_size % 16 != 0 || d.block_size > 256) return PKV_ERR_UNSUPPORTED;
+    if (d.block_size % 16 != 0 || d.block_size > kMaxBlockSize) return PKV_ERR_UNSUPPORTED;
     if ((int64_t)(d.n_blocks + 1) * d.block_size > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
     return PKV_OK;
 }

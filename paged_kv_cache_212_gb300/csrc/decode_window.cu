@@ -964,7 +964,10 @@ int prepare_window(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, void 
     a->n_blocks = dims.n_blocks;
     a->block_size = dims.block_size;
     a->n_kv_heads = dims.n_kv_heads;
-    // ceil(2^32 / n) times a tile index below 2^27 is off by less than 2^27 * 16 / 2^32 < 1 / n
+    // ceil(2^32 / n) is 2^32 / n and less than 1 more, so its product with a tile index below
+    // 2^27, over 2^32, is above index / n by less than 2^27 / 2^32 = 1 / 32.  The next whole
+    // number is at least 1 / n further, which is more for every n up to 32.
+    static_assert(PKV_WINDOW_MAX_TOKENS / kTile < 1 << 27 && kMaxBlockSize / kTile <= 32, "the lookup's rounding");
     a->tiles_per_block = (uint32_t)dims.block_size / kTile;
     a->block_magic = (uint32_t)((0x100000000ull + a->tiles_per_block - 1) / a->tiles_per_block);
     a->tables = block_tables;

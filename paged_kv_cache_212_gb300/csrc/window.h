@@ -12,6 +12,7 @@ namespace pkv {
 int cuda_status(cudaError_t e);
 bool aligned16(const void *p);
 int num_sms_of_current_device(int *out);
+constexpr int32_t kMaxBlockSize = 256;   // tokens; check_dims refuses larger blocks
 int check_dims(const pkv_dims &d);
 
 // Checks of a rotary turn for heads of head_dim elements, and of a stride between
