@@ -27,15 +27,19 @@
 //
 // int8 pages are contracted as fp16 (a code and the value 1152 share one
 // exponent: a byte permute, and one subtraction or, for K, one correction by
-// 1152 times the query's sum).  Queries and weights are rounded once to fp16
-// (2^-11, eight times finer than the bf16 output).  The K scale multiplies the
-// score; the V scale joins the probability, and the weight is multiplied by a
-// running power of two r that keeps the largest one in fp16's range whatever the
-// scales are.
+// 1152 times the query's sum).  The K scale multiplies the score; the V scale joins
+// the probability, and the weight is multiplied by a running power of two r that
+// keeps the largest one in fp16's range whatever the scales are.  Weights are split
+// into an fp16 value and its fp16 remainder in a second product (2^-22 together;
+// 64 sequences, 64 query heads: 30.4 -> 31.4 us).  Queries are multiples of a power of
+// two and rounded once to fp16: a bf16 query is exact there but for elements below
+// 2^-17 of its largest one, which are held to 2^-25 of that; a step's turned query
+// keeps 11 bits, where a turn written to memory between the two calls keeps 8 (its
+// remainders in a second product: a step of 64 sequences 32.0 -> 34.5 us or more).
 //
 // Measured (one launch among others; 8 kv heads of 128, window 1024, 4 first tokens).
 // 64 sequences, bf16 pages, 32 query heads: 41.4 us = 6.28 TB/s, 92 % of the copy rate;
-// memory bounds it.  The same over int8 pages with 64 query heads: 30.3 us, 4.5 TB/s;
+// memory bounds it.  The same over int8 pages with 64 query heads: 31.4 us, 4.3 TB/s;
 // half of the issue slots are taken and the rest is the latency of an SM's 16 warps.
 // Two sequences of 16 K visible tokens, 64 query heads: 26.5 us, 5.1 TB/s.  Four
 // sequences of 68 visible tokens (2 kv heads of 64): 2.7 us, a launch and three
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     constexpr int SLOTS = D / 16;                   // lanes that hold a head row (rope.cuh)
     constexpr int KS = D / 16;                      // 16-element steps over head_dim
     constexpr bool PAIRED = !INT8 && !WIDE;         // remainders in columns 4-7
-    constexpr bool REST2 = !INT8 && WIDE;           // remainders in a second product
+    constexpr bool REST2 = !INT8 && WIDE;           // the queries' remainders in a second product
     constexpr int QROWS = PAIRED ? 4 : 8;           // query rows that the products read
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 255) & ~uintptr_t(255));
@@ -604,15 +608,13 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         }
         uint32_t pa = pack16<INT8>(c[0], c[1]), pb = pack16<INT8>(c[2], c[3]);
         uint32_t ra_t = 0, rb_t = 0;
-        if constexpr (!INT8) {
-            const uint32_t ra = pack16_rest<false>(c[0], c[1], pa), rb = pack16_rest<false>(c[2], c[3], pb);
-            if constexpr (REST2) {
-                ra_t = movmatrix_trans(ra);
-                rb_t = movmatrix_trans(rb);
-            } else if (q4 >= 2) {                    // columns 4-7: the remainders of heads 0-3
-                pa = ra;
-                pb = rb;
-            }
+        const uint32_t ra = pack16_rest<INT8>(c[0], c[1], pa), rb = pack16_rest<INT8>(c[2], c[3], pb);
+        if constexpr (!PAIRED) {
+            ra_t = movmatrix_trans(ra);
+            rb_t = movmatrix_trans(rb);
+        } else if (q4 >= 2) {                        // columns 4-7: the remainders of heads 0-3
+            pa = ra;
+            pb = rb;
         }
         const uint32_t pa_t = movmatrix_trans(pa), pb_t = movmatrix_trans(pb);
 
@@ -631,6 +633,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
                     const uint32_t af[4] = {codes_f16x2<0x4240>(raw[2 * j]), codes_f16x2<0x4341>(raw[2 * j]),
                                             codes_f16x2<0x4240>(raw[2 * j + 1]), codes_f16x2<0x4341>(raw[2 * j + 1])};
                     mma16<true>(o[2 * k2 + j], af, pa_t, pb_t);
+                    mma16<true>(o[2 * k2 + j], af, ra_t, rb_t);
                 }
             }
         } else {

@@ -99,3 +99,30 @@ def test_slow_pairs_near_position_0(P, interleaved):  # noqa: F811
     for got, want in ((cos, angle.cos()), (sin, angle.sin())):
         # bf16's rounding, and 6 steps of binary32
         assert ((got - want).abs() <= (R.U16 + 12 * R.U32) * want.abs()).all()
+
+
+@pytest.mark.parametrize("d,hkv,group,n", [(128, 2, 8, 1), (128, 8, 4, 66), (64, 1, 1, 3), (64, 4, 3, 40), (128, 8, 2, 20)])
+def test_int8_weights_keep_their_bits(P, d, hkv, group, n):  # noqa: F811
+    """Two tokens of the same score and opposite V codes, whose V scales differ by less
+    than 2^-9: what is left is a difference of weights, which shows their rounding."""
+    bs, hq = 16, hkv * group
+    gen = torch.Generator().manual_seed(d + n)
+    row = torch.randint(1, 128, (n, hkv, d), generator=gen, dtype=torch.int8)
+    row[..., 5] = 127
+    kp, vp = (torch.zeros((n + 1, bs, hkv, d), dtype=torch.int8) for _ in range(2))
+    ks, vs = torch.ones((n + 1, bs, hkv)) * 0.01, torch.ones((n + 1, bs, hkv))
+    kp[:n, :2], vp[:n, 0], vp[:n, 1] = row[:, None], row, -row
+    scales = 0.01 * (1 + torch.rand((n, 2, hkv), generator=gen) * 2.0 ** -9)
+    vs[:n, :2] = scales
+    q = torch.randn((n, hq, d), generator=gen).to(torch.bfloat16)
+    tab, ctx = torch.arange(n, dtype=torch.int32)[:, None], torch.full((n,), 2, dtype=torch.int32)
+    q, kp, vp, ks, vs, tab, ctx = _cuda(q, kp, vp, ks, vs, tab, ctx)
+    out = P.paged_decode_attention_window(q, kp, vp, tab, ctx, d ** -0.5, 64, k_scales=ks, v_scales=vs)
+    sc = scales.double()[..., None]
+    want = (sc[:, 0] - sc[:, 1]) * row.double() / 2               # [n, hkv, d]
+    size = (sc[:, 0] + sc[:, 1]) * row.double() / 2
+    # the output's rounding; weights held to 2^-22, and sums of one tile and the joins (as
+    # window_reference.decode_tolerance has them), against a rounding to fp16 of 2^-12 on average
+    tol = R.U16 * want.abs() + size * (2.0 ** -22 + (2 / 16 + 32) * 32 * R.U32)
+    got = out.cpu().double().view(n, hkv, group, d)
+    assert ((got - want[:, :, None]).abs() <= tol[:, :, None]).all()
