@@ -1,12 +1,14 @@
 """The windowed and rotary calls where something is wrong with a call or its
 neighbour: waits that run out with another call behind them, chunks that run past
 the table, and the calls around them, which have to stay right."""
+import threading
+
 import pytest
 import torch
 
 import window_reference as R
 
-from test_gpu_window import P, _cuda, _paged  # noqa: F401  (P: the fixture)
+from test_gpu_window import GARBAGE_ID, P, _check_decode, _cuda, _paged  # noqa: F401  (P: the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +128,183 @@ def test_int8_weights_keep_their_bits(P, d, hkv, group, n):  # noqa: F811
     tol = R.U16 * want.abs() + size * (2.0 ** -22 + (2 / 16 + 32) * 32 * R.U32)
     got = out.cpu().double().view(n, hkv, group, d)
     assert ((got - want[:, :, None]).abs() <= tol[:, :, None]).all()
+
+
+def _quantised(x):
+    """Rows [..., D] (64 bits) as the values of their int8 codes."""
+    step = x.abs().amax(-1, keepdim=True) / 127
+    return torch.where(step > 0, torch.round(x / step.clamp(min=1e-300)).clamp(-127, 127) * step, torch.zeros_like(x))
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("hkv,group,d", [(2, 4, 64), (4, 6, 128)])
+def test_step_with_bad_positions_blocks_and_inactive_sequences(P, hkv, group, d, int8):  # noqa: F811
+    """A new row without a place is reported, written nowhere and not attended; inactive
+    sequences share the scratch block; the other sequences and blocks are as ever."""
+    bs, window, sinks, hq, scale = 16, 40, 4, hkv * group, d ** -0.5
+    #       good  before 0  past the table  bad block  inactive (two)
+    lens = [100, 100, 70, 65, 1, 3]
+    n = len(lens)
+    pools, scales, tables, values = _paged(d, lens, window, sinks, 1, hkv, d, bs, int8)
+    scratch, bad = pools[0].shape[0] - 1, 3
+    start = torch.tensor([x - 1 for x in lens], dtype=torch.int32)
+    start[1], start[2] = -1, tables.shape[1] * bs
+    tables[bad, 64 // bs] = scratch + 1
+    tables[4:] = scratch
+    gen = torch.Generator().manual_seed(7)
+    x = torch.randn((n, 1, hq + 2 * hkv, d), generator=gen).to(torch.bfloat16)
+    q, k, v = x.cuda().split((hq, hkv, hkv), dim=2)
+    kp, vp, ks, vs, tab, sp = _cuda(*pools, *scales, tables, start)
+    ctx = torch.tensor(lens, dtype=torch.int32).cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lse = torch.zeros((n, hq), device="cuda")
+    out = P.paged_decode_step_window(k, v, sp, q[:, 0], kp, vp, tab, ctx, scale, window, sinks, k_scales=ks, v_scales=vs,
+                                     lse_out=lse, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 1 | 2
+    # every block but the scratch one and the good sequence's row is as it was
+    place = int(tables[0, 99 // bs]) * bs + 99 % bs
+    for got, was in ((kp, pools[0]), (vp, pools[1]), (ks, scales[0]), (vs, scales[1])):
+        if was is not None:
+            a, b = (t.cpu().contiguous().view(torch.uint8).view(scratch + 1, bs, -1)[:scratch].reshape(scratch * bs, -1) for t in (got, was))
+            kept = torch.arange(scratch * bs) != place
+            assert torch.equal(a[kept], b[kept])
+    # the good sequence sees its new row, those without a position what the pages held before
+    for which, new in enumerate((k, v)):
+        new = new[0, 0].cpu().double()
+        values[0][which][99] = _quantised(new) if int8 else new
+    pick = [0, 1, 2]
+    _check_decode(out[pick], lse[pick], x[pick, 0, :hq], [values[s] for s in pick], [lens[s] for s in pick], window, sinks, hkv,
+                  scale, int8)
+    # the bad block's tokens are absent
+    seen = R.visible(64, 65, window, sinks)
+    seen[64:] = False
+    for h in range(hkv):
+        o, _, absum, size, top = (t[0] for t in R.attend(x[bad, 0, :hq].double().view(hkv, group, d)[h][None], values[bad][0][:, h],
+                                                         values[bad][1][:, h], seen[None], scale))
+        assert ((out[bad].cpu().double().view(hkv, group, d)[h] - o).abs()
+                <= R.decode_tolerance(o, absum, size, d, int(seen.sum()), top if int8 else None)).all()
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_calls_from_two_threads_on_two_streams(P, native, monkeypatch):  # noqa: F811
+    """Two threads, each with pages, plan and stream of its own, run write, chunk and
+    steps at the same time: the bits of the same calls one after another."""
+    if not native:
+        monkeypatch.setattr(P, "_native", None)
+    bs, window, sinks, hkv, group, d, chunk, steps = 16, 70, 4, 4, 4, 128, 90, 40
+    hq, scale, rope = hkv * group, d ** -0.5, P.Rope(d)
+    # (a sequence more in the second: other cluster and unit counts)
+    inputs = []
+    for n in (2, 3):
+        gen = torch.Generator().manual_seed(n)
+        width = -(-(chunk + steps) // bs)
+        tab = torch.randperm(n * width, generator=gen).to(torch.int32).view(n, width).cuda()
+        xs = torch.randn((steps + 1, n, chunk, hq + 2 * hkv, d), generator=gen).to(torch.bfloat16).cuda()
+        inputs.append((n, width, tab, xs))
+
+    def work(n, width, tab, xs):
+        kp, vp = (torch.zeros((n * width + 1, bs, hkv, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        start = torch.zeros(n, dtype=torch.int32, device="cuda")
+        q, k, v = xs[0].split((hq, hkv, hkv), dim=2)
+        qt = P.paged_kv_write_rope(q, k, v, rope, kp, vp, tab, start)
+        outs = [P.paged_prefill_attention_window(qt, kp, vp, tab, start, scale, window, sinks)]
+        start += chunk
+        ctx = start + 1
+        plan = P.WindowDecodePlan(kp, vp, tab, ctx, scale, hq, window, sinks, rope=rope)
+        for x in xs[1:]:
+            q, k, v = x[:, :1].split((hq, hkv, hkv), dim=2)
+            outs.append(plan.run(q[:, 0], k, v, start).clone())
+            start += 1
+            ctx += 1
+        return outs + [kp, vp]
+
+    want = [work(*i) for i in inputs]
+    torch.cuda.synchronize()
+    got, errors, gate = [None, None], [], threading.Barrier(2)
+
+    def run(i):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                gate.wait(30)
+                got[i] = work(*inputs[i])
+            stream.synchronize()
+        except Exception as e:      # for the test's own thread
+            errors.append(e)
+
+    for _ in range(3):
+        threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not errors, errors
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_chunks_written_then_steps_over_int8_pages(P):  # noqa: F811
+    """Prompts written in chunks into int8 pages, then steps, one of them captured and
+    replayed, blocks behind the window freed as the sequences grow; against one 64-bit
+    attention over what the pages stand for."""
+    window, sinks, hkv, group, d, bs, rot, chunk = 48, 4, 2, 4, 64, 16, 32, 23
+    hq, scale, prompt, steps = hkv * group, d ** -0.5, [70, 45, 20], 24
+    n, total = len(prompt), [p + steps for p in prompt]
+    gen = torch.Generator().manual_seed(45)
+    qkv = [torch.randn((t, hq + 2 * hkv, d), generator=gen).to(torch.bfloat16) for t in total]
+    width = max(-(-t // bs) for t in total)
+    pools = [torch.full((n * width + 1, bs, hkv, d), 127, dtype=torch.int8, device="cuda") for _ in range(2)]
+    scales = [torch.full((n * width + 1, bs, hkv), float("nan"), device="cuda") for _ in range(2)]
+    tables = torch.randperm(n * width, generator=gen).to(torch.int32).view(n, width)
+    whole = tables.clone()
+    rope, st = P.Rope(rot), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for s in range(n):
+        for c0 in range(0, prompt[s], chunk):
+            x = qkv[s][None, c0:min(c0 + chunk, prompt[s])].cuda()
+            q, k, v = x.split((hq, hkv, hkv), dim=2)
+            P.paged_kv_write_rope(q, k, v, rope, *pools, tables[s:s + 1].cuda(), torch.tensor([c0], dtype=torch.int32, device="cuda"),
+                                  k_scales=scales[0], v_scales=scales[1], dev_status=st)
+    start = torch.tensor(prompt, dtype=torch.int32, device="cuda")
+    ctx, tab = start + 1, tables.cuda()
+    lse = torch.zeros((n, hq), device="cuda")
+    plan = P.WindowDecodePlan(*pools, tab, ctx, scale, hq, window, sinks, rope=rope, k_scales=scales[0], v_scales=scales[1],
+                              lse_out=lse, dev_status=st)
+    x = torch.zeros((n, 1, hq + 2 * hkv, d), dtype=torch.bfloat16, device="cuda")
+    q, k, v = x.split((hq, hkv, hkv), dim=2)
+    graph, got = None, []
+    for i in range(steps):
+        for s in range(n):
+            for b in range(width):
+                if not any(t < sinks or t > prompt[s] + i - window for t in range(b * bs, (b + 1) * bs)):
+                    tables[s, b] = GARBAGE_ID
+        tab.copy_(tables)
+        x.copy_(torch.stack([qkv[s][prompt[s] + i] for s in range(n)])[:, None])
+        if i == steps // 2:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                plan.run(q[:, 0], k, v, start)
+        if graph is None:
+            plan.run(q[:, 0], k, v, start)
+        else:
+            graph.replay()
+        got.append((plan.out.cpu(), lse.cpu()))
+        start += 1
+        ctx += 1
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    inv, mag = R.frequencies(rot)
+    for s in range(n):
+        t = torch.arange(total[s])
+        rows = whole[s].long()[t // bs] * bs + t % bs
+        held = [p.cpu().view(-1, hkv, d)[rows].double() * sc.cpu().view(-1, hkv)[rows].double()[..., None] for p, sc in zip(pools, scales)]
+        # the pages: nearest codes of the turned keys and of the values
+        kt, ksize = R.turn(qkv[s][:, hq:hq + hkv].double(), t, inv, mag, False)
+        for x64, size, page, sc in ((kt, ksize, held[0], scales[0]), (qkv[s][:, hq + hkv:].double(), 0, held[1], scales[1])):
+            step = sc.cpu().view(-1, hkv)[rows].double()[..., None]
+            assert ((page - x64).abs() <= step * (0.5 + 2.0 ** -14) + R.TURN * size).all()
+        for i in range(steps):
+            p = prompt[s] + i
+            qt, _ = R.turn(qkv[s][p:p + 1, :hq].double(), torch.tensor([p]), inv, mag, False)
+            _check_decode(got[i][0][s:s + 1], got[i][1][s:s + 1], None, [[h[:p + 1] for h in held]], [p + 1], window, sinks, hkv,
+                          scale, True, qt)
