@@ -65,7 +65,7 @@ int paged_decode_step_window(const pkv_bf16 *k_new, int64_t k_stride, const pkv_
                              int32_t sinks, pkv_bf16 *out, float *lse_out, int32_t *dev_status, pkv_stream_t stream);
 
 /*
- * paged_prefill_attention_window -- paged_prefill_attention under the mask
+ * paged_prefill_attention_window -- paged_prefill_attention (bf16 pages) under the mask
  * above: query i of sequence s sits at position prefix_lens[s] + i.  Key tiles
  * that no query of a CTA's rows sees are not loaded, so the work grows with
  * the window and not with the prefix.  A sequence whose length is bad (prefix_lens[s]

@@ -862,8 +862,9 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 // CTAs that do not fill the machine are spread over it by shared memory that is
 // asked for but not used: placed as they come, behind a kernel that is draining,
 // some SMs take as many as they hold and others none.  Measured (windows of 1024,
-// 8 kv heads of 128, int8 pages, as placed / spread): 8 sequences 10.8 / 9.3 us,
-// 28: 19.7 / 17.0, 56: 29.7 / 25.5; bf16 pages, bound by memory, are 0 to 4 % faster.
+// 8 kv heads of 128, int8 pages, as placed / spread): 28 sequences 19.2 / 16.7 us; no
+// difference at 8 and 56, whose CTAs fill the SMs evenly either way; bf16 pages, bound by
+// memory, are 0 to 4 % faster.
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cudaStream_t stream)
 {
@@ -888,16 +889,16 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cu
 // once the units are more than the larger CTAs' places.  Measured (4 warps / 2 warps;
 // windows of 1024, 8 kv heads of 128): bf16 pages, 32 sequences 23.6 / 24.7 us,
 // 40: 37.9 / 30.3, 64: 45.4 / 42.9, 80: 61.7 / 66.4, 128: 87.5 / 82.3; int8 pages,
-// 12 sequences 11.1 / 11.5, 48: 29.4 / 24.5, 64: 31.0 / 38.6, 80: 43.2 / 39.2,
-// 128: 52.3 / 68.4.
+// 12 sequences 10.0 / 14.7, 48: 24.6 / 25.0, 64: 30.4 / 32.1, 80: 42.8 / 41.0,
+// 128: 52.6 / 69.3.
 //
 // Of 8, for units that are all resident, where that shortens the longest share of a
 // warp (a cluster has 16 CTAs at most), where it needs no cluster and CTAs of 4 do, or
 // where there are more CTAs of 4 than SMs anyway.  Measured (4 warps / 8 warps; window
 // and first tokens together): bf16 pages, 4 sequences of 256 visible tokens 5.4 / 5.0
 // us, 12: 6.4 / 5.4; 1024 tokens, one sequence 5.7 / 6.1, 4: 7.4 / 6.4, 16: 15.0 / 14.1;
-// 16 K tokens, one 19.7 / 17.4, two 26.4 / 27.3; int8 pages, 1024 tokens, 4: 12.1 / 7.1,
-// 16: 13.9 / 11.6; 16 K, one 21.1 / 16.0, two 27.1 / 24.2.
+// 16 K tokens, one 19.7 / 17.4, two 26.4 / 27.3; int8 pages, 1024 tokens, 4: 7.5 / 6.9,
+// 16: 13.1 / 11.7; 16 K, one 21.2 / 16.0, two 27.0 / 24.5.
 template <int D, bool INT8, bool WIDE>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {

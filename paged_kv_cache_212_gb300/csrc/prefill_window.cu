@@ -36,6 +36,12 @@
 // O goes out from registers, a row of head_dim values a thread: the shared memory
 // that could stage it holds the next unit's tiles by then.
 //
+// Rounding.  Scores, maxima, sums and O are binary32.  P is rounded once to bf16 (2^-9 of
+// a probability at most), as in prefill_tc.cu: a product on the tensor cores takes P and
+// V in one type, and P's remainder would need a second product and as many TMEM stores
+// again.  Against 64 bits the outputs are 0.0021 to 0.0023 off (the norm of the difference
+// over theirs), where their own rounding to bf16 makes 0.0016.
+//
 // Measured (32 query and 8 kv heads of 128, kernels back to back).  8 x 512 tokens,
 // window 1024: 74 us with prefixes of 2 to 8 K, and 77.5 with prefixes of 0 to 8 K whose
 // last sequence is the shortest (the halves are small ones then), 818 TFLOP/s of
