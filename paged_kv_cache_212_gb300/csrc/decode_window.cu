@@ -862,9 +862,8 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 // CTAs that do not fill the machine are spread over it by shared memory that is
 // asked for but not used: placed as they come, behind a kernel that is draining,
 // some SMs take as many as they hold and others none.  Measured (windows of 1024,
-// 8 kv heads of 128, int8 pages, as placed / spread): 28 sequences 19.2 / 16.7 us; no
-// difference at 8 and 56, whose CTAs fill the SMs evenly either way; bf16 pages, bound by
-// memory, are 0 to 4 % faster.
+// 8 kv heads of 128, int8 pages, as placed / spread): 28 sequences 19.2 / 16.7 us, no
+// difference at 8 and 56; bf16 pages, bound by memory, are 0 to 4 % faster.
 template <int D, bool INT8, bool WIDE, int WARPS>
 cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cudaStream_t stream)
 {

@@ -36,7 +36,7 @@
 // O goes out from registers, a row of head_dim values a thread: the shared memory
 // that could stage it holds the next unit's tiles by then.
 //
-// Rounding.  Scores, maxima, sums and O are binary32.  P is rounded once to bf16 (2^-9 of
+// Rounding.  Scores, maxima, sums and O are binary32.  P is rounded once to bf16 (2^-8 of
 // a probability at most), as in prefill_tc.cu: a product on the tensor cores takes P and
 // V in one type, and P's remainder would need a second product and as many TMEM stores
 // again.  Against 64 bits the outputs are 0.0021 to 0.0023 off (the norm of the difference
