@@ -73,7 +73,8 @@ enum pkv_dev_status {
     PKV_DEV_BAD_POSITION = 2,        /* a write position < 0 or beyond the table width */
     PKV_DEV_BAD_LENGTH = 4,          /* a length < 0 or > max_blocks * block_size */
     PKV_DEV_WORKSPACE_OVERFLOW = 8,  /* decode work list larger than the workspace holds */
-    PKV_DEV_TIMEOUT = 16             /* a bounded pipeline wait ran out (never expected) */
+    PKV_DEV_TIMEOUT = 16,            /* a bounded pipeline wait ran out (never expected) */
+    PKV_DEV_OUT_OF_BLOCKS = 32       /* paged_step_maps: the free list has run out */
 };
 
 /* KV page formats (libmir-metal paged/mod.rs, KvPageFormat). */

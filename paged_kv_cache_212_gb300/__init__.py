@@ -16,6 +16,7 @@ import ctypes
 import importlib.util
 import os
 import sysconfig
+import typing
 import warnings
 
 import torch
@@ -27,7 +28,7 @@ NATIVE_PATH = os.path.join(HERE, f"_native-{torch.__version__}{sysconfig.get_con
 
 PKV_KV_BF16, PKV_KV_INT8 = 0, 1
 DEV_BAD_BLOCK_ID, DEV_BAD_POSITION, DEV_BAD_LENGTH = 1, 2, 4
-DEV_WORKSPACE_OVERFLOW, DEV_TIMEOUT = 8, 16
+DEV_WORKSPACE_OVERFLOW, DEV_TIMEOUT, DEV_OUT_OF_BLOCKS = 8, 16, 32
 
 EXPORTS = ("pkv_status_string", "pkv_last_cuda_error", "pkv_set_pipeline_wait_ns", "paged_kv_write",
            "paged_kv_write_int8",
@@ -44,7 +45,10 @@ EXPORTS = ("pkv_status_string", "pkv_last_cuda_error", "pkv_set_pipeline_wait_ns
            # rotary positions written into the pages (include/pagedkv_rope.h)
            "pkv_rope_phases", "paged_kv_write_rope",
            # sliding window with first tokens (include/pagedkv_window.h)
-           "paged_decode_attention_window", "paged_decode_step_window", "paged_prefill_attention_window")
+           "paged_decode_attention_window", "paged_decode_step_window", "paged_prefill_attention_window",
+           # batches of requests of any lengths (include/pagedkv_batch.h)
+           "paged_step_maps", "paged_kv_write_slots", "pkv_rows_workspace_bytes", "paged_cross_attention",
+           "paged_decode_attention_shared")
 NOALLOC_DECODE_SCRATCH_BYTES = 16 * 1024 * 1024
 
 
@@ -174,6 +178,16 @@ def load_library(path: str = LIB_PATH):
     lib.paged_prefill_attention_window.argtypes = [P, i32, P, P, Dims, P, i32, P, i32, i32, f32, i32, i32, P, P, P, P]
     for fn in ("pkv_rope_phases", "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
                "paged_prefill_attention_window"):
+        getattr(lib, fn).restype = ctypes.c_int
+    lib.paged_step_maps.argtypes = [P, P, i32, P, i32, P, i32, i32, P, i32, i32, P, P, P, P, P, P, P, P]
+    lib.paged_kv_write_slots.argtypes = [P, i64, P, i64, P, P, P, P, i32, Dims, P, i32, P, P]
+    lib.pkv_rows_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.pkv_rows_workspace_bytes.restype = sz
+    lib.paged_cross_attention.argtypes = [P, i64, i32, P, i32, P, P, P, P, i32, Dims, P, i32, P, i32, f32, P, P, P, sz, P,
+                                          P]
+    lib.paged_decode_attention_shared.argtypes = [P, i64, i32, P, P, P, P, i32, Dims, P, i32, P, i32, P, i32, P, i32, P,
+                                                  f32, P, P, P, sz, P, P]
+    for fn in ("paged_step_maps", "paged_kv_write_slots", "paged_cross_attention", "paged_decode_attention_shared"):
         getattr(lib, fn).restype = ctypes.c_int
     _native = _load_native(lib)
     _lib = lib
@@ -741,6 +755,13 @@ def _empty(shape, dtype, dev, stream):
 
 def _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev):
     """Pools of bf16 or int8 (with scales) pages and their tables; True for int8."""
+    int8 = _check_pool_kinds(k_pool, v_pool, k_scales, v_scales, dev)
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    return int8
+
+
+def _check_pool_kinds(k_pool, v_pool, k_scales, v_scales, dev):
+    """Pools of bf16 or int8 (with scales) pages; True for int8."""
     int8 = k_pool.dtype is torch.int8
     kind = torch.int8 if int8 else torch.bfloat16
     _need(k_pool, "k_pool", kind, 4, dev)
@@ -751,7 +772,6 @@ def _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev):
         _check_pools(k_pool, v_pool, k_scales, v_scales)
     else:
         _check_pools(k_pool, v_pool)
-    _need(block_tables, "block_tables", torch.int32, 2, dev)
     return int8
 
 
@@ -958,6 +978,230 @@ def paged_prefill_attention_window(q, k_pool, v_pool, block_tables, prefix_lens,
                                             _ptr(out), _ptr(lse_out), _ptr(dev_status), _stream(stream))
     _check("paged_prefill_attention_window", st)
     return out
+
+
+# ---- batches of requests of any lengths ---------------------------------------
+
+class StepMaps(typing.NamedTuple):
+    """The maps of a step (paged_step_maps): ctx_lens [n_seqs], token_starts
+    [n_seqs + 1], token_seqs and positions [n_tokens], cursor [1] int32, slots
+    [n_tokens] int64."""
+    ctx_lens: torch.Tensor
+    token_starts: torch.Tensor
+    token_seqs: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    cursor: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_seqs, n_tokens, device, stream=None):
+        """Uninitialised maps for paged_step_maps to write into."""
+        dev = torch.device(device)
+        return cls(*(_empty((n,), torch.int64 if i == 4 else torch.int32, dev, stream)
+                     for i, n in enumerate((n_seqs, n_seqs + 1, n_tokens, n_tokens, n_tokens, 1))))
+
+
+def paged_step_maps(lens, n_new, free_blocks, block_tables, block_size, n_blocks, n_tokens, cursor=None, out=None,
+                    dev_status=None, stream=None):
+    """The block tables and slot maps of a step, built on the device: sequence s
+    holds lens[s] tokens and adds n_new[s]; the blocks that it needs for them are
+    the next of free_blocks (behind the cursor[0] entries that earlier steps
+    have taken) and go into its row of block_tables.  n_tokens: the rows of the
+    packed batch, at least sum(n_new).  ``out`` (a StepMaps) is written into;
+    lens and ctx_lens, cursor and out.cursor have to be different tensors.
+    Returns the StepMaps."""
+    dev = _device_of(block_tables, "block_tables")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_step_maps(lens, n_new, free_blocks, block_tables, block_size, n_blocks, n_tokens, cursor, out,
+                                   dev_status, stream)
+    lib = load_library()
+    _need(block_tables, "block_tables", torch.int32, 2, dev)
+    n_seqs = block_tables.shape[0]
+    for t, name in ((lens, "lens"), (n_new, "n_new")):
+        _need(t, name, torch.int32, 1, dev)
+        _shape(t, name, (n_seqs,))
+    _need(free_blocks, "free_blocks", torch.int32, 1, dev)
+    if cursor is not None:
+        _need(cursor, "cursor", torch.int32, 1, dev)
+        _shape(cursor, "cursor", (1,))
+    _check_status(dev_status, dev)
+    n_tokens = int(n_tokens)
+    if n_tokens < 0:
+        raise ValueError(f"n_tokens must not be negative, got {n_tokens}")
+    if out is None:
+        out = StepMaps.empty(n_seqs, n_tokens, torch.device("cuda", dev), stream)
+    elif not isinstance(out, StepMaps):
+        raise TypeError("out must be a StepMaps")
+    else:
+        for name, n in zip(StepMaps._fields, (n_seqs, n_seqs + 1, n_tokens, n_tokens, n_tokens, 1)):
+            t = getattr(out, name)
+            _need(t, name, torch.int64 if name == "slots" else torch.int32, 1, dev)
+            _shape(t, name, (n,))
+    st = lib.paged_step_maps(_ptr(lens), _ptr(n_new), n_seqs, _ptr(free_blocks), free_blocks.shape[0], _ptr(cursor),
+                             int(n_blocks), int(block_size), _ptr(block_tables), block_tables.shape[1], n_tokens,
+                             _ptr(out.ctx_lens), _ptr(out.token_starts), _ptr(out.token_seqs), _ptr(out.positions),
+                             _ptr(out.slots), _ptr(out.cursor), _ptr(dev_status), _stream(stream))
+    _check("paged_step_maps", st)
+    return out
+
+
+def paged_kv_write_slots(k_new, v_new, k_pool, v_pool, slots, k_scales=None, v_scales=None, dev_status=None,
+                         stream=None):
+    """Packed rows to their pool rows: row i of k_new / v_new [n_rows, Hkv, D]
+    bf16 (they may be parts of a fused projection's rows) goes to pool row
+    slots[i] (int64; negative: nowhere), as it is or, into int8 pools, quantised
+    with k_scales / v_scales."""
+    dev = _device_of(k_pool, "k_pool")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_kv_write_slots(k_new, v_new, k_pool, v_pool, slots, k_scales, v_scales, dev_status, stream)
+    lib = load_library()
+    int8 = _check_pool_kinds(k_pool, v_pool, k_scales, v_scales, dev)
+    ks, vs = _token_stride(k_new, "k_new", 3, dev), _token_stride(v_new, "v_new", 3, dev)
+    n_rows = k_new.shape[0]
+    _shape(k_new, "k_new", (n_rows,) + tuple(k_pool.shape[2:]))
+    _shape(v_new, "v_new", k_new.shape)
+    _need(slots, "slots", torch.int64, 1, dev)
+    _shape(slots, "slots", (n_rows,))
+    _check_status(dev_status, dev)
+    st = lib.paged_kv_write_slots(_ptr(k_new), ks, _ptr(v_new), vs, _ptr(k_pool), _ptr(v_pool), _ptr(k_scales),
+                                  _ptr(v_scales), PKV_KV_INT8 if int8 else PKV_KV_BF16, _dims(k_pool), _ptr(slots),
+                                  n_rows, _ptr(dev_status), _stream(stream))
+    _check("paged_kv_write_slots", st)
+
+
+def rows_workspace_bytes(n_rows, n_q_heads, head_dim) -> int:
+    """Device workspace of paged_cross_attention for n_rows packed query rows, and of
+    paged_decode_attention_shared for n_rows sequences (pkv_rows_workspace_bytes)."""
+    n = load_library().pkv_rows_workspace_bytes(int(n_rows), int(n_q_heads), int(head_dim))
+    if n == 0:
+        raise ValueError("invalid arguments to pkv_rows_workspace_bytes")
+    return int(n)
+
+
+def _rows_buffers(q, out, lse_out, workspace, dev, stream):
+    """out and workspace of a call over packed query rows, made where they are not given."""
+    n_rows, n_q_heads, D = q.shape
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    else:
+        _need(out, "out", torch.bfloat16, 3, dev)
+        _shape(out, "out", q.shape)
+    if lse_out is not None:
+        _need(lse_out, "lse_out", torch.float32, 2, dev)
+        _shape(lse_out, "lse_out", q.shape[:2])
+    if workspace is None:
+        workspace = _empty((rows_workspace_bytes(n_rows, n_q_heads, D),), torch.uint8, dev, stream)
+    _need(workspace, "workspace", torch.uint8, 1, dev)
+    return out, workspace
+
+
+def paged_cross_attention(q, q_starts, k_pool, v_pool, block_tables, key_lens, softmax_scale, k_scales=None,
+                          v_scales=None, out=None, lse_out=None, workspace=None, dev_status=None, stream=None):
+    """Attention of packed queries to keys of another length, without a causal
+    mask: rows q_starts[s] .. q_starts[s + 1] - 1 of q [n_rows, Hq, D] bf16 (its
+    tokens may be a stride apart) see the key_lens[s] tokens of sequence s's
+    pages, bf16 or int8 with k_scales / v_scales.  Rows of no sequence are left
+    as they were.  ``workspace`` (uint8, rows_workspace_bytes) is allocated when
+    not given.  Returns out [n_rows, Hq, D] bf16."""
+    dev = _device_of(q, "q")
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return paged_cross_attention(q, q_starts, k_pool, v_pool, block_tables, key_lens, softmax_scale, k_scales,
+                                         v_scales, out, lse_out, workspace, dev_status, stream)
+    lib = load_library()
+    int8 = _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev)
+    qs = _token_stride(q, "q", 3, dev)
+    n_rows, n_q_heads, D = q.shape
+    if D != k_pool.shape[3]:
+        raise ValueError(f"q has head_dim {D}, the pool {k_pool.shape[3]}")
+    n_seqs = block_tables.shape[0]
+    _need(key_lens, "key_lens", torch.int32, 1, dev)
+    _shape(key_lens, "key_lens", (n_seqs,))
+    _need(q_starts, "q_starts", torch.int32, 1, dev)
+    _shape(q_starts, "q_starts", (n_seqs + 1,))
+    _check_status(dev_status, dev)
+    out, workspace = _rows_buffers(q, out, lse_out, workspace, dev, stream)
+    st = lib.paged_cross_attention(_ptr(q), qs, n_q_heads, _ptr(q_starts), n_rows, _ptr(k_pool), _ptr(v_pool),
+                                   _ptr(k_scales), _ptr(v_scales), PKV_KV_INT8 if int8 else PKV_KV_BF16, _dims(k_pool),
+                                   _ptr(block_tables), block_tables.shape[1], _ptr(key_lens), n_seqs,
+                                   float(softmax_scale), _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
+                                   _ptr(dev_status), _stream(stream))
+    _check("paged_cross_attention", st)
+    return out
+
+
+class SharedDecodePlan:
+    """paged_decode_attention_shared with the arguments that stay the same from
+    call to call checked once, as DecodePlan does for paged_decode_attention (and
+    with the same conditions on the planned tensors; calls of one plan share its
+    workspace, so they must not run at once)."""
+
+    def __init__(self, k_pool, v_pool, block_tables, ctx_lens, group_starts, prefix_tables, prefix_lens, softmax_scale,
+                 n_q_heads, k_scales=None, v_scales=None, out=None, lse_out=None, workspace=None, dev_status=None):
+        dev = _device_of(k_pool, "k_pool")
+        self._lib = load_library()
+        int8 = _check_paged(k_pool, v_pool, k_scales, v_scales, block_tables, dev)
+        n_seqs, D = block_tables.shape[0], k_pool.shape[3]
+        _need(ctx_lens, "ctx_lens", torch.int32, 1, dev)
+        _check_batch(n_seqs, block_tables, ctx_lens, "ctx_lens")
+        _need(prefix_tables, "prefix_tables", torch.int32, 2, dev)
+        _need(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+        _need(group_starts, "group_starts", torch.int32, 1, dev)
+        n_groups = prefix_tables.shape[0]
+        _shape(prefix_lens, "prefix_lens", (n_groups,))
+        _shape(group_starts, "group_starts", (n_groups + 1,))
+        self.q_shape = torch.Size((n_seqs, int(n_q_heads), D))
+        if out is None:
+            out = torch.empty(self.q_shape, dtype=torch.bfloat16, device=dev)
+        _need(out, "out", torch.bfloat16, 3, dev)
+        _shape(out, "out", self.q_shape)
+        if lse_out is not None:
+            _need(lse_out, "lse_out", torch.float32, 2, dev)
+            _shape(lse_out, "lse_out", self.q_shape[:2])
+        if workspace is None:
+            workspace = torch.empty(rows_workspace_bytes(n_seqs, n_q_heads, D), dtype=torch.uint8, device=dev)
+        _need(workspace, "workspace", torch.uint8, 1, dev)
+        _check_status(dev_status, dev)
+        self.device, self.out, self.n_q_heads = dev, out, int(n_q_heads)
+        # held so that the pointers below stay valid
+        self._tensors = (k_pool, v_pool, k_scales, v_scales, block_tables, ctx_lens, group_starts, prefix_tables,
+                         prefix_lens, out, lse_out, workspace, dev_status)
+        self._args = (_ptr(k_pool), _ptr(v_pool), _ptr(k_scales), _ptr(v_scales), PKV_KV_INT8 if int8 else PKV_KV_BF16,
+                      pool_dims(k_pool), _ptr(block_tables), block_tables.shape[1], _ptr(ctx_lens), n_seqs,
+                      _ptr(group_starts), n_groups, _ptr(prefix_tables), prefix_tables.shape[1], _ptr(prefix_lens),
+                      float(softmax_scale), _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
+                      _ptr(dev_status))
+
+    def run(self, q, stream=None):
+        """q [n_seqs, Hq, D] bf16 (its tokens may be a stride apart).  Returns the plan's out."""
+        dev = self.device
+        if _elsewhere(dev):
+            with torch.cuda.device(dev):
+                return self.run(q, stream)
+        qs = _token_stride(q, "q", 3, dev)
+        _shape(q, "q", self.q_shape)
+        st = self._lib.paged_decode_attention_shared(q.data_ptr(), qs, self.n_q_heads, *self._args, _stream(stream))
+        _check("paged_decode_attention_shared", st)
+        return self.out
+
+
+def paged_decode_attention_shared(q, k_pool, v_pool, block_tables, ctx_lens, group_starts, prefix_tables, prefix_lens,
+                                  softmax_scale, k_scales=None, v_scales=None, out=None, lse_out=None, workspace=None,
+                                  dev_status=None, stream=None):
+    """paged_decode_attention for groups of sequences that share their first tokens:
+    sequences group_starts[g] .. group_starts[g + 1] - 1 see the prefix_lens[g]
+    tokens of prefix_tables[g], read once for all of them, and each goes on at
+    that position in its own row of block_tables (entries of blocks wholly within
+    the prefix are not read).  Returns out [n_seqs, Hq, D] bf16."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    out, workspace = _rows_buffers(q, out, lse_out, workspace, dev, stream)
+    plan = SharedDecodePlan(k_pool, v_pool, block_tables, ctx_lens, group_starts, prefix_tables, prefix_lens,
+                            softmax_scale, q.shape[1], k_scales, v_scales, out, lse_out, workspace, dev_status)
+    return plan.run(q, stream=stream)
 
 
 class BlockManager:

@@ -1,0 +1,122 @@
+// write_slots.cu -- packed new K and V rows to the pool rows that a slot map names
+// (pagedkv_batch.h, paged_kv_write_slots), as they are or quantised to int8.
+//
+// A piece is 16 elements of one head row: 32 bytes in, 32 or 16 bytes out.  A thread
+// takes one piece of K or V; a warp's pieces lie behind one another in a row, and the
+// row's slot is loaded beside them, so that the only dependent access is the store.
+// Lanes of a head row (4 or 8 of them) share its largest element.
+#include "common.cuh"
+#include "launch.h"
+#include "rope.cuh"
+#include "window.h"
+#include "../../include/pagedkv_batch.h"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct SlotArgs {
+    const __nv_bfloat16 *k_new, *v_new;
+    int64_t k_stride, v_stride;
+    void *k_pool, *v_pool;
+    float *k_scales, *v_scales;
+    const int64_t *slots;
+    int64_t pool_rows, n_rows;
+    int32_t n_kv_heads;
+    int32_t *dev_status;
+};
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(kThreads) write_slots_kernel(const SlotArgs a)
+{
+    constexpr int SLOTS = D / 16;                        // lanes per head row
+    grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
+    grid_dependency_wait();
+    const int32_t per_row = a.n_kv_heads * SLOTS;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x, half = i / per_row;
+    const int32_t piece = (int32_t)(i - half * per_row);
+    const int64_t r = half >> 1;
+    const bool is_v = half & 1, live = r < a.n_rows;     // (alike for the lanes of a head row)
+    uint4 x0 = make_uint4(0, 0, 0, 0), x1 = x0;
+    int64_t row = -1;
+    if (live) {
+        const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? a.v_new + r * a.v_stride : a.k_new + r * a.k_stride) + piece * 16);
+        x0 = __ldcs(src);
+        x1 = __ldcs(src + 1);
+        row = __ldg(a.slots + r);
+        if (row >= a.pool_rows) {
+            if (piece == 0 && !is_v) report(a.dev_status, PKV_DEV_BAD_POSITION);
+            row = -1;
+        }
+    }
+    const int64_t at = row * a.n_kv_heads * D + (int64_t)piece * 16;
+    if constexpr (!INT8) {
+        if (row < 0) return;
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + at);
+        dst[0] = x0;
+        dst[1] = x1;
+    } else {
+        float x[16];
+        unpack_bf16x8(x0, x);
+        unpack_bf16x8(x1, x + 8);
+        float amax = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, fabsf(x[e]));
+#pragma unroll
+        for (int off = 1; off < SLOTS; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        uint32_t w[4];
+        const float scale = int8_codes16(x, amax, w);
+        if (row < 0) return;
+        *reinterpret_cast<uint4 *>(static_cast<int8_t *>(is_v ? a.v_pool : a.k_pool) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (piece % SLOTS == 0) (is_v ? a.v_scales : a.k_scales)[row * a.n_kv_heads + piece / SLOTS] = scale;
+    }
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" int paged_kv_write_slots(const pkv_bf16 *k_new, int64_t k_stride, const pkv_bf16 *v_new, int64_t v_stride,
+                                    void *k_pool, void *v_pool, float *k_scales, float *v_scales, int32_t kv_dtype,
+                                    pkv_dims dims, const int64_t *slots, int32_t n_rows, int32_t *dev_status,
+                                    pkv_stream_t stream)
+{
+    const int st = check_dims(dims);
+    if (st != PKV_OK) return st;
+    if (n_rows < 0) return PKV_ERR_INVALID_ARG;
+    if (kv_dtype != PKV_KV_BF16 && kv_dtype != PKV_KV_INT8) return PKV_ERR_UNSUPPORTED;
+    if (!row_stride_ok(k_stride, dims.n_kv_heads, dims.head_dim) || !row_stride_ok(v_stride, dims.n_kv_heads, dims.head_dim))
+        return PKV_ERR_INVALID_ARG;
+    if (n_rows == 0) return PKV_OK;
+    const void *p[] = {k_new, v_new, k_pool, v_pool};
+    for (const void *x : p)
+        if (!x || !aligned16(x)) return PKV_ERR_INVALID_ARG;
+    if (!slots || (reinterpret_cast<uintptr_t>(slots) & 7u)) return PKV_ERR_INVALID_ARG;
+    const bool int8 = kv_dtype == PKV_KV_INT8;
+    if (int8 && (!k_scales || !v_scales ||
+                 ((reinterpret_cast<uintptr_t>(k_scales) | reinterpret_cast<uintptr_t>(v_scales)) & 3u)))
+        return PKV_ERR_INVALID_ARG;
+    SlotArgs a{reinterpret_cast<const __nv_bfloat16 *>(k_new), reinterpret_cast<const __nv_bfloat16 *>(v_new), k_stride,
+               v_stride, k_pool, v_pool, k_scales, v_scales, slots, (int64_t)(dims.n_blocks + 1) * dims.block_size, n_rows,
+               dims.n_kv_heads, dev_status};
+    const int64_t pieces = 2 * (int64_t)n_rows * dims.n_kv_heads * (dims.head_dim / 16);
+    const int64_t grid = (pieces + kThreads - 1) / kThreads;
+    if (grid > 0x7fffffffLL) return PKV_ERR_OUT_OF_RANGE;
+    cudaLaunchAttribute pdl[1];
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)grid);
+    lc.blockDim = dim3(kThreads);
+    lc.stream = (cudaStream_t)stream;
+    lc.attrs = pdl;
+    lc.numAttrs = 1;
+    cudaError_t e;
+    if (dims.head_dim == 128)
+        e = int8 ? cudaLaunchKernelEx(&lc, write_slots_kernel<128, true>, a) : cudaLaunchKernelEx(&lc, write_slots_kernel<128, false>, a);
+    else
+        e = int8 ? cudaLaunchKernelEx(&lc, write_slots_kernel<64, true>, a) : cudaLaunchKernelEx(&lc, write_slots_kernel<64, false>, a);
+    return cuda_status(e);
+}
