@@ -9,26 +9,10 @@
 namespace pkv {
 namespace {
 
-constexpr int kMaxCtas = 192;      // CTAs that share out the keys (workspace)
-constexpr int kUnitRows = 256;     // query head rows of a unit
 constexpr int kWarps = 4;
 
-// The run of row r: the last g with starts[g] <= r, if r lies below starts[g + 1]; else -1.
-__device__ __forceinline__ int32_t run_of(const RowsArgs &a, int32_t r)
-{
-    int32_t lo = -1, hi = a.n_runs;
-    while (hi - lo > 1) {
-        const int32_t mid = lo + (hi - lo) / 2;
-        if (__ldg(a.starts + mid) <= r)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo >= 0 && r < __ldg(a.starts + lo + 1) ? lo : -1;
-}
-
 template <int D, bool INT8>
-__global__ void __launch_bounds__(32 * kWarps) rows_kernel(const RowsArgs a)
+__global__ void __launch_bounds__(32 * kWarps) rows_plain_kernel(const RowsArgs a)
 {
     constexpr int PER = D / 32;                      // elements of a lane
     __shared__ float m_s[kWarps], l_s[kWarps], o_s[kWarps][D];
@@ -42,7 +26,7 @@ __global__ void __launch_bounds__(32 * kWarps) rows_kernel(const RowsArgs a)
             const int32_t x = __ldg(a.starts + i);
             if (x < 0 || x > a.n_rows || (i > 0 && x < __ldg(a.starts + i - 1))) report(a.dev_status, PKV_DEV_BAD_LENGTH);
         }
-    const int32_t g = run_of(a, r);
+    const int32_t g = run_of(a.starts, a.n_runs, r);
     const bool decode = a.ctx_lens != nullptr;
     if (g < 0 && !decode) return;                    // a row of no sequence
     int32_t run = g < 0 ? 0 : __ldg(a.run_lens + g), ctx = decode ? __ldg(a.ctx_lens + r) : run;
@@ -114,17 +98,20 @@ __global__ void __launch_bounds__(32 * kWarps) rows_kernel(const RowsArgs a)
 
 }  // namespace
 
-cudaError_t launch_rows(const RowsArgs &a, int num_sms, cudaStream_t stream)
+static cudaError_t launch_rows(const RowsArgs &a, int num_sms, cudaStream_t stream)
 {
-    (void)num_sms;
-    const bool int8 = a.kv_dtype == PKV_KV_INT8;
+    if (a.kv_dtype == PKV_KV_BF16) {
+        if (a.n_runs > 0) {
+            const cudaError_t e = launch_rows_tc(a, num_sms, stream);
+            if (e != cudaSuccess) return e;
+        }
+        return a.ctx_lens ? launch_shared_rest(a, num_sms, stream) : launch_rows_join(a, stream);
+    }
     const dim3 grid((unsigned)a.n_rows, (unsigned)a.n_q_heads);
     if (a.dims.head_dim == 128) {
-        if (int8) rows_kernel<128, true><<<grid, 32 * kWarps, 0, stream>>>(a);
-        else rows_kernel<128, false><<<grid, 32 * kWarps, 0, stream>>>(a);
+        rows_plain_kernel<128, true><<<grid, 32 * kWarps, 0, stream>>>(a);
     } else {
-        if (int8) rows_kernel<64, true><<<grid, 32 * kWarps, 0, stream>>>(a);
-        else rows_kernel<64, false><<<grid, 32 * kWarps, 0, stream>>>(a);
+        rows_plain_kernel<64, true><<<grid, 32 * kWarps, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
@@ -170,6 +157,7 @@ int prepare_rows(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, int32_t
     a->softmax_scale = softmax_scale;
     a->out = out;
     a->lse_out = lse_out;
+    a->partials = carve_rows_workspace(workspace, n_rows, n_q_heads, dims.head_dim);
     a->dev_status = dev_status;
     return PKV_OK;
 }
@@ -184,8 +172,7 @@ extern "C" {
 size_t pkv_rows_workspace_bytes(int32_t n_rows, int32_t n_q_heads, int32_t head_dim)
 {
     if (n_rows < 0 || n_q_heads <= 0 || (head_dim != 64 && head_dim != 128)) return 0;
-    const size_t rows = (size_t)n_rows * (size_t)n_q_heads + (size_t)kMaxCtas * kUnitRows;
-    return rows * ((size_t)head_dim + 2) * sizeof(float) + 512;
+    return rows_workspace_bytes(n_rows, n_q_heads, head_dim);
 }
 
 int paged_cross_attention(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, const int32_t *q_starts,

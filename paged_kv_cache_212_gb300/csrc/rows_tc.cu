@@ -1,0 +1,801 @@
+// rows_tc.cu -- packed query rows that all see the same keys (pagedkv_batch.h): the rows of
+// a cross attention's sequence, or the queries of a group's sequences over the tokens that
+// they share, on the 5th-generation tensor cores.
+//
+// A run (sequence or group) is the product of its rows x G query heads with its keys, one
+// kv head at a time: o = softmax(q K^T) V without a mask inside.  A unit is a run, a kv head
+// and up to 256 rows in two tiles of 128 (TMEM lanes); its keys go by in tiles of 128, as
+// in prefill_window.cu: warps 0-3 and 4-7 are the softmax warpgroups of the two tiles,
+// warps 8 and 10 load K, 11 loads V, 9 issues S = Q K^T and O += P V with P in TMEM.
+//
+// The split.  The units' tiles, one behind the other, are cut into equal shares, one per
+// CTA, wherever the cuts fall: with few rows and long runs (64 rows behind 4096 tokens are
+// 8 units) only a split over the keys fills the machine, and with many it keeps the last
+// round whole.  Every CTA sums the runs' tiles by itself to find its share, since lengths
+// stand in device memory.  A unit that is cut leaves partials in 32 bits (rows.h), at most
+// one more per CTA.
+#include <math.h>
+
+#include "common.cuh"
+#include "rows.h"
+#include "softmax_tc.cuh"
+#include "tcgen05.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTM = 128;           // query head rows per tile (TMEM lanes)
+constexpr int kNQ = 2;             // query tiles per unit
+constexpr int kTN = 128;           // keys per K/V tile
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTileCols = 256;        // TMEM columns per query tile: S / P, O
+constexpr uint32_t kOCol = 128;            // O's column within a query tile's range
+constexpr int kThreads = 384;
+static_assert(kNQ * kTM == kUnitRows, "a unit's rows");
+
+// Ring slots (one 128-key tile each) of K and of V that fit beside the Q tiles.
+template <int D>
+__host__ __device__ constexpr int k_slots() { return D == 128 ? 3 : 6; }
+template <int D>
+__host__ __device__ constexpr int v_slots() { return D == 128 ? 2 : 4; }
+
+// Register split (setmaxnreg), as in prefill_window.cu.
+constexpr int kLaunchRegs = 168;
+constexpr int kRegsIssue = 88;
+constexpr int kRegsSoftmax = 208;
+static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreads * kLaunchRegs, "register split above the launch");
+
+struct RowsParams {
+    int32_t n_q_heads, group, n_rows, n_kv_heads;
+    int32_t n_blocks, block_size;
+    int32_t pool_rows;            // (n_blocks + 1) * block_size: an out-of-range TMA row
+    const int32_t *starts, *run_tables, *run_lens;
+    int32_t n_runs, max_run_blocks;
+    const int32_t *ctx_lens;      // decode: a row sees keys below its own; else null
+    float scale_log2;
+    __nv_bfloat16 *out;           // of units that are not cut (null: partials of all)
+    float *lse_out;
+    RowsPartials part;
+    int32_t *dev_status;
+    int32_t wide_out;             // out is 32-byte aligned
+    unsigned long long wait_ns;   // limit of the pipeline waits
+};
+
+// A CTA's part of a unit: tiles t0 .. t0 + n_kt - 1 of its run's keys.
+struct Unit {
+    int32_t g, kvh, pos, pos_end, len, t0, n_kt;
+    int32_t last;                 // nothing behind it
+    int32_t cut;                  // the unit has other parts
+    int32_t last_cta;             // that has some of it
+};
+
+// Where a CTA stands in the stream of tiles.
+struct Walk {
+    int64_t at, stop, total;      // tile of the stream, end of the share, of the stream
+    int32_t n_ctas;
+    int32_t g, idx, t;            // run, unit within it, tile within that
+};
+
+__device__ __forceinline__ int32_t tiles_of_run(const Run &r) { return (int32_t)(((uint32_t)r.len + kTN - 1u) / kTN); }
+__device__ __forceinline__ int32_t pairs_of_run(const RowsParams &p, const Run &r)
+{
+    const int32_t positions = kNQ * (kTM / p.group);
+    return (int32_t)(((int64_t)r.rows + positions - 1) / positions);
+}
+
+__device__ __forceinline__ Run run_of_params(const RowsParams &p, int32_t g)
+{
+    return run_at(p.starts, p.run_lens, p.n_rows, p.max_run_blocks, p.block_size, g);
+}
+
+// The next part of the share.  One copy of it, out of line (instruction fetches).
+__device__ __noinline__ void next_unit(const RowsParams &p, Walk *w, Unit *out)
+{
+    Run r = run_of_params(p, w->g);
+    int32_t pairs = pairs_of_run(p, r), n_kt = tiles_of_run(r);
+    while (n_kt == 0 || w->idx == pairs * p.n_kv_heads) {      // (the stream goes on, so there is one more)
+        ++w->g;
+        w->idx = 0;
+        r = run_of_params(p, w->g);
+        pairs = pairs_of_run(p, r);
+        n_kt = tiles_of_run(r);
+    }
+    Unit u;
+    u.g = w->g;
+    u.kvh = w->idx / pairs;
+    u.pos = r.row0 + (w->idx - u.kvh * pairs) * (kNQ * (kTM / p.group));
+    u.pos_end = r.row0 + r.rows;
+    u.len = r.len;
+    u.t0 = w->t;
+    u.n_kt = (int32_t)min((int64_t)(n_kt - w->t), w->stop - w->at);
+    u.cut = u.n_kt < n_kt;
+    // the CTA whose share holds the unit's last tile x: the last c with floor(total c / n) <= x
+    u.last_cta = (int32_t)(((w->at - w->t + n_kt) * w->n_ctas - 1) / w->total);
+    w->at += u.n_kt;
+    w->t = 0;
+    ++w->idx;
+    u.last = w->at == w->stop;
+    *out = u;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                           const __grid_constant__ CUtensorMap k_map,
+                                                           const __grid_constant__ CUtensorMap v_map,
+                                                           const __grid_constant__ RowsParams p)
+{
+    constexpr int PANELS = D / 64;                          // 64-column (128-byte) panels of a bf16 row
+    constexpr int NK = k_slots<D>(), NV = v_slots<D>();
+    constexpr uint32_t kQPanel = kTM * 128u;                // 16 KiB: one panel of a 128-row Q tile
+    constexpr uint32_t kQTile = PANELS * kQPanel;
+    constexpr uint32_t kKVPanel = kTN * 128u;               // 16 KiB: one panel of a 128-key K tile
+    constexpr uint32_t kSlotBytes = PANELS * kKVPanel;      // one K or V tile
+    constexpr uint32_t kVGroup = PANELS * 2048u;            // one 16-key group of a V tile (all panels)
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *q_s = base;                                    // kNQ Q tiles
+    // K tile: [panel][128 keys][128 B]; V tile: [16-key group][panel][16 keys][128 B]
+    uint8_t *k_ring = q_s + kNQ * kQTile;                   // NK K tiles
+    uint8_t *v_ring = k_ring + NK * kSlotBytes;             // NV V tiles
+    uint64_t *bars = reinterpret_cast<uint64_t *>(v_ring + NV * kSlotBytes);
+    uint64_t *q_full = bars + 0;                            // a unit's Q tiles
+    uint64_t *q_empty = bars + 1;                           // its last S products have read them
+    uint64_t *k_full = bars + 2;                            // [NK]
+    uint64_t *k_empty = k_full + NK;                        // [NK]
+    uint64_t *v_full = k_empty + NK;                        // [NV]
+    uint64_t *v_empty = v_full + NV;                        // [NV]
+    uint64_t *s_full = v_empty + NV;                        // [kNQ]: S in TMEM
+    uint64_t *p_full = s_full + kNQ;                        // [kNQ]: P in TMEM
+    uint64_t *o_done = p_full + kNQ;                        // [kNQ]: a unit's last P V product done
+    uint64_t *fin_bar = o_done + kNQ;
+    uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(fin_bar + 1);
+    volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(fin_bar + 2);
+    // Units: [4] of the issuer and the softmax warpgroups, written by warp 8 before it
+    // loads a unit's Q (unit i at i % 4: Q i - 1 was loaded, so the S of unit i - 2 were
+    // issued, behind all of the P of unit i - 3 and so the epilogues of unit i - 4), and
+    // [4] of warps 8-11, which run ahead of that.
+    Unit *unit_s = reinterpret_cast<Unit *>(bars + 32);
+    static_assert(2 + 2 * (NK + NV) + 3 * kNQ + 3 <= 32, "barriers fit their 256 bytes");
+    __shared__ Walk walk_s[5];                              // [4]: where the share begins
+    __shared__ int64_t warp_sum[kThreads / 32];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.group;
+    const int pos_per_tile = kTM / G;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&k_full[i], 2);   // the two K producers
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+        }
+        for (int i = 0; i < kNQ; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&o_done[i], 1);
+        }
+        mbar_init(fin_bar, 1);
+        *abort_flag = 0;
+        walk_s[4].at = walk_s[4].stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_base_s)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (warp == 8 && lane == 0) prefetch_tensormap(&q_map);
+    if ((warp == 8 || warp == 10) && lane == 0) prefetch_tensormap(&k_map);
+    if (warp == 11 && lane == 0) prefetch_tensormap(&v_map);
+    // launched as a programmatic dependent: what is above overlaps the preceding
+    // grid's end; no memory that it may write is read before the wait.  The next grid may
+    // start as soon as this one has waited: what it reads before its own wait was written
+    // before this grid.
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    // The share: tiles [total c / n, total (c + 1) / n) of the stream.  A thread sums
+    // neighbouring runs, the block sums the threads.
+    {
+        const int32_t per = (p.n_runs + kThreads - 1) / kThreads;
+        const int32_t g0 = min((int64_t)threadIdx.x * per, (int64_t)p.n_runs), g1 = min((int64_t)g0 + per, (int64_t)p.n_runs);
+        int64_t sum = 0;
+        bool good = true;
+        for (int32_t g = g0; g < g1; ++g) {
+            const Run r = run_of_params(p, g);
+            sum += (int64_t)pairs_of_run(p, r) * p.n_kv_heads * tiles_of_run(r);
+            good = good && r.good;
+        }
+        if (!good && blockIdx.x == 0) report(p.dev_status, PKV_DEV_BAD_LENGTH);
+        int64_t in = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, in, off);
+            if (lane >= off) in += x;
+        }
+        if (lane == 31) warp_sum[warp] = in;
+        __syncthreads();
+        int64_t before = in - sum, total = 0;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += warp_sum[i];
+            total += warp_sum[i];
+        }
+        const int64_t n_ctas = min((int64_t)gridDim.x, total);
+        if (blockIdx.x < n_ctas) {
+            const int64_t at = total * blockIdx.x / n_ctas;
+            if (at >= before && at < before + sum) {           // this thread's runs hold the first tile
+                Walk w;
+                w.at = at;
+                w.stop = total * (blockIdx.x + 1) / n_ctas;
+                w.total = total;
+                w.n_ctas = (int32_t)n_ctas;
+                int64_t left = at - before;
+                for (int32_t g = g0; g < g1; ++g) {
+                    const Run r = run_of_params(p, g);
+                    const int32_t n_kt = tiles_of_run(r);
+                    const int64_t tiles = (int64_t)pairs_of_run(p, r) * p.n_kv_heads * n_kt;
+                    if (left >= tiles) {
+                        left -= tiles;
+                        continue;
+                    }
+                    w.g = g;
+                    w.idx = (int32_t)(left / n_kt);
+                    w.t = (int32_t)(left - (int64_t)w.idx * n_kt);
+                    break;
+                }
+                walk_s[4] = w;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_base_s;
+    const bool any = walk_s[4].stop > walk_s[4].at;
+
+    if (warp >= 4 * kNQ) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue) : "memory");
+        if (!any) {
+        } else if (warp != 9) {
+            // ===================== TMA producers =====================
+            const bool is_v = warp == 11;
+            // this warp's 16-key groups: all eight (V) or four (each K warp)
+            const int n_grp = is_v ? kTN / 16 : kTN / 32;
+            const int grp = is_v ? lane : (warp == 10 ? kTN / 32 : 0) + lane;
+            const int NSL = is_v ? NV : NK;
+            uint64_t *full = is_v ? v_full : k_full;
+            uint64_t *empty = is_v ? v_empty : k_empty;
+            uint8_t *ring = is_v ? v_ring : k_ring;
+            const uint32_t bytes = is_v ? kSlotBytes : kSlotBytes / 2;
+            // block ids are read one tile ahead, across units, and turned into pool rows
+            // when the tile is issued
+            Unit *mine = unit_s + 4 + (warp - 8);
+            Walk *walk = walk_s + (warp - 8);
+            if (lane == 0) *walk = walk_s[4];
+            int32_t kvh = 0, len = 0, t0 = 0, n_kt = 0;
+            const int32_t *trow = nullptr;
+            bool last = false;
+            auto load_unit = [&]() {
+                __syncwarp();
+                if (lane == 0) next_unit(p, walk, mine);
+                __syncwarp();
+                const volatile Unit &w = *mine;
+                kvh = w.kvh;
+                len = w.len;
+                t0 = w.t0;
+                n_kt = w.n_kt;
+                last = w.last;
+                trow = p.run_tables + (int64_t)w.g * p.max_run_blocks;
+            };
+            // the block of this lane's group of tile j of the unit
+            auto load_block = [&](int j) -> int32_t {
+                const int32_t key = (t0 + j) * kTN + grp * 16;
+                return (lane < n_grp && key < len) ? __ldg(trow + key / p.block_size) : 0;
+            };
+            load_unit();
+            int32_t blk = load_block(0);
+            int j = 0, issued = 0, unit = 0, q_loads = 0;   // tile of the unit, tiles so far, unit, Qs that lane 0 has issued
+            bool more = true;
+            while (more) {
+                int32_t row = p.pool_rows;  // out of range: the box reads zeros
+                const int32_t key = (t0 + j) * kTN + grp * 16;
+                if (lane < n_grp && key < len) {
+                    if (blk < 0 || blk > p.n_blocks)
+                        report(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                    else
+                        row = blk * p.block_size + key % p.block_size;
+                }
+                const int32_t t_kvh = kvh, t_unit = unit;          // of this tile
+                const bool first = j == 0;
+                if (warp == 8 && first && lane == 0) unit_s[unit & 3] = *mine;   // handed on with the unit's Q, below
+                if (++j == n_kt) {
+                    j = 0;
+                    ++unit;
+                    more = !last;
+                    if (more) load_unit();
+                }
+                if (more) blk = load_block(j);
+                const int st = issued % NSL, use = issued / NSL;
+                if (lane == 0 && !wait_for(&empty[st], (use & 1) ^ 1, abort_flag, p.wait_ns)) {
+                    report(p.dev_status, PKV_DEV_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+                uint8_t *dst = ring + st * kSlotBytes;
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                __syncwarp();
+                if (lane < n_grp) {
+                    if (is_v) {
+                        tma_load_3d(dst + grp * kVGroup, &v_map, 0, row, t_kvh * PANELS, &full[st]);
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < PANELS; ++h)
+                            tma_load_3d(dst + h * kKVPanel + grp * 2048, &k_map, h * 64, t_kvh, row, &full[st]);
+                    }
+                }
+                ++issued;
+                if (warp == 8 && first) {   // the unit's Q, once the last unit's has been read
+                    if (lane == 0) {
+                        if (!wait_for(q_empty, (t_unit & 1) ^ 1, abort_flag, p.wait_ns)) {
+                            report(p.dev_status, PKV_DEV_TIMEOUT);
+                            *abort_flag = 1;
+                        } else {
+                            // (a group that does not divide 128 leaves the tile's last rows as they
+                            // are: rows of S are independent of one another)
+                            const Unit &w = unit_s[t_unit & 3];
+                            mbar_arrive_expect_tx(q_full, kNQ * PANELS * pos_per_tile * G * 128);
+                            for (int i = 0; i < kNQ; ++i)
+                                for (int h = 0; h < PANELS; ++h)
+                                    tma_load_3d(q_s + i * kQTile + h * kQPanel, &q_map, h * 64, t_kvh * G,
+                                                w.pos + i * pos_per_tile, q_full);
+                            ++q_loads;   // (lane 0's: another role may have raised the flag by now)
+                        }
+                    }
+                    if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+                }
+            }
+            // every copy this warp issued has landed before the CTA can exit
+            if (lane == 0) {
+                if (warp == 8 && q_loads > 0) (void)mbar_wait(q_full, (q_loads - 1) & 1);
+                for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i)
+                    (void)mbar_wait(&full[i % NSL], (i / NSL) & 1);
+            }
+        } else {
+            // ===================== MMA issuer =====================
+            const uint32_t idesc_s = umma_idesc_bf16(kTM, kTN, false, false);
+            const uint32_t idesc_o = umma_idesc_bf16(kTM, D, false, true);
+            const uint32_t leader = elect_one();
+            // The warp's waits keep the default limit, which compiles to the plain wait; when
+            // another role's wait runs out, the abort flag ends these.
+            auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag));
+            };
+            const uint32_t q_addr = smem_u32(q_s) >> 4, k_addr = smem_u32(k_ring) >> 4, v_addr = smem_u32(v_ring) >> 4;
+            const uint64_t kd = umma_desc_sw128(0, 16, 1024), vd = umma_desc_sw128(0, 2048, 1024);
+            const uint32_t k_hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, v_hi = (uint32_t)(vd >> 32), v_lo = (uint32_t)vd;
+            // S = Q_t K^T of the K in a ring slot, then the commit that hands it on; it
+            // covers the product issued before it, too
+            auto issue_s = [&](int t, int slot) {
+                constexpr int STEPS = D / 16;
+                uint32_t qa[STEPS], kb[STEPS];
+#pragma unroll
+                for (int k = 0; k < STEPS; ++k) {
+                    qa[k] = k_lo | (q_addr + (t * kQTile + (k / 4) * kQPanel + (k % 4) * 32) / 16);
+                    kb[k] = k_lo | (k_addr + (slot * kSlotBytes + (k / 4) * kKVPanel + (k % 4) * 32) / 16);
+                }
+                mma_ss<STEPS>(leader, tmem + t * kTileCols, k_hi, qa, kb, idesc_s);
+                commit_one(leader, &s_full[t]);
+            };
+            // O_t += P_t V: A = P (TMEM), B = V (MN-major: 16-key group k at k * kVGroup)
+            auto issue_o = [&](int t, int slot, bool accumulate) {
+                uint32_t vb[kTN / 16];
+#pragma unroll
+                for (int k = 0; k < kTN / 16; ++k) vb[k] = v_lo | (v_addr + (slot * kSlotBytes + k * kVGroup) / 16);
+                mma_ts<kTN / 16>(leader, tmem + t * kTileCols + kOCol, tmem + t * kTileCols, v_hi, vb, idesc_o,
+                                 accumulate ? 1u : 0u);
+            };
+            // The tile at hand is the last of its unit's when left is 1.  The S of the next tile
+            // goes out behind each P V; at a unit's end it waits for the next unit's Q, so both
+            // P V go first.
+            int ks = 0, vs = 0;                   // ring slots of the tile's K and V, and their phases
+            uint32_t k_phase = 0, v_phase = 0, phase = 0;
+            bool ok = wait(q_full, 0) && wait(&k_full[0], 0);
+            int units = 0, n_kt = 1, left = 1;
+            bool last_unit = true;
+            auto read_unit = [&]() {
+                const volatile Unit &w = unit_s[units & 3];
+                n_kt = left = w.n_kt;
+                last_unit = w.last;
+            };
+            if (ok) {
+                read_unit();
+                tc_fence_after();
+#pragma unroll 1
+                for (int t = 0; t < kNQ; ++t) issue_s(t, 0);
+                commit_one(leader, &k_empty[0]);
+                if (n_kt == 1) commit_one(leader, q_empty);
+            }
+            while (ok) {
+                const bool first = left == n_kt, last = left == 1;
+                if (++ks == NK) {
+                    ks = 0;
+                    k_phase ^= 1;
+                }
+                ok = wait(&v_full[vs], v_phase);
+#pragma unroll
+                for (int t = 0; t < kNQ; ++t) {
+                    if (!ok) break;
+                    ok = wait(&p_full[t], phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_o(t, vs, !first);
+                    if (last) {
+                        commit_one(leader, &o_done[t]);
+                    } else {
+                        if (t == 0) {
+                            ok = wait(&k_full[ks], k_phase);
+                            if (!ok) break;
+                            tc_fence_after();
+                        }
+                        issue_s(t, ks);
+                    }
+                }
+                if (!ok) break;
+                commit_one(leader, &v_empty[vs]);
+                if (last) {
+                    if (last_unit) break;
+                    ++units;
+                    ok = wait(&k_full[ks], k_phase) && wait(q_full, units & 1);
+                    if (!ok) break;
+                    read_unit();
+                    tc_fence_after();
+                    // (S_t's columns hold a P that the tensor core reads before)
+#pragma unroll 1
+                    for (int t = 0; t < kNQ; ++t) issue_s(t, ks);
+                    ++left;
+                }
+                commit_one(leader, &k_empty[ks]);
+                if (--left == 1) commit_one(leader, q_empty);   // S of the unit's last tile is issued
+                phase ^= 1;
+                if (++vs == NV) {
+                    vs = 0;
+                    v_phase ^= 1;
+                }
+            }
+            if (!ok) {
+                if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA issued has retired before the TMEM is released
+            commit_one(leader, fin_bar);
+            (void)mbar_wait(fin_bar, 0);
+            __syncwarp();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+        // ===================== softmax warpgroups: row r = TMEM lane r =====================
+        const int qt = warp / 4;
+        const int r = threadIdx.x % kTM;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp % 4) * 32) << 16) + qt * kTileCols;
+        const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+        // (the unit stays in shared memory: a row's scores need the registers)
+        int c = 0;                               // tiles so far
+        bool ok = true, more = any;
+        // V rows of the last group that lie behind the run's last key may hold anything: they
+        // are zeroed once V has landed (both warpgroups write the same zeros).
+        auto clean_v = [&](int from) -> bool {
+            if (!__all_sync(0xffffffffu, wait_for(&v_full[c % NV], (c / NV) & 1, abort_flag, p.wait_ns))) return false;
+            uint8_t *vs = v_ring + (c % NV) * kSlotBytes;
+            for (int i = r; i < (((from + 15) & ~15) - from) * PANELS * 8; i += kTM) {
+                const int row = from + i / (PANELS * 8), pc = i % (PANELS * 8);
+                *reinterpret_cast<uint4 *>(vs + (row / 16) * kVGroup + (pc / 8) * 2048 + swz128(row % 16, pc % 8)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();   // zeroed V rows visible to the tensor core
+            return true;
+        };
+        for (int units = 0; more; ++units) {
+            const volatile Unit &w = unit_s[units & 3];
+            int n_kt = 1;                        // read with the unit's first tile
+            bool live = false, warp_live = false;
+            int32_t pos = 0, limit = 0;
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n_kt; ++j, ++c) {
+                ok = __all_sync(0xffffffffu, wait_for(&s_full[qt], c & 1, abort_flag, p.wait_ns));
+                if (!ok) break;
+                tc_fence_after();
+                // (the first S of a unit says that the unit has been written)
+                if (j == 0) {
+                    n_kt = w.n_kt;
+                    more = !w.last;
+                    pos = w.pos + qt * pos_per_tile + r / G;
+                    live = r < pos_per_tile * G && pos < w.pos_end;
+                    limit = w.len;
+                    if (live && p.ctx_lens) limit = min(limit, max(__ldg(p.ctx_lens + pos), 0));
+                    warp_live = __any_sync(0xffffffffu, live);
+                }
+                const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;
+                if (warp_live) {                 // (others leave P as it is: their rows go nowhere)
+                    uint32_t sv[kTN];
+#pragma unroll
+                    for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
+                    tmem_wait_ld();
+                    // rows whose keys in this tile are all visible need no per-key test
+                    if (__any_sync(0xffffffffu, limit - key0 < kTN)) {
+#pragma unroll
+                        for (int i0 = 0; i0 < kTN; i0 += 32) {
+                            const uint32_t seen = bits_below(limit - key0 - i0);
+                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
+                        }
+                    }
+                    const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
+                    // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
+                    // commit came after it
+                    if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                    // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
+                    // columns it covers were read
+                    const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                    const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
+                    const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
+                    l = l * alpha + (l0 + l1);
+                    tmem_wait_st();
+                }
+                if (tail < kTN && (tail & 15) != 0) {
+                    ok = clean_v(tail);
+                    if (!ok) break;
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[qt]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, wait_for(&o_done[qt], units & 1, abort_flag, p.wait_ns));
+            if (!ok) break;
+            tc_fence_after();
+            // row r of O.  (O is read before this warp's next P is handed over, and the next
+            // unit's first product into O comes after that.)
+            if (warp_live) {
+                const int64_t row = (int64_t)pos * p.n_q_heads + w.kvh * G + r % G;
+                const bool whole = p.out && !w.cut;
+                if (whole) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    __nv_bfloat16 *out = p.out + row * D;
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t v[32];
+                        tmem_ld32_async(lane_base + kOCol + i * 32, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int q2 = 0; q2 < 2; ++q2) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                x[e] = pack_bf16x2(__uint_as_float(v[16 * q2 + 2 * e]) * inv, __uint_as_float(v[16 * q2 + 2 * e + 1]) * inv);
+                            if (!live) continue;
+                            if (p.wide_out) {
+                                st_global_32(out + i * 32 + q2 * 16, x);
+                            } else {
+                                *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16) = make_uint4(x[0], x[1], x[2], x[3]);
+                                *reinterpret_cast<uint4 *>(out + i * 32 + q2 * 16 + 8) = make_uint4(x[4], x[5], x[6], x[7]);
+                            }
+                        }
+                    }
+                    if (live && p.lse_out) p.lse_out[row] = (m + __log2f(l)) * 0.69314718055994531f;
+                    if (live) p.part.stat[row] = make_float4(0.f, 0.f, __int_as_float(-1), __int_as_float(-1));
+                } else {
+                    const bool begins = w.t0 == 0;
+                    const int64_t mine = (int64_t)blockIdx.x * kUnitRows + qt * kTM + r;
+                    float *dst = begins ? p.part.first + row * D : p.part.cont + mine * D;
+#pragma unroll 1
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t v[32];
+                        tmem_ld32_async(lane_base + kOCol + i * 32, v);
+                        tmem_wait_ld();
+                        if (!live) continue;
+#pragma unroll
+                        for (int q2 = 0; q2 < 4; ++q2) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = v[8 * q2 + e];
+                            st_global_32(dst + i * 32 + q2 * 8, x);
+                        }
+                    }
+                    if (live && begins)
+                        p.part.stat[row] = make_float4(m, l, __int_as_float((int)blockIdx.x), __int_as_float(w.last_cta));
+                    else if (live)
+                        p.part.cont_ml[mine] = make_float2(m, l);
+                }
+            }
+            tc_fence_before();
+        }
+        if (!ok) {
+            if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+    // everyone meets here before the TMEM is released
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---- the join of a cross attention's cut rows: a warp to a row and query head -------------
+
+template <int D>
+__global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsParams p)
+{
+    constexpr int PER = D / 32;                     // elements of a lane
+    const int lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+    grid_dependents_launch();
+    // (starts and lengths were written before the grid that this one depends on)
+    int32_t pos = -1, head = 0, g = -1;
+    Run run{};
+    if (row < (int64_t)p.n_rows * p.n_q_heads) {
+        pos = (int32_t)(row / p.n_q_heads);
+        head = (int32_t)(row - (int64_t)pos * p.n_q_heads);
+        g = run_of(p.starts, p.n_runs, pos);
+        if (g >= 0) run = run_of_params(p, g);
+    }
+    grid_dependency_wait();
+    if (g < 0 || run.rows == 0) return;
+    float o[PER], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = 0.f;
+    if (run.len > 0) {
+        const float4 stat = p.part.stat[row];
+        const int32_t c0 = __float_as_int(stat.z), c1 = __float_as_int(stat.w);
+        if (c0 < 0) return;
+        m = stat.x;
+        l = stat.y;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = p.part.first[row * D + lane * PER + e];
+        const int32_t tile = kTM / p.group, in = pos - run.row0, at = in % (kNQ * tile);
+        const int64_t place = (int64_t)(at / tile) * kTM + (at % tile) * p.group + head % p.group;
+        for (int32_t c = c0 + 1; c <= c1; ++c) {
+            const int64_t i = (int64_t)c * kUnitRows + place;
+            const float2 ml = p.part.cont_ml[i];
+            float x[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] = p.part.cont[i * D + lane * PER + e];
+            const float top = fmaxf(m, ml.x);
+            const float a = m == -INFINITY ? 0.f : fast_exp2(m - top), b = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+            m = top;
+            l = l * a + ml.y * b;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[e] = o[e] * a + x[e] * b;
+        }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] *= inv;
+    __nv_bfloat16 *out = p.out + row * D + lane * PER;
+    if constexpr (PER == 4)
+        *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    else
+        *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(o[0], o[1]);
+    if (lane == 0 && p.lse_out) p.lse_out[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+RowsParams params_of(const RowsArgs &a)
+{
+    const pkv_dims &d = a.dims;
+    RowsParams p{};
+    p.n_q_heads = a.n_q_heads;
+    p.group = a.n_q_heads / d.n_kv_heads;
+    p.n_rows = a.n_rows;
+    p.n_kv_heads = d.n_kv_heads;
+    p.n_blocks = d.n_blocks;
+    p.block_size = d.block_size;
+    p.pool_rows = (d.n_blocks + 1) * d.block_size;
+    p.starts = a.starts;
+    p.run_tables = a.run_tables;
+    p.run_lens = a.run_lens;
+    p.n_runs = a.n_runs;
+    p.max_run_blocks = a.max_run_blocks;
+    p.ctx_lens = a.ctx_lens;
+    p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
+    p.out = a.ctx_lens ? nullptr : static_cast<__nv_bfloat16 *>(a.out);
+    p.lse_out = a.lse_out;
+    p.part = a.partials;
+    p.dev_status = a.dev_status;
+    p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+    p.wait_ns = pipeline_wait_ns();
+    return p;
+}
+
+cudaLaunchConfig_t dependent(cudaLaunchAttribute (&pdl)[1], unsigned grid, unsigned threads, size_t smem, cudaStream_t stream)
+{
+    pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    lc.attrs = pdl;
+    lc.numAttrs = 1;
+    return lc;
+}
+
+}  // namespace
+
+cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
+{
+    const pkv_dims &d = a.dims;
+    const RowsParams p = params_of(a);
+    CUtensorMap qmap, kmap, vmap;
+    {
+        const uint64_t dims[3] = {(uint64_t)d.head_dim, (uint64_t)a.n_q_heads, (uint64_t)a.n_rows};
+        const uint64_t strides[2] = {(uint64_t)d.head_dim * 2, (uint64_t)a.q_stride * 2};
+        const uint32_t box[3] = {64u, (uint32_t)p.group, (uint32_t)(kTM / p.group)};
+        if (encode_tensor_map(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const uint64_t rows = (uint64_t)(d.n_blocks + 1) * d.block_size;
+    const uint64_t row_bytes = (uint64_t)d.n_kv_heads * d.head_dim * 2;
+    {
+        // K: {64 columns, kv head, pool row}, one head and 16 rows per box
+        const uint64_t dims[3] = {(uint64_t)d.head_dim, (uint64_t)d.n_kv_heads, rows};
+        const uint64_t strides[2] = {(uint64_t)d.head_dim * 2, row_bytes};
+        const uint32_t box[3] = {64u, 1u, 16u};
+        if (encode_tensor_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.k_pool), dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    {
+        // V: {64 columns, pool row, 64-column panel of all heads}: a box of 16
+        // rows and a head's panels lands as [panel][row][128 B]
+        const uint32_t panels = (uint32_t)d.head_dim / 64u;
+        const uint64_t dims[3] = {64u, rows, (uint64_t)d.n_kv_heads * panels};
+        const uint64_t strides[2] = {row_bytes, 128u};
+        const uint32_t box[3] = {64u, 16u, panels};
+        if (encode_tensor_map(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.v_pool), dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    const int slots = d.head_dim == 128 ? k_slots<128>() + v_slots<128>() : k_slots<64>() + v_slots<64>();
+    const size_t smem = 1024 + (size_t)kNQ * kTM * d.head_dim * 2 + (size_t)slots * kTN * d.head_dim * 2 + 32 * sizeof(uint64_t) +
+                        8 * sizeof(Unit);
+    // The register split assumes the block gets kLaunchRegs per thread: refuse
+    // a build whose kernel was given fewer (its setmaxnreg.inc could not complete).
+    static const bool regs_ok = [] {
+        cudaFuncAttributes fa128{}, fa64{};
+        return cudaFuncGetAttributes(&fa128, rows_kernel<128>) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa64, rows_kernel<64>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
+               fa64.numRegs >= kLaunchRegs;
+    }();
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
+    cudaLaunchAttribute pdl[1];
+    const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)(num_sms < kMaxCtas ? num_sms : kMaxCtas), kThreads, smem, stream);
+    const void *kern = d.head_dim == 128 ? reinterpret_cast<const void *>(rows_kernel<128>) : reinterpret_cast<const void *>(rows_kernel<64>);
+    const cudaError_t e = prepare_kernel(kern, kThreads, smem, nullptr);
+    if (e != cudaSuccess) return e;
+    return d.head_dim == 128 ? cudaLaunchKernelEx(&lc, rows_kernel<128>, qmap, kmap, vmap, p)
+                             : cudaLaunchKernelEx(&lc, rows_kernel<64>, qmap, kmap, vmap, p);
+}
+
+cudaError_t launch_rows_join(const RowsArgs &a, cudaStream_t stream)
+{
+    const RowsParams p = params_of(a);
+    cudaLaunchAttribute pdl[1];
+    const int64_t grid = ((int64_t)a.n_rows * a.n_q_heads + 7) / 8;
+    const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)grid, 256, 0, stream);
+    return a.dims.head_dim == 128 ? cudaLaunchKernelEx(&lc, rows_join_kernel<128>, p) : cudaLaunchKernelEx(&lc, rows_join_kernel<64>, p);
+}
+
+}  // namespace pkv
