@@ -1,10 +1,9 @@
 // decode_shared.cu -- the tokens of a decode's sequences behind those that their group
-// shares: decode_window.cuh's kernels over tokens prefix_lens[g] .. ctx_lens[s] - 1, which
-// join what the rows kernel (rows_tc.cu) left of the group's tokens at the end.
+// shares: decode_window.cuh's kernels over tokens prefix_lens[g] .. ctx_lens[s] - 1, whose
+// partials are joined with those of the group's tokens (rows_tc.cu).
 //
 // The launch is a programmatic dependent of the rows kernel, which lets it start as soon as
-// its own CTAs run: an SM goes on with these units when it is through with its share of the
-// group's tiles, and only the join at a unit's end waits for all of them.
+// its own CTAs run: these units fill the SMs that the group's tiles leave to them.
 #include "decode_window.cuh"
 #include "../../include/pagedkv_batch.h"
 
@@ -40,7 +39,7 @@ cudaError_t launch_shared_rest(const RowsArgs &r, int sms, cudaStream_t stream)
     a.max_prefix_blocks = r.max_run_blocks;
     a.n_seqs = r.n_rows;
     a.part = r.partials;
-    if (r.n_runs == 0) a.part.stat = nullptr;    // no rows kernel before this one
+    a.after_rows = r.n_runs > 0;
     const int64_t units = (int64_t)r.n_rows * dims.n_kv_heads;
     const int64_t tiles = ((int64_t)r.max_blocks * dims.block_size + kTile - 1) / kTile;
     const bool wide = a.group > 4;

@@ -93,6 +93,7 @@ struct WindowArgs {
     const int32_t *group_starts, *prefix_lens;
     int32_t n_groups, max_prefix_blocks, n_seqs;
     RowsPartials part;
+    int32_t after_rows;
 };
 
 template <int D, bool INT8>
@@ -228,8 +229,7 @@ struct Seen {
 };
 
 // WIDE: 5 to 8 query heads per kv head (bf16; int8 pages have one form for all).
-// SHARED: a sequence's tokens behind those that its group shares; the group's come in as
-// partials and are joined at the end.
+// SHARED: a sequence's tokens behind those that its group shares, whose result is a partial.
 template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode_window_kernel(const WindowArgs a)
 {
@@ -259,18 +259,16 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
 
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     // (SHARED behind the rows kernel, which has waited itself before it let this one start:
-    // all that is read was written before that, but for the partials)
-    if (!SHARED || !a.part.stat) grid_dependency_wait();
+    // all that is read was written before that.  One CTA waits at its end, so that the grid
+    // ends behind the rows kernel; if all did, those of the first round would keep the rest
+    // from starting)
+    if (!SHARED || !a.after_rows) grid_dependency_wait();
 
     // 1. the tiles
     const int32_t len = SHARED ? __ldcg(a.ctx_lens + s) : __ldg(a.ctx_lens + s);
     const int32_t t_new = step ? __ldg(a.start_pos + s) : -1;
-    int32_t group = -1;
     Run run{0, 0, 0, true};
-    if constexpr (SHARED) {
-        group = run_of(a.group_starts, a.n_groups, s);
-        if (group >= 0) run = run_at(a.group_starts, a.prefix_lens, a.n_seqs, a.max_prefix_blocks, bs, group);
-    }
+    if constexpr (SHARED) run_of(a.group_starts, a.prefix_lens, a.n_groups, a.n_seqs, a.max_prefix_blocks, bs, s, &run);
     const Seen all(a, len);
     const int32_t L = SHARED && !run.good ? 0 : all.L;
     const Seen seen = SHARED ? Seen(min(run.len, L), L) : all;
@@ -705,8 +703,6 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         }
     }
     __syncthreads();
-    if (SHARED && a.part.stat) grid_dependency_wait();
-
     // 6. joined over the warps, in place of the first warp's, then over the cluster,
     //    where each CTA writes its share of the outputs
     const int64_t head0 = (int64_t)s * a.n_q_heads + (int64_t)h * G;
@@ -720,33 +716,12 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         M = N;
         M2 = N2;
     };
-    auto finish = [&](int g, int d, float4 v, float M, float M2, float sum) {
-        if constexpr (SHARED) {
-            if (run.len > 0 && L > 0) {              // the group's tokens, piece by piece (rows.h)
-                const float4 stat = __ldcg(a.part.stat + head0 + g);
-                join(v, M, M2, sum, __ldcg(reinterpret_cast<const float4 *>(a.part.first + (head0 + g) * D + d)), stat.x, stat.x,
-                     stat.y);
-                const int32_t c1 = __float_as_int(stat.w);
-                const int tile = kUnitRows / 2 / G, in = (s - run.row0) % (2 * tile);
-                const int64_t place = (int64_t)(in / tile) * (kUnitRows / 2) + (in % tile) * G + g;
-                constexpr int kRound = 8;            // pieces in flight
-                for (int32_t c0 = __float_as_int(stat.z) + 1; c0 <= c1; c0 += kRound) {
-                    float4 x[kRound];
-                    float2 ml[kRound];
-#pragma unroll
-                    for (int k = 0; k < kRound; ++k) {
-                        if (c0 + k > c1) break;
-                        const int64_t i = (int64_t)(c0 + k) * kUnitRows + place;
-                        x[k] = __ldcg(reinterpret_cast<const float4 *>(a.part.cont + i * D + d));
-                        ml[k] = __ldcg(a.part.cont_ml + i);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kRound; ++k) {
-                        if (c0 + k > c1) break;
-                        join(v, M, M2, sum, x[k], ml[k].x, ml[k].x, ml[k].y);
-                    }
-                }
-            }
+    auto finish = [&](int g, int d, const float4 &v, float M, float M2, float sum) {
+        if constexpr (SHARED) {                      // a partial, in units of 2^M
+            const float f = M2 == -INFINITY ? 1.f : fast_exp2(M2 - M);
+            *reinterpret_cast<float4 *>(a.part.own + (head0 + g) * D + d) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+            if (d == 0) a.part.own_ml[head0 + g] = make_float2(M, L > 0 ? sum : -1.f);
+            return;
         }
         // o = 2^M2 v / (2^M sum); no token seen: 0
         const float inv = sum == 0.f ? 0.f : (M2 == -INFINITY ? 1.f : INT8 ? fast_exp2(M2 - M) : 1.f) / sum;
@@ -771,6 +746,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             if (d == 0) c_stat[g] = make_float4(M, M2, sum, 0.f);
         }
     }
+    if (SHARED && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
     if (a.splits == 1) return;
     cluster_sync_all();
     for (int i = rank * 32 * WARPS + tid; i < G * (D / 4); i += a.splits * 32 * WARPS) {

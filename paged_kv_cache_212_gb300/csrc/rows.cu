@@ -11,6 +11,19 @@ namespace {
 
 constexpr int kWarps = 4;
 
+__device__ __forceinline__ int32_t run_of(const int32_t *starts, int32_t n_runs, int32_t row)
+{
+    int32_t lo = -1, hi = n_runs;
+    while (hi - lo > 1) {
+        const int32_t mid = lo + (hi - lo) / 2;
+        if (__ldcg(starts + mid) <= row)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo >= 0 && row < __ldcg(starts + lo + 1) ? lo : -1;
+}
+
 template <int D, bool INT8>
 __global__ void __launch_bounds__(32 * kWarps) rows_plain_kernel(const RowsArgs a)
 {
@@ -105,7 +118,11 @@ static cudaError_t launch_rows(const RowsArgs &a, int num_sms, cudaStream_t stre
             const cudaError_t e = launch_rows_tc(a, num_sms, stream);
             if (e != cudaSuccess) return e;
         }
-        return a.ctx_lens ? launch_shared_rest(a, num_sms, stream) : launch_rows_join(a, stream);
+        if (a.ctx_lens) {
+            const cudaError_t e = launch_shared_rest(a, num_sms, stream);
+            if (e != cudaSuccess) return e;
+        }
+        return launch_rows_join(a, num_sms, stream);
     }
     const dim3 grid((unsigned)a.n_rows, (unsigned)a.n_q_heads);
     if (a.dims.head_dim == 128) {

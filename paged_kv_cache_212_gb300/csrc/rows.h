@@ -11,23 +11,32 @@ constexpr int kUnitRows = 256;     // query head rows of a unit
 
 // Where the rows kernel leaves what it has of a (row, query head), unnormalised in 32 bits.
 // The keys of a run are cut at the borders of the CTAs' shares.  The first piece of every
-// row, and how many there are, stand at the row's own place:
-//   stat[row * Hq + head]  (maximum in log2 units, sum, first CTA, last CTA as int bits;
-//                           first CTA -1: the row is finished, nothing is to be joined)
+// row of a cut unit (in a decode: of every row) stands at the row's own place:
+//   stat[row * Hq + head]  (maximum in log2 units, sum, first CTA, last CTA as int bits)
 //   first[row * Hq + head][D]
 // and what CTAs first + 1 .. last add to it at their own, a unit's row each:
 //   cont_ml[cta][256]  (maximum, sum), cont[cta][256][D].
+// A decode's own tokens: own_ml[row * Hq + head] (maximum, sum; a sum of -1: the row sees
+// nothing, not even its run), own[row * Hq + head][D].
+// cuts[cta]: the cut unit that begins in that CTA, the last one of its share.
+struct CutUnit {
+    int32_t pos, pos_end, kvh, last_cta;   // last_cta 0: none
+};
 struct RowsPartials {
     float4 *stat;
     float *first;
     float2 *cont_ml;
     float *cont;
+    CutUnit *cuts;
+    float *own;
+    float2 *own_ml;
 };
 
 inline size_t rows_workspace_bytes(int64_t n_rows, int32_t n_q_heads, int32_t head_dim)
 {
     const size_t rows = (size_t)n_rows * (size_t)n_q_heads, cont = (size_t)kMaxCtas * kUnitRows;
-    return (rows + cont) * (size_t)head_dim * sizeof(float) + rows * sizeof(float4) + cont * sizeof(float2);
+    return (2 * rows + cont) * (size_t)head_dim * sizeof(float) + rows * (sizeof(float4) + sizeof(float2)) +
+           cont * sizeof(float2) + kMaxCtas * sizeof(CutUnit);
 }
 
 inline RowsPartials carve_rows_workspace(void *ws, int64_t n_rows, int32_t n_q_heads, int32_t head_dim)
@@ -36,8 +45,11 @@ inline RowsPartials carve_rows_workspace(void *ws, int64_t n_rows, int32_t n_q_h
     RowsPartials p;
     p.cont = static_cast<float *>(ws);
     p.first = p.cont + cont * head_dim;
-    p.stat = reinterpret_cast<float4 *>(p.first + rows * head_dim);
-    p.cont_ml = reinterpret_cast<float2 *>(p.stat + rows);
+    p.own = p.first + rows * head_dim;
+    p.stat = reinterpret_cast<float4 *>(p.own + rows * head_dim);
+    p.cuts = reinterpret_cast<CutUnit *>(p.stat + rows);
+    p.cont_ml = reinterpret_cast<float2 *>(p.cuts + kMaxCtas);
+    p.own_ml = p.cont_ml + cont;
     return p;
 }
 
@@ -94,26 +106,35 @@ __device__ __forceinline__ Run run_at(const int32_t *starts, const int32_t *run_
     return r;
 }
 
-// The run of a row: the last g with starts[g] <= row, if row < starts[g + 1]; else -1.
-__device__ __forceinline__ int32_t run_of(const int32_t *starts, int32_t n_runs, int32_t row)
+// The run of a row, -1 for none, and what it is: the last g with starts[g] <= row, where
+// row < starts[g + 1].  Asked by a whole warp, 32 runs at a time in one round of loads.
+__device__ __forceinline__ int32_t run_of(const int32_t *starts, const int32_t *run_lens, int32_t n_runs, int32_t n_rows,
+                                          int32_t max_run_blocks, int32_t block_size, int32_t row, Run *out)
 {
-    int32_t lo = -1, hi = n_runs;
-    while (hi - lo > 1) {
-        const int32_t mid = lo + (hi - lo) / 2;
-        if (__ldcg(starts + mid) <= row)
-            lo = mid;
-        else
-            hi = mid;
+    const int lane = threadIdx.x & 31;
+    for (int32_t g0 = 0; g0 < n_runs; g0 += 32) {
+        const int32_t g = g0 + lane;
+        Run r{0, 0, 0, false};
+        if (g < n_runs) r = run_at(starts, run_lens, n_rows, max_run_blocks, block_size, g);
+        const uint32_t here = __ballot_sync(0xffffffffu, row - r.row0 >= 0 && row - r.row0 < r.rows);
+        if (here == 0) continue;
+        const int src = __ffs(here) - 1;
+        out->row0 = __shfl_sync(0xffffffffu, r.row0, src);
+        out->rows = __shfl_sync(0xffffffffu, r.rows, src);
+        out->len = __shfl_sync(0xffffffffu, r.len, src);
+        out->good = __shfl_sync(0xffffffffu, (int)r.good, src);
+        return g0 + src;
     }
-    return lo >= 0 && row < __ldcg(starts + lo + 1) ? lo : -1;
+    *out = Run{0, 0, 0, true};
+    return -1;
 }
 #endif
 
 // The runs' keys: partials (decode), or outputs where a CTA has all of a row's keys.
 cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream);
-// Behind it, a decode: the sequences' own keys, joined with those partials.
+// Behind it, a decode: the sequences' own keys, partials as well.
 cudaError_t launch_shared_rest(const RowsArgs &a, int num_sms, cudaStream_t stream);
-// Behind it: joins the partials of a cross attention's rows.
-cudaError_t launch_rows_join(const RowsArgs &a, cudaStream_t stream);
+// Behind that: joins the partials.
+cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream);
 
 }  // namespace pkv

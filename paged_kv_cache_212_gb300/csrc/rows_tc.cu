@@ -15,6 +15,7 @@
 // stand in device memory.  A unit that is cut leaves partials in 32 bits (rows.h), at most
 // one more per CTA.
 #include <math.h>
+#include <stdlib.h>
 
 #include "common.cuh"
 #include "rows.h"
@@ -53,11 +54,13 @@ struct RowsParams {
     int32_t n_runs, max_run_blocks;
     const int32_t *ctx_lens;      // decode: a row sees keys below its own; else null
     float scale_log2;
-    __nv_bfloat16 *out;           // of units that are not cut (null: partials of all)
+    __nv_bfloat16 *out;
     float *lse_out;
     RowsPartials part;
     int32_t *dev_status;
     int32_t wide_out;             // out is 32-byte aligned
+    int32_t min_tiles;            // of a share
+    float rest_weight;            // what a tile of a decode's own tokens costs an SM, in tiles of a run
     unsigned long long wait_ns;   // limit of the pipeline waits
 };
 
@@ -74,6 +77,7 @@ struct Walk {
     int64_t at, stop, total;      // tile of the stream, end of the share, of the stream
     int32_t n_ctas;
     int32_t g, idx, t;            // run, unit within it, tile within that
+    Run run;                      // g's
 };
 
 __device__ __forceinline__ int32_t tiles_of_run(const Run &r) { return (int32_t)(((uint32_t)r.len + kTN - 1u) / kTN); }
@@ -91,15 +95,14 @@ __device__ __forceinline__ Run run_of_params(const RowsParams &p, int32_t g)
 // The next part of the share.  One copy of it, out of line (instruction fetches).
 __device__ __noinline__ void next_unit(const RowsParams &p, Walk *w, Unit *out)
 {
-    Run r = run_of_params(p, w->g);
-    int32_t pairs = pairs_of_run(p, r), n_kt = tiles_of_run(r);
+    int32_t pairs = pairs_of_run(p, w->run), n_kt = tiles_of_run(w->run);
     while (n_kt == 0 || w->idx == pairs * p.n_kv_heads) {      // (the stream goes on, so there is one more)
-        ++w->g;
+        w->run = run_of_params(p, ++w->g);
         w->idx = 0;
-        r = run_of_params(p, w->g);
-        pairs = pairs_of_run(p, r);
-        n_kt = tiles_of_run(r);
+        pairs = pairs_of_run(p, w->run);
+        n_kt = tiles_of_run(w->run);
     }
+    const Run r = w->run;
     Unit u;
     u.g = w->g;
     u.kvh = w->idx / pairs;
@@ -158,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     Unit *unit_s = reinterpret_cast<Unit *>(bars + 32);
     static_assert(2 + 2 * (NK + NV) + 3 * kNQ + 3 <= 32, "barriers fit their 256 bytes");
     __shared__ Walk walk_s[5];                              // [4]: where the share begins
-    __shared__ int64_t warp_sum[kThreads / 32];
+    __shared__ int64_t warp_sum[kThreads / 32], warp_rest[kThreads / 32];
+    __shared__ CutUnit cut_s;                               // the last unit, where it goes on in the next CTA
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group;
@@ -183,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
         walk_s[4].at = walk_s[4].stop = 0;
+        cut_s.last_cta = 0;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -206,13 +211,16 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     {
         const int32_t per = (p.n_runs + kThreads - 1) / kThreads;
         const int32_t g0 = min((int64_t)threadIdx.x * per, (int64_t)p.n_runs), g1 = min((int64_t)g0 + per, (int64_t)p.n_runs);
-        int64_t sum = 0;
+        int64_t sum = 0, rest = 0;       // tiles of the runs; a decode's own tokens, those that it shares taken off
         bool good = true;
         for (int32_t g = g0; g < g1; ++g) {
             const Run r = run_of_params(p, g);
             sum += (int64_t)pairs_of_run(p, r) * p.n_kv_heads * tiles_of_run(r);
             good = good && r.good;
+            if (p.ctx_lens) rest -= (int64_t)r.rows * r.len;
         }
+        if (p.ctx_lens)
+            for (int32_t i = threadIdx.x; i < p.n_rows; i += kThreads) rest += max(__ldcg(p.ctx_lens + i), 0);
         if (!good && blockIdx.x == 0) report(p.dev_status, PKV_DEV_BAD_LENGTH);
         int64_t in = sum;
 #pragma unroll
@@ -220,14 +228,26 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const int64_t x = __shfl_up_sync(0xffffffffu, in, off);
             if (lane >= off) in += x;
         }
-        if (lane == 31) warp_sum[warp] = in;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
+        if (lane == 31) {
+            warp_sum[warp] = in;
+            warp_rest[warp] = rest;
+        }
         __syncthreads();
         int64_t before = in - sum, total = 0;
+        rest = 0;
         for (int i = 0; i < kThreads / 32; ++i) {
             if (i < warp) before += warp_sum[i];
             total += warp_sum[i];
+            rest += warp_rest[i];
         }
-        const int64_t n_ctas = min((int64_t)gridDim.x, total);
+        int64_t n_ctas = gridDim.x;
+        if (rest > 0) {
+            const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total;
+            n_ctas = max((int64_t)1, (int64_t)((float)gridDim.x * t / (t + r)));
+        }
+        n_ctas = min(n_ctas, (total + p.min_tiles - 1) / p.min_tiles);
         if (blockIdx.x < n_ctas) {
             const int64_t at = total * blockIdx.x / n_ctas;
             if (at >= before && at < before + sum) {           // this thread's runs hold the first tile
@@ -246,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         continue;
                     }
                     w.g = g;
+                    w.run = r;
                     w.idx = (int32_t)(left / n_kt);
                     w.t = (int32_t)(left - (int64_t)w.idx * n_kt);
                     break;
@@ -314,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 }
                 const int32_t t_kvh = kvh, t_unit = unit;          // of this tile
                 const bool first = j == 0;
-                if (warp == 8 && first && lane == 0) unit_s[unit & 3] = *mine;   // handed on with the unit's Q, below
+                if (warp == 8 && first && lane == 0) {
+                    unit_s[unit & 3] = *mine;                      // handed on with the unit's Q, below
+                    if (mine->cut && mine->t0 == 0) cut_s = CutUnit{mine->pos, mine->pos_end, mine->kvh, mine->last_cta};
+                }
                 if (++j == n_kt) {
                     j = 0;
                     ++unit;
@@ -566,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             // unit's first product into O comes after that.)
             if (warp_live) {
                 const int64_t row = (int64_t)pos * p.n_q_heads + w.kvh * G + r % G;
-                const bool whole = p.out && !w.cut;
+                const bool whole = !p.ctx_lens && !w.cut;
                 if (whole) {
                     const float inv = l > 0.f ? 1.f / l : 0.f;
                     __nv_bfloat16 *out = p.out + row * D;
@@ -591,7 +615,6 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                         }
                     }
                     if (live && p.lse_out) p.lse_out[row] = (m + __log2f(l)) * 0.69314718055994531f;
-                    if (live) p.part.stat[row] = make_float4(0.f, 0.f, __int_as_float(-1), __int_as_float(-1));
                 } else {
                     const bool begins = w.t0 == 0;
                     const int64_t mine = (int64_t)blockIdx.x * kUnitRows + qt * kTM + r;
@@ -626,68 +649,135 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     // everyone meets here before the TMEM is released
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) p.part.cuts[blockIdx.x] = cut_s;
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
     }
 }
 
-// ---- the join of a cross attention's cut rows: a warp to a row and query head -------------
+// ---- joins -----------------------------------------------------------------------------
+
+// Joins a piece (maximum xm, sum xl, x) to what was joined before it.  One without a
+// maximum has seen nothing.
+template <int PER>
+__device__ __forceinline__ void join_piece(float xm, float xl, const float (&x)[PER], float &m, float &l, float (&o)[PER])
+{
+    const float top = fmaxf(m, xm);
+    const float a = m == -INFINITY ? 0.f : fast_exp2(m - top), b = xm == -INFINITY ? 0.f : fast_exp2(xm - top);
+    m = top;
+    l = l * a + xl * b;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = o[e] * a + x[e] * b;
+}
+
+// The pieces that CTAs c0 .. c1 have of a unit's row `place`; a lane holds PER elements.
+template <int PER>
+__device__ __forceinline__ void join_pieces(const RowsParams &p, int32_t c0, int32_t c1, int place, float &m, float &l,
+                                            float (&o)[PER])
+{
+    constexpr int kRound = 8;                       // pieces in flight
+    const int lane = threadIdx.x & 31;
+    for (; c0 <= c1; c0 += kRound) {
+        float2 ml[kRound];
+        float x[kRound][PER];
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            if (c0 + k > c1) break;
+            const int64_t i = (int64_t)(c0 + k) * kUnitRows + place;
+            ml[k] = p.part.cont_ml[i];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[k][e] = p.part.cont[(i * 32 + lane) * PER + e];
+        }
+#pragma unroll
+        for (int k = 0; k < kRound; ++k) {
+            if (c0 + k > c1) break;
+            join_piece<PER>(ml[k].x, ml[k].y, x[k], m, l, o);
+        }
+    }
+}
+
+// The row o / l, rounded once, and its log-sum-exp; no key seen: 0 and -inf.
+template <int PER>
+__device__ __forceinline__ void write_row(const RowsParams &p, int64_t row, float m, float l, float (&o)[PER])
+{
+    const int lane = threadIdx.x & 31;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + (row * 32 + lane) * PER);
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+    if (lane == 0 && p.lse_out) p.lse_out[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ---- the join of a cross attention's cut units: a warp to a row, blocks of 8 rows of the
+// unit that begins in CTA blockIdx.x; the last row of blocks writes the rows of empty runs.
 
 template <int D>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsParams p)
 {
     constexpr int PER = D / 32;                     // elements of a lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependents_launch();
+    grid_dependency_wait();
+    const int G = p.group, tile = kTM / G;
+    if (blockIdx.y == gridDim.y - 1) {
+        for (int32_t g = (int32_t)blockIdx.x; g < p.n_runs; g += (int32_t)gridDim.x) {
+            const Run run = run_of_params(p, g);
+            if (run.len > 0) continue;
+            const int64_t row0 = (int64_t)run.row0 * p.n_q_heads, rows = (int64_t)run.rows * p.n_q_heads;
+            for (int64_t i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
+                reinterpret_cast<uint4 *>(p.out + row0 * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse_out)
+                for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) p.lse_out[row0 + i] = -INFINITY;
+        }
+        return;
+    }
+    if (p.n_runs == 0) return;
+    const CutUnit u = p.part.cuts[blockIdx.x];
+    if (u.last_cta == 0) return;
+    const int place = (int)blockIdx.y * 8 + warp, in = place % kTM;
+    const int32_t pos = u.pos + place / kTM * tile + in / G, head = u.kvh * G + in % G;
+    if (in >= tile * G || pos >= u.pos_end) return;
+    const int64_t row = (int64_t)pos * p.n_q_heads + head;
+    const float4 stat = p.part.stat[row];
+    float m = stat.x, l = stat.y, o[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] = p.part.first[row * D + lane * PER + e];
+    join_pieces<PER>(p, (int32_t)blockIdx.x + 1, u.last_cta, place, m, l, o);
+    write_row<PER>(p, row, m, l, o);
+}
+
+// ---- the join of a decode: a warp to a sequence and query head ---------------------------
+
+template <int D>
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ RowsParams p)
+{
+    constexpr int PER = D / 32;
     const int lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     grid_dependents_launch();
-    // (starts and lengths were written before the grid that this one depends on)
-    int32_t pos = -1, head = 0, g = -1;
-    Run run{};
-    if (row < (int64_t)p.n_rows * p.n_q_heads) {
-        pos = (int32_t)(row / p.n_q_heads);
-        head = (int32_t)(row - (int64_t)pos * p.n_q_heads);
-        g = run_of(p.starts, p.n_runs, pos);
-        if (g >= 0) run = run_of_params(p, g);
-    }
     grid_dependency_wait();
-    if (g < 0 || run.rows == 0) return;
-    float o[PER], m = -INFINITY, l = 0.f;
+    if (row >= (int64_t)p.n_rows * p.n_q_heads) return;
+    const int32_t pos = (int32_t)(row / p.n_q_heads), head = (int32_t)(row - (int64_t)pos * p.n_q_heads);
+    const float2 ml = p.part.own_ml[row];
+    const float4 stat = p.part.stat[row];            // (of this call where the run has keys)
+    float m = ml.x, l = ml.y, o[PER], x[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = 0.f;
-    if (run.len > 0) {
-        const float4 stat = p.part.stat[row];
-        const int32_t c0 = __float_as_int(stat.z), c1 = __float_as_int(stat.w);
-        if (c0 < 0) return;
-        m = stat.x;
-        l = stat.y;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] = p.part.first[row * D + lane * PER + e];
-        const int32_t tile = kTM / p.group, in = pos - run.row0, at = in % (kNQ * tile);
-        const int64_t place = (int64_t)(at / tile) * kTM + (at % tile) * p.group + head % p.group;
-        for (int32_t c = c0 + 1; c <= c1; ++c) {
-            const int64_t i = (int64_t)c * kUnitRows + place;
-            const float2 ml = p.part.cont_ml[i];
-            float x[PER];
-#pragma unroll
-            for (int e = 0; e < PER; ++e) x[e] = p.part.cont[i * D + lane * PER + e];
-            const float top = fmaxf(m, ml.x);
-            const float a = m == -INFINITY ? 0.f : fast_exp2(m - top), b = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-            m = top;
-            l = l * a + ml.y * b;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) o[e] = o[e] * a + x[e] * b;
-        }
+    for (int e = 0; e < PER; ++e) {
+        o[e] = p.part.own[row * D + lane * PER + e];
+        x[e] = p.part.first[row * D + lane * PER + e];
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] *= inv;
-    __nv_bfloat16 *out = p.out + row * D + lane * PER;
-    if constexpr (PER == 4)
-        *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-    else
-        *reinterpret_cast<uint32_t *>(out) = pack_bf16x2(o[0], o[1]);
-    if (lane == 0 && p.lse_out) p.lse_out[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    Run run;
+    run_of(p.starts, p.run_lens, p.n_runs, p.n_rows, p.max_run_blocks, p.block_size, pos, &run);
+    if (l < 0.f) {                                   // nothing is seen
+        l = 0.f;
+    } else if (run.len > 0) {
+        join_piece<PER>(stat.x, stat.y, x, m, l, o);
+        const int tile = kTM / p.group, in = (pos - run.row0) % (kNQ * tile);
+        join_pieces<PER>(p, __float_as_int(stat.z) + 1, __float_as_int(stat.w), in / tile * kTM + in % tile * p.group + head % p.group,
+                         m, l, o);
+    }
+    write_row<PER>(p, row, m, l, o);
 }
 
 RowsParams params_of(const RowsArgs &a)
@@ -708,11 +798,13 @@ RowsParams params_of(const RowsArgs &a)
     p.max_run_blocks = a.max_run_blocks;
     p.ctx_lens = a.ctx_lens;
     p.scale_log2 = a.softmax_scale * 1.4426950408889634f;
-    p.out = a.ctx_lens ? nullptr : static_cast<__nv_bfloat16 *>(a.out);
+    p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse_out = a.lse_out;
     p.part = a.partials;
     p.dev_status = a.dev_status;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+    p.rest_weight = getenv("PKV_W") ? atof(getenv("PKV_W")) : 0.7f;
+    p.min_tiles = getenv("PKV_MIN") ? atoi(getenv("PKV_MIN")) : 1;
     p.wait_ns = pipeline_wait_ns();
     return p;
 }
@@ -729,6 +821,17 @@ cudaLaunchConfig_t dependent(cudaLaunchAttribute (&pdl)[1], unsigned grid, unsig
     lc.attrs = pdl;
     lc.numAttrs = 1;
     return lc;
+}
+
+// CTAs that the runs' tiles may be shared out to: one per SM, and no more than there can be tiles.
+unsigned most_shares(const RowsArgs &a, int num_sms)
+{
+    const int64_t positions = kNQ * (kTM / (a.n_q_heads / a.dims.n_kv_heads));
+    const int64_t units = ((int64_t)a.n_rows / positions + a.n_runs) * a.dims.n_kv_heads;
+    const int64_t tiles = units * (((int64_t)a.max_run_blocks * a.dims.block_size + kTN - 1) / kTN);
+    int64_t n = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    if (tiles < n) n = tiles;
+    return (unsigned)(n < 1 ? 1 : n);
 }
 
 }  // namespace
@@ -781,7 +884,7 @@ cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
     }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute pdl[1];
-    const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)(num_sms < kMaxCtas ? num_sms : kMaxCtas), kThreads, smem, stream);
+    const cudaLaunchConfig_t lc = dependent(pdl, most_shares(a, num_sms), kThreads, smem, stream);
     const void *kern = d.head_dim == 128 ? reinterpret_cast<const void *>(rows_kernel<128>) : reinterpret_cast<const void *>(rows_kernel<64>);
     const cudaError_t e = prepare_kernel(kern, kThreads, smem, nullptr);
     if (e != cudaSuccess) return e;
@@ -789,12 +892,18 @@ cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
                              : cudaLaunchKernelEx(&lc, rows_kernel<64>, qmap, kmap, vmap, p);
 }
 
-cudaError_t launch_rows_join(const RowsArgs &a, cudaStream_t stream)
+cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream)
 {
     const RowsParams p = params_of(a);
     cudaLaunchAttribute pdl[1];
-    const int64_t grid = ((int64_t)a.n_rows * a.n_q_heads + 7) / 8;
-    const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)grid, 256, 0, stream);
+    if (a.ctx_lens) {
+        const int64_t grid = ((int64_t)a.n_rows * a.n_q_heads + 7) / 8;
+        const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)grid, 256, 0, stream);
+        return a.dims.head_dim == 128 ? cudaLaunchKernelEx(&lc, shared_join_kernel<128>, p)
+                                      : cudaLaunchKernelEx(&lc, shared_join_kernel<64>, p);
+    }
+    cudaLaunchConfig_t lc = dependent(pdl, most_shares(a, num_sms), 256, 0, stream);
+    lc.gridDim.y = kUnitRows / 8 + 1;
     return a.dims.head_dim == 128 ? cudaLaunchKernelEx(&lc, rows_join_kernel<128>, p) : cudaLaunchKernelEx(&lc, rows_join_kernel<64>, p);
 }
 
