@@ -13,9 +13,11 @@ constexpr int kUnitRows = 256;     // query head rows of a unit
 // The keys of a run are cut at the borders of the CTAs' shares.  The first piece of every
 // row of a cut unit (in a decode: of every row) stands at the row's own place:
 //   stat[row * Hq + head]  (maximum in log2 units, sum, first CTA, last CTA as int bits)
-//   first[row * Hq + head][D]
+//   first[kv head][D / 8][row * G + g][8]
 // and what CTAs first + 1 .. last add to it at their own, a unit's row each:
-//   cont_ml[cta][256]  (maximum, sum), cont[cta][256][D].
+//   cont_ml[cta][256]  (maximum, sum), cont[cta][D / 8][256][8].
+// (Threads hold neighbouring rows, so 8 values of each lie beside one another: with rows of
+// D values the 256 x D store of a unit took 4 us.)
 // A decode's own tokens: own_ml[row * Hq + head] (maximum, sum; a sum of -1: the row sees
 // nothing, not even its run), own[row * Hq + head][D].
 // cuts[cta]: the cut unit that begins in that CTA, the last one of its share.

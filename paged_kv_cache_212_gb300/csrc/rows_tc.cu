@@ -31,20 +31,31 @@ constexpr int kTN = 128;           // keys per K/V tile
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTileCols = 256;        // TMEM columns per query tile: S / P, O
 constexpr uint32_t kOCol = 128;            // O's column within a query tile's range
-constexpr int kThreads = 384;
+constexpr int kBars = 48;          // barriers' room
+constexpr int kScaleTiles = 4;     // int8: tiles whose scales are held
 static_assert(kNQ * kTM == kUnitRows, "a unit's rows");
 
-// Ring slots (one 128-key tile each) of K and of V that fit beside the Q tiles.
-template <int D>
-__host__ __device__ constexpr int k_slots() { return D == 128 ? 3 : 6; }
-template <int D>
-__host__ __device__ constexpr int v_slots() { return D == 128 ? 2 : 4; }
-
-// Register split (setmaxnreg), as in prefill_window.cu.
-constexpr int kLaunchRegs = 168;
-constexpr int kRegsIssue = 88;
-constexpr int kRegsSoftmax = 208;
-static_assert(128 * kRegsIssue + 256 * kRegsSoftmax <= kThreads * kLaunchRegs, "register split above the launch");
+// What depends on the type of the pages: threads, ring slots (one 128-key tile each) of K
+// and of V that fit beside the Q tiles, and the register split (setmaxnreg): bf16 as in
+// prefill_window.cu; int8 has four warps more, which widen the codes.
+template <int D, bool INT8>
+struct Setup {
+    static constexpr int kThreads = INT8 ? 512 : 384;
+    static constexpr int kSlotsK = INT8 ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);
+    static constexpr int kSlotsV = INT8 ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 4);
+    static constexpr int kLaunchRegs = INT8 ? 128 : 168;
+    static constexpr int kRegsIssue = 88;
+    static constexpr int kRegsWiden = 64;
+    static constexpr int kRegsSoftmax = INT8 ? 176 : 208;
+    static_assert(128 * kRegsIssue + (INT8 ? 128 * kRegsWiden : 0) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
+                  "register split above the launch");
+    // (the scales of tile j + kScaleTiles overwrite those of tile j: its V slot is free by the
+    // P V of tile j + kScaleTiles - kSlotsV)
+    static_assert(!INT8 || kScaleTiles > kSlotsV, "scales still in use");
+    static constexpr size_t kSmem = 1024 + (size_t)kNQ * kTM * D * 2 + (size_t)(kSlotsK + kSlotsV) * kTN * D * 2 +
+                                    kBars * sizeof(uint64_t) + 256 + (INT8 ? kScaleTiles * 2 * kTN * sizeof(float) : 0);
+    static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
+};
 
 struct RowsParams {
     int32_t n_q_heads, group, n_rows, n_kv_heads;
@@ -57,9 +68,9 @@ struct RowsParams {
     __nv_bfloat16 *out;
     float *lse_out;
     RowsPartials part;
+    const float *k_scales, *v_scales;   // int8 pages
     int32_t *dev_status;
     int32_t wide_out;             // out is 32-byte aligned
-    int32_t min_tiles;            // of a share
     float rest_weight;            // what a tile of a decode's own tokens costs an SM, in tiles of a run
     unsigned long long wait_ns;   // limit of the pipeline waits
 };
@@ -72,19 +83,32 @@ struct Unit {
     int32_t last_cta;             // that has some of it
 };
 
-// Where a CTA stands in the stream of tiles.
-struct Walk {
-    int64_t at, stop, total;      // tile of the stream, end of the share, of the stream
-    int32_t n_ctas;
-    int32_t g, idx, t;            // run, unit within it, tile within that
-    Run run;                      // g's
+// The stream that the CTAs share: unit behind unit, each kUnitCost places and then a place
+// for each of its tiles, so that a share with many short units is no longer than one with a
+// few long ones.  CTA c has places [c base + min(c, more), ...) of base or (the first `more`)
+// base + 1; base is above kUnitCost, so that every share holds a tile.
+constexpr int kUnitCost = 3;
+
+struct Share {
+    int64_t base, more;
+    __device__ __forceinline__ int64_t start(int64_t c) const { return c * base + min(c, more); }
+    __device__ __forceinline__ int32_t of(int64_t place) const
+    {
+        const int64_t wide = more * (base + 1);
+        return (int32_t)(place < wide ? (uint64_t)place / (uint64_t)(base + 1) : more + (uint64_t)(place - wide) / (uint64_t)base);
+    }
 };
 
 __device__ __forceinline__ int32_t tiles_of_run(const Run &r) { return (int32_t)(((uint32_t)r.len + kTN - 1u) / kTN); }
 __device__ __forceinline__ int32_t pairs_of_run(const RowsParams &p, const Run &r)
 {
     const int32_t positions = kNQ * (kTM / p.group);
-    return (int32_t)(((int64_t)r.rows + positions - 1) / positions);
+    return (int32_t)(((uint32_t)r.rows + (uint32_t)positions - 1u) / (uint32_t)positions);
+}
+__device__ __forceinline__ int64_t places_of_run(const RowsParams &p, const Run &r)
+{
+    const int32_t n_kt = tiles_of_run(r);
+    return n_kt == 0 ? 0 : (int64_t)pairs_of_run(p, r) * p.n_kv_heads * (n_kt + kUnitCost);
 }
 
 __device__ __forceinline__ Run run_of_params(const RowsParams &p, int32_t g)
@@ -92,43 +116,112 @@ __device__ __forceinline__ Run run_of_params(const RowsParams &p, int32_t g)
     return run_at(p.starts, p.run_lens, p.n_rows, p.max_run_blocks, p.block_size, g);
 }
 
-// The next part of the share.  One copy of it, out of line (instruction fetches).
-__device__ __noinline__ void next_unit(const RowsParams &p, Walk *w, Unit *out)
-{
-    int32_t pairs = pairs_of_run(p, w->run), n_kt = tiles_of_run(w->run);
-    while (n_kt == 0 || w->idx == pairs * p.n_kv_heads) {      // (the stream goes on, so there is one more)
-        w->run = run_of_params(p, ++w->g);
-        w->idx = 0;
-        pairs = pairs_of_run(p, w->run);
-        n_kt = tiles_of_run(w->run);
+// The parts of a CTA's share, one after the other, in the registers of a warp: lane i holds
+// run g0 + i and the places before it.
+struct Walker {
+    int64_t at, stop;             // place in the stream, end of the share
+    int32_t g0;
+    Run run;
+    int64_t before, upto;         // places before the lane's run, and with it
+
+    __device__ __forceinline__ void load(const RowsParams &p, int64_t first)
+    {
+        const int lane = threadIdx.x & 31;
+        run = Run{0, 0, 0, true};
+        if (g0 + lane < p.n_runs) run = run_of_params(p, g0 + lane);
+        const int64_t mine = places_of_run(p, run);
+        upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += x;
+        }
+        upto += first;
+        before = upto - mine;
     }
-    const Run r = w->run;
-    Unit u;
-    u.g = w->g;
-    u.kvh = w->idx / pairs;
-    u.pos = r.row0 + (w->idx - u.kvh * pairs) * (kNQ * (kTM / p.group));
-    u.pos_end = r.row0 + r.rows;
-    u.len = r.len;
-    u.t0 = w->t;
-    u.n_kt = (int32_t)min((int64_t)(n_kt - w->t), w->stop - w->at);
-    u.cut = u.n_kt < n_kt;
-    // the CTA whose share holds the unit's last tile x: the last c with floor(total c / n) <= x
-    u.last_cta = (int32_t)(((w->at - w->t + n_kt) * w->n_ctas - 1) / w->total);
-    w->at += u.n_kt;
-    w->t = 0;
-    ++w->idx;
-    u.last = w->at == w->stop;
-    *out = u;
+    __device__ __forceinline__ void next(const RowsParams &p, const Share &share, Unit *u)
+    {
+        uint32_t here;
+        while ((here = __ballot_sync(0xffffffffu, at >= before && at < upto)) == 0) {
+            g0 += 32;
+            if (g0 >= p.n_runs) {      // lengths that another stream changes meanwhile: an end in any case
+                *u = Unit{0, 0, 0, 0, 0, 0, 1, 1, 0, 0};
+                return;
+            }
+            load(p, __shfl_sync(0xffffffffu, upto, 31));
+        }
+        const int src = __ffs(here) - 1;
+        const int32_t row0 = __shfl_sync(0xffffffffu, run.row0, src), rows = __shfl_sync(0xffffffffu, run.rows, src);
+        const int64_t off = at - __shfl_sync(0xffffffffu, before, src);
+        u->len = __shfl_sync(0xffffffffu, run.len, src);
+        u->g = g0 + src;
+        const Run r{row0, rows, u->len, true};
+        const int32_t n_kt = tiles_of_run(r), pairs = pairs_of_run(p, r), places = n_kt + kUnitCost;
+        const int32_t idx = (int32_t)((uint64_t)off / (uint32_t)places);
+        const int32_t in = (int32_t)(off - (int64_t)idx * places);                      // place within the unit
+        const int64_t end = at - in + places;                                           // of the unit
+        u->kvh = (int32_t)((uint32_t)idx / (uint32_t)pairs);
+        u->pos = row0 + (idx - u->kvh * pairs) * (kNQ * (kTM / p.group));
+        u->pos_end = row0 + rows;
+        u->t0 = max(in - kUnitCost, 0);
+        u->n_kt = (int32_t)min((int64_t)n_kt, (int64_t)n_kt - (end - stop)) - u->t0;
+        u->cut = u->n_kt < n_kt;
+        u->last_cta = share.of(end - 1);
+        u->last = stop - end <= kUnitCost;                                              // (no tile of the next one)
+        at = end;
+    }
+};
+
+// Four int8 codes as bf16: with the lower seven bits of a code as the mantissa of a bf16 of
+// exponent 2^7, and 2^7 or (code < 0) 2^8 taken off, which is the code, exactly.
+__device__ __forceinline__ uint2 codes_bf16x4(uint32_t x)
+{
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = __byte_perm(x, 0x43434343u, i ? 0x4342 : 0x4140);
+        const uint32_t low = t & 0xff7fff7fu, off = t & 0xff80ff80u;
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&low), *reinterpret_cast<const __nv_bfloat162 *>(&off));
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint2(r[0], r[1]);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant__ CUtensorMap q_map,
+// A scale to shared memory, 0 where it is not there; and the barrier's arrival of this
+// thread once its copies have landed.
+__device__ __forceinline__ void copy_scale(float *dst, const float *src, bool there)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Whether x holds for all 128 threads of the widening warps, which meet here.
+__device__ __forceinline__ bool widen_all(bool x)
+{
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred a, b;\n\t"
+        "setp.ne.s32 a, %1, 0;\n\t"
+        "barrier.cta.red.and.pred b, 1, 128, a;\n\t"
+        "selp.s32 %0, 1, 0, b;\n\t}"
+        : "=r"(r)
+        : "r"((int)x)
+        : "memory");
+    return r != 0;
+}
+
+template <int D, bool INT8>
+__global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const __grid_constant__ CUtensorMap q_map,
                                                            const __grid_constant__ CUtensorMap k_map,
                                                            const __grid_constant__ CUtensorMap v_map,
                                                            const __grid_constant__ RowsParams p)
 {
     constexpr int PANELS = D / 64;                          // 64-column (128-byte) panels of a bf16 row
-    constexpr int NK = k_slots<D>(), NV = v_slots<D>();
+    using S = Setup<D, INT8>;
+    constexpr int NK = S::kSlotsK, NV = S::kSlotsV, kThreads = S::kThreads;
     constexpr uint32_t kQPanel = kTM * 128u;                // 16 KiB: one panel of a 128-row Q tile
     constexpr uint32_t kQTile = PANELS * kQPanel;
     constexpr uint32_t kKVPanel = kTN * 128u;               // 16 KiB: one panel of a 128-key K tile
@@ -151,16 +244,20 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     uint64_t *s_full = v_empty + NV;                        // [kNQ]: S in TMEM
     uint64_t *p_full = s_full + kNQ;                        // [kNQ]: P in TMEM
     uint64_t *o_done = p_full + kNQ;                        // [kNQ]: a unit's last P V product done
-    uint64_t *fin_bar = o_done + kNQ;
+    // int8: a tile's codes are there, at the beginning of the slot that they are widened into
+    uint64_t *k_codes = INT8 ? o_done + kNQ : k_full;       // [NK]
+    uint64_t *v_codes = INT8 ? k_codes + NK : v_full;       // [NV]
+    uint64_t *sc_full = INT8 ? v_codes + NV : nullptr;      // [kScaleTiles]: their scales
+    uint64_t *fin_bar = INT8 ? sc_full + kScaleTiles : o_done + kNQ;
     uint32_t *tmem_base_s = reinterpret_cast<uint32_t *>(fin_bar + 1);
     volatile int32_t *abort_flag = reinterpret_cast<int32_t *>(fin_bar + 2);
-    // Units: [4] of the issuer and the softmax warpgroups, written by warp 8 before it
+    // [4] units of the issuer and the softmax warpgroups, written by warp 8 before it
     // loads a unit's Q (unit i at i % 4: Q i - 1 was loaded, so the S of unit i - 2 were
-    // issued, behind all of the P of unit i - 3 and so the epilogues of unit i - 4), and
-    // [4] of warps 8-11, which run ahead of that.
-    Unit *unit_s = reinterpret_cast<Unit *>(bars + 32);
-    static_assert(2 + 2 * (NK + NV) + 3 * kNQ + 3 <= 32, "barriers fit their 256 bytes");
-    __shared__ Walk walk_s[5];                              // [4]: where the share begins
+    // issued, behind all of the P of unit i - 3 and so the epilogues of unit i - 4).
+    Unit *unit_s = reinterpret_cast<Unit *>(bars + kBars);
+    float *scale_s = reinterpret_cast<float *>(bars + kBars) + 64;   // int8: [kScaleTiles][K, V][128 keys]
+    __shared__ int32_t last_s[kScaleTiles];                 // int8: whether the tile is the share's last
+    static_assert(2 + (INT8 ? 3 : 2) * (NK + NV) + kScaleTiles + 3 * kNQ + 3 <= kBars && 4 * sizeof(Unit) <= 256, "their room");
     __shared__ int64_t warp_sum[kThreads / 32], warp_rest[kThreads / 32];
     __shared__ CutUnit cut_s;                               // the last unit, where it goes on in the next CTA
 
@@ -172,11 +269,13 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < NK; ++i) {
-            mbar_init(&k_full[i], 2);   // the two K producers
+            mbar_init(&k_codes[i], 2);  // the two K producers
+            if (INT8) mbar_init(&k_full[i], 4);
             mbar_init(&k_empty[i], 1);
         }
         for (int i = 0; i < NV; ++i) {
-            mbar_init(&v_full[i], 1);
+            mbar_init(&v_codes[i], 1);
+            if (INT8) mbar_init(&v_full[i], 4);
             mbar_init(&v_empty[i], 1);
         }
         for (int i = 0; i < kNQ; ++i) {
@@ -184,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             mbar_init(&p_full[i], 4);
             mbar_init(&o_done[i], 1);
         }
+        if (INT8)
+            for (int i = 0; i < kScaleTiles; ++i) mbar_init(&sc_full[i], 32);
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
-        walk_s[4].at = walk_s[4].stop = 0;
         cut_s.last_cta = 0;
         fence_mbar_init();
     }
@@ -206,39 +306,38 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // The share: tiles [total c / n, total (c + 1) / n) of the stream.  A thread sums
-    // neighbouring runs, the block sums the threads.
+    // The share, from the runs' places and a decode's own tokens: each thread sums some runs,
+    // the block sums the threads.
+    Share share{0, 0};
     {
-        const int32_t per = (p.n_runs + kThreads - 1) / kThreads;
-        const int32_t g0 = min((int64_t)threadIdx.x * per, (int64_t)p.n_runs), g1 = min((int64_t)g0 + per, (int64_t)p.n_runs);
-        int64_t sum = 0, rest = 0;       // tiles of the runs; a decode's own tokens, those that it shares taken off
+        int64_t sum = 0, rest = 0;       // places of the runs; own tokens, those that are shared taken off
         bool good = true;
-        for (int32_t g = g0; g < g1; ++g) {
+        for (int32_t g = threadIdx.x; g < p.n_runs; g += kThreads) {
             const Run r = run_of_params(p, g);
-            sum += (int64_t)pairs_of_run(p, r) * p.n_kv_heads * tiles_of_run(r);
+            sum += places_of_run(p, r);
             good = good && r.good;
             if (p.ctx_lens) rest -= (int64_t)r.rows * r.len;
         }
         if (p.ctx_lens)
             for (int32_t i = threadIdx.x; i < p.n_rows; i += kThreads) rest += max(__ldcg(p.ctx_lens + i), 0);
         if (!good && blockIdx.x == 0) report(p.dev_status, PKV_DEV_BAD_LENGTH);
-        int64_t in = sum;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, in, off);
-            if (lane >= off) in += x;
+        for (int off = 16; off > 0; off >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            rest += __shfl_xor_sync(0xffffffffu, rest, off);
         }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) rest += __shfl_xor_sync(0xffffffffu, rest, off);
-        if (lane == 31) {
-            warp_sum[warp] = in;
+        if (lane == 0) {
+            warp_sum[warp] = sum;
             warp_rest[warp] = rest;
         }
-        __syncthreads();
-        int64_t before = in - sum, total = 0;
-        rest = 0;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_base_s;
+    {
+        int64_t total = 0, rest = 0;
         for (int i = 0; i < kThreads / 32; ++i) {
-            if (i < warp) before += warp_sum[i];
             total += warp_sum[i];
             rest += warp_rest[i];
         }
@@ -247,42 +346,59 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total;
             n_ctas = max((int64_t)1, (int64_t)((float)gridDim.x * t / (t + r)));
         }
-        n_ctas = min(n_ctas, (total + p.min_tiles - 1) / p.min_tiles);
+        n_ctas = min(n_ctas, (int64_t)((uint64_t)total / (kUnitCost + 1)));
         if (blockIdx.x < n_ctas) {
-            const int64_t at = total * blockIdx.x / n_ctas;
-            if (at >= before && at < before + sum) {           // this thread's runs hold the first tile
-                Walk w;
-                w.at = at;
-                w.stop = total * (blockIdx.x + 1) / n_ctas;
-                w.total = total;
-                w.n_ctas = (int32_t)n_ctas;
-                int64_t left = at - before;
-                for (int32_t g = g0; g < g1; ++g) {
-                    const Run r = run_of_params(p, g);
-                    const int32_t n_kt = tiles_of_run(r);
-                    const int64_t tiles = (int64_t)pairs_of_run(p, r) * p.n_kv_heads * n_kt;
-                    if (left >= tiles) {
-                        left -= tiles;
-                        continue;
-                    }
-                    w.g = g;
-                    w.run = r;
-                    w.idx = (int32_t)(left / n_kt);
-                    w.t = (int32_t)(left - (int64_t)w.idx * n_kt);
-                    break;
-                }
-                walk_s[4] = w;
-            }
+            share.base = (int64_t)((uint64_t)total / (uint64_t)n_ctas);
+            share.more = total - share.base * n_ctas;
         }
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_base_s;
-    const bool any = walk_s[4].stop > walk_s[4].at;
+    const bool any = share.base > 0;
 
-    if (warp >= 4 * kNQ) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssue) : "memory");
+    if (INT8 && warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsWiden) : "memory");
+        // ===================== codes widened to bf16 =====================
+        // In place: the codes of a tile fill the first half of the slot that their bf16 values
+        // go into; all threads have read theirs before the first writes.
+        constexpr int VECS = D / 16;                        // 16-byte vectors of a code row, and of a thread
+        const int t = threadIdx.x - 384;
+        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase) -> bool {
+            const bool there = wait_for(codes, phase, abort_flag, p.wait_ns);
+            uint4 x[VECS];
+            if (there) {
+#pragma unroll
+                for (int i = 0; i < VECS; ++i) x[i] = *reinterpret_cast<const uint4 *>(slot + (i * 128 + t) * 16);
+            }
+            if (!widen_all(there)) return false;
+            const uint32_t vec = t % VECS, odd = vec / 4 & 1, chunk = vec % 4 * 2;       // VECS divides 128
+#pragma unroll
+            for (int i = 0; i < VECS; ++i) {
+                const uint32_t row = (i * 128 + t) / VECS;
+                uint8_t *dst = slot + (is_v ? row / 16 * kVGroup + odd * 2048 + row % 16 * 128 : odd * kKVPanel + row * 128);
+                const uint2 a = codes_bf16x4(x[i].x), b = codes_bf16x4(x[i].y), d = codes_bf16x4(x[i].z), e = codes_bf16x4(x[i].w);
+                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+                // (the second panel's vectors in the other order: different banks)
+                *reinterpret_cast<uint4 *>(dst + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+                *reinterpret_cast<uint4 *>(dst + (((chunk + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+            }
+            fence_proxy_async_smem();                       // visible to the tensor core
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
+            return true;
+        };
+        bool more = any;
+        for (int c = 0; more; ++c) {
+            const int ks = c % NK, vs = c % NV;
+            bool ok = widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1) &&
+                      widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1);
+            if (!ok) {
+                if (t == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
+                *abort_flag = 1;
+                break;
+            }
+            more = !const_cast<volatile int32_t *>(last_s)[c % kScaleTiles];
+        }
+    } else if (warp >= 4 * kNQ) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsIssue) : "memory");
         if (!any) {
         } else if (warp != 9) {
             // ===================== TMA producers =====================
@@ -291,34 +407,27 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             const int n_grp = is_v ? kTN / 16 : kTN / 32;
             const int grp = is_v ? lane : (warp == 10 ? kTN / 32 : 0) + lane;
             const int NSL = is_v ? NV : NK;
-            uint64_t *full = is_v ? v_full : k_full;
+            uint64_t *full = is_v ? v_codes : k_codes;
             uint64_t *empty = is_v ? v_empty : k_empty;
             uint8_t *ring = is_v ? v_ring : k_ring;
-            const uint32_t bytes = is_v ? kSlotBytes : kSlotBytes / 2;
+            const uint32_t bytes = (is_v ? kSlotBytes : kSlotBytes / 2) / (INT8 ? 2 : 1);
             // block ids are read one tile ahead, across units, and turned into pool rows
             // when the tile is issued
-            Unit *mine = unit_s + 4 + (warp - 8);
-            Walk *walk = walk_s + (warp - 8);
-            if (lane == 0) *walk = walk_s[4];
-            int32_t kvh = 0, len = 0, t0 = 0, n_kt = 0;
+            Unit mine;
+            Walker walk;
+            walk.at = share.start(blockIdx.x);
+            walk.stop = share.start((int64_t)blockIdx.x + 1);
+            walk.g0 = 0;
+            walk.load(p, 0);
             const int32_t *trow = nullptr;
-            bool last = false;
             auto load_unit = [&]() {
-                __syncwarp();
-                if (lane == 0) next_unit(p, walk, mine);
-                __syncwarp();
-                const volatile Unit &w = *mine;
-                kvh = w.kvh;
-                len = w.len;
-                t0 = w.t0;
-                n_kt = w.n_kt;
-                last = w.last;
-                trow = p.run_tables + (int64_t)w.g * p.max_run_blocks;
+                walk.next(p, share, &mine);
+                trow = p.run_tables + (int64_t)mine.g * p.max_run_blocks;
             };
             // the block of this lane's group of tile j of the unit
             auto load_block = [&](int j) -> int32_t {
-                const int32_t key = (t0 + j) * kTN + grp * 16;
-                return (lane < n_grp && key < len) ? __ldg(trow + key / p.block_size) : 0;
+                const int32_t key = (mine.t0 + j) * kTN + grp * 16;
+                return (lane < n_grp && key < mine.len) ? __ldg(trow + key / p.block_size) : 0;
             };
             load_unit();
             int32_t blk = load_block(0);
@@ -326,23 +435,24 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             bool more = true;
             while (more) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
-                const int32_t key = (t0 + j) * kTN + grp * 16;
-                if (lane < n_grp && key < len) {
+                const int32_t key = (mine.t0 + j) * kTN + grp * 16;
+                if (lane < n_grp && key < mine.len) {
                     if (blk < 0 || blk > p.n_blocks)
                         report(p.dev_status, PKV_DEV_BAD_BLOCK_ID);
                     else
                         row = blk * p.block_size + key % p.block_size;
                 }
-                const int32_t t_kvh = kvh, t_unit = unit;          // of this tile
+                const int32_t t_kvh = mine.kvh, t_unit = unit;     // of this tile
+                const int32_t t_here = mine.len - (mine.t0 + j) * kTN;   // int8: keys from its first on
                 const bool first = j == 0;
                 if (warp == 8 && first && lane == 0) {
-                    unit_s[unit & 3] = *mine;                      // handed on with the unit's Q, below
-                    if (mine->cut && mine->t0 == 0) cut_s = CutUnit{mine->pos, mine->pos_end, mine->kvh, mine->last_cta};
+                    unit_s[unit & 3] = mine;                       // handed on with the unit's Q, below
+                    if (mine.cut && mine.t0 == 0) cut_s = CutUnit{mine.pos, mine.pos_end, mine.kvh, mine.last_cta};
                 }
-                if (++j == n_kt) {
+                if (++j == mine.n_kt) {
                     j = 0;
                     ++unit;
-                    more = !last;
+                    more = !mine.last;
                     if (more) load_unit();
                 }
                 if (more) blk = load_block(j);
@@ -353,10 +463,25 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 }
                 if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
                 uint8_t *dst = ring + st * kSlotBytes;
+                if (INT8 && is_v) {                                // the tile's scales, four keys to a lane
+                    float *sc = scale_s + (issued % kScaleTiles) * 2 * kTN;
+#pragma unroll
+                    for (int i = 0; i < kTN; i += 32) {
+                        const int32_t r0 = __shfl_sync(0xffffffffu, row, (i + lane) / 16);
+                        const bool in = i + lane < t_here && r0 != p.pool_rows;      // else 0: a row of zeros
+                        const int64_t at = in ? ((int64_t)r0 + (lane & 15)) * p.n_kv_heads + t_kvh : 0;
+                        copy_scale(sc + i + lane, p.k_scales + at, in);
+                        copy_scale(sc + kTN + i + lane, p.v_scales + at, in);
+                    }
+                    copies_arrive(&sc_full[issued % kScaleTiles]);
+                    if (lane == 0) last_s[issued % kScaleTiles] = !more;
+                }
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
                 __syncwarp();
                 if (lane < n_grp) {
-                    if (is_v) {
+                    if (INT8) {
+                        tma_load_3d(dst + grp * 16 * D, is_v ? &v_map : &k_map, 0, t_kvh, row, &full[st]);
+                    } else if (is_v) {
                         tma_load_3d(dst + grp * kVGroup, &v_map, 0, row, t_kvh * PANELS, &full[st]);
                     } else {
 #pragma unroll
@@ -386,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 }
             }
             // every copy this warp issued has landed before the CTA can exit
+            if (INT8) asm volatile("cp.async.wait_all;" ::: "memory");
             if (lane == 0) {
                 if (warp == 8 && q_loads > 0) (void)mbar_wait(q_full, (q_loads - 1) & 1);
                 for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i)
@@ -503,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
             __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax) : "memory");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegsSoftmax) : "memory");
         // ===================== softmax warpgroups: row r = TMEM lane r =====================
         const int qt = warp / 4;
         const int r = threadIdx.x % kTM;
@@ -546,35 +672,78 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                     warp_live = __any_sync(0xffffffffu, live);
                 }
                 const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;
+                if constexpr (INT8) {
+                    ok = __all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns));
+                    if (!ok) break;
+                }
                 if (warp_live) {                 // (others leave P as it is: their rows go nowhere)
-                    uint32_t sv[kTN];
-#pragma unroll
-                    for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
-                    tmem_wait_ld();
+                    const bool masked = __any_sync(0xffffffffu, limit - key0 < kTN);
                     // rows whose keys in this tile are all visible need no per-key test
-                    if (__any_sync(0xffffffffu, limit - key0 < kTN)) {
+                    auto mask32 = [&](uint32_t *x, int i0) {
+                        const uint32_t seen = bits_below(limit - key0 - i0);
+                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
 #pragma unroll
-                        for (int i0 = 0; i0 < kTN; i0 += 32) {
-                            const uint32_t seen = bits_below(limit - key0 - i0);
-                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+                        for (int i = 0; i < 32; ++i)
+                            if (!((seen >> i) & 1)) x[i] = __float_as_uint(-INFINITY);
+                    };
+                    if constexpr (!INT8) {
+                        uint32_t sv[kTN];
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
+                        for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
+                        tmem_wait_ld();
+                        if (masked) {
+#pragma unroll
+                            for (int i0 = 0; i0 < kTN; i0 += 32) mask32(sv + i0, i0);
                         }
+                        const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
+                        // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
+                        // commit came after it
+                        if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                        // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
+                        // columns it covers were read
+                        const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                        const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
+                        const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
+                        l = l * alpha + (l0 + l1);
+                    } else {
+                        // Half a row at a time, the second half twice: with the scales beside them 128
+                        // scores do not fit the registers of 512 threads.
+                        const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN;
+                        auto load64 = [&](uint32_t (&x)[64], int i0) {      // times the keys' scales, masked
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) tmem_ld32_async(lane_base + i0 + i * 32, x + i * 32);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 64; i += 4) {
+                                const float4 k = *reinterpret_cast<const float4 *>(sc + i0 + i);
+                                const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k.x, k.y));
+                                const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k.z, k.w));
+                                x[i] = __float_as_uint(a.x);
+                                x[i + 1] = __float_as_uint(a.y);
+                                x[i + 2] = __float_as_uint(b.x);
+                                x[i + 3] = __float_as_uint(b.y);
+                            }
+                            if (masked) {
+                                mask32(x, i0);
+                                mask32(x + 32, i0 + 32);
+                            }
+                        };
+                        uint32_t sv[64];
+                        load64(sv, 64);
+                        float top = largest(sv);
+                        load64(sv, 0);
+                        top = fmaxf(top, largest(sv));
+                        const float alpha = move_maximum(m, top * p.scale_log2);
+                        if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                        const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                        const float l0 = weighed64<0>(sv, sc2, nm2, sc + kTN, lane_base);
+                        load64(sv, 64);
+                        const float l1 = weighed64<0>(sv, sc2, nm2, sc + kTN + 64, lane_base + 32);
+                        l = l * alpha + (l0 + l1);
                     }
-                    const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
-                    // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
-                    // commit came after it
-                    if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
-                    // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
-                    // columns it covers were read
-                    const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                    const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
-                    const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
-                    l = l * alpha + (l0 + l1);
                     tmem_wait_st();
                 }
-                if (tail < kTN && (tail & 15) != 0) {
+                if (!INT8 && tail < kTN && (tail & 15) != 0) {   // (int8: their scales are 0)
                     ok = clean_v(tail);
                     if (!ok) break;
                 }
@@ -618,7 +787,10 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                 } else {
                     const bool begins = w.t0 == 0;
                     const int64_t mine = (int64_t)blockIdx.x * kUnitRows + qt * kTM + r;
-                    float *dst = begins ? p.part.first + row * D : p.part.cont + mine * D;
+                    const int64_t rows = (int64_t)p.n_rows * G;
+                    const int64_t step = begins ? rows * 8 : kUnitRows * 8;              // to a row's next 8 values
+                    float *dst = begins ? p.part.first + (w.kvh * (D / 8) * rows + (int64_t)pos * G + r % G) * 8
+                                        : p.part.cont + ((int64_t)blockIdx.x * (D / 8) * kUnitRows + qt * kTM + r) * 8;
 #pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
                         uint32_t v[32];
@@ -630,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1) rows_kernel(const __grid_constant
                             uint32_t x[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e) x[e] = v[8 * q2 + e];
-                            st_global_32(dst + i * 32 + q2 * 8, x);
+                            st_global_32(dst + (i * 4 + q2) * step, x);
                         }
                     }
                     if (live && begins)
@@ -671,6 +843,19 @@ __device__ __forceinline__ void join_piece(float xm, float xl, const float (&x)[
     for (int e = 0; e < PER; ++e) o[e] = o[e] * a + x[e] * b;
 }
 
+// A lane's PER elements of the first piece of (row, query head).
+template <int PER>
+__device__ __forceinline__ void load_first(const RowsParams &p, int32_t pos, int32_t head, float (&x)[PER])
+{
+    const int lane = threadIdx.x & 31;
+    const int32_t kvh = head / p.group;
+    const int64_t rows = (int64_t)p.n_rows * p.group;
+    const float *src = p.part.first + ((kvh * (4 * PER) + lane * PER / 8) * rows + (int64_t)pos * p.group + head - kvh * p.group) * 8 +
+                       lane * PER % 8;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) x[e] = src[e];
+}
+
 // The pieces that CTAs c0 .. c1 have of a unit's row `place`; a lane holds PER elements.
 template <int PER>
 __device__ __forceinline__ void join_pieces(const RowsParams &p, int32_t c0, int32_t c1, int place, float &m, float &l,
@@ -687,7 +872,8 @@ __device__ __forceinline__ void join_pieces(const RowsParams &p, int32_t c0, int
             const int64_t i = (int64_t)(c0 + k) * kUnitRows + place;
             ml[k] = p.part.cont_ml[i];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) x[k][e] = p.part.cont[(i * 32 + lane) * PER + e];
+            for (int e = 0; e < PER; ++e)
+                x[k][e] = p.part.cont[(((int64_t)(c0 + k) * (4 * PER) + lane * PER / 8) * kUnitRows + place) * 8 + lane * PER % 8 + e];
         }
 #pragma unroll
         for (int k = 0; k < kRound; ++k) {
@@ -716,7 +902,7 @@ template <int D>
 __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsParams p)
 {
     constexpr int PER = D / 32;                     // elements of a lane
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
     grid_dependents_launch();
     grid_dependency_wait();
     const int G = p.group, tile = kTM / G;
@@ -741,8 +927,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
     const int64_t row = (int64_t)pos * p.n_q_heads + head;
     const float4 stat = p.part.stat[row];
     float m = stat.x, l = stat.y, o[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = p.part.first[row * D + lane * PER + e];
+    load_first<PER>(p, pos, head, o);
     join_pieces<PER>(p, (int32_t)blockIdx.x + 1, u.last_cta, place, m, l, o);
     write_row<PER>(p, row, m, l, o);
 }
@@ -763,10 +948,8 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
     const float4 stat = p.part.stat[row];            // (of this call where the run has keys)
     float m = ml.x, l = ml.y, o[PER], x[PER];
 #pragma unroll
-    for (int e = 0; e < PER; ++e) {
-        o[e] = p.part.own[row * D + lane * PER + e];
-        x[e] = p.part.first[row * D + lane * PER + e];
-    }
+    for (int e = 0; e < PER; ++e) o[e] = p.part.own[row * D + lane * PER + e];
+    load_first<PER>(p, pos, head, x);
     Run run;
     run_of(p.starts, p.run_lens, p.n_runs, p.n_rows, p.max_run_blocks, p.block_size, pos, &run);
     if (l < 0.f) {                                   // nothing is seen
@@ -801,10 +984,11 @@ RowsParams params_of(const RowsArgs &a)
     p.out = static_cast<__nv_bfloat16 *>(a.out);
     p.lse_out = a.lse_out;
     p.part = a.partials;
+    p.k_scales = a.k_scales;
+    p.v_scales = a.v_scales;
     p.dev_status = a.dev_status;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     p.rest_weight = getenv("PKV_W") ? atof(getenv("PKV_W")) : 0.7f;
-    p.min_tiles = getenv("PKV_MIN") ? atoi(getenv("PKV_MIN")) : 1;
     p.wait_ns = pipeline_wait_ns();
     return p;
 }
@@ -834,6 +1018,25 @@ unsigned most_shares(const RowsArgs &a, int num_sms)
     return (unsigned)(n < 1 ? 1 : n);
 }
 
+template <int D, bool INT8>
+cudaError_t launch_as(const CUtensorMap &qmap, const CUtensorMap &kmap, const CUtensorMap &vmap, const RowsParams &p, unsigned grid,
+                      cudaStream_t stream)
+{
+    using S = Setup<D, INT8>;
+    // The register split assumes the block gets kLaunchRegs per thread: refuse
+    // a build whose kernel was given fewer (its setmaxnreg.inc could not complete).
+    static const bool regs_ok = [] {
+        cudaFuncAttributes fa{};
+        return cudaFuncGetAttributes(&fa, rows_kernel<D, INT8>) == cudaSuccess && fa.numRegs >= S::kLaunchRegs;
+    }();
+    if (!regs_ok) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(rows_kernel<D, INT8>), S::kThreads, S::kSmem, nullptr);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute pdl[1];
+    const cudaLaunchConfig_t lc = dependent(pdl, grid, S::kThreads, S::kSmem, stream);
+    return cudaLaunchKernelEx(&lc, rows_kernel<D, INT8>, qmap, kmap, vmap, p);
+}
+
 }  // namespace
 
 cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
@@ -850,46 +1053,39 @@ cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
             return cudaErrorInvalidValue;
     }
     const uint64_t rows = (uint64_t)(d.n_blocks + 1) * d.block_size;
-    const uint64_t row_bytes = (uint64_t)d.n_kv_heads * d.head_dim * 2;
-    {
-        // K: {64 columns, kv head, pool row}, one head and 16 rows per box
+    const bool int8 = a.kv_dtype == PKV_KV_INT8;
+    const uint64_t row_bytes = (uint64_t)d.n_kv_heads * d.head_dim * (int8 ? 1 : 2);
+    if (int8) {
+        // {codes of a row, kv head, pool row}: 16 rows of one head lie behind one another
         const uint64_t dims[3] = {(uint64_t)d.head_dim, (uint64_t)d.n_kv_heads, rows};
-        const uint64_t strides[2] = {(uint64_t)d.head_dim * 2, row_bytes};
-        const uint32_t box[3] = {64u, 1u, 16u};
-        if (encode_tensor_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.k_pool), dims, strides,
-                              box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+        const uint64_t strides[2] = {(uint64_t)d.head_dim, row_bytes};
+        const uint32_t box[3] = {(uint32_t)d.head_dim, 1u, 16u};
+        if (encode_tensor_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(a.k_pool), dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS ||
+            encode_tensor_map(&vmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(a.v_pool), dims, strides,
+                              box, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
-    }
-    {
+    } else {
+        // K: {64 columns, kv head, pool row}, one head and 16 rows per box
+        const uint64_t kdims[3] = {(uint64_t)d.head_dim, (uint64_t)d.n_kv_heads, rows};
+        const uint64_t kstrides[2] = {(uint64_t)d.head_dim * 2, row_bytes};
+        const uint32_t kbox[3] = {64u, 1u, 16u};
         // V: {64 columns, pool row, 64-column panel of all heads}: a box of 16
         // rows and a head's panels lands as [panel][row][128 B]
         const uint32_t panels = (uint32_t)d.head_dim / 64u;
-        const uint64_t dims[3] = {64u, rows, (uint64_t)d.n_kv_heads * panels};
-        const uint64_t strides[2] = {row_bytes, 128u};
-        const uint32_t box[3] = {64u, 16u, panels};
-        if (encode_tensor_map(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.v_pool), dims, strides,
-                              box, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+        const uint64_t vdims[3] = {64u, rows, (uint64_t)d.n_kv_heads * panels};
+        const uint64_t vstrides[2] = {row_bytes, 128u};
+        const uint32_t vbox[3] = {64u, 16u, panels};
+        if (encode_tensor_map(&kmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.k_pool), kdims, kstrides,
+                              kbox, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+            encode_tensor_map(&vmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.v_pool), vdims, vstrides,
+                              vbox, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    const int slots = d.head_dim == 128 ? k_slots<128>() + v_slots<128>() : k_slots<64>() + v_slots<64>();
-    const size_t smem = 1024 + (size_t)kNQ * kTM * d.head_dim * 2 + (size_t)slots * kTN * d.head_dim * 2 + 32 * sizeof(uint64_t) +
-                        8 * sizeof(Unit);
-    // The register split assumes the block gets kLaunchRegs per thread: refuse
-    // a build whose kernel was given fewer (its setmaxnreg.inc could not complete).
-    static const bool regs_ok = [] {
-        cudaFuncAttributes fa128{}, fa64{};
-        return cudaFuncGetAttributes(&fa128, rows_kernel<128>) == cudaSuccess &&
-               cudaFuncGetAttributes(&fa64, rows_kernel<64>) == cudaSuccess && fa128.numRegs >= kLaunchRegs &&
-               fa64.numRegs >= kLaunchRegs;
-    }();
-    if (!regs_ok) return cudaErrorInvalidConfiguration;
-    cudaLaunchAttribute pdl[1];
-    const cudaLaunchConfig_t lc = dependent(pdl, most_shares(a, num_sms), kThreads, smem, stream);
-    const void *kern = d.head_dim == 128 ? reinterpret_cast<const void *>(rows_kernel<128>) : reinterpret_cast<const void *>(rows_kernel<64>);
-    const cudaError_t e = prepare_kernel(kern, kThreads, smem, nullptr);
-    if (e != cudaSuccess) return e;
-    return d.head_dim == 128 ? cudaLaunchKernelEx(&lc, rows_kernel<128>, qmap, kmap, vmap, p)
-                             : cudaLaunchKernelEx(&lc, rows_kernel<64>, qmap, kmap, vmap, p);
+    const unsigned grid = most_shares(a, num_sms);
+    if (d.head_dim == 128)
+        return int8 ? launch_as<128, true>(qmap, kmap, vmap, p, grid, stream) : launch_as<128, false>(qmap, kmap, vmap, p, grid, stream);
+    return int8 ? launch_as<64, true>(qmap, kmap, vmap, p, grid, stream) : launch_as<64, false>(qmap, kmap, vmap, p, grid, stream);
 }
 
 cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream)
