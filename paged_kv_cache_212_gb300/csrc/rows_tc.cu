@@ -49,9 +49,9 @@ struct Setup {
     static constexpr int kRegsSoftmax = INT8 ? 176 : 208;
     static_assert(128 * kRegsIssue + (INT8 ? 128 * kRegsWiden : 0) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
                   "register split above the launch");
-    // (the scales of tile j + kScaleTiles overwrite those of tile j: its V slot is free by the
-    // P V of tile j + kScaleTiles - kSlotsV)
-    static_assert(!INT8 || kScaleTiles > kSlotsV, "scales still in use");
+    // (the scales of tile j + kScaleTiles overwrite those of tile j: its K slot is free by the
+    // S of tile j + kScaleTiles - kSlotsK, whose K was widened behind the V of tile j)
+    static_assert(!INT8 || kScaleTiles > kSlotsK, "scales still in use");
     static constexpr size_t kSmem = 1024 + (size_t)kNQ * kTM * D * 2 + (size_t)(kSlotsK + kSlotsV) * kTN * D * 2 +
                                     kBars * sizeof(uint64_t) + 256 + (INT8 ? kScaleTiles * 2 * kTN * sizeof(float) : 0);
     static_assert(kSmem <= 227 * 1024 - 512, "shared memory");
@@ -172,19 +172,16 @@ struct Walker {
     }
 };
 
-// Four int8 codes as bf16: with the lower seven bits of a code as the mantissa of a bf16 of
-// exponent 2^7, and 2^7 or (code < 0) 2^8 taken off, which is the code, exactly.
-__device__ __forceinline__ uint2 codes_bf16x4(uint32_t x)
+// Four int8 codes (code + 128 in x) times a scale as bf16: with a byte as the low one of
+// the binary32 value 2^23 + byte, which the subtraction leaves as the code, exactly.
+__device__ __forceinline__ uint2 widened4(uint32_t x, float scale)
 {
-    uint32_t r[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t t = __byte_perm(x, 0x43434343u, i ? 0x4342 : 0x4140);
-        const uint32_t low = t & 0xff7fff7fu, off = t & 0xff80ff80u;
-        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&low), *reinterpret_cast<const __nv_bfloat162 *>(&off));
-        r[i] = *reinterpret_cast<const uint32_t *>(&v);
-    }
-    return make_uint2(r[0], r[1]);
+    const float2 bias = make_float2(-8388736.f, -8388736.f), s2 = make_float2(scale, scale);      // -(2^23 + 128)
+    float2 a = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7441)));
+    float2 b = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7442)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7443)));
+    a = __fmul2_rn(__fadd2_rn(a, bias), s2);
+    b = __fmul2_rn(__fadd2_rn(b, bias), s2);
+    return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 
 // A scale to shared memory, 0 where it is not there; and the barrier's arrival of this
@@ -198,19 +195,15 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Whether x holds for all 128 threads of the widening warps, which meet here.
-__device__ __forceinline__ bool widen_all(bool x)
+// int8: where in a slot the codes of 16 rows go.
+// The bf16 values of a row are one piece of 128 bytes in each panel; head_dim 128: a row's
+// codes lie in its piece of the second panel.  head_dim 64: the codes of 16 rows in the
+// pieces of their last 8.
+template <int D>
+__device__ __forceinline__ uint32_t codes_at(bool is_v, uint32_t row)
 {
-    int r;
-    asm volatile(
-        "{\n\t.reg .pred a, b;\n\t"
-        "setp.ne.s32 a, %1, 0;\n\t"
-        "barrier.cta.red.and.pred b, 1, 128, a;\n\t"
-        "selp.s32 %0, 1, 0, b;\n\t}"
-        : "=r"(r)
-        : "r"((int)x)
-        : "memory");
-    return r != 0;
+    if (D == 64) return row / 16 * 2048 + 1024;
+    return is_v ? row / 16 * 4096 + 2048 + row % 16 * 128 : kTN * 128u + row * 128;
 }
 
 template <int D, bool INT8>
@@ -284,7 +277,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             mbar_init(&o_done[i], 1);
         }
         if (INT8)
-            for (int i = 0; i < kScaleTiles; ++i) mbar_init(&sc_full[i], 32);
+            for (int i = 0; i < kScaleTiles; ++i) mbar_init(&sc_full[i], 64);   // the K producers' lanes
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
         cut_s.last_cta = 0;
@@ -356,29 +349,35 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
 
     if (INT8 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsWiden) : "memory");
-        // ===================== codes widened to bf16 =====================
-        // In place: the codes of a tile fill the first half of the slot that their bf16 values
-        // go into; all threads have read theirs before the first writes.
-        constexpr int VECS = D / 16;                        // 16-byte vectors of a code row, and of a thread
-        const int t = threadIdx.x - 384;
-        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase) -> bool {
-            const bool there = wait_for(codes, phase, abort_flag, p.wait_ns);
-            uint4 x[VECS];
-            if (there) {
+        // ===================== codes widened to bf16, times their scales =====================
+        // In place: the codes of a row (head_dim 64: of 16 rows) lie where bf16 values of the
+        // same rows go, so a warp reads some rows, then writes them.  (Loops, not unrolled code:
+        // all reads before all writes, with 32 registers of codes, took 2.5 us a K tile.)
+        constexpr int VECS = D / 16;                        // 16-byte vectors of a code row
+        constexpr int AT_ONCE = D == 128 ? 4 : 2;           // vectors of a lane: 16 rows
+        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase, const float *sc) -> bool {
+            if (!__all_sync(0xffffffffu, wait_for(codes, phase, abort_flag, p.wait_ns))) return false;
+            const uint32_t vec = lane % VECS, odd = vec / 4 & 1, chunk = vec % 4 * 2;
+#pragma unroll 1
+            for (uint32_t row0 = (warp - 12) * 32; row0 < (warp - 12) * 32 + 32; row0 += 16) {
+                uint4 x[AT_ONCE];
+                float scale[AT_ONCE];
 #pragma unroll
-                for (int i = 0; i < VECS; ++i) x[i] = *reinterpret_cast<const uint4 *>(slot + (i * 128 + t) * 16);
-            }
-            if (!widen_all(there)) return false;
-            const uint32_t vec = t % VECS, odd = vec / 4 & 1, chunk = vec % 4 * 2;       // VECS divides 128
+                for (int i = 0; i < AT_ONCE; ++i) scale[i] = sc[row0 + (i * 32 + lane) / VECS];
 #pragma unroll
-            for (int i = 0; i < VECS; ++i) {
-                const uint32_t row = (i * 128 + t) / VECS;
-                uint8_t *dst = slot + (is_v ? row / 16 * kVGroup + odd * 2048 + row % 16 * 128 : odd * kKVPanel + row * 128);
-                const uint2 a = codes_bf16x4(x[i].x), b = codes_bf16x4(x[i].y), d = codes_bf16x4(x[i].z), e = codes_bf16x4(x[i].w);
-                const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
-                // (the second panel's vectors in the other order: different banks)
-                *reinterpret_cast<uint4 *>(dst + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-                *reinterpret_cast<uint4 *>(dst + (((chunk + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+                for (int i = 0; i < AT_ONCE; ++i) x[i] = *reinterpret_cast<const uint4 *>(slot + codes_at<D>(is_v, row0) + (i * 32 + lane) * 16);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < AT_ONCE; ++i) {
+                    const uint32_t row = row0 + (i * 32 + lane) / VECS;
+                    uint8_t *dst = slot + (is_v ? row / 16 * kVGroup + odd * 2048 + row % 16 * 128 : odd * kKVPanel + row * 128);
+                    const uint2 a = widened4(x[i].x ^ 0x80808080u, scale[i]), b = widened4(x[i].y ^ 0x80808080u, scale[i]);
+                    const uint2 d = widened4(x[i].z ^ 0x80808080u, scale[i]), e = widened4(x[i].w ^ 0x80808080u, scale[i]);
+                    const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
+                    // (the second panel's vectors in the other order: different banks)
+                    *reinterpret_cast<uint4 *>(dst + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
+                    *reinterpret_cast<uint4 *>(dst + (((chunk + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+                }
             }
             fence_proxy_async_smem();                       // visible to the tensor core
             __syncwarp();
@@ -388,10 +387,11 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         bool more = any;
         for (int c = 0; more; ++c) {
             const int ks = c % NK, vs = c % NV;
-            bool ok = widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1) &&
-                      widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1);
-            if (!ok) {
-                if (t == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
+            const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN;
+            if (!__all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns)) ||
+                !widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1, sc) ||
+                !widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1, sc + kTN)) {
+                if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
                 *abort_flag = 1;
                 break;
             }
@@ -463,24 +463,25 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 }
                 if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
                 uint8_t *dst = ring + st * kSlotBytes;
-                if (INT8 && is_v) {                                // the tile's scales, four keys to a lane
-                    float *sc = scale_s + (issued % kScaleTiles) * 2 * kTN;
+                if (INT8 && !is_v) {                               // the scales of the warp's keys
+                    const int key0 = warp == 10 ? kTN / 2 : 0;
+                    float *sc = scale_s + (issued % kScaleTiles) * 2 * kTN + key0 + lane;
 #pragma unroll
-                    for (int i = 0; i < kTN; i += 32) {
+                    for (int i = 0; i < kTN / 2; i += 32) {
                         const int32_t r0 = __shfl_sync(0xffffffffu, row, (i + lane) / 16);
-                        const bool in = i + lane < t_here && r0 != p.pool_rows;      // else 0: a row of zeros
+                        const bool in = key0 + i + lane < t_here && r0 != p.pool_rows;      // else 0: a row of zeros
                         const int64_t at = in ? ((int64_t)r0 + (lane & 15)) * p.n_kv_heads + t_kvh : 0;
-                        copy_scale(sc + i + lane, p.k_scales + at, in);
-                        copy_scale(sc + kTN + i + lane, p.v_scales + at, in);
+                        copy_scale(sc + i, p.k_scales + at, in);
+                        copy_scale(sc + kTN + i, p.v_scales + at, in);
                     }
                     copies_arrive(&sc_full[issued % kScaleTiles]);
-                    if (lane == 0) last_s[issued % kScaleTiles] = !more;
+                    if (warp == 8 && lane == 0) last_s[issued % kScaleTiles] = !more;
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
                 __syncwarp();
                 if (lane < n_grp) {
                     if (INT8) {
-                        tma_load_3d(dst + grp * 16 * D, is_v ? &v_map : &k_map, 0, t_kvh, row, &full[st]);
+                        tma_load_3d(dst + codes_at<D>(is_v, grp * 16), is_v ? &v_map : &k_map, 0, t_kvh, row, &full[st]);
                     } else if (is_v) {
                         tma_load_3d(dst + grp * kVGroup, &v_map, 0, row, t_kvh * PANELS, &full[st]);
                     } else {
@@ -672,78 +673,35 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     warp_live = __any_sync(0xffffffffu, live);
                 }
                 const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;
-                if constexpr (INT8) {
-                    ok = __all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns));
-                    if (!ok) break;
-                }
                 if (warp_live) {                 // (others leave P as it is: their rows go nowhere)
-                    const bool masked = __any_sync(0xffffffffu, limit - key0 < kTN);
+                    uint32_t sv[kTN];
+#pragma unroll
+                    for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
+                    tmem_wait_ld();
                     // rows whose keys in this tile are all visible need no per-key test
-                    auto mask32 = [&](uint32_t *x, int i0) {
-                        const uint32_t seen = bits_below(limit - key0 - i0);
-                        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
+                    if (__any_sync(0xffffffffu, limit - key0 < kTN)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((seen >> i) & 1)) x[i] = __float_as_uint(-INFINITY);
-                    };
-                    if constexpr (!INT8) {
-                        uint32_t sv[kTN];
+                        for (int i0 = 0; i0 < kTN; i0 += 32) {
+                            const uint32_t seen = bits_below(limit - key0 - i0);
+                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
-                        for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
-                        tmem_wait_ld();
-                        if (masked) {
-#pragma unroll
-                            for (int i0 = 0; i0 < kTN; i0 += 32) mask32(sv + i0, i0);
+                            for (int i = 0; i < 32; ++i)
+                                if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);
                         }
-                        const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
-                        // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
-                        // commit came after it
-                        if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
-                        // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
-                        // columns it covers were read
-                        const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                        const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
-                        const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
-                        l = l * alpha + (l0 + l1);
-                    } else {
-                        // Half a row at a time, the second half twice: with the scales beside them 128
-                        // scores do not fit the registers of 512 threads.
-                        const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN;
-                        auto load64 = [&](uint32_t (&x)[64], int i0) {      // times the keys' scales, masked
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) tmem_ld32_async(lane_base + i0 + i * 32, x + i * 32);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int i = 0; i < 64; i += 4) {
-                                const float4 k = *reinterpret_cast<const float4 *>(sc + i0 + i);
-                                const float2 a = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(k.x, k.y));
-                                const float2 b = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(k.z, k.w));
-                                x[i] = __float_as_uint(a.x);
-                                x[i + 1] = __float_as_uint(a.y);
-                                x[i + 2] = __float_as_uint(b.x);
-                                x[i + 3] = __float_as_uint(b.y);
-                            }
-                            if (masked) {
-                                mask32(x, i0);
-                                mask32(x + 32, i0 + 32);
-                            }
-                        };
-                        uint32_t sv[64];
-                        load64(sv, 64);
-                        float top = largest(sv);
-                        load64(sv, 0);
-                        top = fmaxf(top, largest(sv));
-                        const float alpha = move_maximum(m, top * p.scale_log2);
-                        if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
-                        const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                        const float l0 = weighed64<0>(sv, sc2, nm2, sc + kTN, lane_base);
-                        load64(sv, 64);
-                        const float l1 = weighed64<0>(sv, sc2, nm2, sc + kTN + 64, lane_base + 32);
-                        l = l * alpha + (l0 + l1);
                     }
+                    const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
+                    // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
+                    // commit came after it
+                    if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                    // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
+                    // columns it covers were read
+                    const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
+                    const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
+                    const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
+                    l = l * alpha + (l0 + l1);
                     tmem_wait_st();
                 }
-                if (!INT8 && tail < kTN && (tail & 15) != 0) {   // (int8: their scales are 0)
+                if (!INT8 && tail < kTN && (tail & 15) != 0) {   // (int8: zeros, by their scales)
                     ok = clean_v(tail);
                     if (!ok) break;
                 }
