@@ -89,12 +89,16 @@ struct WindowArgs {
     int64_t k_stride, v_stride;
     const int32_t *start_pos;
     RopeArgs rope;
-    // shared first tokens (SHARED): the groups, and what the rows kernel has of their tokens
-    const int32_t *group_starts, *prefix_lens;
-    int32_t n_groups, max_prefix_blocks, n_seqs;
-    RowsPartials part;
+    // runs (rows.h): where rows, which may be more than sequences, have keys in common
+    const int32_t *run_starts, *run_lens, *run_tables;
+    int32_t n_runs, max_run_blocks, n_rows;
+    RowsPartials part;                 // kRest
     int32_t after_rows;
 };
+
+// What a kernel does with runs: there are none; a row's own tokens alone, as a partial; a
+// run's tokens and then a row's own (a cross attention, which has no ctx_lens: no own ones).
+enum { kNoRuns, kRest, kWhole };
 
 template <int D, bool INT8>
 struct Shape {
@@ -207,14 +211,21 @@ struct Seen {
         w_tile = max(low / kTile, n_first);
         tiles = n_first + max(0, (L + kTile - 1) / kTile - w_tile);
     }
-    // tokens low .. L - 1 alone
-    __device__ __forceinline__ Seen(int32_t from, int32_t stop)
+    // runs: tokens 0 .. n - 1 of the run, then tokens from .. stop - 1 of the row's own
+    __device__ __forceinline__ Seen(int32_t n, int32_t from, int32_t stop)
     {
         L = stop;
-        first = n_first = 0;
+        first = n;
+        n_first = (first + kTile - 1) / kTile;
         low = from;
         w_tile = low / kTile;
-        tiles = low < L ? (L + kTile - 1) / kTile - w_tile : 0;
+        tiles = n_first + (low < L ? (L + kTile - 1) / kTile - w_tile : 0);
+    }
+    __device__ __forceinline__ uint32_t mask_of_run(int32_t t) const { return first - t >= kTile ? 0xffffu : (1u << (first - t)) - 1u; }
+    __device__ __forceinline__ uint32_t mask_of_own(int32_t t) const
+    {
+        const uint32_t below_L = L - t >= kTile ? 0xffffu : (1u << max(L - t, 0)) - 1u;
+        return below_L & (low <= t ? 0xffffu : 0xffffu << (low - t));
     }
     // the place of tile i in the sequence, in tiles, and which of its 16 tokens are seen
     __device__ __forceinline__ int32_t place(int32_t i) const { return i < n_first ? i : w_tile + i - n_first; }
@@ -229,8 +240,7 @@ struct Seen {
 };
 
 // WIDE: 5 to 8 query heads per kv head (bf16; int8 pages have one form for all).
-// SHARED: a sequence's tokens behind those that its group shares, whose result is a partial.
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode_window_kernel(const WindowArgs a)
 {
     using S = Shape<D, INT8>;
@@ -258,32 +268,43 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + (S::kShared ? 0 : warp) * 2 * S::kRow;   // a step's K and V row
 
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
-    // (SHARED behind the rows kernel, which has waited itself before it let this one start:
+    // (kRest behind the rows kernel, which has waited itself before it let this one start:
     // all that is read was written before that.  One CTA waits at its end, so that the grid
     // ends behind the rows kernel; if all did, those of the first round would keep the rest
     // from starting)
-    if (!SHARED || !a.after_rows) grid_dependency_wait();
+    if (RUNS != kRest || !a.after_rows) grid_dependency_wait();
 
     // 1. the tiles
-    const int32_t len = SHARED ? __ldcg(a.ctx_lens + s) : __ldg(a.ctx_lens + s);
     const int32_t t_new = step ? __ldg(a.start_pos + s) : -1;
+    int32_t len = 0, g_run = -1;
     Run run{0, 0, 0, true};
-    if constexpr (SHARED) run_of(a.group_starts, a.prefix_lens, a.n_groups, a.n_seqs, a.max_prefix_blocks, bs, s, &run);
+    if constexpr (RUNS == kNoRuns) {
+        len = __ldg(a.ctx_lens + s);
+    } else {
+        if (a.ctx_lens) len = __ldcg(a.ctx_lens + s);
+        g_run = run_of(a.run_starts, a.run_lens, a.n_runs, a.n_rows, a.max_run_blocks, bs, s, &run);
+    }
     const Seen all(a, len);
-    const int32_t L = SHARED && !run.good ? 0 : all.L;
-    const Seen seen = SHARED ? Seen(min(run.len, L), L) : all;
     if (tid == 0 && h == 0 && rank == 0 && len != all.L) report(a.dev_status, PKV_DEV_BAD_LENGTH);
+    const int32_t L = RUNS == kNoRuns ? all.L : !run.good ? 0 : RUNS == kWhole && !a.ctx_lens ? run.len : all.L;
+    const Seen seen = RUNS == kNoRuns ? all : Seen(RUNS == kWhole ? min(run.len, L) : 0, min(run.len, L), L);
+    const int32_t *run_row = RUNS == kWhole ? a.run_tables + (int64_t)g_run * a.max_run_blocks : nullptr;
+    if (RUNS == kWhole && blockIdx.x == 0)
+        for (int32_t i = tid; i < a.n_runs; i += 32 * WARPS)
+            if (!run_at(a.run_starts, a.run_lens, a.n_rows, a.max_run_blocks, bs, i).good) report(a.dev_status, PKV_DEV_BAD_LENGTH);
     const int n_workers = WARPS * a.splits, worker = rank * WARPS + warp;
 
     // 2. the warp's copies, which run ahead of its products by kStages - 1 tiles
     int32_t a_tile = worker, a_token = 0, a_off = 0, id = 0;
+    bool a_run = false;                             // a tile of the run
     auto look_up = [&]() {                          // the block of the next tile to copy
         if (a_tile >= seen.tiles) return;
         const uint32_t at = (uint32_t)seen.place(a_tile);
         const uint32_t blk = a.tiles_per_block == 1 ? at : __umulhi(at, a.block_magic);
         a_token = (int32_t)at * kTile;
         a_off = (int32_t)(at - blk * a.tiles_per_block) * kTile;
-        id = SHARED ? __ldcg(trow + blk) : __ldg(trow + blk);
+        a_run = RUNS == kWhole && a_tile < seen.n_first;
+        id = RUNS == kNoRuns ? __ldg(trow + blk) : __ldcg((a_run ? run_row : trow) + blk);
     };
     look_up();
     const uint32_t lane_dst = S::at(lane / S::kVecs, lane % S::kVecs);   // of the lane's first vector in a tile
@@ -294,8 +315,8 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     constexpr int RPI = 32 / S::kVecs;              // rows that the warp copies at once
     auto issue = [&](int st) {
         if (a_tile < seen.tiles) {
-            uint32_t there = seen.mask(a_token);
-            const uint32_t zeros = there;            // SHARED: a bad block's tokens are seen as rows of zeros
+            uint32_t there = RUNS == kNoRuns ? seen.mask(a_token) : a_run ? seen.mask_of_run(a_token) : seen.mask_of_own(a_token);
+            const uint32_t zeros = there;            // runs: a bad block's tokens are seen as rows of zeros
             if (id < 0 || id > a.n_blocks) {
                 if (lane == 0) report(a.dev_status, PKV_DEV_BAD_BLOCK_ID);
                 there = 0;
@@ -303,7 +324,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             const int32_t row = there ? id * bs + a_off : 0;
             // bits 0-15: there; 16-31: the step's new token, which comes from new_rows
             const uint32_t fresh = step && (uint32_t)(t_new - a_token) < (uint32_t)kTile ? there & (1u << (t_new - a_token)) : 0u;
-            if (lane == 0) present_s[warp][st] = (SHARED ? zeros : there) | (fresh << 16);
+            if (lane == 0) present_s[warp][st] = (RUNS == kNoRuns ? there : zeros) | (fresh << 16);
             a_tile += n_workers;
             look_up();
             const uint32_t dst = smem_u32(my_ring + st * S::kStage);
@@ -717,12 +738,13 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         M2 = N2;
     };
     auto finish = [&](int g, int d, const float4 &v, float M, float M2, float sum) {
-        if constexpr (SHARED) {                      // a partial, in units of 2^M
+        if constexpr (RUNS == kRest) {              // a partial, in units of 2^M
             const float f = M2 == -INFINITY ? 1.f : fast_exp2(M2 - M);
             *reinterpret_cast<float4 *>(a.part.own + (head0 + g) * D + d) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
             if (d == 0) a.part.own_ml[head0 + g] = make_float2(M, L > 0 ? sum : -1.f);
             return;
         }
+        if (RUNS == kWhole && !a.ctx_lens && g_run < 0) return;     // a row of no sequence
         // o = 2^M2 v / (2^M sum); no token seen: 0
         const float inv = sum == 0.f ? 0.f : (M2 == -INFINITY ? 1.f : INT8 ? fast_exp2(M2 - M) : 1.f) / sum;
         *reinterpret_cast<uint2 *>(a.out + (head0 + g) * D + d) =
@@ -746,7 +768,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             if (d == 0) c_stat[g] = make_float4(M, M2, sum, 0.f);
         }
     }
-    if (SHARED && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+    if (RUNS == kRest && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
     if (a.splits == 1) return;
     cluster_sync_all();
     for (int i = rank * 32 * WARPS + tid; i < G * (D / 4); i += a.splits * 32 * WARPS) {
@@ -788,7 +810,7 @@ constexpr size_t smem_for(size_t need, int per_sm)
     return most > need ? most : need;
 }
 
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 cudaLaunchConfig_t launch_config(cudaLaunchAttribute (&at)[2], int64_t units, int splits, int per_sm, cudaStream_t stream)
 {
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -811,7 +833,7 @@ constexpr int kDevices = 16;   // whose occupancies are remembered
 
 // How many CTAs an SM of the current device holds; asked once, when the kernel's
 // limit of shared memory is raised to the most that a launch asks for.
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 cudaError_t resident_ctas(int *out)
 {
     static std::atomic<int> known[kDevices];   // 0: not asked yet
@@ -819,7 +841,7 @@ cudaError_t resident_ctas(int *out)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < kDevices && (*out = known[dev]) > 0) return cudaSuccess;
-    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, SHARED, WARPS>);
+    const void *kern = reinterpret_cast<const void *>(decode_window_kernel<D, INT8, WIDE, RUNS, WARPS>);
     e = prepare_kernel(kern, 32 * WARPS, smem_for(Shape<D, INT8>::smem(WARPS), 1), nullptr);
     if (e != cudaSuccess) return e;
     e = prepare_kernel(kern, 32 * WARPS, Shape<D, INT8>::smem(WARPS), out);
@@ -832,12 +854,12 @@ cudaError_t resident_ctas(int *out)
 // How many clusters of `splits` CTAs are resident at once on the current device with
 // at most `per_sm` CTAs on an SM (clusters stay within a GPC, so not every SM can
 // hold one); asked once.
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 cudaError_t resident_clusters(int splits, int per_sm, int *out)
 {
     constexpr int kPerSm = 32;
     static std::atomic<int> known[kDevices][kMaxSplits + 1][kPerSm + 1];   // the number + 1; 0: not asked yet
-    const auto kern = decode_window_kernel<D, INT8, WIDE, SHARED, WARPS>;
+    const auto kern = decode_window_kernel<D, INT8, WIDE, RUNS, WARPS>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -851,7 +873,7 @@ cudaError_t resident_clusters(int splits, int per_sm, int *out)
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute at[2];
-    cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, SHARED, WARPS>(at, 1, splits, per_sm, nullptr);
+    cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, RUNS, WARPS>(at, 1, splits, per_sm, nullptr);
     lc.attrs = at + 1;
     lc.numAttrs = 1;
     e = cudaOccupancyMaxActiveClusters(out, kern, &lc);
@@ -868,10 +890,10 @@ cudaError_t resident_clusters(int splits, int per_sm, int *out)
 // over int8 pages 9.9 us with the 8 CTAs (of 4 warps) that two tiles a warp allow, 8.2
 // with the 6 that give the longest share, three tiles, as well, and 12.0 with one
 // tile a warp.
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 {
-    cudaError_t e = resident_ctas<D, INT8, WIDE, SHARED, WARPS>(&c->occupancy);
+    cudaError_t e = resident_ctas<D, INT8, WIDE, RUNS, WARPS>(&c->occupancy);
     if (e != cudaSuccess) return e;
     c->places = (int64_t)sms * c->occupancy;
     int64_t n = c->places / units;
@@ -882,7 +904,7 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
         n = (tiles + share * WARPS - 1) / (share * WARPS);
         if (n == 1) break;
         int clusters = 0;
-        e = resident_clusters<D, INT8, WIDE, SHARED, WARPS>((int)n, c->occupancy, &clusters);
+        e = resident_clusters<D, INT8, WIDE, RUNS, WARPS>((int)n, c->occupancy, &clusters);
         if (e != cudaSuccess) return e;
         if (clusters >= units) break;
     }
@@ -897,7 +919,7 @@ cudaError_t choose(int64_t units, int64_t tiles, int sms, Choice *c)
 // some SMs take as many as they hold and others none.  Measured (windows of 1024,
 // 8 kv heads of 128, int8 pages, as placed / spread): 28 sequences 19.2 / 16.7 us, no
 // difference at 8 and 56; bf16 pages, bound by memory, are 0 to 4 % faster.
-template <int D, bool INT8, bool WIDE, bool SHARED, int WARPS>
+template <int D, bool INT8, bool WIDE, int RUNS, int WARPS>
 cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cudaStream_t stream)
 {
     a.splits = c.splits;
@@ -906,13 +928,13 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cu
     cudaError_t e;
     for (; c.splits > 1 && per_sm < c.occupancy; ++per_sm) {
         int clusters = 0;
-        e = resident_clusters<D, INT8, WIDE, SHARED, WARPS>(c.splits, per_sm, &clusters);
+        e = resident_clusters<D, INT8, WIDE, RUNS, WARPS>(c.splits, per_sm, &clusters);
         if (e != cudaSuccess) return e;
         if (clusters >= units) break;
     }
     cudaLaunchAttribute at[2];
-    const cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, SHARED, WARPS>(at, units, c.splits, per_sm, stream);
-    return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, SHARED, WARPS>, a);
+    const cudaLaunchConfig_t lc = launch_config<D, INT8, WIDE, RUNS, WARPS>(at, units, c.splits, per_sm, stream);
+    return cudaLaunchKernelEx(&lc, decode_window_kernel<D, INT8, WIDE, RUNS, WARPS>, a);
 }
 
 // CTAs of 4 warps, of 2 or of 8.
@@ -931,22 +953,29 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cu
 // us, 12: 6.4 / 5.4; 1024 tokens, one sequence 5.7 / 6.1, 4: 7.4 / 6.4, 16: 15.0 / 14.1;
 // 16 K tokens, one 19.7 / 17.4, two 26.4 / 27.3; int8 pages, 1024 tokens, 4: 7.5 / 6.9,
 // 16: 13.1 / 11.7; 16 K, one 21.2 / 16.0, two 27.0 / 24.5.
-template <int D, bool INT8, bool WIDE, bool SHARED = false>
+//
+// Of 8 too for whole rows of more than 1024 tokens (kWhole): their lengths are as ragged as
+// the sequences', and the longest rows of small CTAs end long after the rest.  Measured (rule
+// above / 4 warps / 8; rows of 512 to 4096 tokens): bf16 pages, 32 rows 64.2 / 64.3 / 57.0 us,
+// 64: 121 / 116 / 106, 150: 255 / 236 / 228; int8 pages, 64: 91.3 / 91.8 / 82.9; but rows of
+// 512 to 1024, 64: 39.1 / 37.6 / 39.6.
+template <int D, bool INT8, bool WIDE, int RUNS = kNoRuns>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
     Choice c4, c2, c8;
-    cudaError_t e = choose<D, INT8, WIDE, SHARED, 4>(units, tiles, sms, &c4);
+    cudaError_t e = choose<D, INT8, WIDE, RUNS, 4>(units, tiles, sms, &c4);
     if (e != cudaSuccess) return e;
-    e = choose<D, INT8, WIDE, SHARED, 2>(units, tiles, sms, &c2);
+    e = choose<D, INT8, WIDE, RUNS, 2>(units, tiles, sms, &c2);
     if (e != cudaSuccess) return e;
-    e = choose<D, INT8, WIDE, SHARED, 8>(units, tiles, sms, &c8);
+    e = choose<D, INT8, WIDE, RUNS, 8>(units, tiles, sms, &c8);
     if (e != cudaSuccess) return e;
+    if (RUNS == kWhole && tiles > 64) return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
     const bool alone = c8.splits == 1 && c4.splits > 1 && c8.share <= c4.share;
     if (units <= c8.places && (alone || c8.share < c4.share || (units * c4.splits > sms && c8.room <= c4.room)))
-        return launch_as<D, INT8, WIDE, SHARED, 8>(a, c8, units, sms, stream);
+        return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
     const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
-    return small ? launch_as<D, INT8, WIDE, SHARED, 2>(a, c2, units, sms, stream)
-                 : launch_as<D, INT8, WIDE, SHARED, 4>(a, c4, units, sms, stream);
+    return small ? launch_as<D, INT8, WIDE, RUNS, 2>(a, c2, units, sms, stream)
+                 : launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
 }
 
 // The constants of the kernel's block lookup.

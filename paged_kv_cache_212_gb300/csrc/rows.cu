@@ -8,14 +8,33 @@
 namespace pkv {
 namespace {
 
+// Whether rows are attended one by one, each reading its run's keys again (from the L2, where
+// they are shared), in one launch: where every sequence of a cross attention has a row at
+// most, and where what the rows can read, by the width of their table rows, is below what the
+// two or three launches of the other way cost.  Measured (8 kv heads of 128, bf16 pages; all
+// at once / one by one): cross attention of one row each, 8 sequences of 512 .. 4096 keys
+// 31.1 / 20.4 us, 64: 124.6 / 121.1, 64 over int8 pages 234 / 91, but with two rows each 125.6
+// / 159.5; decode behind a shared prefix, 32 sequences behind 256 tokens (38 MB) 18.7 / 7.4,
+// 4 behind 4096 (68 MB) 21.2 / 11.4, 16 behind 4096 (285 MB) 24.2 / 26.9.
+constexpr int64_t kOneByOneBytes = 192 << 20;       // as bf16
+
+bool one_by_one(const RowsArgs &a)
+{
+    if (a.n_q_heads / a.dims.n_kv_heads > 8) return false;
+    if (!a.ctx_lens && a.n_rows <= a.n_runs) return true;
+    const int64_t tokens = (int64_t)(a.ctx_lens ? a.max_blocks : a.max_run_blocks) * a.dims.block_size;
+    return tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows;
+}
+
 cudaError_t launch_rows(const RowsArgs &a, int num_sms, cudaStream_t stream)
 {
+    if (one_by_one(a)) return launch_rows_whole(a, num_sms, stream);
     if (a.n_runs > 0) {
         const cudaError_t e = launch_rows_tc(a, num_sms, stream);
         if (e != cudaSuccess) return e;
     }
     if (a.ctx_lens) {
-        const cudaError_t e = launch_shared_rest(a, num_sms, stream);
+        const cudaError_t e = launch_rows_rest(a, num_sms, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_rows_join(a, num_sms, stream);

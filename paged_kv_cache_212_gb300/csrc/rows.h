@@ -135,8 +135,11 @@ __device__ __forceinline__ int32_t run_of(const int32_t *starts, const int32_t *
 // The runs' keys: partials (decode), or outputs where a CTA has all of a row's keys.
 cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream);
 // Behind it, a decode: the sequences' own keys, partials as well.
-cudaError_t launch_shared_rest(const RowsArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rows_rest(const RowsArgs &a, int num_sms, cudaStream_t stream);
 // Behind that: joins the partials.
 cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream);
+
+// All of it in one launch, each row by itself.
+cudaError_t launch_rows_whole(const RowsArgs &a, int num_sms, cudaStream_t stream);
 
 }  // namespace pkv
