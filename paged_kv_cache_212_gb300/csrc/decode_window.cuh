@@ -741,7 +741,11 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         if constexpr (RUNS == kRest) {              // a partial, in units of 2^M
             const float f = M2 == -INFINITY ? 1.f : fast_exp2(M2 - M);
             *reinterpret_cast<float4 *>(a.part.own + (head0 + g) * D + d) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
-            if (d == 0) a.part.own_ml[head0 + g] = make_float2(M, L > 0 ? sum : -1.f);
+            if (d == 0) {
+                const int tile = kUnitRows / 2 / G, in = (s - run.row0) % (2 * tile);
+                const int place = run.len > 0 && L > 0 ? in / tile * (kUnitRows / 2) + in % tile * G : -1;
+                a.part.own_stat[head0 + g] = make_float4(M, sum, __int_as_float(place), 0.f);
+            }
             return;
         }
         if (RUNS == kWhole && !a.ctx_lens && g_run < 0) return;     // a row of no sequence

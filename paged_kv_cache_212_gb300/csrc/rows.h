@@ -18,8 +18,8 @@ constexpr int kUnitRows = 256;     // query head rows of a unit
 //   cont_ml[cta][256]  (maximum, sum), cont[cta][D / 8][256][8].
 // (Threads hold neighbouring rows, so 8 values of each lie beside one another: with rows of
 // D values the 256 x D store of a unit took 4 us.)
-// A decode's own tokens: own_ml[row * Hq + head] (maximum, sum; a sum of -1: the row sees
-// nothing, not even its run), own[row * Hq + head][D].
+// A decode's own tokens: own_stat[row * Hq + head] (maximum, sum, as int bits where the row's
+// first query head lies in its unit, or -1 where no run is to be joined), own[row * Hq + head][D].
 // cuts[cta]: the cut unit that begins in that CTA, the last one of its share.
 struct CutUnit {
     int32_t pos, pos_end, kvh, last_cta;   // last_cta 0: none
@@ -31,13 +31,13 @@ struct RowsPartials {
     float *cont;
     CutUnit *cuts;
     float *own;
-    float2 *own_ml;
+    float4 *own_stat;
 };
 
 inline size_t rows_workspace_bytes(int64_t n_rows, int32_t n_q_heads, int32_t head_dim)
 {
     const size_t rows = (size_t)n_rows * (size_t)n_q_heads, cont = (size_t)kMaxCtas * kUnitRows;
-    return (2 * rows + cont) * (size_t)head_dim * sizeof(float) + rows * (sizeof(float4) + sizeof(float2)) +
+    return (2 * rows + cont) * (size_t)head_dim * sizeof(float) + rows * 2 * sizeof(float4) +
            cont * sizeof(float2) + kMaxCtas * sizeof(CutUnit);
 }
 
@@ -49,9 +49,9 @@ inline RowsPartials carve_rows_workspace(void *ws, int64_t n_rows, int32_t n_q_h
     p.first = p.cont + cont * head_dim;
     p.own = p.first + rows * head_dim;
     p.stat = reinterpret_cast<float4 *>(p.own + rows * head_dim);
-    p.cuts = reinterpret_cast<CutUnit *>(p.stat + rows);
+    p.own_stat = p.stat + rows;
+    p.cuts = reinterpret_cast<CutUnit *>(p.own_stat + rows);
     p.cont_ml = reinterpret_cast<float2 *>(p.cuts + kMaxCtas);
-    p.own_ml = p.cont_ml + cont;
     return p;
 }
 

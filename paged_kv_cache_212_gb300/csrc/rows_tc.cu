@@ -87,7 +87,7 @@ struct Unit {
 // for each of its tiles, so that a share with many short units is no longer than one with a
 // few long ones.  CTA c has places [c base + min(c, more), ...) of base or (the first `more`)
 // base + 1; base is above kUnitCost, so that every share holds a tile.
-constexpr int kUnitCost = 3;
+constexpr int kUnitCost = 2;
 
 struct Share {
     int64_t base, more;
@@ -429,9 +429,22 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 const int32_t key = (mine.t0 + j) * kTN + grp * 16;
                 return (lane < n_grp && key < mine.len) ? __ldg(trow + key / p.block_size) : 0;
             };
+            int q_loads = 0;                                // that lane 0 has issued
+            // (a group that does not divide 128 leaves the tile's last rows as they are: rows of
+            // S are independent of one another)
+            auto load_q = [&](const Unit &w) {
+                mbar_arrive_expect_tx(q_full, kNQ * PANELS * pos_per_tile * G * 128);
+#pragma unroll 1
+                for (int i = 0; i < kNQ * PANELS; ++i) {
+                    const int t = i / PANELS, h = i % PANELS;
+                    tma_load_3d(q_s + t * kQTile + h * kQPanel, &q_map, h * 64, w.kvh * G, w.pos + t * pos_per_tile, q_full);
+                }
+                ++q_loads;
+            };
             load_unit();
+            if (warp == 8 && lane == 0) load_q(mine);       // the first unit's, before its block is known
             int32_t blk = load_block(0);
-            int j = 0, issued = 0, unit = 0, q_loads = 0;   // tile of the unit, tiles so far, unit, Qs that lane 0 has issued
+            int j = 0, issued = 0, unit = 0;                // tile of the unit, tiles so far, unit
             bool more = true;
             while (more) {
                 int32_t row = p.pool_rows;  // out of range: the box reads zeros
@@ -491,21 +504,13 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     }
                 }
                 ++issued;
-                if (warp == 8 && first) {   // the unit's Q, once the last unit's has been read
+                if (warp == 8 && first && t_unit > 0) {   // the unit's Q, once the last unit's has been read
                     if (lane == 0) {
                         if (!wait_for(q_empty, (t_unit & 1) ^ 1, abort_flag, p.wait_ns)) {
                             report(p.dev_status, PKV_DEV_TIMEOUT);
                             *abort_flag = 1;
                         } else {
-                            // (a group that does not divide 128 leaves the tile's last rows as they
-                            // are: rows of S are independent of one another)
-                            const Unit &w = unit_s[t_unit & 3];
-                            mbar_arrive_expect_tx(q_full, kNQ * PANELS * pos_per_tile * G * 128);
-                            for (int i = 0; i < kNQ; ++i)
-                                for (int h = 0; h < PANELS; ++h)
-                                    tma_load_3d(q_s + i * kQTile + h * kQPanel, &q_map, h * 64, t_kvh * G,
-                                                w.pos + i * pos_per_tile, q_full);
-                            ++q_loads;   // (lane 0's: another role may have raised the flag by now)
+                            load_q(unit_s[t_unit & 3]);
                         }
                     }
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
@@ -786,84 +791,85 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     }
 }
 
-// ---- joins -----------------------------------------------------------------------------
+// ---- joins: a thread to 16 columns of a row, neighbouring rows to neighbouring threads --------
+
+constexpr int kCols = 16;
+
+struct Joined {
+    float m, l, o[kCols];
+};
+
+__device__ __forceinline__ void load8(float *x, const float *src)
+{
+    const float4 a = __ldcg(reinterpret_cast<const float4 *>(src)), b = __ldcg(reinterpret_cast<const float4 *>(src) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
 
 // Joins a piece (maximum xm, sum xl, x) to what was joined before it.  One without a
 // maximum has seen nothing.
-template <int PER>
-__device__ __forceinline__ void join_piece(float xm, float xl, const float (&x)[PER], float &m, float &l, float (&o)[PER])
+__device__ __forceinline__ void join_piece(Joined &j, float xm, float xl, const float (&x)[kCols])
 {
-    const float top = fmaxf(m, xm);
-    const float a = m == -INFINITY ? 0.f : fast_exp2(m - top), b = xm == -INFINITY ? 0.f : fast_exp2(xm - top);
-    m = top;
-    l = l * a + xl * b;
+    const float top = fmaxf(j.m, xm);
+    const float a = j.m == -INFINITY ? 0.f : fast_exp2(j.m - top), b = xm == -INFINITY ? 0.f : fast_exp2(xm - top);
+    j.m = top;
+    j.l = j.l * a + xl * b;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = o[e] * a + x[e] * b;
+    for (int e = 0; e < kCols; ++e) j.o[e] = j.o[e] * a + x[e] * b;
 }
 
-// A lane's PER elements of the first piece of (row, query head).
-template <int PER>
-__device__ __forceinline__ void load_first(const RowsParams &p, int32_t pos, int32_t head, float (&x)[PER])
+// Columns kCols part .. of the first piece of row i = pos * G + g of a kv head.
+template <int D>
+__device__ __forceinline__ void load_first(const RowsParams &p, int32_t kvh, int64_t i, int part, float (&x)[kCols])
 {
-    const int lane = threadIdx.x & 31;
-    const int32_t kvh = head / p.group;
     const int64_t rows = (int64_t)p.n_rows * p.group;
-    const float *src = p.part.first + ((kvh * (4 * PER) + lane * PER / 8) * rows + (int64_t)pos * p.group + head - kvh * p.group) * 8 +
-                       lane * PER % 8;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) x[e] = src[e];
+    for (int k = 0; k < kCols / 8; ++k) load8(x + 8 * k, p.part.first + ((kvh * (D / 8) + kCols / 8 * part + k) * rows + i) * 8);
 }
 
-// The pieces that CTAs c0 .. c1 have of a unit's row `place`; a lane holds PER elements.
-template <int PER>
-__device__ __forceinline__ void join_pieces(const RowsParams &p, int32_t c0, int32_t c1, int place, float &m, float &l,
-                                            float (&o)[PER])
+// The pieces that CTAs c0 .. c1 have of a unit's row `place`.
+template <int D>
+__device__ __forceinline__ void join_pieces(const RowsParams &p, Joined &j, int32_t c0, int32_t c1, int place, int part)
 {
-    constexpr int kRound = 8;                       // pieces in flight
-    const int lane = threadIdx.x & 31;
+    constexpr int kRound = 4;                       // pieces in flight
     for (; c0 <= c1; c0 += kRound) {
         float2 ml[kRound];
-        float x[kRound][PER];
+        float x[kRound][kCols];
 #pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            if (c0 + k > c1) break;
-            const int64_t i = (int64_t)(c0 + k) * kUnitRows + place;
-            ml[k] = p.part.cont_ml[i];
+        for (int i = 0; i < kRound; ++i) {
+            if (c0 + i > c1) break;
+            ml[i] = __ldcg(p.part.cont_ml + (int64_t)(c0 + i) * kUnitRows + place);
 #pragma unroll
-            for (int e = 0; e < PER; ++e)
-                x[k][e] = p.part.cont[(((int64_t)(c0 + k) * (4 * PER) + lane * PER / 8) * kUnitRows + place) * 8 + lane * PER % 8 + e];
+            for (int k = 0; k < kCols / 8; ++k)
+                load8(x[i] + 8 * k, p.part.cont + (((int64_t)(c0 + i) * (D / 8) + kCols / 8 * part + k) * kUnitRows + place) * 8);
         }
 #pragma unroll
-        for (int k = 0; k < kRound; ++k) {
-            if (c0 + k > c1) break;
-            join_piece<PER>(ml[k].x, ml[k].y, x[k], m, l, o);
+        for (int i = 0; i < kRound; ++i) {
+            if (c0 + i > c1) break;
+            join_piece(j, ml[i].x, ml[i].y, x[i]);
         }
     }
 }
 
-// The row o / l, rounded once, and its log-sum-exp; no key seen: 0 and -inf.
-template <int PER>
-__device__ __forceinline__ void write_row(const RowsParams &p, int64_t row, float m, float l, float (&o)[PER])
+// The columns of a row, o / l rounded once, and its log-sum-exp; no key seen: 0 and -inf.
+template <int D>
+__device__ __forceinline__ void write_joined(const RowsParams &p, const Joined &j, int64_t row, int part)
 {
-    const int lane = threadIdx.x & 31;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + (row * 32 + lane) * PER);
+    const float inv = j.l > 0.f ? 1.f / j.l : 0.f;
+    uint4 *out = reinterpret_cast<uint4 *>(p.out + row * D + kCols * part);
 #pragma unroll
-    for (int e = 0; e < PER; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
-    if (lane == 0 && p.lse_out) p.lse_out[row] = l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+    for (int k = 0; k < kCols / 8; ++k)
+        out[k] = make_uint4(pack_bf16x2(j.o[8 * k] * inv, j.o[8 * k + 1] * inv), pack_bf16x2(j.o[8 * k + 2] * inv, j.o[8 * k + 3] * inv),
+                            pack_bf16x2(j.o[8 * k + 4] * inv, j.o[8 * k + 5] * inv), pack_bf16x2(j.o[8 * k + 6] * inv, j.o[8 * k + 7] * inv));
+    if (part == 0 && p.lse_out) p.lse_out[row] = j.l > 0.f ? (j.m + __log2f(j.l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// ---- the join of a cross attention's cut units: a warp to a row, blocks of 8 rows of the
-// unit that begins in CTA blockIdx.x; the last row of blocks writes the rows of empty runs.
-
+// A cross attention: the cut unit that begins in CTA blockIdx.x; the last blockIdx.y writes the
+// rows of empty runs.
 template <int D>
-__global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ RowsParams p)
+__global__ void __launch_bounds__(kTM) rows_join_kernel(const __grid_constant__ RowsParams p)
 {
-    constexpr int PER = D / 32;                     // elements of a lane
-    const int warp = threadIdx.x >> 5;
     grid_dependents_launch();
     grid_dependency_wait();
-    const int G = p.group, tile = kTM / G;
     if (blockIdx.y == gridDim.y - 1) {
         for (int32_t g = (int32_t)blockIdx.x; g < p.n_runs; g += (int32_t)gridDim.x) {
             const Run run = run_of_params(p, g);
@@ -876,49 +882,47 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const __grid_constant__ 
         }
         return;
     }
-    if (p.n_runs == 0) return;
     const CutUnit u = p.part.cuts[blockIdx.x];
     if (u.last_cta == 0) return;
-    const int place = (int)blockIdx.y * 8 + warp, in = place % kTM;
-    const int32_t pos = u.pos + place / kTM * tile + in / G, head = u.kvh * G + in % G;
-    if (in >= tile * G || pos >= u.pos_end) return;
+    const int part = (int)blockIdx.y % (D / kCols), qt = (int)blockIdx.y / (D / kCols), r = threadIdx.x;
+    const int G = p.group, tile = kTM / G;
+    const int32_t pos = u.pos + qt * tile + r / G, head = u.kvh * G + r % G;
+    if (r >= tile * G || pos >= u.pos_end) return;
     const int64_t row = (int64_t)pos * p.n_q_heads + head;
     const float4 stat = p.part.stat[row];
-    float m = stat.x, l = stat.y, o[PER];
-    load_first<PER>(p, pos, head, o);
-    join_pieces<PER>(p, (int32_t)blockIdx.x + 1, u.last_cta, place, m, l, o);
-    write_row<PER>(p, row, m, l, o);
+    Joined j;
+    j.m = stat.x;
+    j.l = stat.y;
+    load_first<D>(p, u.kvh, (int64_t)pos * G + r % G, part, j.o);
+    join_pieces<D>(p, j, (int32_t)blockIdx.x + 1, u.last_cta, qt * kTM + r, part);
+    write_joined<D>(p, j, row, part);
 }
 
-// ---- the join of a decode: a warp to a sequence and query head ---------------------------
-
+// A decode: rows 128 blockIdx.x .. of the sequences' query heads of kv head blockIdx.y.
 template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ RowsParams p)
+__global__ void __launch_bounds__(kTM) shared_join_kernel(const __grid_constant__ RowsParams p)
 {
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     grid_dependents_launch();
     grid_dependency_wait();
-    if (row >= (int64_t)p.n_rows * p.n_q_heads) return;
-    const int32_t pos = (int32_t)(row / p.n_q_heads), head = (int32_t)(row - (int64_t)pos * p.n_q_heads);
-    const float2 ml = p.part.own_ml[row];
-    const float4 stat = p.part.stat[row];            // (of this call where the run has keys)
-    float m = ml.x, l = ml.y, o[PER], x[PER];
+    const int part = (int)blockIdx.z, G = p.group;
+    const int64_t i = (int64_t)blockIdx.x * kTM + threadIdx.x;
+    if (i >= (int64_t)p.n_rows * G) return;
+    const int32_t kvh = (int32_t)blockIdx.y, pos = (int32_t)(i / G), g = (int32_t)(i - (int64_t)pos * G);
+    const int64_t row = (int64_t)pos * p.n_q_heads + kvh * G + g;
+    const float4 own = __ldcg(p.part.own_stat + row), stat = __ldcg(p.part.stat + row);   // (stat: of this call where `place` says so)
+    Joined j;
+    float x[kCols];
+    j.m = own.x;
+    j.l = own.y;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) o[e] = p.part.own[row * D + lane * PER + e];
-    load_first<PER>(p, pos, head, x);
-    Run run;
-    run_of(p.starts, p.run_lens, p.n_runs, p.n_rows, p.max_run_blocks, p.block_size, pos, &run);
-    if (l < 0.f) {                                   // nothing is seen
-        l = 0.f;
-    } else if (run.len > 0) {
-        join_piece<PER>(stat.x, stat.y, x, m, l, o);
-        const int tile = kTM / p.group, in = (pos - run.row0) % (kNQ * tile);
-        join_pieces<PER>(p, __float_as_int(stat.z) + 1, __float_as_int(stat.w), in / tile * kTM + in % tile * p.group + head % p.group,
-                         m, l, o);
+    for (int k = 0; k < kCols / 8; ++k) load8(j.o + 8 * k, p.part.own + row * D + kCols * part + 8 * k);
+    const int place = __float_as_int(own.z);
+    if (place >= 0) {
+        load_first<D>(p, kvh, i, part, x);
+        join_piece(j, stat.x, stat.y, x);
+        join_pieces<D>(p, j, __float_as_int(stat.z) + 1, __float_as_int(stat.w), place + g, part);
     }
-    write_row<PER>(p, row, m, l, o);
+    write_joined<D>(p, j, row, part);
 }
 
 RowsParams params_of(const RowsArgs &a)
@@ -1051,13 +1055,15 @@ cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream
     const RowsParams p = params_of(a);
     cudaLaunchAttribute pdl[1];
     if (a.ctx_lens) {
-        const int64_t grid = ((int64_t)a.n_rows * a.n_q_heads + 7) / 8;
-        const cudaLaunchConfig_t lc = dependent(pdl, (unsigned)grid, 256, 0, stream);
+        const int64_t grid = ((int64_t)a.n_rows * p.group + kTM - 1) / kTM;
+        cudaLaunchConfig_t lc = dependent(pdl, (unsigned)grid, kTM, 0, stream);
+        lc.gridDim.y = (unsigned)a.dims.n_kv_heads;
+        lc.gridDim.z = (unsigned)a.dims.head_dim / kCols;
         return a.dims.head_dim == 128 ? cudaLaunchKernelEx(&lc, shared_join_kernel<128>, p)
                                       : cudaLaunchKernelEx(&lc, shared_join_kernel<64>, p);
     }
-    cudaLaunchConfig_t lc = dependent(pdl, most_shares(a, num_sms), 256, 0, stream);
-    lc.gridDim.y = kUnitRows / 8 + 1;
+    cudaLaunchConfig_t lc = dependent(pdl, most_shares(a, num_sms), kTM, 0, stream);
+    lc.gridDim.y = kNQ * (unsigned)a.dims.head_dim / kCols + 1;
     return a.dims.head_dim == 128 ? cudaLaunchKernelEx(&lc, rows_join_kernel<128>, p) : cudaLaunchKernelEx(&lc, rows_join_kernel<64>, p);
 }
 

@@ -99,7 +99,7 @@ def test_shared_refusals(P):
 def test_workspace_sizes(P):
     f = P.load_library().pkv_rows_workspace_bytes
     assert f(-1, 8, 64) == 0 and f(4, 0, 64) == 0 and f(4, 8, 96) == 0
-    assert f(100, 8, 64) - f(0, 8, 64) == 100 * 8 * (2 * 64 + 6) * 4
+    assert f(100, 8, 64) - f(0, 8, 64) == 100 * 8 * (2 * 64 + 8) * 4
     with pytest.raises(ValueError):
         P.rows_workspace_bytes(1, 8, 100)
 
