@@ -4,9 +4,9 @@ sm_103a CUDA kernels behind the C ABI of ``libpagedkv.so`` (``include/pagedkv.h`
 
 This module is argument marshalling only: it checks tensor shapes, dtypes and
 devices, passes raw device pointers and the current CUDA stream to the
-library, and turns a non-zero status into an exception.  (The rotary and
-windowed calls are marshalled in native code, binding/native.cpp, as long as
-they pass its checks; the ones here then say what is wrong.)  Every step of the
+library, and turns a non-zero status into an exception.  (The rotary, windowed
+and ragged-batch calls are marshalled in native code, binding/native.cpp, as
+long as they pass its checks; the ones here then say what is wrong.)  Every step of the
 computation runs in the library's kernels; there is no CPU or PyTorch
 fallback, and using any call without the built library raises.
 """
@@ -96,6 +96,9 @@ def _load_native(lib):
     mod.set_functions(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
         "paged_kv_write_rope", "paged_decode_attention_window", "paged_decode_step_window",
         "paged_prefill_attention_window")))
+    mod.set_batch_functions(*(ctypes.cast(getattr(lib, fn), ctypes.c_void_p).value for fn in (
+        "paged_step_maps", "paged_kv_write_slots", "pkv_rows_workspace_bytes", "paged_cross_attention",
+        "paged_decode_attention_shared")))
     return mod
 
 
@@ -1010,6 +1013,13 @@ def paged_step_maps(lens, n_new, free_blocks, block_tables, block_size, n_blocks
     packed batch, at least sum(n_new).  ``out`` (a StepMaps) is written into;
     lens and ctx_lens, cursor and out.cursor have to be different tensors.
     Returns the StepMaps."""
+    if stream is None and _native is not None and type(out) is StepMaps:
+        st = _native.step_maps(lens, n_new, free_blocks, block_tables, block_size, n_blocks, n_tokens, cursor, out,
+                               dev_status)
+        if st is not None:
+            if st:
+                _check("paged_step_maps", st)
+            return out
     dev = _device_of(block_tables, "block_tables")
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -1052,6 +1062,12 @@ def paged_kv_write_slots(k_new, v_new, k_pool, v_pool, slots, k_scales=None, v_s
     bf16 (they may be parts of a fused projection's rows) goes to pool row
     slots[i] (int64; negative: nowhere), as it is or, into int8 pools, quantised
     with k_scales / v_scales."""
+    if stream is None and _native is not None:
+        st = _native.write_slots(k_new, v_new, k_pool, v_pool, slots, k_scales, v_scales, dev_status)
+        if st is not None:
+            if st:
+                _check("paged_kv_write_slots", st)
+            return
     dev = _device_of(k_pool, "k_pool")
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -1105,6 +1121,13 @@ def paged_cross_attention(q, q_starts, k_pool, v_pool, block_tables, key_lens, s
     pages, bf16 or int8 with k_scales / v_scales.  Rows of no sequence are left
     as they were.  ``workspace`` (uint8, rows_workspace_bytes) is allocated when
     not given.  Returns out [n_rows, Hq, D] bf16."""
+    if stream is None and _native is not None:
+        done = _native.cross(q, q_starts, k_pool, v_pool, block_tables, key_lens, softmax_scale, k_scales, v_scales, out,
+                             lse_out, workspace, dev_status)
+        if done is not None:
+            if type(done) is int:
+                _check("paged_cross_attention", done)
+            return done
     dev = _device_of(q, "q")
     if _elsewhere(dev):
         with torch.cuda.device(dev):
@@ -1173,9 +1196,21 @@ class SharedDecodePlan:
                       _ptr(group_starts), n_groups, _ptr(prefix_tables), prefix_tables.shape[1], _ptr(prefix_lens),
                       float(softmax_scale), _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.numel(),
                       _ptr(dev_status))
+        self._plan = None
+        if _native is not None:
+            kp, vp, ks, vs, kind, dims, tab, width, ctx, n, gs, ng, pt, pw, pl, scale, o, lse, ws, wsb, st = self._args
+            self._plan = _native.make_shared_plan(dev, self.n_q_heads, kp, vp, ks or 0, vs or 0, kind, dims.n_blocks,
+                                                  dims.block_size, dims.n_kv_heads, dims.head_dim, tab, width, ctx, n, gs,
+                                                  ng, pt, pw, pl, scale, o, lse or 0, ws, wsb, st or 0)
 
     def run(self, q, stream=None):
         """q [n_seqs, Hq, D] bf16 (its tokens may be a stride apart).  Returns the plan's out."""
+        if stream is None and self._plan is not None:
+            st = _native.run_shared_plan(self._plan, q)
+            if st is not None:
+                if st:
+                    _check("paged_decode_attention_shared", st)
+                return self.out
         dev = self.device
         if _elsewhere(dev):
             with torch.cuda.device(dev):

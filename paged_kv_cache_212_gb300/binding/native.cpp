@@ -1,5 +1,5 @@
-// native.cpp -- the rotary and windowed calls' argument marshalling in native
-// code (CPython extension over torch's C++ API).  A call of the Python binding
+// native.cpp -- argument marshalling of the rotary, windowed and ragged-batch calls
+// in native code (CPython extension over torch's C++ API).  A call of the Python binding
 // costs 15 to 20 us of host time, most of it tensor attribute look-ups and
 // ctypes conversions, which is more than the small calls' kernels take; here it
 // costs 2 to 3 us, the launch among them.
@@ -19,6 +19,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/pagedkv.h"
+#include "../../include/pagedkv_batch.h"
 #include "../../include/pagedkv_rope.h"
 #include "../../include/pagedkv_window.h"
 
@@ -28,6 +29,11 @@ decltype(&paged_kv_write_rope) g_write_rope;
 decltype(&paged_decode_attention_window) g_decode_window;
 decltype(&paged_decode_step_window) g_step_window;
 decltype(&paged_prefill_attention_window) g_prefill_window;
+decltype(&paged_step_maps) g_step_maps;
+decltype(&paged_kv_write_slots) g_write_slots;
+decltype(&pkv_rows_workspace_bytes) g_rows_workspace_bytes;
+decltype(&paged_cross_attention) g_cross;
+decltype(&paged_decode_attention_shared) g_shared;
 
 // Lets other Python threads run while it lives: a launch waits where the stream's queue
 // is full.  (The caller holds the arguments meanwhile.)
@@ -77,7 +83,7 @@ struct Pools {
     int32_t kv_dtype;
 };
 
-// The pools (with scales when they are int8) and tables of a call.
+// The pools (with scales when they are int8) and, where a call has them, tables.
 bool pools(Pools *p, PyObject *k, PyObject *v, PyObject *ks, PyObject *vs, PyObject *tables, int dev)
 {
     const at::Tensor *kt = tensor(k);
@@ -86,8 +92,8 @@ bool pools(Pools *p, PyObject *k, PyObject *v, PyObject *ks, PyObject *vs, PyObj
     const at::ScalarType type = int8 ? at::kChar : at::kBFloat16;
     p->k = need(k, type, 4, dev);
     p->v = need(v, type, 4, dev);
-    p->tables = need(tables, at::kInt, 2, dev);
-    if (!p->k || !p->v || !p->tables || p->v->sizes() != p->k->sizes()) return false;
+    p->tables = tables ? need(tables, at::kInt, 2, dev) : nullptr;
+    if (!p->k || !p->v || (tables && !p->tables) || p->v->sizes() != p->k->sizes()) return false;
     p->ks = p->vs = nullptr;
     const auto size = p->k->sizes();
     if (int8) {
@@ -339,6 +345,226 @@ PyObject *run_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
     }
 }
 
+// An int32 (or int64) vector of n elements on device dev, or null.
+const at::Tensor *vector(PyObject *o, int64_t n, int dev, at::ScalarType type = at::kInt)
+{
+    const at::Tensor *t = need(o, type, 1, dev);
+    return t && t->size(0) == n ? t : nullptr;
+}
+
+pkv_stream_t current_stream(int dev) { return reinterpret_cast<pkv_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream()); }
+
+// A non-negative Python int below 2^31, or -1.
+int32_t count_arg(PyObject *o)
+{
+    if (!PyLong_CheckExact(o)) return -1;
+    const long x = PyLong_AsLong(o);
+    if (x == -1 && PyErr_Occurred()) PyErr_Clear();
+    return small(x) ? (int32_t)x : -1;
+}
+
+// step_maps(lens, n_new, free_blocks, block_tables, block_size, n_blocks, n_tokens, cursor,
+//           out (six tensors), dev_status) -> a status, or None
+PyObject *step_maps(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 10 || !PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 6) return none();
+    try {
+        const at::Tensor *t = tensor(a[3]);
+        if (!t || !t->is_cuda()) return none();
+        const int dev = t->get_device();
+        const at::Tensor *tables = need(a[3], at::kInt, 2, dev), *free = need(a[2], at::kInt, 1, dev);
+        const int32_t bs = count_arg(a[4]), n_blocks = count_arg(a[5]), n_tokens = count_arg(a[6]);
+        if (!tables || !free || dev != c10::cuda::current_device() || bs < 0 || n_blocks < 0 || n_tokens < 0 ||
+            !small(tables->size(0)) || !small(tables->size(1)) || !small(free->size(0)))
+            return none();
+        const int64_t n_seqs = tables->size(0);
+        const at::Tensor *lens = vector(a[0], n_seqs, dev), *n_new = vector(a[1], n_seqs, dev), *cursor = nullptr;
+        if (!lens || !n_new || (a[7] != Py_None && !(cursor = vector(a[7], 1, dev)))) return none();
+        const int64_t sizes[6] = {n_seqs, n_seqs + 1, n_tokens, n_tokens, n_tokens, 1};
+        const at::Tensor *out[6];
+        for (int i = 0; i < 6; ++i)
+            if (!(out[i] = vector(PyTuple_GET_ITEM(a[8], i), sizes[i], dev, i == 4 ? at::kLong : at::kInt))) return none();
+        int32_t *status;
+        if (!status_arg(a[9], dev, &status)) return none();
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_step_maps(ptr<const int32_t>(lens), ptr<const int32_t>(n_new), (int32_t)n_seqs, ptr<const int32_t>(free),
+                             (int32_t)free->size(0), ptr<const int32_t>(cursor), n_blocks, bs, ptr<int32_t>(tables),
+                             (int32_t)tables->size(1), n_tokens, ptr<int32_t>(out[0]), ptr<int32_t>(out[1]), ptr<int32_t>(out[2]),
+                             ptr<int32_t>(out[3]), ptr<int64_t>(out[4]), ptr<int32_t>(out[5]), status, current_stream(dev));
+        }
+        return status_result(st);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// write_slots(k_new, v_new, k_pool, v_pool, slots, k_scales, v_scales, dev_status) -> a
+// status, or None
+PyObject *write_slots(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 8) return none();
+    try {
+        const at::Tensor *k = tensor(a[0]), *v = tensor(a[1]), *kp = tensor(a[2]);
+        if (!k || !v || !kp || !kp->is_cuda()) return none();
+        const int dev = kp->get_device();
+        Pools p;
+        if (dev != c10::cuda::current_device() || !pools(&p, a[2], a[3], a[5], a[6], nullptr, dev)) return none();
+        const int64_t ks = token_stride(*k, 3, dev), vs = token_stride(*v, 3, dev);
+        if (ks < 0 || vs < 0 || !small(k->size(0))) return none();
+        const int64_t rows = k->size(0), size[3] = {rows, p.dims.n_kv_heads, p.dims.head_dim};
+        const at::Tensor *slots = vector(a[4], rows, dev, at::kLong);
+        int32_t *status;
+        if (!slots || k->sizes() != at::IntArrayRef(size, 3) || v->sizes() != k->sizes() || !status_arg(a[7], dev, &status)) return none();
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_write_slots(ptr<const pkv_bf16>(k), ks, ptr<const pkv_bf16>(v), vs, p.k->data_ptr(), p.v->data_ptr(),
+                               ptr<float>(p.ks), ptr<float>(p.vs), p.kv_dtype, p.dims, ptr<const int64_t>(slots), (int32_t)rows,
+                               status, current_stream(dev));
+        }
+        return status_result(st);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// cross(q, q_starts, k_pool, v_pool, tables, key_lens, scale, k_scales, v_scales, out,
+//       lse_out, workspace, dev_status) -> out, a status, or None
+PyObject *cross(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 13 || !PyFloat_Check(a[6])) return none();
+    try {
+        const at::Tensor *q = tensor(a[0]);
+        if (!q || !q->is_cuda()) return none();
+        const int dev = q->get_device();
+        Pools p;
+        if (dev != c10::cuda::current_device() || !pools(&p, a[2], a[3], a[7], a[8], a[4], dev)) return none();
+        const int64_t qs = token_stride(*q, 3, dev), n_seqs = p.tables->size(0);
+        const at::Tensor *starts = vector(a[1], n_seqs + 1, dev), *lens = vector(a[5], n_seqs, dev);
+        int32_t *status;
+        if (qs < 0 || !starts || !lens || q->size(2) != p.dims.head_dim || !small(q->size(0)) || !small(q->size(1)) ||
+            !small(n_seqs) || !small(p.tables->size(1)) || !status_arg(a[12], dev, &status))
+            return none();
+        float *lse = nullptr;
+        if (a[10] != Py_None) {
+            const at::Tensor *l = need(a[10], at::kFloat, 2, dev);
+            if (!l || l->sizes() != q->sizes().slice(0, 2)) return none();
+            lse = l->data_ptr<float>();
+        }
+        at::Tensor out, ws;
+        if (a[9] == Py_None) {
+            out = new_like(*q);
+        } else {
+            const at::Tensor *o = need(a[9], at::kBFloat16, 3, dev);
+            if (!o || o->sizes() != q->sizes()) return none();
+            out = *o;
+        }
+        if (a[11] == Py_None) {
+            const size_t bytes = g_rows_workspace_bytes((int32_t)q->size(0), (int32_t)q->size(1), p.dims.head_dim);
+            if (bytes == 0) return none();
+            const int64_t size[1] = {(int64_t)bytes};
+            ws = at::Tensor(at::detail::empty_cuda(at::IntArrayRef(size, 1), at::kByte, q->device(), std::nullopt));
+        } else {
+            const at::Tensor *w = need(a[11], at::kByte, 1, dev);
+            if (!w) return none();
+            ws = *w;
+        }
+        const float scale = (float)PyFloat_AS_DOUBLE(a[6]);
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_cross(ptr<const pkv_bf16>(q), qs, (int32_t)q->size(1), ptr<const int32_t>(starts), (int32_t)q->size(0),
+                         p.k->data_ptr(), p.v->data_ptr(), ptr<const float>(p.ks), ptr<const float>(p.vs), p.kv_dtype, p.dims,
+                         ptr<const int32_t>(p.tables), (int32_t)p.tables->size(1), ptr<const int32_t>(lens), (int32_t)n_seqs, scale,
+                         ptr<pkv_bf16>(&out), lse, ws.data_ptr(), (size_t)ws.numel(), status, current_stream(dev));
+        }
+        if (st != 0) return status_result(st);
+        if (a[9] != Py_None) {
+            Py_INCREF(a[9]);
+            return a[9];
+        }
+        return THPVariable_Wrap(std::move(out));
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
+// The arguments of a shared decode plan that stay the same, as Plan.
+struct SharedPlan {
+    int dev;
+    int32_t n_q_heads, n_seqs, max_blocks, kv_dtype, n_groups, max_prefix_blocks;
+    pkv_dims dims;
+    float scale;
+    void *k_pool, *v_pool, *workspace;
+    float *k_scales, *v_scales, *lse_out;
+    const int32_t *tables, *ctx_lens, *group_starts, *prefix_tables, *prefix_lens;
+    pkv_bf16 *out;
+    unsigned long long workspace_bytes;
+    int32_t *dev_status;
+};
+
+void free_shared_plan(PyObject *capsule) { delete static_cast<SharedPlan *>(PyCapsule_GetPointer(capsule, "pkv_shared_plan")); }
+
+// make_shared_plan(device, n_q_heads, k_pool, v_pool, k_scales, v_scales, kv_dtype, n_blocks,
+//                  block_size, n_kv_heads, head_dim, tables, max_blocks, ctx_lens, n_seqs,
+//                  group_starts, n_groups, prefix_tables, max_prefix_blocks, prefix_lens,
+//                  scale, out, lse_out, workspace, workspace_bytes, dev_status): as make_plan
+PyObject *make_shared_plan(PyObject *, PyObject *args)
+{
+    unsigned long long k, v, ks, vs, tables, ctx, starts, ptables, plens, out, lse, ws, status;
+    SharedPlan p{};
+    if (!PyArg_ParseTuple(args, "iiKKKKiiiiiKiKiKiKiKfKKKKK", &p.dev, &p.n_q_heads, &k, &v, &ks, &vs, &p.kv_dtype, &p.dims.n_blocks,
+                          &p.dims.block_size, &p.dims.n_kv_heads, &p.dims.head_dim, &tables, &p.max_blocks, &ctx, &p.n_seqs,
+                          &starts, &p.n_groups, &ptables, &p.max_prefix_blocks, &plens, &p.scale, &out, &lse, &ws,
+                          &p.workspace_bytes, &status))
+        return nullptr;
+    p.k_pool = reinterpret_cast<void *>(k);
+    p.v_pool = reinterpret_cast<void *>(v);
+    p.k_scales = reinterpret_cast<float *>(ks);
+    p.v_scales = reinterpret_cast<float *>(vs);
+    p.tables = reinterpret_cast<const int32_t *>(tables);
+    p.ctx_lens = reinterpret_cast<const int32_t *>(ctx);
+    p.group_starts = reinterpret_cast<const int32_t *>(starts);
+    p.prefix_tables = reinterpret_cast<const int32_t *>(ptables);
+    p.prefix_lens = reinterpret_cast<const int32_t *>(plens);
+    p.out = reinterpret_cast<pkv_bf16 *>(out);
+    p.lse_out = reinterpret_cast<float *>(lse);
+    p.workspace = reinterpret_cast<void *>(ws);
+    p.dev_status = reinterpret_cast<int32_t *>(status);
+    return PyCapsule_New(new SharedPlan(p), "pkv_shared_plan", free_shared_plan);
+}
+
+// run_shared_plan(plan, q) -> a status, or None
+PyObject *run_shared_plan(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    if (n != 2) return none();
+    try {
+        const SharedPlan *p = static_cast<const SharedPlan *>(PyCapsule_GetPointer(a[0], "pkv_shared_plan"));
+        if (!p) return nullptr;
+        const at::Tensor *q = tensor(a[1]);
+        if (!q || !q->is_cuda() || p->dev != c10::cuda::current_device()) return none();
+        const int64_t size[3] = {p->n_seqs, p->n_q_heads, p->dims.head_dim}, qs = token_stride(*q, 3, p->dev);
+        if (qs < 0 || q->sizes() != at::IntArrayRef(size, 3)) return none();
+        int st;
+        {
+            const Unlocked other_threads_run;
+            st = g_shared(ptr<const pkv_bf16>(q), qs, p->n_q_heads, p->k_pool, p->v_pool, p->k_scales, p->v_scales, p->kv_dtype,
+                          p->dims, p->tables, p->max_blocks, p->ctx_lens, p->n_seqs, p->group_starts, p->n_groups,
+                          p->prefix_tables, p->max_prefix_blocks, p->prefix_lens, p->scale, p->out, p->lse_out, p->workspace,
+                          (size_t)p->workspace_bytes, p->dev_status, current_stream(p->dev));
+        }
+        return status_result(st);
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+        return nullptr;
+    }
+}
+
 // set_functions(write_rope, decode_window, step_window, prefill_window): the
 // library's entry points
 PyObject *set_functions(PyObject *, PyObject *args)
@@ -352,8 +578,28 @@ PyObject *set_functions(PyObject *, PyObject *args)
     Py_RETURN_NONE;
 }
 
+// set_batch_functions(step_maps, write_slots, rows_workspace_bytes, cross, shared): the
+// same for those of ragged batches
+PyObject *set_batch_functions(PyObject *, PyObject *args)
+{
+    unsigned long long f[5];
+    if (!PyArg_ParseTuple(args, "KKKKK", f, f + 1, f + 2, f + 3, f + 4)) return nullptr;
+    g_step_maps = reinterpret_cast<decltype(g_step_maps)>(f[0]);
+    g_write_slots = reinterpret_cast<decltype(g_write_slots)>(f[1]);
+    g_rows_workspace_bytes = reinterpret_cast<decltype(g_rows_workspace_bytes)>(f[2]);
+    g_cross = reinterpret_cast<decltype(g_cross)>(f[3]);
+    g_shared = reinterpret_cast<decltype(g_shared)>(f[4]);
+    Py_RETURN_NONE;
+}
+
 PyMethodDef methods[] = {
     {"set_functions", set_functions, METH_VARARGS, nullptr},
+    {"set_batch_functions", set_batch_functions, METH_VARARGS, nullptr},
+    {"make_shared_plan", make_shared_plan, METH_VARARGS, nullptr},
+    {"run_shared_plan", (PyCFunction)(void (*)(void))run_shared_plan, METH_FASTCALL, nullptr},
+    {"step_maps", (PyCFunction)(void (*)(void))step_maps, METH_FASTCALL, nullptr},
+    {"write_slots", (PyCFunction)(void (*)(void))write_slots, METH_FASTCALL, nullptr},
+    {"cross", (PyCFunction)(void (*)(void))cross, METH_FASTCALL, nullptr},
     {"make_plan", make_plan, METH_VARARGS, nullptr},
     {"run_plan", (PyCFunction)(void (*)(void))run_plan, METH_FASTCALL, nullptr},
     {"write_rope", (PyCFunction)(void (*)(void))write_rope, METH_FASTCALL, nullptr},

@@ -15,7 +15,6 @@
 // stand in device memory.  A unit that is cut leaves partials in 32 bits (rows.h), at most
 // one more per CTA.
 #include <math.h>
-#include <stdlib.h>
 
 #include "common.cuh"
 #include "rows.h"
@@ -925,6 +924,13 @@ __global__ void __launch_bounds__(kTM) shared_join_kernel(const __grid_constant_
     write_joined<D>(p, j, row, part);
 }
 
+// What 128 of a decode's own tokens cost an SM, in tiles of a run: the share of the SMs that
+// the runs' tiles get.  Measured (weights 0.3 / 0.5 / 0.7 / 0.9): bf16 pages, 64 sequences of
+// 16 to 512 own tokens behind 4096 41.6 / 36.5 / 33.6 / 34 us, 256 of up to 700 in 6 groups,
+// eight query heads per kv head 164 / 165 / 173 / 181; int8 pages (whose runs' tiles take
+// longer), 96 in two groups 65 / 61 / 67 / 70.
+constexpr float kRestWeight = 0.6f, kRestWeightInt8 = 0.5f;
+
 RowsParams params_of(const RowsArgs &a)
 {
     const pkv_dims &d = a.dims;
@@ -950,7 +956,7 @@ RowsParams params_of(const RowsArgs &a)
     p.v_scales = a.v_scales;
     p.dev_status = a.dev_status;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-    p.rest_weight = getenv("PKV_W") ? atof(getenv("PKV_W")) : 0.7f;
+    p.rest_weight = a.kv_dtype == PKV_KV_INT8 ? kRestWeightInt8 : kRestWeight;
     p.wait_ns = pipeline_wait_ns();
     return p;
 }
