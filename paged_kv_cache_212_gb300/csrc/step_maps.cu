@@ -4,7 +4,8 @@
 // With need(s) = ceil((lens + n_new) / bs) - ceil(lens / bs), everything follows from two
 // exclusive sums over the sequences: of n_new (the packed batch's starts) and of need
 // (places in the free list).  One launch: every CTA sums all sequences by itself, 2048 at
-// a time, and then fills its own part, 512 tokens and some of the table rows.  A second
+// a time (in 32 bits, at 2^31 - 1 at most), and then fills its own part, 512 tokens and some of
+// the table rows.  A second
 // launch, or a wait between CTAs, would cost more than sums that all CTAs repeat from L2.
 // A token's block comes from the free list or, in the block that its sequence holds
 // already, from a table entry that the call does not write, so no CTA waits for another.
@@ -35,7 +36,10 @@ struct MapArgs {
     int32_t *dev_status;
 };
 
-__device__ __forceinline__ int32_t clip32(int64_t x) { return (int32_t)(x > 0x7fffffffLL ? 0x7fffffffLL : x); }
+constexpr uint32_t kMost = 0x7fffffffu;
+
+// The sum of two numbers up to 2^31 - 1, or that.
+__device__ __forceinline__ uint32_t add_clipped(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 
 // What sequence s holds and adds (0 and 0, and false, where its length is bad).
 __device__ __forceinline__ bool sequence(const MapArgs &a, int32_t s, int32_t &len, int32_t &add)
@@ -71,8 +75,8 @@ __device__ __forceinline__ int32_t free_block(const MapArgs &a, int64_t at, int3
 
 __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
 {
-    __shared__ int64_t tok_s[kRound], blk_s[kRound];     // exclusive sums within the batch
-    __shared__ int64_t warp_tok[kThreads / 32], warp_blk[kThreads / 32];
+    __shared__ uint32_t tok_s[kRound], blk_s[kRound];    // exclusive sums within the batch
+    __shared__ uint32_t warp_tok[kThreads / 32], warp_blk[kThreads / 32];
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,13 +84,17 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
     const int64_t token = (int64_t)blockIdx.x * kThreads + tid;
     const int64_t cursor = a.cursor ? (int64_t)__ldg(a.cursor) : 0;
     const int64_t first_free = cursor < 0 ? (int64_t)a.n_free : cursor;   // a negative one: nothing is left
-    const int32_t n_warps = (int32_t)(gridDim.x * (kThreads / 32)), my_warp = (int32_t)(blockIdx.x * (kThreads / 32)) + warp;
-    int64_t tok0 = 0, blk0 = 0;                          // sums of the rounds before
+    // a table row is the work of `team` warps, or a warp's are several rows
+    const int64_t n_warps = (int64_t)gridDim.x * (kThreads / 32), my_warp = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+    const int32_t team = (int32_t)max((int64_t)1, min(n_warps / max(a.n_seqs, 1), (int64_t)1024));
+    const int64_t n_teams = n_warps / team, my_team = my_warp / team;
+    const int32_t member = (int32_t)(my_warp - my_team * team);
+    uint32_t tok0 = 0, blk0 = 0;                         // sums of the rounds before
     bool mapped = false;
     for (int64_t s0 = 0; s0 < a.n_seqs; s0 += kRound) {
         // 1. the round's sums
         int32_t add[kPer], need[kPer];
-        int64_t tok = 0, blk = 0;
+        uint32_t tok = 0, blk = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int64_t s = s0 + tid * kPer + i;
@@ -96,50 +104,57 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
                 if (!sequence(a, (int32_t)s, len, add[i]) && blockIdx.x == 0) report(a.dev_status, PKV_DEV_BAD_LENGTH);
                 need[i] = blocks_of(len + add[i], bs) - blocks_of(len, bs);
             }
-            tok += add[i];
-            blk += need[i];
+            tok = add_clipped(tok, add[i]);
+            blk = add_clipped(blk, need[i]);
         }
-        int64_t tok_in = tok, blk_in = blk;              // inclusive over the warp's lanes
+        uint32_t tok_in = tok, blk_in = blk;             // inclusive over the warp's lanes
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t t = __shfl_up_sync(0xffffffffu, tok_in, off), b = __shfl_up_sync(0xffffffffu, blk_in, off);
+            const uint32_t t = __shfl_up_sync(0xffffffffu, tok_in, off), b = __shfl_up_sync(0xffffffffu, blk_in, off);
             if (lane >= off) {
-                tok_in += t;
-                blk_in += b;
+                tok_in = add_clipped(tok_in, t);
+                blk_in = add_clipped(blk_in, b);
             }
         }
+        uint32_t tok_at = __shfl_up_sync(0xffffffffu, tok_in, 1), blk_at = __shfl_up_sync(0xffffffffu, blk_in, 1);
+        if (lane == 0) tok_at = blk_at = 0;
         if (lane == 31) {
             warp_tok[warp] = tok_in;
             warp_blk[warp] = blk_in;
         }
         __syncthreads();
-        int64_t tok_at = tok0 + tok_in - tok, blk_at = blk0 + blk_in - blk;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) {
-                tok_at += warp_tok[w];
-                blk_at += warp_blk[w];
-            }
-            tok0 += warp_tok[w];
-            blk0 += warp_blk[w];
+        // (lane w has warp w's sums; those of the warps before this one, and of all)
+        uint32_t t = lane < kThreads / 32 ? warp_tok[lane] : 0u, b = lane < kThreads / 32 ? warp_blk[lane] : 0u;
+        uint32_t t_before = lane < warp ? t : 0u, b_before = lane < warp ? b : 0u;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            t = add_clipped(t, __shfl_xor_sync(0xffffffffu, t, off));
+            b = add_clipped(b, __shfl_xor_sync(0xffffffffu, b, off));
+            t_before = add_clipped(t_before, __shfl_xor_sync(0xffffffffu, t_before, off));
+            b_before = add_clipped(b_before, __shfl_xor_sync(0xffffffffu, b_before, off));
         }
+        tok_at = add_clipped(tok_at, add_clipped(tok0, t_before));
+        blk_at = add_clipped(blk_at, add_clipped(blk0, b_before));
+        tok0 = add_clipped(tok0, t);
+        blk0 = add_clipped(blk0, b);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             tok_s[tid * kPer + i] = tok_at;
             blk_s[tid * kPer + i] = blk_at;
-            tok_at += add[i];
-            blk_at += need[i];
+            tok_at = add_clipped(tok_at, add[i]);
+            blk_at = add_clipped(blk_at, need[i]);
         }
         __syncthreads();
 
         // 2. this thread's token, where it is one of the round's: the last sequence that
         //    starts at or before it
         const int32_t n_here = (int32_t)min((int64_t)kRound, a.n_seqs - s0);
-        if (!mapped && token < a.n_tokens && token < tok0) {
+        if (!mapped && token < a.n_tokens && token < (int64_t)tok0) {
             mapped = true;
             int32_t lo = 0, hi = n_here;                 // tok_s[lo] <= token < tok_s[hi]
             while (hi - lo > 1) {
                 const int32_t mid = (lo + hi) >> 1;
-                if (tok_s[mid] <= token)
+                if ((int64_t)tok_s[mid] <= token)
                     lo = mid;
                 else
                     hi = mid;
@@ -157,29 +172,30 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
                     b = -1;
                 }
             } else {
-                b = free_block(a, first_free + blk_s[lo] + (at - held), nullptr);   // reported with the table entry
+                b = free_block(a, first_free + (int64_t)blk_s[lo] + (at - held), nullptr);   // reported with the table entry
             }
             a.token_seqs[token] = s;
             a.positions[token] = pos;
             a.slots[token] = b < 0 ? -1 : (int64_t)b * bs + (pos - at * bs);
         }
 
-        // 3. the table rows, one to a warp
-        for (int32_t i = (my_warp - (int32_t)(s0 % n_warps) + n_warps) % n_warps; i < n_here; i += n_warps) {
-            const int32_t s = (int32_t)s0 + i;
+        // 3. the table rows, team t's t, t + n_teams, ...
+        for (int64_t s_at = my_team < s0 ? my_team + (s0 - my_team + n_teams - 1) / n_teams * n_teams : my_team;
+             my_team < n_teams && s_at < s0 + n_here; s_at += n_teams) {
+            const int32_t s = (int32_t)s_at, i = (int32_t)(s_at - s0);
             int32_t len, n;
             const bool good = sequence(a, s, len, n);
-            if (lane == 0) {
+            if (lane == 0 && member == 0) {
                 a.ctx_lens[s] = len + n;
-                a.token_starts[s] = clip32(tok_s[i]);
+                a.token_starts[s] = (int32_t)tok_s[i];
             }
             if (!good) continue;
             const int32_t held = blocks_of(len, bs), want = blocks_of(len + n, bs);
             int32_t *row = a.tables + (int64_t)s * a.max_blocks;
             const int32_t stop = len == 0 ? a.max_blocks : want;
-            for (int32_t j = held + lane; j < stop; j += 32) {
+            for (int64_t j = held + member * 32 + lane; j < stop; j += 32 * team) {
                 int32_t b = -1;
-                if (j < want) b = free_block(a, first_free + blk_s[i] + (j - held), a.dev_status);
+                if (j < want) b = free_block(a, first_free + (int64_t)blk_s[i] + (j - held), a.dev_status);
                 row[j] = b < 0 ? a.n_blocks : b;
             }
         }
@@ -191,9 +207,9 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
         a.slots[token] = -1;
     }
     if (blockIdx.x == 0 && tid == 0) {
-        a.token_starts[a.n_seqs] = clip32(tok0);
-        *a.cursor_out = clip32(cursor + blk0);
-        if (tok0 > a.n_tokens) report(a.dev_status, PKV_DEV_BAD_POSITION);
+        a.token_starts[a.n_seqs] = (int32_t)tok0;
+        *a.cursor_out = (int32_t)min(cursor + (int64_t)blk0, (int64_t)kMost);
+        if ((int64_t)tok0 > a.n_tokens) report(a.dev_status, PKV_DEV_BAD_POSITION);
     }
 }
 
