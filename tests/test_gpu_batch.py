@@ -166,6 +166,33 @@ def test_write_slots(P, n, hkv, d, bs, strided, int8):
     assert int(st.item()) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_write_slots_int8_codes(P, d):
+    """Codes and scales bit for bit as paged_kv_write_int8 stores them, over rows of any size: halves
+    and other simple fractions of the largest element (ties), subnormal scales, infinities, NaN."""
+    gen = torch.Generator().manual_seed(d)
+    hkv, bs, n = 4, 16, 4096
+    x = torch.randn((2, n, hkv, d), generator=gen)
+    top = x.abs().amax(-1, keepdim=True)
+    share = torch.randint(-254, 255, x.shape, generator=gen) / 254.0           # multiples of half a step
+    x = torch.where(torch.rand(x.shape, generator=gen) < 0.3, top * share, x)
+    x = x * 2.0 ** torch.randint(-140, 120, (2, n, hkv, 1), generator=gen)
+    odd = torch.rand((2, n, hkv, 1), generator=gen)
+    at = torch.randint(0, d, (2, n, hkv, 1), generator=gen)
+    for low, value in ((0.02, float("nan")), (0.04, float("inf")), (0.06, -float("inf")), (0.08, 0.0)):
+        x = torch.where((odd < low) & (odd >= low - 0.02), x.scatter(-1, at, value) if value else torch.zeros_like(x), x)
+    k, v = x.to(torch.bfloat16).cuda()
+    pools = [[torch.zeros((n // bs + 1, bs, hkv, d), dtype=torch.int8, device="cuda") for _ in range(2)] for _ in range(2)]
+    scales = [[torch.zeros((n // bs + 1, bs, hkv), device="cuda") for _ in range(2)] for _ in range(2)]
+    P.paged_kv_write_slots(k, v, *pools[0], torch.arange(n, device="cuda"), *scales[0])
+    P.paged_kv_write_int8(k.unsqueeze(0), v.unsqueeze(0), *pools[1], *scales[1], torch.arange(n // bs, dtype=torch.int32, device="cuda").view(1, -1),
+                          _ints([0]))
+    for a, b in zip(pools[0], pools[1]):
+        assert torch.equal(a, b)
+    for a, b in zip(scales[0], scales[1]):
+        assert torch.equal(a.view(torch.int32), b.view(torch.int32))
+
+
 @pytest.mark.parametrize("int8", [False, True])
 def test_write_slots_outside_the_pool(P, int8):
     n_blocks, bs, hkv, d = 3, 16, 2, 64
