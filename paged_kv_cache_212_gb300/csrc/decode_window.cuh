@@ -963,6 +963,9 @@ cudaError_t launch_as(WindowArgs &a, const Choice &c, int64_t units, int sms, cu
 // above / 4 warps / 8; rows of 512 to 4096 tokens): bf16 pages, 32 rows 64.2 / 64.3 / 57.0 us,
 // 64: 121 / 116 / 106, 150: 255 / 236 / 228; int8 pages, 64: 91.3 / 91.8 / 82.9; but rows of
 // 512 to 1024, 64: 39.1 / 37.6 / 39.6.
+//
+// Of 4 for own tokens behind runs (kRest), which are few to a unit: 64 sequences of 16 to 512
+// 35.0 / 32.9 us (CTAs of 2 / 4), 256 of up to 700 172.5 / 168.7, 64 of 1000 to 2000 80.6 / 78.7.
 template <int D, bool INT8, bool WIDE, int RUNS = kNoRuns>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
@@ -974,6 +977,7 @@ cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, c
     e = choose<D, INT8, WIDE, RUNS, 8>(units, tiles, sms, &c8);
     if (e != cudaSuccess) return e;
     if (RUNS == kWhole && tiles > 64) return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
+    if (RUNS == kRest) return launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
     const bool alone = c8.splits == 1 && c4.splits > 1 && c8.share <= c4.share;
     if (units <= c8.places && (alone || c8.share < c4.share || (units * c4.splits > sms && c8.room <= c4.room)))
         return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);

@@ -1,6 +1,8 @@
 // rows.cu -- the calls over packed query rows (pagedkv_batch.h): host checks, and the
 // launches of rows_tc.cu and decode_shared.cu one behind the other.
 #include <math.h>
+#include <stdlib.h>
+#include <string.h>
 
 #include "rows.h"
 #include "../../include/pagedkv_batch.h"
@@ -21,6 +23,8 @@ constexpr int64_t kOneByOneBytes = 192 << 20;       // as bf16
 bool one_by_one(const RowsArgs &a)
 {
     if (a.n_q_heads / a.dims.n_kv_heads > 8) return false;
+    const char *impl = getenv("PKV_ROWS_IMPL");
+    if (impl && (strcmp(impl, "one") == 0 || strcmp(impl, "all") == 0)) return impl[0] == 'o';
     if (!a.ctx_lens && a.n_rows <= a.n_runs) return true;
     const int64_t tokens = (int64_t)(a.ctx_lens ? a.max_blocks : a.max_run_blocks) * a.dims.block_size;
     return tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows;

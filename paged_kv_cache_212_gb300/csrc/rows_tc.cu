@@ -16,6 +16,8 @@
 // one more per CTA.
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "rows.h"
 #include "softmax_tc.cuh"
@@ -31,6 +33,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTileCols = 256;        // TMEM columns per query tile: S / P, O
 constexpr uint32_t kOCol = 128;            // O's column within a query tile's range
 constexpr int kBars = 48;          // barriers' room
+constexpr int kDevices = 16;       // whose occupancies are remembered
 constexpr int kScaleTiles = 4;     // int8: tiles whose scales are held
 static_assert(kNQ * kTM == kUnitRows, "a unit's rows");
 
@@ -183,6 +186,14 @@ __device__ __forceinline__ uint2 widened4(uint32_t x, float scale)
     return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
 }
 
+// A box of a tensor map to the L2.
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
+}
+
 // A scale to shared memory, 0 where it is not there; and the barrier's arrival of this
 // thread once its copies have landed.
 __device__ __forceinline__ void copy_scale(float *dst, const float *src, bool there)
@@ -298,6 +309,9 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     grid_dependency_wait();
     grid_dependents_launch();
 
+    Walker walk;                       // (the producers')
+    walk.g0 = 0;
+    if (warp >= 8 && warp < 12) walk.load(p, 0);
     // The share, from the runs' places and a decode's own tokens: each thread sums some runs,
     // the block sums the threads.
     Share share{0, 0};
@@ -337,6 +351,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         if (rest > 0) {
             const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total;
             n_ctas = max((int64_t)1, (int64_t)((float)gridDim.x * t / (t + r)));
+            n_ctas += n_ctas & 1;                      // whole TPCs (launch_as)
         }
         n_ctas = min(n_ctas, (int64_t)((uint64_t)total / (kUnitCost + 1)));
         if (blockIdx.x < n_ctas) {
@@ -413,11 +428,8 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             // block ids are read one tile ahead, across units, and turned into pool rows
             // when the tile is issued
             Unit mine;
-            Walker walk;
             walk.at = share.start(blockIdx.x);
             walk.stop = share.start((int64_t)blockIdx.x + 1);
-            walk.g0 = 0;
-            walk.load(p, 0);
             const int32_t *trow = nullptr;
             auto load_unit = [&]() {
                 walk.next(p, share, &mine);
@@ -439,6 +451,11 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     tma_load_3d(q_s + t * kQTile + h * kQPanel, &q_map, h * 64, w.kvh * G, w.pos + t * pos_per_tile, q_full);
                 }
                 ++q_loads;
+            };
+            auto prefetch_q = [&](const Unit &w) {          // to the L2 (a unit's switch: 1.7 us of loading)
+#pragma unroll 1
+                for (int i = 0; i < kNQ * PANELS; ++i)
+                    tma_prefetch_3d(&q_map, i % PANELS * 64, w.kvh * G, w.pos + i / PANELS * pos_per_tile);
             };
             load_unit();
             if (warp == 8 && lane == 0) load_q(mine);       // the first unit's, before its block is known
@@ -505,6 +522,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 ++issued;
                 if (warp == 8 && first && t_unit > 0) {   // the unit's Q, once the last unit's has been read
                     if (lane == 0) {
+                        prefetch_q(unit_s[t_unit & 3]);
                         if (!wait_for(q_empty, (t_unit & 1) ^ 1, abort_flag, p.wait_ns)) {
                             report(p.dev_status, PKV_DEV_TIMEOUT);
                             *abort_flag = 1;
@@ -532,7 +550,9 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag));
             };
-            const uint32_t q_addr = smem_u32(q_s) >> 4, k_addr = smem_u32(k_ring) >> 4, v_addr = smem_u32(v_ring) >> 4;
+            // (a descriptor holds 18 bits of an address; in a cluster there is the CTA's rank above them)
+            auto address = [](const void *x) -> uint32_t { return (smem_u32(x) & 0x3ffffu) >> 4; };
+            const uint32_t q_addr = address(q_s), k_addr = address(k_ring), v_addr = address(v_ring);
             const uint64_t kd = umma_desc_sw128(0, 16, 1024), vd = umma_desc_sw128(0, 2048, 1024);
             const uint32_t k_hi = (uint32_t)(kd >> 32), k_lo = (uint32_t)kd, v_hi = (uint32_t)(vd >> 32), v_lo = (uint32_t)vd;
             // S = Q_t K^T of the K in a ring slot, then the commit that hands it on; it
@@ -925,11 +945,12 @@ __global__ void __launch_bounds__(kTM) shared_join_kernel(const __grid_constant_
 }
 
 // What 128 of a decode's own tokens cost an SM, in tiles of a run: the share of the SMs that
-// the runs' tiles get.  Measured (weights 0.3 / 0.5 / 0.7 / 0.9): bf16 pages, 64 sequences of
-// 16 to 512 own tokens behind 4096 41.6 / 36.5 / 33.6 / 34 us, 256 of up to 700 in 6 groups,
-// eight query heads per kv head 164 / 165 / 173 / 181; int8 pages (whose runs' tiles take
-// longer), 96 in two groups 65 / 61 / 67 / 70.
-constexpr float kRestWeight = 0.6f, kRestWeightInt8 = 0.5f;
+// the runs' tiles get.  Measured (weights 0.4 / 0.6 / 0.8 / 1.0 / 1.3): bf16 pages, 64
+// sequences of 16 to 512 own tokens behind 4096 35.8 / 33.2 / 32.9 / 34.1 / 36.9 us, of 1000
+// to 2000 80.3 / 79.0 / 77.4 / 97.9 / 97.4, 128 in four groups behind 1000 to 3000 51.8 / 49.9
+// / 49.7 / 48.2 / 51.8; int8 pages (whose runs' tiles take longer), 96 sequences in two groups
+// 56.6 / 59.7 / 64.7 / 70.1 / 77.5.
+constexpr float kRestWeight = 0.85f, kRestWeightInt8 = 0.4f;
 
 RowsParams params_of(const RowsArgs &a)
 {
@@ -998,10 +1019,34 @@ cudaError_t launch_as(const CUtensorMap &qmap, const CUtensorMap &kmap, const CU
         return cudaFuncGetAttributes(&fa, rows_kernel<D, INT8>) == cudaSuccess && fa.numRegs >= S::kLaunchRegs;
     }();
     if (!regs_ok) return cudaErrorInvalidConfiguration;
-    const cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(rows_kernel<D, INT8>), S::kThreads, S::kSmem, nullptr);
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(rows_kernel<D, INT8>), S::kThreads, S::kSmem, nullptr);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute pdl[1];
-    const cudaLaunchConfig_t lc = dependent(pdl, grid, S::kThreads, S::kSmem, stream);
+    cudaLaunchAttribute at[2];
+    cudaLaunchConfig_t lc = dependent(reinterpret_cast<cudaLaunchAttribute(&)[1]>(at), grid, S::kThreads, S::kSmem, stream);
+    // A decode's own tokens run beside this kernel.  The two SMs of a TPC share their way to
+    // memory, and a CTA whose neighbour streams own tokens takes up to 1.4 times as long; as
+    // clusters of two, which lie on one TPC, the CTAs with a share have each other for
+    // neighbours (256 sequences in six groups: the last CTA done after 120 us, not 163).
+    if (p.ctx_lens && grid % 2 == 0) {
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = 2;
+        at[1].val.clusterDim.y = 1;
+        at[1].val.clusterDim.z = 1;
+        // (all of them have to be resident at once, as the shares are dealt out to all)
+        static std::atomic<int> pairs[kDevices];     // + 1; 0: not asked yet
+        int dev = 0;
+        e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        int n = dev < kDevices ? pairs[dev].load() - 1 : -1;
+        if (n < 0) {
+            cudaLaunchConfig_t ask = lc;
+            ask.attrs = at + 1;
+            e = cudaOccupancyMaxActiveClusters(&n, rows_kernel<D, INT8>, &ask);
+            if (e != cudaSuccess) return e;
+            if (dev < kDevices) pairs[dev] = n + 1;
+        }
+        if (n >= (int)grid / 2) lc.numAttrs = 2;
+    }
     return cudaLaunchKernelEx(&lc, rows_kernel<D, INT8>, qmap, kmap, vmap, p);
 }
 
