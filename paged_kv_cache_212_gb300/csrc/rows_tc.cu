@@ -52,7 +52,7 @@ struct Setup {
     static_assert(128 * kRegsIssue + (INT8 ? 128 * kRegsWiden : 0) + 256 * kRegsSoftmax <= kThreads * kLaunchRegs,
                   "register split above the launch");
     // (the scales of tile j + kScaleTiles overwrite those of tile j: its K slot is free by the
-    // S of tile j + kScaleTiles - kSlotsK, whose K was widened behind the V of tile j)
+    // S of tile j + kScaleTiles - kSlotsK, which was issued behind the P of the tile before)
     static_assert(!INT8 || kScaleTiles > kSlotsK, "scales still in use");
     static constexpr size_t kSmem = 1024 + (size_t)kNQ * kTM * D * 2 + (size_t)(kSlotsK + kSlotsV) * kTN * D * 2 +
                                     kBars * sizeof(uint64_t) + 256 + (INT8 ? kScaleTiles * 2 * kTN * sizeof(float) : 0);
@@ -174,16 +174,19 @@ struct Walker {
     }
 };
 
-// Four int8 codes (code + 128 in x) times a scale as bf16: with a byte as the low one of
-// the binary32 value 2^23 + byte, which the subtraction leaves as the code, exactly.
-__device__ __forceinline__ uint2 widened4(uint32_t x, float scale)
+// Four int8 codes as bf16: with the lower seven bits of a code as the mantissa of a bf16 of
+// exponent 2^7, and 2^7 or (code < 0) 2^8 taken off, which is the code, exactly.
+__device__ __forceinline__ uint2 codes_bf16x4(uint32_t x)
 {
-    const float2 bias = make_float2(-8388736.f, -8388736.f), s2 = make_float2(scale, scale);      // -(2^23 + 128)
-    float2 a = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7441)));
-    float2 b = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7442)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7443)));
-    a = __fmul2_rn(__fadd2_rn(a, bias), s2);
-    b = __fmul2_rn(__fadd2_rn(b, bias), s2);
-    return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y));
+    uint32_t r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t t = __byte_perm(x, 0x43434343u, i ? 0x4342 : 0x4140);
+        const uint32_t low = t & 0xff7fff7fu, off = t & 0xff80ff80u;
+        const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&low), *reinterpret_cast<const __nv_bfloat162 *>(&off));
+        r[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint2(r[0], r[1]);
 }
 
 // A box of a tensor map to the L2.
@@ -363,21 +366,21 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
 
     if (INT8 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsWiden) : "memory");
-        // ===================== codes widened to bf16, times their scales =====================
+        // ===================== codes widened to bf16 =====================
+        // (A bf16 holds a code; K's scales multiply the scores, V's the probabilities.  Rounded
+        // into K and V here they cost the softmax nothing, but outputs were off by twice as much
+        // as over bf16 pages.)
         // In place: the codes of a row (head_dim 64: of 16 rows) lie where bf16 values of the
         // same rows go, so a warp reads some rows, then writes them.  (Loops, not unrolled code:
         // all reads before all writes, with 32 registers of codes, took 2.5 us a K tile.)
         constexpr int VECS = D / 16;                        // 16-byte vectors of a code row
         constexpr int AT_ONCE = D == 128 ? 4 : 2;           // vectors of a lane: 16 rows
-        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase, const float *sc) -> bool {
+        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase) -> bool {
             if (!__all_sync(0xffffffffu, wait_for(codes, phase, abort_flag, p.wait_ns))) return false;
             const uint32_t vec = lane % VECS, odd = vec / 4 & 1, chunk = vec % 4 * 2;
 #pragma unroll 1
             for (uint32_t row0 = (warp - 12) * 32; row0 < (warp - 12) * 32 + 32; row0 += 16) {
                 uint4 x[AT_ONCE];
-                float scale[AT_ONCE];
-#pragma unroll
-                for (int i = 0; i < AT_ONCE; ++i) scale[i] = sc[row0 + (i * 32 + lane) / VECS];
 #pragma unroll
                 for (int i = 0; i < AT_ONCE; ++i) x[i] = *reinterpret_cast<const uint4 *>(slot + codes_at<D>(is_v, row0) + (i * 32 + lane) * 16);
                 __syncwarp();
@@ -385,8 +388,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 for (int i = 0; i < AT_ONCE; ++i) {
                     const uint32_t row = row0 + (i * 32 + lane) / VECS;
                     uint8_t *dst = slot + (is_v ? row / 16 * kVGroup + odd * 2048 + row % 16 * 128 : odd * kKVPanel + row * 128);
-                    const uint2 a = widened4(x[i].x ^ 0x80808080u, scale[i]), b = widened4(x[i].y ^ 0x80808080u, scale[i]);
-                    const uint2 d = widened4(x[i].z ^ 0x80808080u, scale[i]), e = widened4(x[i].w ^ 0x80808080u, scale[i]);
+                    const uint2 a = codes_bf16x4(x[i].x), b = codes_bf16x4(x[i].y), d = codes_bf16x4(x[i].z), e = codes_bf16x4(x[i].w);
                     const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
                     // (the second panel's vectors in the other order: different banks)
                     *reinterpret_cast<uint4 *>(dst + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
@@ -401,10 +403,8 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         bool more = any;
         for (int c = 0; more; ++c) {
             const int ks = c % NK, vs = c % NV;
-            const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN;
-            if (!__all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns)) ||
-                !widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1, sc) ||
-                !widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1, sc + kTN)) {
+            if (!widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1) ||
+                !widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1)) {
                 if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
                 *abort_flag = 1;
                 break;
@@ -697,11 +697,28 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     warp_live = __any_sync(0xffffffffu, live);
                 }
                 const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;
+                if constexpr (INT8) {
+                    ok = __all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns));
+                    if (!ok) break;
+                }
                 if (warp_live) {                 // (others leave P as it is: their rows go nowhere)
                     uint32_t sv[kTN];
 #pragma unroll
                     for (int i = 0; i < kTN / 32; ++i) tmem_ld32_async(lane_base + i * 32, sv + i * 32);
                     tmem_wait_ld();
+                    if constexpr (INT8) {        // scores of codes times the keys' scales
+                        const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN;
+#pragma unroll
+                        for (int i = 0; i < kTN; i += 4) {
+                            const float4 k = *reinterpret_cast<const float4 *>(sc + i);
+                            const float2 a = __fmul2_rn(make_float2(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])), make_float2(k.x, k.y));
+                            const float2 b = __fmul2_rn(make_float2(__uint_as_float(sv[i + 2]), __uint_as_float(sv[i + 3])), make_float2(k.z, k.w));
+                            sv[i] = __float_as_uint(a.x);
+                            sv[i + 1] = __float_as_uint(a.y);
+                            sv[i + 2] = __float_as_uint(b.x);
+                            sv[i + 3] = __float_as_uint(b.y);
+                        }
+                    }
                     // rows whose keys in this tile are all visible need no per-key test
                     if (__any_sync(0xffffffffu, limit - key0 < kTN)) {
 #pragma unroll
@@ -720,12 +737,19 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
                     // columns it covers were read
                     const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                    const float l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
-                    const float l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
+                    float l0, l1;
+                    if constexpr (INT8) {
+                        const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN + kTN;
+                        l0 = weighed64<0>(sv, sc2, nm2, sc, lane_base);
+                        l1 = weighed64<64>(sv, sc2, nm2, sc + 64, lane_base + 32);
+                    } else {
+                        l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
+                        l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
+                    }
                     l = l * alpha + (l0 + l1);
                     tmem_wait_st();
                 }
-                if (!INT8 && tail < kTN && (tail & 15) != 0) {   // (int8: zeros, by their scales)
+                if (!INT8 && tail < kTN && (tail & 15) != 0) {   // (int8: their scales are 0)
                     ok = clean_v(tail);
                     if (!ok) break;
                 }

@@ -22,6 +22,16 @@ def P():
     return P
 
 
+@pytest.fixture(params=["all", "one", "auto"])
+def rows_impl(request, monkeypatch):
+    """Rows contracted all at once or one by one (PKV_ROWS_IMPL), and as the sizes say."""
+    if request.param == "auto":
+        monkeypatch.delenv("PKV_ROWS_IMPL", raising=False)
+    else:
+        monkeypatch.setenv("PKV_ROWS_IMPL", request.param)
+    return request.param
+
+
 def _ints(x, kind=torch.int32):
     return torch.tensor(x, dtype=kind, device="cuda")
 
@@ -233,7 +243,7 @@ CROSS = [
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("n_q,keys,hkv,group,d,bs", CROSS)
-def test_cross(P, n_q, keys, hkv, group, d, bs, int8):
+def test_cross(P, n_q, keys, hkv, group, d, bs, int8, rows_impl):
     n, hq, scale = len(n_q), hkv * group, d ** -0.5
     pages = Paged(sum(n_q) + d, sum(-(-x // bs) for x in keys) + 1, hkv, d, bs, int8)
     width = max(-(-x // bs) for x in keys) + 2
@@ -262,7 +272,7 @@ def test_cross(P, n_q, keys, hkv, group, d, bs, int8):
     assert torch.equal(again[2:total - 3], out[2:total - 3])
 
 
-def test_cross_with_bad_input(P):
+def test_cross_with_bad_input(P, rows_impl):
     hkv, group, d, bs, scale = 2, 2, 64, 16, 0.125
     pages = Paged(3, 20, hkv, d, bs, False)
     added = [pages.add(0, 64, 4) for _ in range(4)]
@@ -340,7 +350,7 @@ def _shared_case(sizes, prefixes, behind, loose, hkv, d, bs, int8, seed):
 
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("sizes,prefixes,behind,loose,hkv,group,d,bs", SHARED)
-def test_shared(P, sizes, prefixes, behind, loose, hkv, group, d, bs, int8):
+def test_shared(P, sizes, prefixes, behind, loose, hkv, group, d, bs, int8, rows_impl):
     hq, scale = hkv * group, d ** -0.5
     pages, tables, ctx, starts, ptables, values = _shared_case(sizes, prefixes, behind, loose, hkv, d, bs, int8, len(behind))
     kp, vp, ks, vs = pages.cuda()
@@ -360,7 +370,7 @@ def test_shared(P, sizes, prefixes, behind, loose, hkv, group, d, bs, int8):
 
 
 @pytest.mark.parametrize("int8", [False, True])
-def test_shared_sequences_that_end_within_the_prefix(P, int8):
+def test_shared_sequences_that_end_within_the_prefix(P, int8, rows_impl):
     """A sequence sees no more of its group's tokens than ctx_lens says; 0: an idle slot."""
     hkv, group, d, bs, scale = 2, 4, 128, 16, 0.09
     pages, tables, ctx, starts, ptables, values = _shared_case([9], [700], [3] * 9, 0, hkv, d, bs, int8, 4)
@@ -376,7 +386,7 @@ def test_shared_sequences_that_end_within_the_prefix(P, int8):
         check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *(v[:x] for v in values[s]), scale, int8)
 
 
-def test_shared_equals_plain_decode_without_groups(P):
+def test_shared_equals_plain_decode_without_groups(P, rows_impl):
     """No group at all: the outputs of paged_decode_attention, within the bounds of both."""
     hkv, group, d, bs, scale = 2, 4, 64, 16, 0.125
     pages = Paged(8, 60, hkv, d, bs, False)
@@ -391,7 +401,7 @@ def test_shared_equals_plain_decode_without_groups(P):
         check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *x[1], scale, False)
 
 
-def test_shared_with_bad_input(P):
+def test_shared_with_bad_input(P, rows_impl):
     hkv, group, d, bs, scale = 2, 2, 64, 16, 0.125
     sizes, prefixes = [3, 2, 2], [40, 64, 30]
     pages, tables, ctx, starts, ptables, values = _shared_case(sizes, prefixes, [9] * 7, 0, hkv, d, bs, False, 4)
@@ -435,7 +445,7 @@ def test_shared_with_bad_input(P):
 
 # ---- any call: streams, graphs, threads, large pools ---------------------------------------------
 
-def test_rows_of_a_large_pool(P):
+def test_rows_of_a_large_pool(P, rows_impl):
     """Pool offsets that pass 2^32 bytes and 2^31 elements."""
     hkv, group, d, bs, scale = 8, 1, 128, 16, 0.1
     n_blocks = 2 ** 31 // (bs * hkv * d) + 40
@@ -476,7 +486,7 @@ def _step_state(P, seed, n=6, prefix=70, hkv=2, group=4, d=64, bs=16):
                 hkv=hkv, hq=hkv * group, d=d, bs=bs, n_blocks=n_blocks)
 
 
-def test_steps_together_in_a_graph(P):
+def test_steps_together_in_a_graph(P, rows_impl):
     """Maps, slot writes and shared decode as a step of a layer, captured once and replayed with
     other tokens: every step against the 64-bit values of all tokens so far."""
     w = _step_state(P, 1)
@@ -530,7 +540,7 @@ def test_steps_together_in_a_graph(P):
         check()
 
 
-def test_maps_feed_cross_attention(P):
+def test_maps_feed_cross_attention(P, rows_impl):
     """A packed batch from step maps: its queries against an encoder's pages."""
     new, keys, hkv, group, d, bs = [3, 0, 9, 1], [50, 7, 333, 16], 2, 4, 64, 16
     pages = Paged(6, 40, hkv, d, bs, False)
@@ -547,7 +557,7 @@ def test_maps_feed_cross_attention(P):
             check_rows(out[a:b], lse[a:b], q[a:b], *x[1], 0.1, False)
 
 
-def test_calls_on_other_streams_and_threads(P):
+def test_calls_on_other_streams_and_threads(P, rows_impl):
     """Two threads, each on a stream of its own with tensors of its own."""
     hkv, group, d, bs, scale = 4, 4, 128, 16, 0.09
     results, errors = {}, []
