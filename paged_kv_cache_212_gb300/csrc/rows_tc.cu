@@ -73,6 +73,7 @@ struct RowsParams {
     const float *k_scales, *v_scales;   // int8 pages
     int32_t *dev_status;
     int32_t wide_out;             // out is 32-byte aligned
+    int32_t sms;
     float rest_weight;            // what a tile of a decode's own tokens costs an SM, in tiles of a run
     unsigned long long wait_ns;   // limit of the pipeline waits
 };
@@ -90,6 +91,7 @@ struct Unit {
 // few long ones.  CTA c has places [c base + min(c, more), ...) of base or (the first `more`)
 // base + 1; base is above kUnitCost, so that every share holds a tile.
 constexpr int kUnitCost = 2;
+constexpr float kLate = 2.f;       // places by which a share's first tile is later than an own token's
 
 struct Share {
     int64_t base, more;
@@ -352,9 +354,12 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         }
         int64_t n_ctas = gridDim.x;
         if (rest > 0) {
-            const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total;
-            n_ctas = max((int64_t)1, (int64_t)((float)gridDim.x * t / (t + r)));
-            n_ctas += n_ctas & 1;                      // whole TPCs (launch_as)
+            // n SMs for t places, the others for own tokens worth r of them, so that both are done
+            // at once: t / n + kLate = r / (sms - n)
+            const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total, sms = (float)p.sms;
+            const float h = t + r - kLate * sms;
+            n_ctas = min(n_ctas, max((int64_t)1, (int64_t)((sqrtf(h * h + 4.f * kLate * t * sms) - h) / (2.f * kLate))));
+            n_ctas = min(n_ctas + (n_ctas & 1), (int64_t)gridDim.x);   // whole TPCs (launch_as)
         }
         n_ctas = min(n_ctas, (int64_t)((uint64_t)total / (kUnitCost + 1)));
         if (blockIdx.x < n_ctas) {
@@ -976,7 +981,7 @@ __global__ void __launch_bounds__(kTM) shared_join_kernel(const __grid_constant_
 // 56.6 / 59.7 / 64.7 / 70.1 / 77.5.
 constexpr float kRestWeight = 0.85f, kRestWeightInt8 = 0.4f;
 
-RowsParams params_of(const RowsArgs &a)
+RowsParams params_of(const RowsArgs &a, int num_sms)
 {
     const pkv_dims &d = a.dims;
     RowsParams p{};
@@ -1001,6 +1006,7 @@ RowsParams params_of(const RowsArgs &a)
     p.v_scales = a.v_scales;
     p.dev_status = a.dev_status;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
+    p.sms = num_sms;
     p.rest_weight = a.kv_dtype == PKV_KV_INT8 ? kRestWeightInt8 : kRestWeight;
     p.wait_ns = pipeline_wait_ns();
     return p;
@@ -1079,7 +1085,7 @@ cudaError_t launch_as(const CUtensorMap &qmap, const CUtensorMap &kmap, const CU
 cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
 {
     const pkv_dims &d = a.dims;
-    const RowsParams p = params_of(a);
+    const RowsParams p = params_of(a, num_sms);
     CUtensorMap qmap, kmap, vmap;
     {
         const uint64_t dims[3] = {(uint64_t)d.head_dim, (uint64_t)a.n_q_heads, (uint64_t)a.n_rows};
@@ -1127,7 +1133,7 @@ cudaError_t launch_rows_tc(const RowsArgs &a, int num_sms, cudaStream_t stream)
 
 cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream)
 {
-    const RowsParams p = params_of(a);
+    const RowsParams p = params_of(a, num_sms);
     cudaLaunchAttribute pdl[1];
     if (a.ctx_lens) {
         const int64_t grid = ((int64_t)a.n_rows * p.group + kTM - 1) / kTM;
