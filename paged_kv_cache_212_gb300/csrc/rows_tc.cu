@@ -879,6 +879,9 @@ template <int D>
 __device__ __forceinline__ void join_pieces(const RowsParams &p, Joined &j, int32_t c0, int32_t c1, int place, int part)
 {
     constexpr int kRound = 4;                       // pieces in flight
+    // (within the workspace whatever a rows kernel that ran out of time has left there)
+    c0 = max(c0, 0);
+    c1 = min(c1, kMaxCtas - 1);
     for (; c0 <= c1; c0 += kRound) {
         float2 ml[kRound];
         float x[kRound][kCols];
