@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "rows.h"
@@ -35,6 +36,8 @@ constexpr uint32_t kOCol = 128;            // O's column within a query tile's r
 constexpr int kBars = 48;          // barriers' room
 constexpr int kDevices = 16;       // whose occupancies are remembered
 constexpr int kScaleTiles = 4;     // int8: tiles whose scales are held
+constexpr float kUp = 7.f;         // int8: log2 of what multiplies the probabilities
+static_assert(kUp + kRescaleThreshold <= 15.f, "within fp16's range");
 static_assert(kNQ * kTM == kUnitRows, "a unit's rows");
 
 // What depends on the type of the pages: threads, ring slots (one 128-key tile each) of K
@@ -191,6 +194,33 @@ __device__ __forceinline__ uint2 codes_bf16x4(uint32_t x)
     return make_uint2(r[0], r[1]);
 }
 
+// Four int8 codes (code + 128 in x) times a scale as fp16: with a byte as the low one of
+// the binary32 value 2^23 + byte, which the subtraction leaves as the code, exactly.
+__device__ __forceinline__ uint2 scaled_f16x4(uint32_t x, float scale)
+{
+    const float2 bias = make_float2(-8388736.f, -8388736.f), s2 = make_float2(scale, scale);      // -(2^23 + 128)
+    float2 a = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7441)));
+    float2 b = make_float2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7442)), __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7443)));
+    a = __fmul2_rn(__fadd2_rn(a, bias), s2);
+    b = __fmul2_rn(__fadd2_rn(b, bias), s2);
+    return make_uint2(pack_f16x2(a.x, a.y), pack_f16x2(b.x, b.y));
+}
+
+// int8: an exponent e with every V scale of a tile below 2^e (asked by a whole warp), and 2^e.
+// Values are held as multiples of the power of two above the largest scale so far of their
+// part of a unit, so that codes times scales stay within fp16's range and the largest keep
+// its 11 bits; where it grows the softmax rescales O.  It is made from the same scales by the
+// warps that widen and by the softmax.
+__device__ __forceinline__ int value_exponent(const float *vs)
+{
+    const float4 x = *reinterpret_cast<const float4 *>(vs + 4 * (threadIdx.x & 31));
+    float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    return min(max((int)(__float_as_uint(top) >> 23) - 126, -126), 126);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float((uint32_t)(127 + max(e, -126)) << 23); }
+
 // A box of a tensor map to the L2.
 __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t c0, int32_t c1, int32_t c2)
 {
@@ -264,7 +294,8 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     // issued, behind all of the P of unit i - 3 and so the epilogues of unit i - 4).
     Unit *unit_s = reinterpret_cast<Unit *>(bars + kBars);
     float *scale_s = reinterpret_cast<float *>(bars + kBars) + 64;   // int8: [kScaleTiles][K, V][128 keys]
-    __shared__ int32_t last_s[kScaleTiles];                 // int8: whether the tile is the share's last
+    __shared__ int32_t tile_s[kScaleTiles];                 // int8: what a tile is
+    constexpr int32_t kFirstTile = 1, kLastTile = 2;        // of a part, of the share
     static_assert(2 + (INT8 ? 3 : 2) * (NK + NV) + kScaleTiles + 3 * kNQ + 3 <= kBars && 4 * sizeof(Unit) <= 256, "their room");
     __shared__ int64_t warp_sum[kThreads / 32], warp_rest[kThreads / 32];
     __shared__ CutUnit cut_s;                               // the last unit, where it goes on in the next CTA
@@ -372,15 +403,18 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     if (INT8 && warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsWiden) : "memory");
         // ===================== codes widened to bf16 =====================
-        // (A bf16 holds a code; K's scales multiply the scores, V's the probabilities.  Rounded
-        // into K and V here they cost the softmax nothing, but outputs were off by twice as much
-        // as over bf16 pages.)
+        // K's codes as bf16, which holds them, and the softmax multiplies the scores by their
+        // scales.  V's, with P in fp16, as code times scale in fp16, rounded once (2^-11), under
+        // the unit's power of two (value_exponent).  (Scales of V on the probabilities, fetched by
+        // every row's thread: 380 us where this takes 325; all scales rounded to bf16 here: 323,
+        // but outputs twice as far off as over bf16 pages.)
         // In place: the codes of a row (head_dim 64: of 16 rows) lie where bf16 values of the
         // same rows go, so a warp reads some rows, then writes them.  (Loops, not unrolled code:
         // all reads before all writes, with 32 registers of codes, took 2.5 us a K tile.)
         constexpr int VECS = D / 16;                        // 16-byte vectors of a code row
         constexpr int AT_ONCE = D == 128 ? 4 : 2;           // vectors of a lane: 16 rows
-        auto widen = [&](bool is_v, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase) -> bool {
+        auto widen = [&](auto kind, uint8_t *slot, uint64_t *codes, uint64_t *full, uint32_t phase, const float *vs, float down) -> bool {
+            constexpr bool is_v = decltype(kind)::value;
             if (!__all_sync(0xffffffffu, wait_for(codes, phase, abort_flag, p.wait_ns))) return false;
             const uint32_t vec = lane % VECS, odd = vec / 4 & 1, chunk = vec % 4 * 2;
 #pragma unroll 1
@@ -388,12 +422,28 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 uint4 x[AT_ONCE];
 #pragma unroll
                 for (int i = 0; i < AT_ONCE; ++i) x[i] = *reinterpret_cast<const uint4 *>(slot + codes_at<D>(is_v, row0) + (i * 32 + lane) * 16);
+                float scale[AT_ONCE];
+                if constexpr (is_v) {
+#pragma unroll
+                    for (int i = 0; i < AT_ONCE; ++i) scale[i] = vs[row0 + (i * 32 + lane) / VECS] * down;
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < AT_ONCE; ++i) {
                     const uint32_t row = row0 + (i * 32 + lane) / VECS;
                     uint8_t *dst = slot + (is_v ? row / 16 * kVGroup + odd * 2048 + row % 16 * 128 : odd * kKVPanel + row * 128);
-                    const uint2 a = codes_bf16x4(x[i].x), b = codes_bf16x4(x[i].y), d = codes_bf16x4(x[i].z), e = codes_bf16x4(x[i].w);
+                    uint2 a, b, d, e;
+                    if constexpr (is_v) {
+                        a = scaled_f16x4(x[i].x ^ 0x80808080u, scale[i]);
+                        b = scaled_f16x4(x[i].y ^ 0x80808080u, scale[i]);
+                        d = scaled_f16x4(x[i].z ^ 0x80808080u, scale[i]);
+                        e = scaled_f16x4(x[i].w ^ 0x80808080u, scale[i]);
+                    } else {
+                        a = codes_bf16x4(x[i].x);
+                        b = codes_bf16x4(x[i].y);
+                        d = codes_bf16x4(x[i].z);
+                        e = codes_bf16x4(x[i].w);
+                    }
                     const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(d.x, d.y, e.x, e.y);
                     // (the second panel's vectors in the other order: different banks)
                     *reinterpret_cast<uint4 *>(dst + (((chunk + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
@@ -406,15 +456,23 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             return true;
         };
         bool more = any;
+        int exponent = 0;
         for (int c = 0; more; ++c) {
             const int ks = c % NK, vs = c % NV;
-            if (!widen(false, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1) ||
-                !widen(true, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1)) {
+            const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN + kTN;
+            bool ok = widen(std::false_type{}, k_ring + ks * kSlotBytes, &k_codes[ks], &k_full[ks], (c / NK) & 1, sc, 1.f) &&
+                      __all_sync(0xffffffffu, wait_for(&sc_full[c % kScaleTiles], (c / kScaleTiles) & 1, abort_flag, p.wait_ns));
+            if (ok) {
+                const int flags = const_cast<volatile int32_t *>(tile_s)[c % kScaleTiles], e = value_exponent(sc);
+                exponent = flags & kFirstTile ? e : max(exponent, e);
+                more = !(flags & kLastTile);
+                ok = widen(std::true_type{}, v_ring + vs * kSlotBytes, &v_codes[vs], &v_full[vs], (c / NV) & 1, sc, power_of_two(-exponent));
+            }
+            if (!ok) {
                 if (lane == 0) report(p.dev_status, PKV_DEV_TIMEOUT);
                 *abort_flag = 1;
                 break;
             }
-            more = !const_cast<volatile int32_t *>(last_s)[c % kScaleTiles];
         }
     } else if (warp >= 4 * kNQ) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::kRegsIssue) : "memory");
@@ -509,7 +567,8 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                         copy_scale(sc + kTN + i, p.v_scales + at, in);
                     }
                     copies_arrive(&sc_full[issued % kScaleTiles]);
-                    if (warp == 8 && lane == 0) last_s[issued % kScaleTiles] = !more;
+                    // (ahead of the tile's codes, whose barrier hands it on)
+                    if (warp == 8 && lane == 0) tile_s[issued % kScaleTiles] = (first ? kFirstTile : 0) | (more ? 0 : kLastTile);
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
                 __syncwarp();
@@ -548,7 +607,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         } else {
             // ===================== MMA issuer =====================
             const uint32_t idesc_s = umma_idesc_bf16(kTM, kTN, false, false);
-            const uint32_t idesc_o = umma_idesc_bf16(kTM, D, false, true);
+            const uint32_t idesc_o = INT8 ? umma_idesc_f16(kTM, D, false, true) : umma_idesc_bf16(kTM, D, false, true);
             const uint32_t leader = elect_one();
             // The warp's waits keep the default limit, which compiles to the plain wait; when
             // another role's wait runs out, the abort flag ends these.
@@ -687,6 +746,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             bool live = false, warp_live = false;
             int32_t pos = 0, limit = 0;
             float m = -INFINITY, l = 0.f;
+            int exponent = 0;                    // int8: O is in units of 2^exponent
             for (int j = 0; j < n_kt; ++j, ++c) {
                 ok = __all_sync(0xffffffffu, wait_for(&s_full[qt], c & 1, abort_flag, p.wait_ns));
                 if (!ok) break;
@@ -736,21 +796,23 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                         }
                     }
                     const float alpha = move_maximum(m, largest(sv) * p.scale_log2);
+                    float alpha_o = alpha;
+                    if constexpr (INT8) {
+                        const int e = value_exponent(scale_s + (c % kScaleTiles) * 2 * kTN + kTN), old = exponent;
+                        exponent = j == 0 ? e : max(old, e);
+                        if (j > 0) alpha_o *= power_of_two(old - exponent);
+                    }
                     // O row rescale (rare): O holds P V up to tile j - 1, complete since this S's
                     // commit came after it
-                    if (__any_sync(0xffffffffu, alpha != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha);
+                    if (__any_sync(0xffffffffu, alpha_o != 1.f) && j > 0) rescale_o<D>(lane_base + kOCol, alpha_o);
                     // P (bf16 pairs) over S's first 64 columns, each 16-column store after the S
                     // columns it covers were read
-                    const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m, -m);
-                    float l0, l1;
-                    if constexpr (INT8) {
-                        const float *sc = scale_s + (c % kScaleTiles) * 2 * kTN + kTN;
-                        l0 = weighed64<0>(sv, sc2, nm2, sc, lane_base);
-                        l1 = weighed64<64>(sv, sc2, nm2, sc + 64, lane_base + 32);
-                    } else {
-                        l0 = probabilities64<0>(sv, sc2, nm2, lane_base);
-                        l1 = probabilities64<64>(sv, sc2, nm2, lane_base + 32);
-                    }
+                    // (fp16: 2^kUp times them, so that the largest is below 2^15 and what is below
+                    // fp16's range is below 2^-31 of it)
+                    const float up = INT8 ? kUp - m : -m;
+                    const float2 nm2 = m == -INFINITY ? make_float2(0.f, 0.f) : make_float2(up, up);
+                    const float l0 = probabilities64<0, INT8>(sv, sc2, nm2, lane_base);
+                    const float l1 = probabilities64<64, INT8>(sv, sc2, nm2, lane_base + 32);
                     l = l * alpha + (l0 + l1);
                     tmem_wait_st();
                 }
@@ -768,11 +830,13 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             tc_fence_after();
             // row r of O.  (O is read before this warp's next P is handed over, and the next
             // unit's first product into O comes after that.)
+            const float unit_o = INT8 ? power_of_two(exponent) : 1.f;
+            if (INT8) m -= kUp;
             if (warp_live) {
                 const int64_t row = (int64_t)pos * p.n_q_heads + w.kvh * G + r % G;
                 const bool whole = !p.ctx_lens && !w.cut;
                 if (whole) {
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    const float inv = l > 0.f ? unit_o / l : 0.f;
                     __nv_bfloat16 *out = p.out + row * D;
 #pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
@@ -812,7 +876,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                         for (int q2 = 0; q2 < 4; ++q2) {
                             uint32_t x[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = v[8 * q2 + e];
+                            for (int e = 0; e < 8; ++e) x[e] = INT8 ? __float_as_uint(__uint_as_float(v[8 * q2 + e]) * unit_o) : v[8 * q2 + e];
                             st_global_32(dst + (i * 4 + q2) * step, x);
                         }
                     }

@@ -146,8 +146,8 @@ __device__ __forceinline__ float move_maximum(float &m, float mx)
 }
 
 // Probabilities of 64 scores from sv[I0] on (packed two-lane FMA for the exponent
-// arguments), as bf16 pairs into 32 TMEM columns from taddr on; their sum.
-template <int I0, int NC>
+// arguments), as bf16 (or fp16) pairs into 32 TMEM columns from taddr on; their sum.
+template <int I0, bool F16 = false, int NC>
 __device__ __forceinline__ float probabilities64(const uint32_t (&sv)[NC], float2 sc2, float2 nm2, uint32_t taddr)
 {
     float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
@@ -163,35 +163,7 @@ __device__ __forceinline__ float probabilities64(const uint32_t (&sv)[NC], float
                 lb = __fadd2_rn(lb, ee);
             else
                 la = __fadd2_rn(la, ee);
-            pk[e] = pack_bf16x2(ee.x, ee.y);
-        }
-        tmem_st16_async(taddr + i * 16, pk);
-    }
-    return (la.x + la.y) + (lb.x + lb.y);
-}
-
-// The same for int8 pages: what is stored is weighed by vs[0 .. 63], the V scales of the
-// keys (shared memory); the sum is that of the probabilities.
-template <int I0, int NC>
-__device__ __forceinline__ float weighed64(const uint32_t (&sv)[NC], float2 sc2, float2 nm2, const float *vs, uint32_t taddr)
-{
-    float2 la = make_float2(0.f, 0.f), lb = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-            const int k = I0 + i * 32 + 2 * e;
-            const float4 v = *reinterpret_cast<const float4 *>(vs + i * 32 + 2 * e);
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[k]), __uint_as_float(sv[k + 1])), sc2, nm2);
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[k + 2]), __uint_as_float(sv[k + 3])), sc2, nm2);
-            float2 ex = make_float2(fast_exp2(x.x), fast_exp2(x.y)), ey = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            la = __fadd2_rn(la, ex);
-            lb = __fadd2_rn(lb, ey);
-            ex = __fmul2_rn(ex, make_float2(v.x, v.y));
-            ey = __fmul2_rn(ey, make_float2(v.z, v.w));
-            pk[e] = pack_bf16x2(ex.x, ex.y);
-            pk[e + 1] = pack_bf16x2(ey.x, ey.y);
+            pk[e] = F16 ? pack_f16x2(ee.x, ee.y) : pack_bf16x2(ee.x, ee.y);
         }
         tmem_st16_async(taddr + i * 16, pk);
     }

@@ -53,13 +53,15 @@ class Paged:
         return [None if t is None else t.cuda() for t in self.pools + self.scales]
 
 
-def check_rows(out, lse, q, k, v, scale, int8):
+def check_rows(out, lse, q, k, v, scale, int8, most=0.0):
     """out [m, Hq, D] and lse [m, Hq] of queries q [m, Hq, D] that all see k, v [n, Hkv, D] (64 bits).
 
     The error: roundings of a prefill (probabilities to bf16 once) or, for a sequence's own
     tokens, those of a decode; keys may be in up to 192 pieces, whose joins round a sum 4
-    times each.  (int8 pages that many rows read: what is rounded once is a probability times
-    the V scale, which sum p |v| knows already.)"""
+    times each.  int8 pages that many rows read: probabilities and values are rounded to fp16
+    (2^-11, less than U16 together), values to 2^-25 of a power of two at most twice the largest
+    scale at least, which `most` is (0: scales within 2^13 of one another, whose values are all
+    in fp16's normal range), and probabilities to 2^-32 of one at least, of n keys."""
     m, hq, d = out.shape
     n, hkv, _ = k.shape
     g = hq // hkv
@@ -72,7 +74,7 @@ def check_rows(out, lse, q, k, v, scale, int8):
         o, ls, absum, size, top = R.attend(q[:, h * g:(h + 1) * g], k[:, h], v[:, h], seen, scale)
         tol = R.prefill_tolerance(o, absum, size, d, n) + absum * (192 * 4 * R.U32)
         if int8:
-            tol = tol + R.decode_tolerance(o, absum, size, d, n, top)
+            tol = tol + R.decode_tolerance(o, absum, size, d, n, top) + 2.0 ** -24 * most
         got = out[:, h * g:(h + 1) * g]
         assert torch.isfinite(got).all(), h
         over = (got - o).abs() - tol

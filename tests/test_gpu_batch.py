@@ -272,6 +272,26 @@ def test_cross(P, n_q, keys, hkv, group, d, bs, int8, rows_impl):
     assert torch.equal(again[2:total - 3], out[2:total - 3])
 
 
+@pytest.mark.parametrize("ramp", [(-6, 2), (2, -6), (-37, -30), (25, 30)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_over_scales_of_any_size(P, d, ramp, rows_impl):
+    """int8 pages whose V scales grow or shrink over a sequence by many orders of magnitude, or are
+    all tiny or huge."""
+    hkv, group, bs, scale, n = 2, 3, 16, d ** -0.5, 900
+    pages = Paged(9, 60, hkv, d, bs, True)
+    row, (k, v) = pages.add(0, n, 60)
+    slots = row[torch.arange(n) // bs].long() * bs + torch.arange(n) % bs
+    factor = 10.0 ** torch.linspace(*ramp, n)[:, None].expand(n, hkv)
+    flat = pages.scales[1].view(-1, hkv)
+    flat[slots] = (flat[slots].double() * factor).float()
+    v = pages.pools[1].view(-1, hkv, d)[slots].double() * flat[slots].double()[..., None]
+    kp, vp, ks, vs = pages.cuda()
+    q = torch.randn((170, hkv * group, d), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    lse = torch.empty((170, hkv * group), device="cuda")
+    out = P.paged_cross_attention(q, _ints([0, 170]), kp, vp, row.view(1, -1).cuda(), _ints([n]), scale, k_scales=ks, v_scales=vs, lse_out=lse)
+    check_rows(out, lse, q, k, v, scale, True, float(flat[slots].max()))
+
+
 def test_cross_with_bad_input(P, rows_impl):
     hkv, group, d, bs, scale = 2, 2, 64, 16, 0.125
     pages = Paged(3, 20, hkv, d, bs, False)
