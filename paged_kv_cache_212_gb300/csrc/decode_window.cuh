@@ -1,6 +1,7 @@
 // decode_window.cuh -- decode attention under a sliding window with first tokens
 // that stay visible (pagedkv_window.h), over bf16 or int8 pages, alone or as one
-// layer's step with the rotary turn and the page write of the new token.
+// layer's step with the rotary turn and the page write of the new token.  Also (RUNS,
+// decode_shared.cu) over the tokens of a run that rows have in common and a row's own.
 //
 // The host knows how many tokens a query can see (window + sinks), so no plan
 // and no workspace is needed: a (sequence, kv head) unit is the work of one

@@ -14,6 +14,19 @@
 // round whole.  Every CTA sums the runs' tiles by itself to find its share, since lengths
 // stand in device memory.  A unit that is cut leaves partials in 32 bits (rows.h), at most
 // one more per CTA.
+//
+// Rounding.  Scores, maxima, sums and O are binary32.  P is rounded once to bf16, as in
+// prefill_window.cu; over int8 pages to fp16, as the values are (value_exponent).  Against 64
+// bits outputs are 0.0023 off over bf16 pages and 0.0017 over int8 pages, where their own
+// rounding to bf16 makes 0.0016.
+//
+// Measured.  4135 queries of 8 sequences, 1000 to 8191 keys, 32 query and 8 kv heads of 128:
+// 165 us (175 under the power cap of a long run), 1.17 PFLOP/s of needed work; a tile of 128
+// keys takes 1.52 us (1.68 PFLOP/s on 152 SMs), bound by the chain of S, softmax and P V of a
+// query tile, a change of unit 3.2 us more (the output's stores, the next queries' load), the
+// start 8 us and the join 8.  64 sequences behind 4096 tokens: 32 us.  1642 queries over int8
+// pages, 24 and 8 heads of 64: 39.8 us; the same 4135 queries over int8 pages 331 us, 2.5 us a
+// tile, bound by the warps that widen the codes.
 #include <math.h>
 
 #include <atomic>
