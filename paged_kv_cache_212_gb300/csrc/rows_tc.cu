@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             // n SMs for t places, the others for own tokens worth r of them, so that both are done
             // at once: t / n + kLate = r / (sms - n)
             const float r = (float)rest * p.n_kv_heads * p.rest_weight / kTN, t = (float)total, sms = (float)p.sms;
-            const float h = t + r - kLate * sms;
-            n_ctas = min(n_ctas, max((int64_t)1, (int64_t)((sqrtf(h * h + 4.f * kLate * t * sms) - h) / (2.f * kLate))));
+            const float h = t + r - kLate * sms, d = sqrtf(h * h + 4.f * kLate * t * sms);
+            const float n = h > 0.f ? 2.f * t * sms / (d + h) : (d - h) / (2.f * kLate);
+            n_ctas = min(n_ctas, max((int64_t)1, (int64_t)n));
             n_ctas = min(n_ctas + (n_ctas & 1), (int64_t)gridDim.x);   // whole TPCs (launch_as)
         }
         n_ctas = min(n_ctas, (int64_t)((uint64_t)total / (kUnitCost + 1)));
