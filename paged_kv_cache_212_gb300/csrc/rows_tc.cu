@@ -25,7 +25,7 @@
 // keys takes 1.52 us (1.68 PFLOP/s on 152 SMs), bound by the chain of S, softmax and P V of a
 // query tile, a change of unit 3.2 us more (the output's stores, the next queries' load), the
 // start 8 us and the join 8.  64 sequences behind 4096 tokens: 32 us.  1642 queries over int8
-// pages, 24 and 8 heads of 64: 39.8 us; the same 4135 queries over int8 pages 331 us, 2.5 us a
+// pages, 24 and 8 heads of 64: 39.8 us; the same 4135 queries over int8 pages 331 us, 3.2 us a
 // tile, bound by the warps that widen the codes.
 #include <math.h>
 
