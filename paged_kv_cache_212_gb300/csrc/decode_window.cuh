@@ -392,8 +392,9 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             const __nv_bfloat16 *src = source(member + i * TEAM);
             x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
             if (src) {
-                x0[i] = __ldg(reinterpret_cast<const uint4 *>(src) + v0);
-                x1[i] = __ldg(reinterpret_cast<const uint4 *>(src) + v1);
+                const uint4 *at = reinterpret_cast<const uint4 *>(src);
+                x0[i] = RUNS == kNoRuns ? __ldg(at + v0) : at[v0];
+                x1[i] = RUNS == kNoRuns ? __ldg(at + v1) : at[v1];
             }
         }
         float c[8], sn[8];

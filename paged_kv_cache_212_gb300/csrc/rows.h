@@ -109,26 +109,35 @@ __device__ __forceinline__ Run run_at(const int32_t *starts, const int32_t *run_
 }
 
 // The run of a row, -1 for none, and what it is: the last g with starts[g] <= row, where
-// row < starts[g + 1].  Asked by a whole warp, 32 runs at a time in one round of loads.
+// row < starts[g + 1].  Asked by a whole warp: it narrows the runs down to 32 by the starts of
+// 32 of them at a time, and then reads those.  (A row each for 1024 and 4096 sequences of 64
+// keys: 213 and 1124 us when all starts before a row's were read, 113 and 290 so.)
 __device__ __forceinline__ int32_t run_of(const int32_t *starts, const int32_t *run_lens, int32_t n_runs, int32_t n_rows,
                                           int32_t max_run_blocks, int32_t block_size, int32_t row, Run *out)
 {
     const int lane = threadIdx.x & 31;
-    for (int32_t g0 = 0; g0 < n_runs; g0 += 32) {
-        const int32_t g = g0 + lane;
-        Run r{0, 0, 0, false};
-        if (g < n_runs) r = run_at(starts, run_lens, n_rows, max_run_blocks, block_size, g);
-        const uint32_t here = __ballot_sync(0xffffffffu, row - r.row0 >= 0 && row - r.row0 < r.rows);
-        if (here == 0) continue;
-        const int src = __ffs(here) - 1;
-        out->row0 = __shfl_sync(0xffffffffu, r.row0, src);
-        out->rows = __shfl_sync(0xffffffffu, r.rows, src);
-        out->len = __shfl_sync(0xffffffffu, r.len, src);
-        out->good = __shfl_sync(0xffffffffu, (int)r.good, src);
-        return g0 + src;
+    int32_t g0 = 0, n = n_runs;                     // it is one of g0 .. g0 + n - 1
+    while (n > 32) {
+        const int32_t step = (int32_t)(((uint32_t)n + 31u) / 32u), at = lane * step;
+        const uint32_t upto = __ballot_sync(0xffffffffu, at < n && __ldcg(starts + g0 + at) <= row);
+        const int32_t skip = upto == 0 ? 0 : (31 - __clz(upto)) * step;
+        g0 += skip;
+        n = min(n - skip, step);
     }
-    *out = Run{0, 0, 0, true};
-    return -1;
+    const int32_t g = g0 + lane;
+    Run r{0, 0, 0, false};
+    if (lane < n) r = run_at(starts, run_lens, n_rows, max_run_blocks, block_size, g);
+    const uint32_t here = __ballot_sync(0xffffffffu, row - r.row0 >= 0 && row - r.row0 < r.rows);
+    if (here == 0) {
+        *out = Run{0, 0, 0, true};
+        return -1;
+    }
+    const int src = __ffs(here) - 1;
+    out->row0 = __shfl_sync(0xffffffffu, r.row0, src);
+    out->rows = __shfl_sync(0xffffffffu, r.rows, src);
+    out->len = __shfl_sync(0xffffffffu, r.len, src);
+    out->good = __shfl_sync(0xffffffffu, (int)r.good, src);
+    return g0 + src;
 }
 #endif
 

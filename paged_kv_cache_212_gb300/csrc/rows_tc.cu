@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             // the block of this lane's group of tile j of the unit
             auto load_block = [&](int j) -> int32_t {
                 const int32_t key = (mine.t0 + j) * kTN + grp * 16;
-                return (lane < n_grp && key < mine.len) ? __ldg(trow + key / p.block_size) : 0;
+                return (lane < n_grp && key < mine.len) ? __ldcg(trow + key / p.block_size) : 0;
             };
             int q_loads = 0;                                // that lane 0 has issued
             // (a group that does not divide 128 leaves the tile's last rows as they are: rows of
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     pos = w.pos + qt * pos_per_tile + r / G;
                     live = r < pos_per_tile * G && pos < w.pos_end;
                     limit = w.len;
-                    if (live && p.ctx_lens) limit = min(limit, max(__ldg(p.ctx_lens + pos), 0));
+                    if (live && p.ctx_lens) limit = min(limit, max(__ldcg(p.ctx_lens + pos), 0));
                     warp_live = __any_sync(0xffffffffu, live);
                 }
                 const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;

@@ -10,8 +10,8 @@
 // A token's block comes from the free list or, in the block that its sequence holds
 // already, from a table entry that the call does not write, so no CTA waits for another.
 //
-// Measured: a step of 64 sequences 4.3 us (the launch and three dependent reads), 500
-// sequences with 65 K new tokens 7.3, 4096 sequences of one token 11.2 (two rounds of sums),
+// Measured: a step of 64 sequences 4.0 us (the launch and three dependent reads), 500
+// sequences with 65 K new tokens 7.6, 4096 sequences of one token 11.2 (two rounds of sums),
 // four prompts of 30 K tokens in all 6.1.
 #include "common.cuh"
 #include "launch.h"
@@ -45,16 +45,20 @@ constexpr uint32_t kMost = 0x7fffffffu;
 // The sum of two numbers up to 2^31 - 1, or that.
 __device__ __forceinline__ uint32_t add_clipped(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 
-// What sequence s holds and adds (0 and 0, and false, where its length is bad).
-__device__ __forceinline__ bool sequence(const MapArgs &a, int32_t s, int32_t &len, int32_t &add)
+// What a sequence holds and adds, as they are or (false) 0 and 0 where its length is bad.
+__device__ __forceinline__ bool good_lengths(const MapArgs &a, int32_t &len, int32_t &add)
 {
-    len = __ldg(a.lens + s);
-    add = __ldg(a.n_new + s);
     if (len < 0 || add < 0 || (int64_t)len + add > (int64_t)a.max_blocks * a.block_size) {
         len = add = 0;
         return false;
     }
     return true;
+}
+__device__ __forceinline__ bool sequence(const MapArgs &a, int32_t s, int32_t &len, int32_t &add)
+{
+    len = a.lens[s];
+    add = a.n_new[s];
+    return good_lengths(a, len, add);
 }
 
 __device__ __forceinline__ int32_t blocks_of(int32_t tokens, int32_t bs)
@@ -69,7 +73,7 @@ __device__ __forceinline__ int32_t free_block(const MapArgs &a, int64_t at, int3
         report(dev_status, PKV_DEV_OUT_OF_BLOCKS);
         return -1;
     }
-    const int32_t b = __ldg(a.free_blocks + at);
+    const int32_t b = a.free_blocks[at];
     if (b < 0 || b >= a.n_blocks) {
         report(dev_status, PKV_DEV_BAD_BLOCK_ID);
         return -1;
@@ -80,13 +84,14 @@ __device__ __forceinline__ int32_t free_block(const MapArgs &a, int64_t at, int3
 __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
 {
     __shared__ uint32_t tok_s[kRound], blk_s[kRound];    // exclusive sums within the batch
+    __shared__ int32_t len_s[kRound];
     __shared__ uint32_t warp_tok[kThreads / 32], warp_blk[kThreads / 32];
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t bs = a.block_size;
     const int64_t token = (int64_t)blockIdx.x * kThreads + tid;
-    const int64_t cursor = a.cursor ? (int64_t)__ldg(a.cursor) : 0;
+    const int64_t cursor = a.cursor ? (int64_t)*a.cursor : 0;
     const int64_t first_free = cursor < 0 ? (int64_t)a.n_free : cursor;   // a negative one: nothing is left
     // a table row is the work of `team` warps, or a warp's are several rows
     const int64_t n_warps = (int64_t)gridDim.x * (kThreads / 32), my_warp = (int64_t)blockIdx.x * (kThreads / 32) + warp;
@@ -97,17 +102,21 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
     bool mapped = false;
     for (int64_t s0 = 0; s0 < a.n_seqs; s0 += kRound) {
         // 1. the round's sums
-        int32_t add[kPer], need[kPer];
+        int32_t len[kPer], add[kPer], need[kPer];
         uint32_t tok = 0, blk = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int64_t s = s0 + tid * kPer + i;
-            add[i] = need[i] = 0;
+            len[i] = add[i] = 0;
             if (s < a.n_seqs) {
-                int32_t len;
-                if (!sequence(a, (int32_t)s, len, add[i]) && blockIdx.x == 0) report(a.dev_status, PKV_DEV_BAD_LENGTH);
-                need[i] = blocks_of(len + add[i], bs) - blocks_of(len, bs);
+                len[i] = a.lens[s];
+                add[i] = a.n_new[s];
             }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (!good_lengths(a, len[i], add[i]) && blockIdx.x == 0) report(a.dev_status, PKV_DEV_BAD_LENGTH);
+            need[i] = blocks_of(len[i] + add[i], bs) - blocks_of(len[i], bs);
             tok = add_clipped(tok, add[i]);
             blk = add_clipped(blk, need[i]);
         }
@@ -145,6 +154,7 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
         for (int i = 0; i < kPer; ++i) {
             tok_s[tid * kPer + i] = tok_at;
             blk_s[tid * kPer + i] = blk_at;
+            len_s[tid * kPer + i] = len[i];
             tok_at = add_clipped(tok_at, add[i]);
             blk_at = add_clipped(blk_at, need[i]);
         }
@@ -164,13 +174,12 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
                     hi = mid;
             }
             const int32_t s = (int32_t)s0 + lo;
-            int32_t len, n;
-            sequence(a, s, len, n);
+            const int32_t len = len_s[lo];
             const int32_t pos = len + (int32_t)(token - tok_s[lo]);
             const int32_t at = (int32_t)((uint32_t)pos / (uint32_t)bs), held = blocks_of(len, bs);
             int32_t b;
             if (at < held) {
-                b = __ldg(a.tables + (int64_t)s * a.max_blocks + at);
+                b = __ldcg(a.tables + (int64_t)s * a.max_blocks + at);   // (no old copy of a line that others write stays in the L1)
                 if (b < 0 || b > a.n_blocks) {
                     report(a.dev_status, PKV_DEV_BAD_BLOCK_ID);
                     b = -1;

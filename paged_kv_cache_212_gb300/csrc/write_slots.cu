@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) write_slots_kernel(const SlotArgs a)
         const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? a.v_new + r * a.v_stride : a.k_new + r * a.k_stride) + piece * 16);
         x0 = __ldcs(src);
         x1 = __ldcs(src + 1);
-        row = __ldg(a.slots + r);
+        row = a.slots[r];
         if (row >= a.pool_rows) {
             if (piece == 0 && !is_v) report(a.dev_status, PKV_DEV_BAD_POSITION);
             row = -1;

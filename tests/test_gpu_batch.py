@@ -272,6 +272,36 @@ def test_cross(P, n_q, keys, hkv, group, d, bs, int8, rows_impl):
     assert torch.equal(again[2:total - 3], out[2:total - 3])
 
 
+@pytest.mark.parametrize("n", [33, 64, 65, 1030])
+def test_cross_of_many_sequences(P, n, rows_impl):
+    """Sequences whose rows are looked up in several steps, some of them without rows or keys."""
+    r = random.Random(n)
+    n_q = [r.choice([0, 0, 1, 1, 2, 3]) for _ in range(n)]
+    n_q[:3], n_q[-2:] = [0, 0, 1], [2, 0]
+    keys = [r.choice([0, 1, 16, 17, 40, 130]) for _ in range(n)]
+    hkv, group, d, bs, scale = 1, 2, 64, 16, 0.125
+    pages = Paged(n, sum(-(-x // bs) for x in keys) + 1, hkv, d, bs, False)
+    added = [pages.add(0, x, 9) for x in keys]
+    kp, vp, _, _ = pages.cuda()
+    tables = torch.stack([row for row, _ in added]).cuda()
+    starts = [5]
+    for x in n_q:
+        starts.append(starts[-1] + x)
+    total = starts[-1] + 40
+    q = torch.randn((total, hkv * group, d), generator=torch.Generator().manual_seed(7)).to(torch.bfloat16).cuda()
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    st = _status()
+    P.paged_cross_attention(q, _ints(starts), kp, vp, tables, _ints(keys), scale, out=out, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    for rows in (slice(0, 5), slice(total - 40, total)):
+        assert (out[rows] == 7).all() and (lse[rows] == 7).all()
+    for s in range(n):
+        a, b = starts[s], starts[s + 1]
+        if a < b:
+            check_rows(out[a:b], lse[a:b], q[a:b], *added[s][1], scale, False)
+
+
 @pytest.mark.parametrize("ramp", [(-6, 2), (2, -6), (-37, -30), (25, 30)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_cross_over_scales_of_any_size(P, d, ramp, rows_impl):
@@ -387,6 +417,25 @@ def test_shared(P, sizes, prefixes, behind, loose, hkv, group, d, bs, int8, rows
     again = P.paged_decode_attention_shared(q, kp, vp, tables.cuda(), _ints(ctx), _ints(starts), ptables.cuda(),
                                             _ints(prefixes), scale, k_scales=ks, v_scales=vs)
     assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("groups", [33, 200])
+def test_shared_of_many_groups(P, groups, rows_impl):
+    r = random.Random(groups)
+    sizes = [r.choice([0, 1, 2, 5]) for _ in range(groups)]
+    prefixes = [r.choice([0, 1, 16, 100, 129]) for _ in range(groups)]
+    behind = [r.choice([0, 1, 20]) for _ in range(sum(sizes))]
+    hkv, group, d, bs, scale = 2, 2, 64, 16, 0.125
+    pages, tables, ctx, starts, ptables, values = _shared_case(sizes, prefixes, behind, 3, hkv, d, bs, False, groups)
+    kp, vp, _, _ = pages.cuda()
+    q = torch.randn((len(ctx), hkv * group, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    lse = torch.full((len(ctx), hkv * group), 7.0, device="cuda")
+    st = _status()
+    out = P.paged_decode_attention_shared(q, kp, vp, tables.cuda(), _ints(ctx), _ints(starts), ptables.cuda(),
+                                          _ints(prefixes), scale, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    for s in range(len(ctx)):
+        check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, False)
 
 
 @pytest.mark.parametrize("int8", [False, True])
