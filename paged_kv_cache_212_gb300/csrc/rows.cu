@@ -11,13 +11,16 @@ namespace pkv {
 namespace {
 
 // Whether rows are attended one by one, each reading its run's keys again (from the L2, where
-// they are shared), in one launch: where every sequence of a cross attention has a row at
-// most, and where what the rows can read, by the width of their table rows, is below what the
-// two or three launches of the other way cost.  Measured (8 kv heads of 128, bf16 pages; all
-// at once / one by one): cross attention of one row each, 8 sequences of 512 .. 4096 keys
-// 31.1 / 20.4 us, 64: 124.6 / 121.1, 64 over int8 pages 234 / 91, but with two rows each 125.6
-// / 159.5; decode behind a shared prefix, 32 sequences behind 256 tokens (38 MB) 18.7 / 7.4,
-// 4 behind 4096 (68 MB) 21.2 / 11.4, 16 behind 4096 (285 MB) 24.2 / 26.9.
+// they are shared), in one launch: where what the rows can read, by the width of their table
+// rows, is below what the two or three launches of the other way cost, and where a run has so
+// few rows, on the average, that products of 256 rows are mostly empty.  Measured (8 kv heads
+// of 128; all at once / one by one, us): decode behind a shared prefix, 32 sequences behind 256
+// tokens (38 MB) 18.7 / 7.4, 4 behind 4096 (68 MB) 21.2 / 11.4, 16 behind 4096 (285 MB) 24.2 /
+// 26.9.  Rows per run: cross attention of 64 sequences to 512 .. 4096 keys, 1 row 124.6 / 121.1
+// (int8 pages 234 / 91), 2 rows 118.9 / 138.7 (247 / 145), 3 rows 119.5 / 189.6 (246 / 213), of
+// 512 to 200 .. 256 int8 keys, 4 rows 284 / 261; decode of 64 sequences behind 2000 tokens, 1 a
+// group 110.6 / 93.1 (218 / 73.4), 2 67.9 / 67.8 (120 / 69.5), 4 46.9 / 60.3 (69.7 / 68.7), of
+// 256 behind 200 to 600, 2 a group 92.5 / 68.7 (138 / 66).
 constexpr int64_t kOneByOneBytes = 192 << 20;       // as bf16
 
 bool one_by_one(const RowsArgs &a)
@@ -25,7 +28,8 @@ bool one_by_one(const RowsArgs &a)
     if (a.n_q_heads / a.dims.n_kv_heads > 8) return false;
     const char *impl = getenv("PKV_ROWS_IMPL");
     if (impl && (strcmp(impl, "one") == 0 || strcmp(impl, "all") == 0)) return impl[0] == 'o';
-    if (!a.ctx_lens && a.n_rows <= a.n_runs) return true;
+    const int64_t few = a.kv_dtype == PKV_KV_INT8 ? 3 : a.ctx_lens ? 2 : 1;
+    if (a.n_rows <= few * a.n_runs) return true;
     const int64_t tokens = (int64_t)(a.ctx_lens ? a.max_blocks : a.max_run_blocks) * a.dims.block_size;
     return tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows;
 }
