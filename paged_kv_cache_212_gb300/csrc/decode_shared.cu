@@ -5,7 +5,8 @@
 // programmatic dependent of the rows kernel, which lets it start as soon as its own CTAs run:
 // these units fill the SMs that the group's tiles leave to them.
 //
-// launch_rows_whole: a run's tokens and a row's own, each row by itself, in one launch.
+// launch_rows_whole: a run's tokens and a row's own, each row by itself, in one launch, for all
+// rows or for those of short runs.
 #include "decode_window.cuh"
 #include "../../include/pagedkv_batch.h"
 
@@ -44,7 +45,8 @@ WindowArgs window_args(const RowsArgs &r)
     a.max_run_blocks = r.max_run_blocks;
     a.n_rows = r.n_rows;
     a.part = r.partials;
-    a.after_rows = r.n_runs > 0;
+    a.after_rows = r.n_runs > 0 && r.few < kAllRows;
+    a.few = r.few;
     return a;
 }
 

@@ -95,6 +95,7 @@ struct WindowArgs {
     int32_t n_runs, max_run_blocks, n_rows;
     RowsPartials part;                 // kRest
     int32_t after_rows;
+    int32_t few;                       // rows of runs of more rows are not kWhole's but kRest's
 };
 
 // What a kernel does with runs: there are none; a row's own tokens alone, as a partial; a
@@ -269,11 +270,14 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + (S::kShared ? 0 : warp) * 2 * S::kRow;   // a step's K and V row
 
     grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
-    // (kRest behind the rows kernel, which has waited itself before it let this one start:
-    // all that is read was written before that.  One CTA waits at its end, so that the grid
-    // ends behind the rows kernel; if all did, those of the first round would keep the rest
-    // from starting)
-    if (RUNS != kRest || !a.after_rows) grid_dependency_wait();
+    // (Behind the rows kernel, which has waited itself before it let this one start, or behind
+    // another of these: all that is read was written before that.  One CTA waits at its end, so
+    // that the grid ends behind the rows kernel; if all did, those of the first round would keep
+    // the rest from starting.)
+    if (RUNS == kNoRuns || !a.after_rows) grid_dependency_wait();
+    auto wait_for_rows = [&]() {
+        if (RUNS != kNoRuns && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+    };
 
     // 1. the tiles
     const int32_t t_new = step ? __ldg(a.start_pos + s) : -1;
@@ -293,6 +297,12 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     if (RUNS == kWhole && blockIdx.x == 0)
         for (int32_t i = tid; i < a.n_runs; i += 32 * WARPS)
             if (!run_at(a.run_starts, a.run_lens, a.n_rows, a.max_run_blocks, bs, i).good) report(a.dev_status, PKV_DEV_BAD_LENGTH);
+    if (RUNS != kNoRuns && (RUNS == kWhole) != (run.rows <= a.few)) {       // the other launch's
+        if (RUNS == kRest && rank == 0 && tid < G)
+            a.part.own_stat[(int64_t)s * a.n_q_heads + h * G + tid] = make_float4(0.f, 0.f, __int_as_float(kDone), 0.f);
+        wait_for_rows();
+        return;
+    }
     const int n_workers = WARPS * a.splits, worker = rank * WARPS + warp;
 
     // 2. the warp's copies, which run ahead of its products by kStages - 1 tiles
@@ -774,7 +784,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             if (d == 0) c_stat[g] = make_float4(M, M2, sum, 0.f);
         }
     }
-    if (RUNS == kRest && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
+    wait_for_rows();
     if (a.splits == 1) return;
     cluster_sync_all();
     for (int i = rank * 32 * WARPS + tid; i < G * (D / 4); i += a.splits * 32 * WARPS) {

@@ -21,31 +21,40 @@ namespace {
 // 512 to 200 .. 256 int8 keys, 4 rows 284 / 261; decode of 64 sequences behind 2000 tokens, 1 a
 // group 110.6 / 93.1 (218 / 73.4), 2 67.9 / 67.8 (120 / 69.5), 4 46.9 / 60.3 (69.7 / 68.7), of
 // 256 behind 200 to 600, 2 a group 92.5 / 68.7 (138 / 66).
+//
+// As many rows as runs are a row each, as in a step.  Any other mean says little of single runs
+// (idle ones beside one of many rows), so there each run goes its own way: those of up to that
+// many rows one by one, beside the others at once.  Measured (so / all at once / one by one):
+// one of 64 sequences has 60 rows and 8192 keys 31.0 / 26.6 / 171, over int8 pages 36.5 / 33.7
+// / 216; one has 100 rows and 16384 int8 keys, 60 have one and 2048, 137 / 245 / 682; 64
+// sequences of one row, as above, 108 / 110 / 101 and 88 / 226 / 81.
 constexpr int64_t kOneByOneBytes = 192 << 20;       // as bf16
 
-bool one_by_one(const RowsArgs &a)
+// Runs of up to how many rows are attended row by row (-1: none).
+int32_t rows_one_by_one(const RowsArgs &a)
 {
-    if (a.n_q_heads / a.dims.n_kv_heads > 8) return false;
-    const char *impl = getenv("PKV_ROWS_IMPL");
-    if (impl && (strcmp(impl, "one") == 0 || strcmp(impl, "all") == 0)) return impl[0] == 'o';
-    const int64_t few = a.kv_dtype == PKV_KV_INT8 ? 3 : a.ctx_lens ? 2 : 1;
-    if (a.n_rows <= few * a.n_runs) return true;
+    if (a.n_q_heads / a.dims.n_kv_heads > 8) return -1;
+    const int32_t few = a.kv_dtype == PKV_KV_INT8 ? 3 : a.ctx_lens ? 2 : 1;
+    if (const char *impl = getenv("PKV_ROWS_IMPL")) {
+        if (strcmp(impl, "all") == 0) return -1;
+        if (strcmp(impl, "one") == 0) return kAllRows;
+        if (strcmp(impl, "both") == 0) return few;
+    }
     const int64_t tokens = (int64_t)(a.ctx_lens ? a.max_blocks : a.max_run_blocks) * a.dims.block_size;
-    return tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows;
+    if (tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows) return kAllRows;
+    if (a.n_rows == a.n_runs) return kAllRows;
+    return a.n_rows <= (int64_t)few * a.n_runs ? few : -1;
 }
 
-cudaError_t launch_rows(const RowsArgs &a, int num_sms, cudaStream_t stream)
+cudaError_t launch_rows(RowsArgs &a, int num_sms, cudaStream_t stream)
 {
-    if (one_by_one(a)) return launch_rows_whole(a, num_sms, stream);
-    if (a.n_runs > 0) {
-        const cudaError_t e = launch_rows_tc(a, num_sms, stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (a.ctx_lens) {
-        const cudaError_t e = launch_rows_rest(a, num_sms, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_rows_join(a, num_sms, stream);
+    a.few = rows_one_by_one(a);
+    if (a.few == kAllRows) return launch_rows_whole(a, num_sms, stream);
+    cudaError_t e = cudaSuccess;
+    if (a.n_runs > 0) e = launch_rows_tc(a, num_sms, stream);
+    if (e == cudaSuccess && a.few >= 0) e = launch_rows_whole(a, num_sms, stream);
+    if (e == cudaSuccess && a.ctx_lens) e = launch_rows_rest(a, num_sms, stream);
+    return e == cudaSuccess ? launch_rows_join(a, num_sms, stream) : e;
 }
 
 // Checks that the two calls share; fills what they share of *a.

@@ -19,11 +19,13 @@ constexpr int kUnitRows = 256;     // query head rows of a unit
 // (Threads hold neighbouring rows, so 8 values of each lie beside one another: with rows of
 // D values the 256 x D store of a unit took 4 us.)
 // A decode's own tokens: own_stat[row * Hq + head] (maximum, sum, as int bits where the row's
-// first query head lies in its unit, or -1 where no run is to be joined), own[row * Hq + head][D].
+// first query head lies in its unit, -1 where no run is to be joined or kDone where the outputs
+// are written by another launch), own[row * Hq + head][D].
 // cuts[cta]: the cut unit that begins in that CTA, the last one of its share.
 struct CutUnit {
     int32_t pos, pos_end, kvh, last_cta;   // last_cta 0: none
 };
+constexpr int kDone = -2;
 struct RowsPartials {
     float4 *stat;
     float *first;
@@ -77,6 +79,7 @@ struct RowsArgs {
     float *lse_out;
     RowsPartials partials;
     int32_t *dev_status;
+    int32_t few;                  // rows of runs of up to so many are attended one by one
 };
 
 // Run g's rows and keys, none of either where they are bad.
@@ -148,7 +151,9 @@ cudaError_t launch_rows_rest(const RowsArgs &a, int num_sms, cudaStream_t stream
 // Behind that: joins the partials.
 cudaError_t launch_rows_join(const RowsArgs &a, int num_sms, cudaStream_t stream);
 
-// All of it in one launch, each row by itself.
+// The rows of runs of up to a.few, all of a row in one launch, each by itself; beside the rows
+// kernel where there is one (a.few below kAllRows).
+constexpr int32_t kAllRows = 0x7fffffff;
 cudaError_t launch_rows_whole(const RowsArgs &a, int num_sms, cudaStream_t stream);
 
 }  // namespace pkv

@@ -90,6 +90,7 @@ struct RowsParams {
     int32_t *dev_status;
     int32_t wide_out;             // out is 32-byte aligned
     int32_t sms;
+    int32_t few;                  // runs of up to so many rows are another launch's
     float rest_weight;            // what a tile of a decode's own tokens costs an SM, in tiles of a run
     unsigned long long wait_ns;   // limit of the pipeline waits
 };
@@ -133,7 +134,9 @@ __device__ __forceinline__ int64_t places_of_run(const RowsParams &p, const Run 
 
 __device__ __forceinline__ Run run_of_params(const RowsParams &p, int32_t g)
 {
-    return run_at(p.starts, p.run_lens, p.n_rows, p.max_run_blocks, p.block_size, g);
+    Run r = run_at(p.starts, p.run_lens, p.n_rows, p.max_run_blocks, p.block_size, g);
+    if (r.rows <= p.few) r.rows = 0;
+    return r;
 }
 
 // The parts of a CTA's share, one after the other, in the registers of a warp: lane i holds
@@ -1046,6 +1049,7 @@ __global__ void __launch_bounds__(kTM) shared_join_kernel(const __grid_constant_
 #pragma unroll
     for (int k = 0; k < kCols / 8; ++k) load8(j.o + 8 * k, p.part.own + row * D + kCols * part + 8 * k);
     const int place = __float_as_int(own.z);
+    if (place == kDone) return;
     if (place >= 0) {
         load_first<D>(p, kvh, i, part, x);
         join_piece(j, stat.x, stat.y, x);
@@ -1088,6 +1092,7 @@ RowsParams params_of(const RowsArgs &a, int num_sms)
     p.dev_status = a.dev_status;
     p.wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     p.sms = num_sms;
+    p.few = a.few;
     p.rest_weight = a.kv_dtype == PKV_KV_INT8 ? kRestWeightInt8 : kRestWeight;
     p.wait_ns = pipeline_wait_ns();
     return p;

@@ -22,9 +22,9 @@ def P():
     return P
 
 
-@pytest.fixture(params=["all", "one", "auto"])
+@pytest.fixture(params=["all", "one", "both", "auto"])
 def rows_impl(request, monkeypatch):
-    """Rows contracted all at once or one by one (PKV_ROWS_IMPL), and as the sizes say."""
+    """Rows contracted all at once, one by one or each run its own way (PKV_ROWS_IMPL), and as the sizes say."""
     if request.param == "auto":
         monkeypatch.delenv("PKV_ROWS_IMPL", raising=False)
     else:
