@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                 const int64_t row = (int64_t)pos * p.n_q_heads + w.kvh * G + r % G;
                 const bool whole = !p.ctx_lens && !w.cut;
                 if (whole) {
-                    const float inv = l > 0.f ? unit_o / l : 0.f;
+                    const float inv = l == 0.f ? 0.f : unit_o / l;      // (a NaN stays one)
                     __nv_bfloat16 *out = p.out + row * D;
 #pragma unroll 1
                     for (int i = 0; i < D / 32; ++i) {
@@ -982,17 +982,18 @@ __device__ __forceinline__ void join_pieces(const RowsParams &p, Joined &j, int3
     }
 }
 
-// The columns of a row, o / l rounded once, and its log-sum-exp; no key seen: 0 and -inf.
+// The columns of a row, o / l rounded once, and its log-sum-exp; no key seen: 0 and -inf.  (A sum
+// that is no number, from a NaN or an infinity among what the row sees, passes on to both.)
 template <int D>
 __device__ __forceinline__ void write_joined(const RowsParams &p, const Joined &j, int64_t row, int part)
 {
-    const float inv = j.l > 0.f ? 1.f / j.l : 0.f;
+    const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
     uint4 *out = reinterpret_cast<uint4 *>(p.out + row * D + kCols * part);
 #pragma unroll
     for (int k = 0; k < kCols / 8; ++k)
         out[k] = make_uint4(pack_bf16x2(j.o[8 * k] * inv, j.o[8 * k + 1] * inv), pack_bf16x2(j.o[8 * k + 2] * inv, j.o[8 * k + 3] * inv),
                             pack_bf16x2(j.o[8 * k + 4] * inv, j.o[8 * k + 5] * inv), pack_bf16x2(j.o[8 * k + 6] * inv, j.o[8 * k + 7] * inv));
-    if (part == 0 && p.lse_out) p.lse_out[row] = j.l > 0.f ? (j.m + __log2f(j.l)) * 0.69314718055994531f : -INFINITY;
+    if (part == 0 && p.lse_out) p.lse_out[row] = j.l == 0.f ? -INFINITY : (j.m + __log2f(j.l)) * 0.69314718055994531f;
 }
 
 // A cross attention: the cut unit that begins in CTA blockIdx.x; the last blockIdx.y writes the

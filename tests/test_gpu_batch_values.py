@@ -1,0 +1,86 @@
+"""The calls for ragged batches over values that are no numbers, that a sequence must not see, or
+whose scales are far apart."""
+import pytest
+import torch
+
+from batch_reference import Paged, check_rows
+from test_gpu_batch import P, _ints, _shared_case, _status, rows_impl      # noqa: F401 - fixtures
+
+pytestmark = pytest.mark.gpu
+
+
+def _rows_of(table, first, stop, bs):
+    t = torch.arange(first, stop)
+    return table[t // bs].long() * bs + t % bs
+
+
+# ---- NaN that a row sees -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("keys", [[40, 128, 100], [1000, 40, 3100]])       # runs of one tile, and runs that CTAs share
+@pytest.mark.parametrize("where", ["query", "key", "value"])
+def test_cross_passes_nan_on(P, int8, keys, where, rows_impl):     # noqa: F811
+    """A NaN in a query, a key or a value makes NaN of what it reaches, and of nothing else."""
+    hkv, group, d, bs, scale, n_q = 2, 3, 64, 16, 0.125, [50, 3, 90]
+    pages = Paged(7, sum(-(-x // bs) for x in keys) + 1, hkv, d, bs, int8)
+    added = [pages.add(0, x, max(-(-y // bs) for y in keys)) for x in keys]
+    starts = [0, 50, 53, 143]
+    q = torch.randn((143, hkv * group, d), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16)
+    bad = torch.zeros((143, hkv * group, d), dtype=torch.bool)          # outputs that are no numbers
+    bad_lse = torch.zeros((143, hkv * group), dtype=torch.bool)
+    if where == "query":
+        for row, head in ((0, 0), (49, 5), (51, 2), (53, 3), (142, 4)):
+            q[row, head, (row * 7) % d] = float("nan")
+            bad[row, head] = bad_lse[row, head] = True
+    else:
+        # a key or value of each sequence's second kv head (int8: its scale), in the last token
+        for s, x in enumerate(keys):
+            at = _rows_of(added[s][0], x - 1, x, bs)
+            if int8:
+                pages.scales[where == "value"].view(-1, hkv)[at, 1] = float("nan")
+            else:
+                pages.pools[where == "value"].view(-1, hkv, d)[at, 1, 5] = float("nan")
+        if where == "key":
+            bad[:, group:] = bad_lse[:, group:] = True
+        elif int8:
+            bad[:, group:] = True
+        else:
+            bad[:, group:, 5] = True
+    kp, vp, ks, vs = pages.cuda()
+    lse, st = torch.full((143, hkv * group), 7.0, device="cuda"), _status()
+    out = P.paged_cross_attention(q.cuda(), _ints(starts), kp, vp, torch.stack([t for t, _ in added]).cuda(), _ints(keys), scale,
+                                  k_scales=ks, v_scales=vs, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    assert torch.equal(out.cpu().isnan(), bad) and torch.equal(lse.cpu().isnan(), bad_lse)
+    # the others are right: beside the NaN, whose places take the values without it
+    clean = q.nan_to_num(0.0)
+    for s in range(3):
+        a, b = starts[s], starts[s + 1]
+        o, ls = out[a:b].cpu().clone(), lse[a:b].cpu().clone()
+        k, v = (x.nan_to_num(0.0) for x in added[s][1])
+        sc = torch.einsum("mhgd,nhd->mhgn", clean[a:b].double().view(b - a, hkv, group, d), k) * scale
+        ref = torch.einsum("mhgn,nhd->mhgd", torch.softmax(sc, -1), v).reshape(b - a, hkv * group, d)
+        o = torch.where(bad[a:b], ref.to(torch.bfloat16), o)
+        ls = torch.where(bad_lse[a:b], torch.logsumexp(sc, -1).reshape(b - a, -1).float(), ls)
+        check_rows(o, ls, clean[a:b], k, v, scale, int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_shared_passes_nan_on(P, int8, rows_impl):     # noqa: F811
+    """The same behind a prefix: a NaN query, in a sequence of a long and of a short group."""
+    hkv, group, d, bs, scale = 2, 4, 128, 16, 0.09
+    pages, tables, ctx, starts, ptables, values = _shared_case([20, 1], [2500, 60], [i % 5 for i in range(21)], 1, hkv, d, bs, int8, 6)
+    kp, vp, ks, vs = pages.cuda()
+    q = torch.randn((22, hkv * group, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    bad = torch.zeros((22, hkv * group), dtype=torch.bool)
+    for s, head in ((0, 1), (1, 0), (7, 7), (21, 3)):
+        q[s, head, 9] = float("nan")
+        bad[s, head] = True
+    lse, st = torch.full((22, hkv * group), 7.0, device="cuda"), _status()
+    out = P.paged_decode_attention_shared(q.cuda(), kp, vp, tables.cuda(), _ints(ctx), _ints(starts), ptables.cuda(), _ints([2500, 60]),
+                                          scale, k_scales=ks, v_scales=vs, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    assert torch.equal(out.cpu().isnan(), bad[..., None].expand(out.shape)) and torch.equal(lse.cpu().isnan(), bad)
+    for s in range(22):
+        if not bad[s].any():
+            check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, int8)
