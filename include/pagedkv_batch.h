@@ -138,7 +138,9 @@ int paged_cross_attention(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads
  *   q (with q_stride), pools, scales, out, lse_out, workspace  as above
  * Sequence s of group g sees tokens 0 .. min(ctx_lens[s], prefix_lens[g]) - 1
  * of the group and prefix_lens[g] .. ctx_lens[s] - 1 of its own; the outputs
- * are paged_decode_attention's over the two one behind the other.  n_q_heads /
+ * are paged_decode_attention's over the two one behind the other.  A sequence
+ * that ends within the prefix is attended by itself; what the tokens behind its
+ * end hold (pages that are not written yet, say) does not reach it.  n_q_heads /
  * n_kv_heads in 1 .. 8, any number of kv heads for int8 pages too.
  * ctx_lens[s] == 0 gives o = 0 and lse = -inf; so do a bad length of the
  * sequence or of its group (PKV_DEV_BAD_LENGTH).  Bad starts and block ids as

@@ -98,8 +98,9 @@ struct WindowArgs {
     int32_t few;                       // rows of runs of more rows are not kWhole's but kRest's
 };
 
-// What a kernel does with runs: there are none; a row's own tokens alone, as a partial; a
-// run's tokens and then a row's own (a cross attention, which has no ctx_lens: no own ones).
+// What a kernel does with runs: there are none; a row's own tokens alone (those of the run too
+// where the row ends within them), as a partial; a run's tokens and then a row's own (a cross
+// attention, which has no ctx_lens: no own ones).
 enum { kNoRuns, kRest, kWhole };
 
 template <int D, bool INT8>
@@ -292,8 +293,12 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     const Seen all(a, len);
     if (tid == 0 && h == 0 && rank == 0 && len != all.L) report(a.dev_status, PKV_DEV_BAD_LENGTH);
     const int32_t L = RUNS == kNoRuns ? all.L : !run.good ? 0 : RUNS == kWhole && !a.ctx_lens ? run.len : all.L;
-    const Seen seen = RUNS == kNoRuns ? all : Seen(RUNS == kWhole ? min(run.len, L) : 0, min(run.len, L), L);
-    const int32_t *run_row = RUNS == kWhole ? a.run_tables + (int64_t)g_run * a.max_run_blocks : nullptr;
+    // (kRest: a row that ends within its run's tokens sees those below its end here, by itself: the
+    // rows kernel's products take all tokens of a run, and 0 times what a row must not see is not 0
+    // where that is not finite)
+    const bool within = RUNS == kWhole || (RUNS == kRest && L < run.len);
+    const Seen seen = RUNS == kNoRuns ? all : Seen(within ? min(run.len, L) : 0, min(run.len, L), L);
+    const int32_t *run_row = RUNS == kNoRuns ? nullptr : a.run_tables + (int64_t)g_run * a.max_run_blocks;
     if (RUNS == kWhole && blockIdx.x == 0)
         for (int32_t i = tid; i < a.n_runs; i += 32 * WARPS)
             if (!run_at(a.run_starts, a.run_lens, a.n_rows, a.max_run_blocks, bs, i).good) report(a.dev_status, PKV_DEV_BAD_LENGTH);
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         const uint32_t blk = a.tiles_per_block == 1 ? at : __umulhi(at, a.block_magic);
         a_token = (int32_t)at * kTile;
         a_off = (int32_t)(at - blk * a.tiles_per_block) * kTile;
-        a_run = RUNS == kWhole && a_tile < seen.n_first;
+        a_run = RUNS != kNoRuns && a_tile < seen.n_first;
         id = RUNS == kNoRuns ? __ldg(trow + blk) : __ldcg((a_run ? run_row : trow) + blk);
     };
     look_up();
@@ -755,7 +760,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             *reinterpret_cast<float4 *>(a.part.own + (head0 + g) * D + d) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
             if (d == 0) {
                 const int tile = kUnitRows / 2 / G, in = (s - run.row0) % (2 * tile);
-                const int place = run.len > 0 && L > 0 ? in / tile * (kUnitRows / 2) + in % tile * G : -1;
+                const int place = run.len > 0 && L >= run.len ? in / tile * (kUnitRows / 2) + in % tile * G : -1;
                 a.part.own_stat[head0 + g] = make_float4(M, sum, __int_as_float(place), 0.f);
             }
             return;

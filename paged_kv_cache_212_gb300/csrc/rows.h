@@ -61,7 +61,8 @@ inline RowsPartials carve_rows_workspace(void *ws, int64_t n_rows, int32_t n_q_h
 // starts[g] .. starts[g + 1] - 1 are run g's; all of them see its keys 0 .. run_lens[g] - 1
 // at run_tables[g].  In a decode (ctx_lens not null) row s is a sequence, which sees of its
 // run's keys those below ctx_lens[s], and goes on with keys run_lens[g] .. ctx_lens[s] - 1
-// of its own at tables[s].
+// of its own at tables[s].  Sequences that end before their run does (ctx_lens[s] < run_lens[g])
+// are attended one by one, as they see other keys than the rest.
 struct RowsArgs {
     const void *q;
     int64_t q_stride;

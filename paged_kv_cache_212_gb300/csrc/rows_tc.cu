@@ -81,7 +81,7 @@ struct RowsParams {
     int32_t pool_rows;            // (n_blocks + 1) * block_size: an out-of-range TMA row
     const int32_t *starts, *run_tables, *run_lens;
     int32_t n_runs, max_run_blocks;
-    const int32_t *ctx_lens;      // decode: a row sees keys below its own; else null
+    const int32_t *ctx_lens;      // decode: rows that end before their run does are not this kernel's; else null
     float scale_log2;
     __nv_bfloat16 *out;
     float *lse_out;
@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
             const volatile Unit &w = unit_s[units & 3];
             int n_kt = 1;                        // read with the unit's first tile
             bool live = false, warp_live = false;
-            int32_t pos = 0, limit = 0;
+            int32_t pos = 0;
             float m = -INFINITY, l = 0.f;
             int exponent = 0;                    // int8: O is in units of 2^exponent
             for (int j = 0; j < n_kt; ++j, ++c) {
@@ -773,9 +773,10 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     n_kt = w.n_kt;
                     more = !w.last;
                     pos = w.pos + qt * pos_per_tile + r / G;
+                    // (every live row sees all keys of the run: a masked score would leave 0 times a
+                    // value, and over int8 pages its scale, in the row's sums)
                     live = r < pos_per_tile * G && pos < w.pos_end;
-                    limit = w.len;
-                    if (live && p.ctx_lens) limit = min(limit, max(__ldcg(p.ctx_lens + pos), 0));
+                    if (live && p.ctx_lens) live = __ldcg(p.ctx_lens + pos) >= w.len;
                     warp_live = __any_sync(0xffffffffu, live);
                 }
                 const int32_t key0 = (w.t0 + j) * kTN, tail = w.len - key0;
@@ -801,12 +802,11 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                             sv[i + 3] = __float_as_uint(b.y);
                         }
                     }
-                    // rows whose keys in this tile are all visible need no per-key test
-                    if (__any_sync(0xffffffffu, limit - key0 < kTN)) {
+                    if (tail < kTN) {            // the run ends in this tile
 #pragma unroll
                         for (int i0 = 0; i0 < kTN; i0 += 32) {
-                            const uint32_t seen = bits_below(limit - key0 - i0);
-                            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+                            const uint32_t seen = bits_below(tail - i0);
+                            if (seen == 0xffffffffu) continue;
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
                                 if (!((seen >> i) & 1)) sv[i0 + i] = __float_as_uint(-INFINITY);

@@ -14,6 +14,38 @@ def _rows_of(table, first, stop, bs):
     return table[t // bs].long() * bs + t % bs
 
 
+# ---- tokens behind a sequence's end, within its group's prefix ---------------------------------
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 8)])
+@pytest.mark.parametrize("seen", [False, True])
+def test_shared_tokens_behind_a_sequence_are_not_seen(P, int8, d, group, seen, rows_impl):     # noqa: F811
+    """Tokens of a prefix that are not written yet (NaN, infinities, scales of any size) reach none of
+    the sequences that end before them, whether another one of the group sees them or not."""
+    hkv, bs, scale, end, prefix = 2, 16, d ** -0.5, 650, 700
+    pages, tables, ctx, starts, ptables, values = _shared_case([9, 5], [prefix, 300], [20] * 14, 0, hkv, d, bs, int8, 4)
+    ctx[:9] = [0, 1, 127, 128, 129, 640, end - 1, end, prefix + 20 if seen else 500]
+    rows = _rows_of(ptables[0], end, prefix, bs)
+    for which in range(2):
+        if int8:
+            s = pages.scales[which].view(-1, hkv)
+            s[rows[:20]], s[rows[20:30]], s[rows[30:]] = 1e30, float("nan"), float("inf")
+        else:
+            v = pages.pools[which].view(-1, hkv, d)
+            v[rows[:20]], v[rows[20:]] = float("inf"), float("nan")
+    kp, vp, ks, vs = pages.cuda()
+    q = torch.randn((14, hkv * group, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    lse, st = torch.full((14, hkv * group), 7.0, device="cuda"), _status()
+    out = P.paged_decode_attention_shared(q, kp, vp, tables.cuda(), _ints(ctx), _ints(starts), ptables.cuda(), _ints([prefix, 300]),
+                                          scale, k_scales=ks, v_scales=vs, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    for s in range(14):
+        if s == 8 and seen:
+            assert out[s].isnan().all() and lse[s].isnan().all()
+        else:
+            check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *(v[:ctx[s]] for v in values[s]), scale, int8)
+
+
 # ---- NaN that a row sees -------------------------------------------------------------------------
 
 @pytest.mark.parametrize("int8", [False, True])
