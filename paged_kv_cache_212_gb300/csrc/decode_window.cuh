@@ -270,12 +270,20 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     uint8_t *my_ring = ring + (size_t)warp * S::kStages * S::kStage;
     uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + (S::kShared ? 0 : warp) * 2 * S::kRow;   // a step's K and V row
 
-    grid_dependents_launch();   // a programmatic dependent: nothing is read before the wait
-    // (Behind the rows kernel, which has waited itself before it let this one start, or behind
-    // another of these: all that is read was written before that.  One CTA waits at its end, so
-    // that the grid ends behind the rows kernel; if all did, those of the first round would keep
-    // the rest from starting.)
-    if (RUNS == kNoRuns || !a.after_rows) grid_dependency_wait();
+    // A programmatic dependent: nothing is read before the wait.  (Behind the rows kernel, which
+    // has waited itself before it let this one start, or behind another of these, all that is read
+    // was written and complete before that.  An SM's L1 may still have what an earlier kernel found,
+    // so it is read past that, but for the scales of int8 pages: copies of 4 bytes pass through the
+    // L1, which the fence empties.  One CTA waits at its end, so that the grid ends behind the rows
+    // kernel; if all did, those of the first round would keep the rest from starting.  Measured: 96
+    // sequences in two groups over int8 pages 59.4 us without the fence, 60.6 with it, 65.3 with
+    // scales that pass through registers; 64 behind one prefix over bf16 pages 33.2 with queries
+    // from the L1, 34.5 past it, 35.6 with a fence in its place.)
+    grid_dependents_launch();
+    if (RUNS == kNoRuns || !a.after_rows)
+        grid_dependency_wait();
+    else if (INT8)
+        asm volatile("fence.acq_rel.gpu;" ::: "memory");
     auto wait_for_rows = [&]() {
         if (RUNS != kNoRuns && a.after_rows && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
     };
@@ -408,8 +416,8 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
             x0[i] = x1[i] = make_uint4(0, 0, 0, 0);
             if (src) {
                 const uint4 *at = reinterpret_cast<const uint4 *>(src);
-                x0[i] = RUNS == kNoRuns ? __ldg(at + v0) : at[v0];
-                x1[i] = RUNS == kNoRuns ? __ldg(at + v1) : at[v1];
+                x0[i] = RUNS == kNoRuns ? __ldg(at + v0) : __ldcg(at + v0);
+                x1[i] = RUNS == kNoRuns ? __ldg(at + v1) : __ldcg(at + v1);
             }
         }
         float c[8], sn[8];

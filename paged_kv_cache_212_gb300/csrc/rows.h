@@ -25,6 +25,7 @@ constexpr int kUnitRows = 256;     // query head rows of a unit
 struct CutUnit {
     int32_t pos, pos_end, kvh, last_cta;   // last_cta 0: none
 };
+static_assert(sizeof(CutUnit) == 16, "read as one vector");
 constexpr int kDone = -2;
 struct RowsPartials {
     float4 *stat;

@@ -1015,14 +1015,15 @@ __global__ void __launch_bounds__(kTM) rows_join_kernel(const __grid_constant__ 
         }
         return;
     }
-    const CutUnit u = p.part.cuts[blockIdx.x];
+    const int4 c = __ldcg(reinterpret_cast<const int4 *>(p.part.cuts + blockIdx.x));
+    const CutUnit u{c.x, c.y, c.z, c.w};
     if (u.last_cta == 0) return;
     const int part = (int)blockIdx.y % (D / kCols), qt = (int)blockIdx.y / (D / kCols), r = threadIdx.x;
     const int G = p.group, tile = kTM / G;
     const int32_t pos = u.pos + qt * tile + r / G, head = u.kvh * G + r % G;
     if (r >= tile * G || pos >= u.pos_end) return;
     const int64_t row = (int64_t)pos * p.n_q_heads + head;
-    const float4 stat = p.part.stat[row];
+    const float4 stat = __ldcg(p.part.stat + row);
     Joined j;
     j.m = stat.x;
     j.l = stat.y;
