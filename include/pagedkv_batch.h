@@ -110,9 +110,12 @@ size_t pkv_rows_workspace_bytes(int32_t n_rows, int32_t n_q_heads, int32_t head_
  * Starts that decrease or pass n_rows: PKV_DEV_BAD_LENGTH, outputs undefined.
  * Rows are contracted all at once, up to 256 of a sequence in one product, or,
  * where that is less work, one by one, with up to 8 query heads per kv head (the
- * same results within the tolerances).  PKV_ROWS_IMPL in the environment, read at
- * every call here and in paged_decode_attention_shared, takes a way: all, one, or
- * both (sequences or groups of few rows one by one, the others at once).
+ * same results within the tolerances).  A call of as many rows as sequences is
+ * taken for a step, of a row each, and goes one by one; where most of the rows
+ * are a few sequences', one row more (of no sequence) sends those at once.
+ * PKV_ROWS_IMPL in the environment, read at every call here and in
+ * paged_decode_attention_shared, takes a way: all, one, or both (sequences or
+ * groups of few rows one by one, the others at once).
  */
 int paged_cross_attention(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, const int32_t *q_starts,
                           int32_t n_rows, const void *k_pool, const void *v_pool, const float *k_scales,

@@ -22,12 +22,16 @@ namespace {
 // group 110.6 / 93.1 (218 / 73.4), 2 67.9 / 67.8 (120 / 69.5), 4 46.9 / 60.3 (69.7 / 68.7), of
 // 256 behind 200 to 600, 2 a group 92.5 / 68.7 (138 / 66).
 //
-// As many rows as runs are a row each, as in a step.  Any other mean says little of single runs
-// (idle ones beside one of many rows), so there each run goes its own way: those of up to that
-// many rows one by one, beside the others at once.  Measured (so / all at once / one by one):
-// one of 64 sequences has 60 rows and 8192 keys 31.0 / 26.6 / 171, over int8 pages 36.5 / 33.7
-// / 216; one has 100 rows and 16384 int8 keys, 60 have one and 2048, 137 / 245 / 682; 64
-// sequences of one row, as above, 108 / 110 / 101 and 88 / 226 / 81.
+// The mean says little of single runs (idle ones beside one of many rows), so each run goes its
+// own way: those of up to that many rows one by one, beside the others at once.  Measured (so /
+// all at once / one by one): one of 64 sequences has 60 rows and 8192 keys 31.0 / 26.6 / 171, over
+// int8 pages 36.5 / 33.7 / 216; one has 100 rows and 16384 int8 keys, 60 have one and 2048, 137 /
+// 245 / 682; 64 sequences of one row, as above, 110 / 111 / 104 and 91 / 256 / 83.  A cross
+// attention of as many rows as sequences is taken for a step, whose sequences have a row each, and
+// spared those 6 us (where 60 of 64 rows are one sequence's: 41 / 27 / 171).  Not a decode: room
+// for as many groups as sequences is the fixed shape of a captured step, whatever the groups hold.
+// 64 sequences with room for 64 groups, all in one of 4096 tokens 38.6 / 32.4 / 103, over int8
+// pages 44 / 32 / 128; a group of 2000 each 112 / 117 / 106 and 90 / 235 / 80.
 constexpr int64_t kOneByOneBytes = 192 << 20;       // as bf16
 
 // Runs of up to how many rows are attended row by row (-1: none).
@@ -42,7 +46,7 @@ int32_t rows_one_by_one(const RowsArgs &a)
     }
     const int64_t tokens = (int64_t)(a.ctx_lens ? a.max_blocks : a.max_run_blocks) * a.dims.block_size;
     if (tokens * a.dims.n_kv_heads * a.dims.head_dim * 4 <= kOneByOneBytes / a.n_rows) return kAllRows;
-    if (a.n_rows == a.n_runs) return kAllRows;
+    if (!a.ctx_lens && a.n_rows == a.n_runs) return kAllRows;
     return a.n_rows <= (int64_t)few * a.n_runs ? few : -1;
 }
 

@@ -116,3 +116,31 @@ def test_shared_passes_nan_on(P, int8, rows_impl):     # noqa: F811
     for s in range(22):
         if not bad[s].any():
             check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, int8)
+
+
+# ---- the way that a call takes ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_as_many_groups_as_sequences_do_not_mean_one_each(P, int8, monkeypatch):     # noqa: F811
+    """64 sequences and room for 64 groups, 58 sequences in one of them: those go at once, as with
+    room for one group more."""
+    hkv, group, d, bs, scale = 8, 4, 128, 16, 0.09
+    sizes, prefixes = [1] * 6 + [58] + [0] * 57, [100] * 6 + [3000] + [16] * 57
+    pages, tables, ctx, starts, ptables, values = _shared_case(sizes, prefixes, [i % 7 for i in range(64)], 0, hkv, d, bs, int8, 5)
+    kp, vp, ks, vs = pages.cuda()
+    wide = torch.zeros((64, 256), dtype=torch.int32)
+    wide[:, :tables.shape[1]] = tables
+    args = (kp, vp, wide.cuda(), _ints(ctx), _ints(starts), ptables.cuda(), _ints(prefixes), scale)
+    q = torch.randn((64, hkv * group, d), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    outs = []
+    for impl in (None, "both", "one"):
+        if impl:
+            monkeypatch.setenv("PKV_ROWS_IMPL", impl)
+        else:
+            monkeypatch.delenv("PKV_ROWS_IMPL", raising=False)
+        lse = torch.empty((64, hkv * group), device="cuda")
+        outs.append(P.paged_decode_attention_shared(q, *args, k_scales=ks, v_scales=vs, lse_out=lse))
+        for s in range(64):
+            check_rows(outs[-1][s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, int8)
+    assert torch.equal(outs[0], outs[1])
+    assert not torch.equal(outs[0], outs[2])       # (probabilities are rounded in other places)
