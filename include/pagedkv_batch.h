@@ -51,7 +51,12 @@ extern "C" {
  * that) or names an id outside [0, n_blocks) (PKV_DEV_BAD_BLOCK_ID), the entry
  * is the scratch id and the block's tokens have slot -1; so have the tokens
  * that fall into a held block whose id is outside [0, n_blocks]
- * (PKV_DEV_BAD_BLOCK_ID).  When the batch has more than n_tokens tokens, those
+ * (PKV_DEV_BAD_BLOCK_ID), or that is the scratch block in a row which begins with
+ * another one (PKV_DEV_OUT_OF_BLOCKS: an earlier step found no block for it, and
+ * the caller has not put one in its place).  A row that begins with the scratch
+ * block is an inactive sequence's: its tokens have slots in the scratch block,
+ * and a sequence that found no block for its first tokens is one until the
+ * caller has given it some.  When the batch has more than n_tokens tokens, those
  * behind them are in no map (PKV_DEV_BAD_POSITION).  Sums that pass 2^31 - 1
  * are written as that.  block_size is a multiple of 16, at most 256.  Outputs
  * must not overlap inputs (lens is not ctx_lens, cursor not cursor_out).
@@ -69,7 +74,8 @@ int paged_step_maps(const int32_t *lens, const int32_t *n_new, int32_t n_seqs, c
  *   k_new, v_new  bf16, n_kv_heads rows of head_dim behind one another per
  *            row, k_stride / v_stride elements apart (a multiple of 8, at least
  *            a row's length: they may be parts of a fused projection's rows)
- *   slots    int64 [n_rows]; distinct where they are not negative
+ *   slots    int64 [n_rows]; distinct where they are not negative and not of the
+ *            scratch block (what rows with the same slot leave there is any of theirs)
  * A row of a negative slot is skipped; one of a slot outside the pool
  * (>= (n_blocks + 1) * block_size) too, with PKV_DEV_BAD_POSITION.
  * n_rows == 0 is a no-op.

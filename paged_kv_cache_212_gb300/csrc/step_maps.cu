@@ -180,8 +180,11 @@ __global__ void __launch_bounds__(kThreads) step_maps_kernel(const MapArgs a)
             int32_t b;
             if (at < held) {
                 b = __ldcg(a.tables + (int64_t)s * a.max_blocks + at);   // (no old copy of a line that others write stays in the L1)
-                if (b < 0 || b > a.n_blocks) {
-                    report(a.dev_status, PKV_DEV_BAD_BLOCK_ID);
+                // (a scratch block in a row that begins with another one is not an inactive sequence's:
+                // an earlier step found no block for it)
+                const bool none = b == a.n_blocks && __ldcg(a.tables + (int64_t)s * a.max_blocks) != b;
+                if (b < 0 || b > a.n_blocks || none) {
+                    report(a.dev_status, none ? PKV_DEV_OUT_OF_BLOCKS : PKV_DEV_BAD_BLOCK_ID);
                     b = -1;
                 }
             } else {

@@ -84,3 +84,33 @@ def test_steps_that_read_what_the_kernel_before_them_writes(P, int8, d, group, r
         for i in range(steps):
             check_rows(outs[0][i, s:s + 1], outs[1][i, s:s + 1], all_q[i, s:s + 1], *(x[:prefixes[g] + i + 1] for x in both), scale, int8)
             check_rows(outs[2][i, s:s + 1], outs[3][i, s:s + 1], all_q[i, s:s + 1], *shared[g][1], scale, int8)
+
+
+def test_maps_of_a_step_behind_one_that_ran_out(P):     # noqa: F811
+    """A sequence that found no block gets no slots in the step after that either, until it is given
+    one; an inactive sequence, whose row is all scratch, writes to the scratch block."""
+    bs, scratch = 16, 50
+    tables = torch.full((5, 4), scratch, dtype=torch.int32)
+    tables[:4, 0] = torch.tensor([7, 8, 9, 10])
+    tables = tables.cuda()
+    lens, free, cursor = _ints([16, 16, 16, 3, 5]), _ints([3]), _ints([0])
+
+    def step(lens, cursor, new):
+        st = _status()
+        m = P.paged_step_maps(lens, _ints(new), free, tables, bs, scratch, sum(new), cursor=cursor, dev_status=st)
+        return m, m.slots.tolist(), int(st.item())
+
+    m, slots, status = step(lens, cursor, [3, 3, 20, 1, 1])     # the second and third sequence find no block
+    assert slots == [48, 49, 50] + [-1] * 23 + [163, 805] and status == P.DEV_OUT_OF_BLOCKS
+    assert tables.tolist() == [[7, 3, 50, 50], [8, 50, 50, 50], [9, 50, 50, 50], [10, 50, 50, 50], [50] * 4]
+    m, slots, status = step(m.ctx_lens, m.cursor, [1] * 5)
+    assert slots == [51, -1, -1, 164, 806] and status == P.DEV_OUT_OF_BLOCKS
+    assert m.positions.tolist() == [19, 19, 36, 4, 6] and m.ctx_lens.tolist() == [20, 20, 37, 5, 7]
+    tables[1, 1], tables[2, 1], tables[2, 2] = 20, 21, 22
+    m, slots, status = step(m.ctx_lens, m.cursor, [1] * 5)
+    assert slots == [52, 20 * 16 + 4, 22 * 16 + 5, 165, 807] and status == 0
+    # the scratch block takes the rows of idle sequences, whatever they are
+    k, v = (torch.randn((5, 2, 64), device="cuda").to(torch.bfloat16) for _ in range(2))
+    pools = [torch.zeros((scratch + 1, bs, 2, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    P.paged_kv_write_slots(k, v, *pools, m.slots)
+    assert torch.equal(pools[0].view(-1, 2, 64)[m.slots], k)
