@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     constexpr int32_t kFirstTile = 1, kLastTile = 2;        // of a part, of the share
     static_assert(2 + (INT8 ? 3 : 2) * (NK + NV) + kScaleTiles + 3 * kNQ + 3 <= kBars && 4 * sizeof(Unit) <= 256, "their room");
     __shared__ int64_t warp_sum[kThreads / 32], warp_rest[kThreads / 32];
+    __shared__ int32_t issued_s[2];                         // tiles that the K producers issued
     __shared__ CutUnit cut_s;                               // the last unit, where it goes on in the next CTA
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
         cut_s.last_cta = 0;
+        issued_s[0] = issued_s[1] = 0;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -614,12 +616,16 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
                 }
             }
-            // every copy this warp issued has landed before the CTA can exit
+            // every copy this warp issued has landed before the CTA can exit (K's: all that is
+            // issued is contracted, or settle_pair waits for it below)
             if (INT8) asm volatile("cp.async.wait_all;" ::: "memory");
             if (lane == 0) {
                 if (warp == 8 && q_loads > 0) (void)mbar_wait(q_full, (q_loads - 1) & 1);
-                for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i)
-                    (void)mbar_wait(&full[i % NSL], (i / NSL) & 1);
+                if (is_v) {
+                    for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i) (void)mbar_wait(&full[i % NSL], (i / NSL) & 1);
+                } else {
+                    issued_s[warp == 10] = issued;
+                }
             }
         } else {
             // ===================== MMA issuer =====================
@@ -914,6 +920,7 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) p.part.cuts[blockIdx.x] = cut_s;
+    if (*abort_flag && (warp == 8 || warp == 10) && lane == 0) settle_pair(issued_s[warp == 10], issued_s[warp != 10], k_codes, NK);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

@@ -45,6 +45,23 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     }
 }
 
+// After a wait that ran out: the copies of two warps that fill a ring of K, half a slot each
+// (full[] counts both arrivals), have landed when this returns; asked by a lane of each, behind a
+// barrier of the CTA that both came to, with the tiles that it has issued and the other one has.
+// Where one of them left early, it has not arrived at slots that the other one's copies are on
+// their way into, and a wait for those would run its 4 s for each of them.  So whoever is ahead,
+// by the ring at most, arrives there in its place.  (A slot's copies wait for its last use, which
+// waited for both arrivals, so that each of these slots is in the phase that only that arrival is
+// missing from; and what is further back than the ring, seen from whoever is ahead, has landed.)
+static __device__ __noinline__ void settle_pair(int issued, int other, uint64_t *full, int slots)
+{
+    const int ahead = max(issued, other);
+#pragma unroll 1
+    for (int i = other; i < issued; ++i) mbar_arrive(&full[i % slots]);
+#pragma unroll 1
+    for (int i = max(ahead - slots, 0); i < issued; ++i) (void)mbar_wait(&full[i % slots], (i / slots) & 1);
+}
+
 // ---- products issued by one lane of a converged warp ----------------------------
 // The issuing warp runs as a whole and the instructions carry the elected lane's
 // predicate, so that the compiler keeps descriptors and addresses in uniform
