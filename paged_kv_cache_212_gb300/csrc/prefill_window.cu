@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     // Half units: a warp of one softmax warpgroup meets the one with the same rows of the
     // other; their maxima and sums go through the second Q tile, which a half unit leaves.
     __shared__ uint64_t pair_bar[4];
+    __shared__ int32_t issued_s[2];                         // tiles that the K producers issued
     float *pair_s = reinterpret_cast<float *>(q_s + kQTile);   // [2][2 warpgroups][128 rows]
     const int n_mine = (p.n_units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // units of this CTA
     static_assert(2 + 2 * (NK + NV) + 3 * kNQ + 3 <= 32, "barriers fit their 256 bytes");
@@ -386,11 +387,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                     if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
                 }
             }
-            // every copy this warp issued has landed before the CTA can exit
+            // every copy this warp issued has landed before the CTA can exit (K's: all that is
+            // issued is contracted, or settle_pair waits for it below)
             if (lane == 0) {
                 if (warp == 8 && q_loads > 0) (void)mbar_wait(q_full, (q_loads - 1) & 1);
-                for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i)
-                    (void)mbar_wait(&full[i % NSL], (i / NSL) & 1);
+                if (is_v) {
+                    for (int i = issued > NSL ? issued - NSL : 0; i < issued; ++i) (void)mbar_wait(&full[i % NSL], (i / NSL) & 1);
+                } else {
+                    issued_s[warp == 10] = issued;
+                }
             }
         } else {
             // ===================== MMA issuer =====================
@@ -714,6 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     // everyone meets here before the TMEM is released
     tc_fence_before();
     __syncthreads();
+    if (*abort_flag && (warp == 8 || warp == 10) && lane == 0) settle_pair(issued_s[warp == 10], issued_s[warp != 10], k_full, NK);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
