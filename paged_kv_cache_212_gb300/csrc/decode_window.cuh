@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
     const int hkv = a.n_kv_heads, G = a.group, bs = a.block_size;
     const int rank = (int)(blockIdx.x % a.splits), unit = (int)(blockIdx.x / a.splits);
     const int s = unit / hkv, h = unit % hkv;
-    const bool step = a.k_new != nullptr;
+    const bool step = RUNS == kNoRuns && a.k_new != nullptr;
     const int32_t *trow = a.tables + (int64_t)s * a.max_blocks;
     uint8_t *my_ring = ring + (size_t)warp * S::kStages * S::kStage;
     uint8_t *new_rows = ring + (size_t)WARPS * S::kStages * S::kStage + (S::kShared ? 0 : warp) * 2 * S::kRow;   // a step's K and V row
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(32 * WARPS, INT8 && WARPS == 4 ? 4 : 1) decode
         uint8_t *q_s = S::kShared ? new_rows + 2 * S::kRow : my_ring + (S::kStages - 1) * S::kStage;
         const int slot = lane % SLOTS;
         int v0, v1;
-        const bool turn = rope_vectors(a.rope, slot, v0, v1);
+        const bool turn = rope_vectors(a.rope, slot, v0, v1) && RUNS == kNoRuns;
         // row it * PER + lane / SLOTS of the queries; the last round is K and V
         auto source = [&](int it) -> const __nv_bfloat16 * {
             const int r = it * PER + lane / SLOTS;
@@ -995,20 +995,26 @@ template <int D, bool INT8, bool WIDE, int RUNS = kNoRuns>
 cudaError_t launch_sized(WindowArgs &a, int64_t units, int64_t tiles, int sms, cudaStream_t stream)
 {
     Choice c4, c2, c8;
-    cudaError_t e = choose<D, INT8, WIDE, RUNS, 4>(units, tiles, sms, &c4);
-    if (e != cudaSuccess) return e;
-    e = choose<D, INT8, WIDE, RUNS, 2>(units, tiles, sms, &c2);
-    if (e != cudaSuccess) return e;
-    e = choose<D, INT8, WIDE, RUNS, 8>(units, tiles, sms, &c8);
-    if (e != cudaSuccess) return e;
-    if (RUNS == kWhole && tiles > 64) return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
-    if (RUNS == kRest) return launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
-    const bool alone = c8.splits == 1 && c4.splits > 1 && c8.share <= c4.share;
-    if (units <= c8.places && (alone || c8.share < c4.share || (units * c4.splits > sms && c8.room <= c4.room)))
-        return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
-    const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
-    return small ? launch_as<D, INT8, WIDE, RUNS, 2>(a, c2, units, sms, stream)
-                 : launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
+    cudaError_t e = cudaSuccess;
+    if constexpr (RUNS == kRest) {
+        e = choose<D, INT8, WIDE, RUNS, 4>(units, tiles, sms, &c4);
+        if (e != cudaSuccess) return e;
+        return launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
+    } else {
+        e = choose<D, INT8, WIDE, RUNS, 8>(units, tiles, sms, &c8);
+        if (e != cudaSuccess) return e;
+        if (RUNS == kWhole && tiles > 64) return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
+        e = choose<D, INT8, WIDE, RUNS, 4>(units, tiles, sms, &c4);
+        if (e != cudaSuccess) return e;
+        e = choose<D, INT8, WIDE, RUNS, 2>(units, tiles, sms, &c2);
+        if (e != cudaSuccess) return e;
+        const bool alone = c8.splits == 1 && c4.splits > 1 && c8.share <= c4.share;
+        if (units <= c8.places && (alone || c8.share < c4.share || (units * c4.splits > sms && c8.room <= c4.room)))
+            return launch_as<D, INT8, WIDE, RUNS, 8>(a, c8, units, sms, stream);
+        const bool small = units > c4.places ? c2.room <= c4.room : 5 * c2.room < 4 * c4.room;
+        return small ? launch_as<D, INT8, WIDE, RUNS, 2>(a, c2, units, sms, stream)
+                     : launch_as<D, INT8, WIDE, RUNS, 4>(a, c4, units, sms, stream);
+    }
 }
 
 // The constants of the kernel's block lookup.
