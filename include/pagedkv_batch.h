@@ -116,12 +116,21 @@ size_t pkv_rows_workspace_bytes(int32_t n_rows, int32_t n_q_heads, int32_t head_
  * Starts that decrease or pass n_rows: PKV_DEV_BAD_LENGTH, outputs undefined.
  * Rows are contracted all at once, up to 256 of a sequence in one product, or,
  * where that is less work, one by one, with up to 8 query heads per kv head (the
- * same results within the tolerances).  A call of as many rows as sequences is
+ * same results within the bounds below).  A call of as many rows as sequences is
  * taken for a step, of a row each, and goes one by one; where most of the rows
  * are a few sequences', one row more (of no sequence) sends those at once.
  * PKV_ROWS_IMPL in the environment, read at every call here and in
  * paged_decode_attention_shared, takes a way: all, one, or both (sequences or
  * groups of few rows one by one, the others at once).
+ * Rounding: scores, maxima, sums and unfinished outputs are binary32, outputs are
+ * rounded once to bf16.  bf16 pages: probabilities are rounded to bf16 (2^-8 of
+ * each) at once, as in the prefills, and held to 2^-16 one by one.  int8 pages:
+ * at once, probabilities and values (code times scale) are rounded to fp16, 2^-11
+ * of each, where probabilities below 2^-21 are held to 2^-32 and values of a scale below 2^-13 of the largest V scale of their kv
+ * head in the sequence (or the group's prefix) to 2^-24 of that scale; one by
+ * one, queries are rounded to fp16 multiples of a power of two of their own
+ * (bf16 queries exactly but for elements below 2^-17 of the largest) and the
+ * weights, each with its scale, held to 2^-22, whatever the other scales are.
  */
 int paged_cross_attention(const pkv_bf16 *q, int64_t q_stride, int32_t n_q_heads, const int32_t *q_starts,
                           int32_t n_rows, const void *k_pool, const void *v_pool, const float *k_scales,

@@ -118,6 +118,58 @@ def test_shared_passes_nan_on(P, int8, rows_impl):     # noqa: F811
             check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, int8)
 
 
+# ---- scales far apart ------------------------------------------------------------------------------
+
+def _most(impl, scales):
+    """What check_rows adds for values far below the largest scale: nothing one by one."""
+    return 0.0 if impl == "one" else float(scales.max())
+
+
+@pytest.mark.parametrize("ramp", [(-6, 2), (2, -6), (-20, -14), (25, 30)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_cross_over_scales_one_by_one(P, d, ramp, monkeypatch):     # noqa: F811
+    """V scales over many orders of magnitude: one by one they join the weights, so that the bound has
+    no term of the largest scale."""
+    monkeypatch.setenv("PKV_ROWS_IMPL", "one")
+    hkv, group, bs, scale, n = 2, 3, 16, d ** -0.5, 900
+    pages = Paged(9, 60, hkv, d, bs, True)
+    row, (k, _) = pages.add(0, n, 60)
+    slots = _rows_of(row, 0, n, bs)
+    flat = pages.scales[1].view(-1, hkv)
+    flat[slots] = (flat[slots].double() * 10.0 ** torch.linspace(*ramp, n)[:, None]).float()
+    v = pages.pools[1].view(-1, hkv, d)[slots].double() * flat[slots].double()[..., None]
+    kp, vp, ks, vs = pages.cuda()
+    q = torch.randn((40, hkv * group, d), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    lse = torch.empty((40, hkv * group), device="cuda")
+    out = P.paged_cross_attention(q, _ints([0, 40]), kp, vp, row.view(1, -1).cuda(), _ints([n]), scale, k_scales=ks, v_scales=vs, lse_out=lse)
+    check_rows(out, lse, q, k, v, scale, True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("small_first", [False, True])
+def test_cross_that_sees_the_small_scales_alone(P, d, small_first, rows_impl):     # noqa: F811
+    """Queries whose weight lies on one key, of a V scale 2^-28 of the others': rows at once hold its
+    values to 2^-24 of the largest scale, rows one by one to 2^-11 of themselves."""
+    hkv, group, bs, scale, n = 2, 3, 16, d ** -0.5, 600
+    pages = Paged(11, 40, hkv, d, bs, True)
+    row, _ = pages.add(0, n, 40)
+    slots = _rows_of(row, 0, n, bs)
+    small = torch.arange(n) == (0 if small_first else n - 1)
+    gen = torch.Generator().manual_seed(1)
+    codes, sk, sv = pages.pools[0].view(-1, hkv, d), pages.scales[0].view(-1, hkv), pages.scales[1].view(-1, hkv)
+    codes[slots] = torch.where(small[:, None, None], torch.randint(80, 128, (n, hkv, d), generator=gen),
+                               torch.randint(-127, -79, (n, hkv, d), generator=gen)).to(torch.int8)
+    sk[slots] = 0.02
+    sv[slots] = torch.where(small[:, None], 0.01 * 2.0 ** -28, 0.01).expand(n, hkv).contiguous()
+    k = codes[slots].double() * sk[slots].double()[..., None]
+    v = pages.pools[1].view(-1, hkv, d)[slots].double() * sv[slots].double()[..., None]
+    kp, vp, ks, vs = pages.cuda()
+    q = (torch.rand((170, hkv * group, d), generator=gen) + 3).to(torch.bfloat16).cuda()     # scores 70 apart or more
+    lse = torch.empty((170, hkv * group), device="cuda")
+    out = P.paged_cross_attention(q, _ints([0, 170]), kp, vp, row.view(1, -1).cuda(), _ints([n]), scale, k_scales=ks, v_scales=vs, lse_out=lse)
+    check_rows(out, lse, q, k, v, scale, True, _most(rows_impl, sv[slots]))
+
+
 # ---- the way that a call takes ---------------------------------------------------------------------
 
 @pytest.mark.parametrize("int8", [False, True])
