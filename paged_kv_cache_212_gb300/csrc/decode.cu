@@ -531,9 +531,10 @@ __global__ void __launch_bounds__(128, kMergeCtasPerSm) decode_merge_kernel(Deco
     const int64_t n_warps = (int64_t)gridDim.x * (blockDim.x >> 5);
     const int64_t idx0 = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
     // the plan's results are read before the wait: the first pair's pieces
-    // (with one pair per warp, the only ones) and the overflow flag
-    const uint32_t overflow = ws.header[kHdrOverflow];
-    const int2 sg0 = idx0 < n_pairs ? ws.seg[idx0 / n_q_heads] : make_int2(0, 0);
+    // (with one pair per warp, the only ones) and the overflow flag; past the
+    // L1, which may still have those of the step before
+    const uint32_t overflow = __ldcg(ws.header + kHdrOverflow);
+    const int2 sg0 = idx0 < n_pairs ? __ldcg(ws.seg + idx0 / n_q_heads) : make_int2(0, 0);
     grid_dependency_wait();
     if (overflow != 0) return;
     const uint64_t drop = l2_evict_first_policy();
