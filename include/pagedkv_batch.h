@@ -126,9 +126,9 @@ size_t pkv_rows_workspace_bytes(int32_t n_rows, int32_t n_q_heads, int32_t head_
  * rounded once to bf16.  bf16 pages: probabilities are rounded to bf16 (2^-8 of
  * each) at once, as in the prefills, and held to 2^-16 one by one.  int8 pages:
  * at once, probabilities and values (code times scale) are rounded to fp16, 2^-11
- * of each, where probabilities below 2^-21 are held to 2^-32 and values of a scale below 2^-13 of the largest V scale of their kv
- * head in the sequence (or the group's prefix) to 2^-24 of that scale; one by
- * one, queries are rounded to fp16 multiples of a power of two of their own
+ * of each, where probabilities below 2^-21 are held to 2^-32 and values of a
+ * scale below 2^-13 of the largest V scale of their kv head in the sequence (or
+ * the group's prefix) to 2^-24 of that scale; one by one, queries are rounded to fp16 multiples of a power of two of their own
  * (bf16 queries exactly but for elements below 2^-17 of the largest) and the
  * weights, each with its scale, held to 2^-22, whatever the other scales are.
  */

@@ -21,11 +21,11 @@
 // rounding to bf16 makes 0.0016.
 //
 // Measured.  4135 queries of 8 sequences, 1000 to 8191 keys, 32 query and 8 kv heads of 128:
-// 165 us (175 under the power cap of a long run), 1.17 PFLOP/s of needed work; a tile of 128
+// 163 us (174 to 178 under the power cap of a long run), 1.09 to 1.18 PFLOP/s of needed work; a tile of 128
 // keys takes 1.52 us (1.68 PFLOP/s on 152 SMs), bound by the chain of S, softmax and P V of a
 // query tile, a change of unit 3.2 us more (the output's stores, the next queries' load), the
-// start 8 us and the join 8.  64 sequences behind 4096 tokens: 32 us.  1642 queries over int8
-// pages, 24 and 8 heads of 64: 39.8 us; the same 4135 queries over int8 pages 331 us, 3.2 us a
+// start 8 us and the join 8.  64 sequences behind 4096 tokens: 34 us.  1642 queries over int8
+// pages, 24 and 8 heads of 64: 39.8 us; the same 4135 queries over int8 pages 338 us, 3.3 us a
 // tile, bound by the warps that widen the codes.
 #include <math.h>
 

@@ -6,7 +6,7 @@
 // row's slot is loaded beside them, so that the only dependent access is the store.
 // Lanes of a head row (4 or 8 of them) share its largest element.
 //
-// Measured: 9550 rows of 8 heads of 128 12.5 us, 6.3 TB/s = 92 % of the copy rate; into int8
+// Measured: 9550 rows of 8 heads of 128 12.5 to 13.7 us, 84 to 92 % of the copy rate; into int8
 // pages 15.0 to 16.1, 55 to 58 %, with 32 warps of 64 registers on an SM; 64 rows 1.6 and 1.9.
 // Not faster: K and V of a piece in one thread (14.3, 18.5), persistent threads that load a
 // piece ahead (13.7, 21.8), fewer registers (spills: 23 to 30).
