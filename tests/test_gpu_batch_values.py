@@ -1,5 +1,5 @@
 """The calls for ragged batches over values that are no numbers, that a sequence must not see, or
-whose scales are far apart."""
+whose scales are far apart; head counts and alignments at their limits; the way that a call takes."""
 import pytest
 import torch
 
@@ -168,6 +168,50 @@ def test_cross_that_sees_the_small_scales_alone(P, d, small_first, rows_impl):  
     lse = torch.empty((170, hkv * group), device="cuda")
     out = P.paged_cross_attention(q, _ints([0, 170]), kp, vp, row.view(1, -1).cuda(), _ints([n]), scale, k_scales=ks, v_scales=vs, lse_out=lse)
     check_rows(out, lse, q, k, v, scale, True, _most(rows_impl, sv[slots]))
+
+
+# ---- heads and alignment ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group", [9, 11, 13, 15, 16])
+def test_cross_of_many_heads_and_outputs_of_16_bytes(P, group, d, int8):     # noqa: F811
+    """9 to 16 query heads per kv head, which do not divide a product's 128 rows; whole and cut runs;
+    outputs and queries aligned to 16 bytes and no more."""
+    hkv, bs, scale, n_q, keys = 2, 16, d ** -0.5, [1, 40, 3], [700, 2300, 100]
+    hq, total = hkv * group, 44
+    pages = Paged(group, sum(-(-x // bs) for x in keys) + 1, hkv, d, bs, int8)
+    added = [pages.add(0, x, 150) for x in keys]
+    kp, vp, ks, vs = pages.cuda()
+    gen = torch.Generator().manual_seed(5)
+    q = torch.randn(total * hq * d + 8, generator=gen).to(torch.bfloat16).cuda()[8:].view(total, hq, d)
+    out = torch.zeros(total * hq * d + 8, dtype=torch.bfloat16, device="cuda")[8:].view(total, hq, d)
+    assert q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+    lse, st = torch.zeros((total, hq), device="cuda"), _status()
+    starts, tables = _ints([0, 1, 41, 44]), torch.stack([t for t, _ in added]).cuda()
+    P.paged_cross_attention(q, starts, kp, vp, tables, _ints(keys), scale, k_scales=ks, v_scales=vs, out=out, lse_out=lse, dev_status=st)
+    assert int(st.item()) == 0
+    for s, (a, b) in enumerate(((0, 1), (1, 41), (41, 44))):
+        check_rows(out[a:b], lse[a:b], q[a:b], *added[s][1], scale, int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+def test_rows_into_outputs_of_16_bytes(P, int8, rows_impl):     # noqa: F811
+    """Runs of one tile, which are whole, and outputs aligned to 16 bytes and no more, both calls."""
+    hkv, group, d, bs, scale = 2, 4, 64, 16, 0.125
+    pages, tables, ctx, starts, ptables, values = _shared_case([30, 5], [100, 128], [i % 20 for i in range(35)], 0, hkv, d, bs, int8, 8)
+    kp, vp, ks, vs = pages.cuda()
+    q = torch.randn((35, hkv * group, d), generator=torch.Generator().manual_seed(3)).to(torch.bfloat16).cuda()
+    out = torch.zeros(q.numel() + 8, dtype=torch.bfloat16, device="cuda")[8:].view(q.shape)
+    lse = torch.zeros((35, hkv * group), device="cuda")
+    prefixes = _ints([100, 128])
+    P.paged_decode_attention_shared(q, kp, vp, tables.cuda(), _ints(ctx), _ints(starts), ptables.cuda(), prefixes, scale, k_scales=ks,
+                                    v_scales=vs, out=out, lse_out=lse)
+    for s in range(35):
+        check_rows(out[s:s + 1], lse[s:s + 1], q[s:s + 1], *values[s], scale, int8)
+    P.paged_cross_attention(q, _ints(starts), kp, vp, ptables.cuda(), prefixes, scale, k_scales=ks, v_scales=vs, out=out, lse_out=lse)
+    for (a, b), n in zip(((0, 30), (30, 35)), (100, 128)):
+        check_rows(out[a:b], lse[a:b], q[a:b], *(x[:n] for x in values[a]), scale, int8)
 
 
 # ---- the way that a call takes ---------------------------------------------------------------------
