@@ -239,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
     // Half units: a warp of one softmax warpgroup meets the one with the same rows of the
     // other; their maxima and sums go through the second Q tile, which a half unit leaves.
     __shared__ uint64_t pair_bar[4];
+    // Half units: P of an even and of an odd tile is in TMEM.  S of the tile behind is ready before
+    // that, so that a warp can be done with it while another one still is at this tile: with one
+    // barrier its second arrival would count for the other warp's first.
+    __shared__ uint64_t p_half[2];
     __shared__ int32_t issued_s[2];                         // tiles that the K producers issued
     float *pair_s = reinterpret_cast<float *>(q_s + kQTile);   // [2][2 warpgroups][128 rows]
     const int n_mine = (p.n_units - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;   // units of this CTA
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
             mbar_init(&o_done[i], 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 2);
+        for (int i = 0; i < 2; ++i) mbar_init(&p_half[i], 8);
         mbar_init(fin_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -509,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
 #pragma unroll 1
                 for (int j = -1; j < n_kt; ++j) {   // P V of tile j, S of tile j + 2
                     if (j >= 0) {
-                        ok = wait(&v_full[vs], v_phase) && wait(&p_full[0], phase) && wait(&p_full[1], phase);
+                        ok = wait(&v_full[vs], v_phase) && wait(&p_half[j & 1], (j / 2) & 1);
                         if (!ok) break;
                         tc_fence_after();
                         issue_o(0, j & 1, vs, j > 0);
@@ -695,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_window_kernel(const __gri
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[qt]);
+                if (lane == 0) mbar_arrive(&p_half[j & 1]);
             }
             if (ok) {
                 const float other = swap(n_kt, l);
