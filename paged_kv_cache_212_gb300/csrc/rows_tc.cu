@@ -920,7 +920,9 @@ __global__ void __launch_bounds__(Setup<D, INT8>::kThreads, 1) rows_kernel(const
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) p.part.cuts[blockIdx.x] = cut_s;
-    if (*abort_flag && (warp == 8 || warp == 10) && lane == 0) settle_pair(issued_s[warp == 10], issued_s[warp != 10], k_codes, NK);
+    // (unequal without a wait that ran out: lengths that changed while the two read them)
+    if ((*abort_flag || issued_s[0] != issued_s[1]) && (warp == 8 || warp == 10) && lane == 0)
+        settle_pair(issued_s[warp == 10], issued_s[warp != 10], k_codes, NK);
     if (warp == 9) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
